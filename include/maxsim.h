@@ -54,13 +54,14 @@ typedef enum {
     MAXSIM_ERR_DEVICE_INPUT = 6  /* device: an input failed a device-side check */
 } maxsim_status;
 
-typedef enum { MAXSIM_F16 = 0, MAXSIM_BF16 = 1 } maxsim_dtype;
+/* MAXSIM_F32 is taken only where an entry point says so. */
+typedef enum { MAXSIM_F16 = 0, MAXSIM_BF16 = 1, MAXSIM_F32 = 2 } maxsim_dtype;
 
 /* Operation codes for maxsim_workspace_size(). */
 enum { MAXSIM_OP_FWD = 0, MAXSIM_OP_FWD_VARLEN = 1, MAXSIM_OP_BWD = 2, MAXSIM_OP_FWD_INT8 = 3,
        MAXSIM_OP_SCORE_PAIRS = 4, MAXSIM_OP_CHAMFER_FWD = 5, MAXSIM_OP_CHAMFER_BWD = 6,
        MAXSIM_OP_TWO_STAGE = 7, MAXSIM_OP_FWD_STREAMED = 8, MAXSIM_OP_BWD_VARLEN = 9,
-       MAXSIM_OP_FWD_VARLEN_STREAMED = 10 };
+       MAXSIM_OP_FWD_VARLEN_STREAMED = 10, MAXSIM_OP_LINEAR_INT8 = 11 };
 
 /*
  * Dense forward.
@@ -340,6 +341,81 @@ maxsim_status maxsim_fwd_varlen_streamed(const void *Q, const int32_t *cu_seqlen
                                          float *scores, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * The token head: what lies between an encoder's hidden states and the
+ * scoring above. In serving it runs on 8-bit integers (quantise the hidden
+ * states per token and the weights per channel, maxsim_linear_int8, then
+ * quantise the embeddings with `normalize`: the rows and scales that
+ * maxsim_fwd_int8 and maxsim_two_stage_topk read); in training with dropout
+ * on the hidden states.
+ *
+ * These entry points take matrices whose rows are `ld` elements apart
+ * (ld >= the row's length), with each pointer aligned to its element; rows on
+ * 16-byte boundaries are faster. An output must not overlap an input unless
+ * its comment says so.
+ */
+
+/*
+ * Symmetric row quantisation to INT8.
+ *   x      [rows, cols] f16 / bf16 / f32, rows ld_x elements apart
+ *   q      [rows, cols] i8 (out), rows ld_q bytes apart
+ *   scale  [rows] f32 (out)
+ *   a = max |x|;  s = max(a / 127, 2^-126);  q = clamp(rint(x / s), -127, 127)
+ * with fp32 division and ties to even. scale is s, so that q * scale is the
+ * quantised row; with `normalize` (nonzero) it is 1 / ||x / s||_2, so that
+ * q * scale is the quantised row of unit length. A row of zeros gives q = 0
+ * and scale = 2^-126 either way (the scoring wants a positive scale). A row
+ * that holds a NaN or an infinity gives q = 0 and scale = NaN.
+ * 0 <= rows, cols < 2^31.
+ */
+maxsim_status maxsim_quantize_rows(const void *x, maxsim_dtype dtype, int64_t rows, int64_t cols, int64_t ld_x,
+                                   int normalize, int8_t *q, int64_t ld_q, float *scale, void *stream);
+
+/*
+ * Matrix product of 8-bit integers with a scale for each token and channel:
+ *   out[m, n] = (sum_k x[m, k] * w[n, k]) * x_scale[m] * w_scale[n] + bias[n]
+ *   x [M, K] i8, rows ld_x apart;  x_scale [M] f32
+ *   w [N, K] i8, rows ld_w apart;  w_scale [N] f32;  bias [N] f32 or NULL
+ *   out [M, N] f16 / bf16 / f32 (out_dtype), rows ld_out elements apart
+ * All of [-128, 127] is taken. Up to 64 tokens the sum is an exact 32-bit
+ * integer; beyond, 16-bit tensor-core products are summed in fp32 (products
+ * are exact, sums are exact while they stay below 2^24). K = 0 gives the bias.
+ * Scales and bias need 4-byte alignment. 0 <= M, N < 2^31, K <= 131071.
+ * An operand whose pointer, row stride or K is not a multiple of 16 is copied
+ * into the workspace first. Workspace: maxsim_workspace_size(
+ * MAXSIM_OP_LINEAR_INT8, M, N, K, ld_x, ld_w), with 1 in the place of the
+ * stride of an operand whose pointer is not 16-byte aligned; 256-byte aligned.
+ */
+maxsim_status maxsim_linear_int8(const int8_t *x, int64_t ld_x, const float *x_scale, const int8_t *w, int64_t ld_w,
+                                 const float *w_scale, const float *bias, int64_t M, int64_t N, int64_t K,
+                                 maxsim_dtype out_dtype, void *out, int64_t ld_out, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/*
+ * Dropout from a counter-based generator; the mask is never stored.
+ *   x, residual, y  [rows, cols] f16 / bf16 / f32, rows ld elements apart
+ *   y[i] = (keep_i ? x[i] * s : 0) + residual[i]     (residual may be NULL)
+ * With T = rint(p * 65536): element i of the row-major [rows, cols] matrix
+ * (whatever its strides) draws the 16 bits u_i and is kept when u_i >= T, and
+ * s = 65536 / (65536 - T) as fp32. u_i is half i % 2 (low half first) of word
+ * (i % 8) / 2 of Philox4x32-10 (Salmon et al., "Parallel random numbers: as
+ * easy as 1, 2, 3", 2011) with key = (seed low, seed high) and counter =
+ * (b low, b high, offset low, offset high), b = i / 8. Calls that must draw
+ * independent masks differ in seed or offset; the backward takes its
+ * forward's. A dropped NaN or infinity gives 0. p in [0, 1]; p = 1 drops all.
+ * y may be x or residual itself (same pointer and stride).
+ */
+maxsim_status maxsim_dropout_fwd(const void *x, maxsim_dtype dtype, int64_t rows, int64_t cols, int64_t ld_x,
+                                 const void *residual, int64_t ld_residual, double p, uint64_t seed, uint64_t offset,
+                                 void *y, int64_t ld_y, void *stream);
+
+/*
+ * Its gradient in x, from the same p, seed and offset: dx[i] = keep_i ? grad[i] * s : 0.
+ * (The gradient in residual is grad itself.) dx may be grad itself.
+ */
+maxsim_status maxsim_dropout_bwd(const void *grad, maxsim_dtype dtype, int64_t rows, int64_t cols, int64_t ld_grad,
+                                 double p, uint64_t seed, uint64_t offset, void *dx, int64_t ld_dx, void *stream);
+
+/*
  * Bytes of device workspace an operation needs for a shape (0 if none).
  *   MAXSIM_OP_FWD / MAXSIM_OP_FWD_INT8: (Nq, Lq, Nd, Ld, dim)
  *   MAXSIM_OP_FWD_VARLEN:              (Nq, max_lq, Nd, total_d, dim); assumes
@@ -356,6 +432,7 @@ maxsim_status maxsim_fwd_varlen_streamed(const void *Q, const int32_t *cu_seqlen
  *                                      the CSR outputs are NULL (an upper bound)
  *   MAXSIM_OP_FWD_VARLEN_STREAMED:     (Nq, max_lq, block_docs, block_tokens, dim);
  *                                      independent of the corpus size
+ *   MAXSIM_OP_LINEAR_INT8:             (M, N, K, ld_x, ld_w)
  * Returns (size_t)-1 for an invalid shape.
  */
 size_t maxsim_workspace_size(int op, int64_t Nq, int64_t Lq, int64_t Nd, int64_t Ld, int64_t dim);

@@ -27,11 +27,12 @@ STATUS = {
 
 OP_FWD, OP_FWD_VARLEN, OP_BWD, OP_FWD_INT8, OP_SCORE_PAIRS = 0, 1, 2, 3, 4
 OP_CHAMFER_FWD, OP_CHAMFER_BWD, OP_TWO_STAGE, OP_FWD_STREAMED, OP_BWD_VARLEN = 5, 6, 7, 8, 9
-OP_FWD_VARLEN_STREAMED = 10
-F16, BF16 = 0, 1
+OP_FWD_VARLEN_STREAMED, OP_LINEAR_INT8 = 10, 11
+F16, BF16, F32 = 0, 1, 2
 
 # Every symbol the header declares, with its ctypes signature.
 _I64, _VP, _SZ, _I = ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
+_U64, _D = ctypes.c_uint64, ctypes.c_double
 SIGNATURES = {
     "maxsim_fwd": (_I, [_VP, _VP, _I, _I64, _I64, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
     "maxsim_fwd_varlen": (_I, [_VP, _VP, _I64, _VP, _VP, _I64, _I, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP, _SZ,
@@ -54,6 +55,10 @@ SIGNATURES = {
                                         _VP, _SZ, _VP]),
     "maxsim_two_stage_topk": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _I, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _VP,
                                    _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "maxsim_quantize_rows": (_I, [_VP, _I, _I64, _I64, _I64, _I, _VP, _I64, _VP, _VP]),
+    "maxsim_linear_int8": (_I, [_VP, _I64, _VP, _VP, _I64, _VP, _VP, _I64, _I64, _I64, _I, _VP, _I64, _VP, _SZ, _VP]),
+    "maxsim_dropout_fwd": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _I64, _D, _U64, _U64, _VP, _I64, _VP]),
+    "maxsim_dropout_bwd": (_I, [_VP, _I, _I64, _I64, _I64, _D, _U64, _U64, _VP, _I64, _VP]),
     "maxsim_workspace_size": (_SZ, [_I, _I64, _I64, _I64, _I64, _I64]),
     "maxsim_status_string": (ctypes.c_char_p, [_I]),
     "maxsim_device_status": (_I, [_VP]),

@@ -79,3 +79,21 @@ def maxsim_varlen(Q: torch.Tensor, cu_seqlens_q, max_lq: int, D: torch.Tensor, c
     """Differentiable MaxSim over packed documents (and optionally packed
     queries): scores [Nq, Nd]."""
     return _MaxSimVarlen.apply(Q, cu_seqlens_q, max_lq, D, cu_seqlens_d, max_ld)
+
+
+class _Dropout(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, p, seed, offset):
+        ctx.args = (p, seed, offset)
+        return ops.dropout_fwd(x, p, seed, offset, residual)
+
+    @staticmethod
+    def backward(ctx, grad):
+        dx = ops.dropout_bwd(grad, *ctx.args) if ctx.needs_input_grad[0] else None
+        return dx, grad if ctx.needs_input_grad[1] else None, None, None, None
+
+
+def dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0, residual=None) -> torch.Tensor:
+    """Differentiable dropout of x (plus `residual` where given): nothing is
+    saved but (p, seed, offset), from which the backward draws the mask again."""
+    return _Dropout.apply(x, residual, p, seed, offset)

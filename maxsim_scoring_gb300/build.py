@@ -13,7 +13,7 @@ LIB = os.path.join(HERE, "libmaxsim.so")
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
     "-lineinfo", "-O3", "-std=c++17",
-    "-Xcompiler", "-fPIC", "-shared",
+    "-Xcompiler", "-fPIC",
     "-I", os.path.join(ROOT, "include"),
 ]
 
@@ -23,7 +23,8 @@ def _sources():
 
 
 def _inputs():
-    return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [os.path.join(ROOT, "include", "maxsim.h")]
+    return (_sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")))
+            + [os.path.join(ROOT, "include", "maxsim.h")])
 
 
 def up_to_date() -> bool:
@@ -38,11 +39,24 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *NVCC_FLAGS, "-o", tmp, *_sources()]
-    if verbose:
-        print(" ".join(cmd))
-    subprocess.check_call(cmd)
-    os.replace(tmp, LIB)
+    # the translation units side by side, then one link
+    objects = [(src, f"{tmp}.{os.path.basename(src)}.o") for src in _sources()]
+    cmds = [[nvcc, *NVCC_FLAGS, "-c", "-o", obj, src] for src, obj in objects]
+    link = [nvcc, *NVCC_FLAGS, "-shared", "-o", tmp, *(obj for _, obj in objects)]
+    try:
+        if verbose:
+            print("\n".join(" ".join(cmd) for cmd in [*cmds, link]))
+        running = [subprocess.Popen(cmd) for cmd in cmds]
+        codes = [p.wait() for p in running]
+        for cmd, code in zip(cmds, codes):
+            if code != 0:
+                raise subprocess.CalledProcessError(code, cmd)
+        subprocess.check_call(link)
+        os.replace(tmp, LIB)
+    finally:
+        for _, obj in objects:
+            if os.path.exists(obj):
+                os.remove(obj)
     return LIB
 
 

@@ -12,6 +12,7 @@
 #include <mutex>
 
 #include "maxsim.h"
+#include "host_util.h"
 #include "bwd_kernels.cuh"
 #include "chamfer_kernels.cuh"
 #include "chamfer_tc.cuh"
@@ -45,9 +46,6 @@ DeviceInfo g_dev[kMaxDevices];
 // forward launch.
 std::atomic<uint64_t> g_inject_wait_ns{0};
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiledFn g_encode = nullptr;
 
 maxsim_status device_info(DeviceInfo** out) {
@@ -1157,6 +1155,18 @@ maxsim_status run_bwd(const void* Q, const int32_t* cu_q, int64_t Lq, const void
 }  // namespace
 }  // namespace maxsim
 
+maxsim_status maxsim::host_device(HostDevice* out) {
+    DeviceInfo* dev = nullptr;
+    const maxsim_status rc = device_info(&dev);
+    if (rc != MAXSIM_OK) return rc;
+    if (cudaGetDevice(&out->index) != cudaSuccess) return MAXSIM_ERR_CUDA;
+    out->num_sms = dev->num_sms;
+    out->smem_optin = dev->smem_optin;
+    out->status = dev->status;
+    out->encode = g_encode;
+    return MAXSIM_OK;
+}
+
 using namespace maxsim;
 
 extern "C" {
@@ -1237,6 +1247,8 @@ size_t maxsim_workspace_size(int op, int64_t Nq, int64_t Lq, int64_t Nd, int64_t
     case MAXSIM_OP_CHAMFER_BWD:
         if (check_chamfer_shape(Nq, Lq, Nd, dim) == MAXSIM_ERR_INVALID_ARG) return static_cast<size_t>(-1);
         return plan_chamfer_bwd(Nq, Lq, Nd).ws_bytes;
+    case MAXSIM_OP_LINEAR_INT8:  // (M, N, K, ld_x, ld_w)
+        return linear_int8_ws_bytes(Nq, Lq, Nd, Ld, dim);
     default: return static_cast<size_t>(-1);
     }
 }

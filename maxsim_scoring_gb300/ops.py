@@ -7,6 +7,7 @@ CUDA kernels behind that call.
 """
 from __future__ import annotations
 
+import ctypes
 from typing import Optional
 
 import torch
@@ -14,6 +15,10 @@ import torch
 from . import _native
 
 _DT = {torch.float16: _native.F16, torch.bfloat16: _native.BF16}
+_DT_ANY = {**_DT, torch.float32: _native.F32}
+
+
+_SIZE_MAX = ctypes.c_size_t(-1).value
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -52,8 +57,7 @@ def workspace_size(op: int, Nq: int, Lq: int, Nd: int, Ld: int, dim: int) -> int
 
 
 def ctypes_size_max() -> int:
-    import ctypes
-    return ctypes.c_size_t(-1).value
+    return _SIZE_MAX
 
 
 def _workspace(nbytes: int, device, ws: Optional[torch.Tensor]):
@@ -407,6 +411,139 @@ def maxsim_fwd_varlen_streamed(Q: torch.Tensor, cu_seqlens_q: Optional[torch.Ten
                                                   _stream(dev))
     _native.check(rc, "maxsim_fwd_varlen_streamed")
     return scores
+
+
+def _rows(t: torch.Tensor, name: str):
+    """(tensor, rows, cols, row stride) of a CUDA tensor [..., cols] whose rows
+    the library can read in place; copied where its strides do not allow it."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() == 0:
+        raise ValueError(f"{name} must have at least one dimension")
+    cols = t.shape[-1]
+    if not t.is_contiguous():
+        # rows one fixed stride apart (a slice of a wider buffer) are read where they are
+        ld = t.stride(-2) if t.dim() > 1 else cols
+        if cols and t.stride(-1) == 1 and ld >= cols and all(
+                t.stride(i) == t.stride(i + 1) * t.shape[i + 1] for i in range(t.dim() - 2)):
+            return t, t.numel() // cols, cols, ld
+        t = t.contiguous()
+    return t, (t.numel() // cols if cols else t.shape[:-1].numel()), cols, cols
+
+
+def _given(out: Optional[torch.Tensor], name: str, shape, dtype, device):
+    """The caller's output buffer, checked, or a new one: contiguous rows."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if out.shape != shape or out.dtype != dtype or out.device != device or not out.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return out
+
+
+def quantize_rows(x: torch.Tensor, *, normalize: bool = False, q: Optional[torch.Tensor] = None,
+                  scale: Optional[torch.Tensor] = None):
+    """(q int8, scale f32): symmetric INT8 codes of x [..., K] (f16 / bf16 / f32)
+    with one scale for each row; q * scale[..., None] is the quantised row, or
+    with `normalize` the quantised row of unit L2 length."""
+    dt = _DT_ANY.get(x.dtype)
+    if dt is None:
+        raise TypeError(f"x must be float16, bfloat16 or float32, got {x.dtype}")
+    shape, dev = x.shape, x.device
+    x, rows, cols, ld = _rows(x, "x")
+    q = _given(q, "q", shape, torch.int8, dev)
+    scale = _given(scale, "scale", shape[:-1], torch.float32, dev)
+    rc = _native.lib().maxsim_quantize_rows(x.data_ptr(), dt, rows, cols, ld, 1 if normalize else 0, q.data_ptr(),
+                                            cols, scale.data_ptr(), _stream(dev))
+    if rc:
+        _native.check(rc, "maxsim_quantize_rows")
+    return q, scale
+
+
+def linear_int8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+                bias: Optional[torch.Tensor] = None, *, out_dtype: torch.dtype = torch.bfloat16,
+                out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """[..., N] in out_dtype: (x @ w.T) * x_scale[..., None] * w_scale + bias for
+    int8 x [..., K] with a scale for each row and int8 w [N, K] with a scale for
+    each channel (as quantize_rows gives them); x_scale, w_scale and bias [N] f32."""
+    dt = _DT_ANY.get(out_dtype)
+    if dt is None:
+        raise TypeError(f"out_dtype must be float16, bfloat16 or float32, got {out_dtype}")
+    if x.dtype != torch.int8 or w.dtype != torch.int8:
+        raise TypeError("x and w must be int8")
+    if x_scale.dtype != torch.float32 or w_scale.dtype != torch.float32 or (
+            bias is not None and bias.dtype != torch.float32):
+        raise TypeError("x_scale, w_scale and bias must be float32")
+    shape, dev = x.shape, x.device
+    x, M, K, ld_x = _rows(x, "x")
+    w, N, Kw, ld_w = _rows(w, "w")
+    if w.dim() != 2 or Kw != K:
+        raise ValueError("w must be [N, K] with x's K")
+    if x_scale.shape != shape[:-1] or w_scale.shape != (N,) or (bias is not None and bias.shape != (N,)):
+        raise ValueError("x_scale must have x's leading shape, w_scale and bias [N]")
+    x_scale, w_scale = x_scale.contiguous(), w_scale.contiguous()
+    if bias is not None:
+        bias = bias.contiguous()
+        if bias.device != dev:
+            raise ValueError(f"bias is on {bias.device}, expected {dev}")
+    if w.device != dev or x_scale.device != dev or w_scale.device != dev:
+        raise ValueError("x, w and their scales must be on one device")
+    out = _given(out, "out", shape[:-1] + (N,), out_dtype, dev)
+    px, pw = x.data_ptr(), w.data_ptr()
+    lib = _native.lib()
+    need = lib.maxsim_workspace_size(_native.OP_LINEAR_INT8, M, N, K, ld_x if px % 16 == 0 else 1,
+                                     max(ld_w, 1) if pw % 16 == 0 else 1)
+    if need == _SIZE_MAX:
+        _native.check(2, "maxsim_linear_int8")
+    ws, nbytes = _workspace(need, dev, workspace)
+    rc = lib.maxsim_linear_int8(px, ld_x, x_scale.data_ptr(), pw, ld_w, w_scale.data_ptr(),
+                                None if bias is None else bias.data_ptr(), M, N, K, dt, out.data_ptr(), N,
+                                None if ws is None else ws.data_ptr(), nbytes, _stream(dev))
+    if rc:
+        _native.check(rc, "maxsim_linear_int8")
+    return out
+
+
+def dropout_fwd(x: torch.Tensor, p: float, seed: int, offset: int = 0, residual: Optional[torch.Tensor] = None, *,
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """x with each element dropped with probability p (in steps of 2**-16) and
+    the kept ones scaled by 1 / (1 - p), plus `residual` where given. The mask
+    is a function of (seed, offset) and the element's place alone: the backward
+    draws it again, and calls that need independent masks take other offsets."""
+    dt = _DT_ANY.get(x.dtype)
+    if dt is None:
+        raise TypeError(f"x must be float16, bfloat16 or float32, got {x.dtype}")
+    shape, dev = x.shape, x.device
+    if residual is not None:
+        if residual.shape != shape or residual.dtype != x.dtype or residual.device != dev:
+            raise ValueError("residual must have x's shape, dtype and device")
+        residual, _, _, ld_r = _rows(residual, "residual")
+        pr = residual.data_ptr()
+    else:
+        pr, ld_r = None, 0
+    x, rows, cols, ld = _rows(x, "x")
+    out = _given(out, "out", shape, x.dtype, dev)
+    rc = _native.lib().maxsim_dropout_fwd(x.data_ptr(), dt, rows, cols, ld, pr, ld_r, p, seed, offset, out.data_ptr(),
+                                          cols, _stream(dev))
+    if rc:
+        _native.check(rc, "maxsim_dropout_fwd")
+    return out
+
+
+def dropout_bwd(grad: torch.Tensor, p: float, seed: int, offset: int = 0, *,
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gradient in x of dropout_fwd(x, p, seed, offset) (that in `residual`
+    is grad itself)."""
+    dt = _DT_ANY.get(grad.dtype)
+    if dt is None:
+        raise TypeError(f"grad must be float16, bfloat16 or float32, got {grad.dtype}")
+    shape, dev = grad.shape, grad.device
+    grad, rows, cols, ld = _rows(grad, "grad")
+    out = _given(out, "out", shape, grad.dtype, dev)
+    rc = _native.lib().maxsim_dropout_bwd(grad.data_ptr(), dt, rows, cols, ld, p, seed, offset, out.data_ptr(), cols,
+                                          _stream(dev))
+    if rc:
+        _native.check(rc, "maxsim_dropout_bwd")
+    return out
 
 
 def device_status(device=None) -> int:
