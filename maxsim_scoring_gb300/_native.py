@@ -77,6 +77,8 @@ class MaxSimError(RuntimeError):
 def lib():
     """The loaded library; raises if it was not built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -16,7 +17,8 @@ namespace maxsim {
 namespace {
 
 constexpr int64_t kI32Max = 2147483647;
-constexpr int64_t kLinearMaxK = 131071;  // 131071 * 128 * 128 < 2^31
+constexpr int64_t kLinearMaxK = 131071;             // 131071 * 128 * 128 < 2^31
+constexpr int64_t kLinearMaxRows = 2147483647 - 1023;  // a tile past the last row still has 32-bit coordinates
 
 inline int elem_bytes(maxsim_dtype t) { return t == MAXSIM_F32 ? 4 : 2; }
 inline bool any_dtype(maxsim_dtype t) { return t == MAXSIM_F16 || t == MAXSIM_BF16 || t == MAXSIM_F32; }
@@ -32,24 +34,88 @@ inline bool rows_fit(int64_t rows, int64_t cols, int64_t ld) {
     return ld >= cols && (rows <= 1 || ld <= (int64_t(1) << 60) / std::max<int64_t>(rows, 1));
 }
 
-template <typename T>
-maxsim_status launch_quantize(const void* x, int64_t rows, int64_t cols, int64_t ld_x, int normalize, int8_t* q,
-                              int64_t ld_q, float* scale, const HostDevice& dev, cudaStream_t st) {
-    quantize_rows_kernel<T><<<grid_of(rows, 1, int64_t(dev.num_sms) * 8), 256, 0, st>>>(
-        static_cast<const T*>(x), rows, static_cast<int32_t>(cols), ld_x, normalize, q, ld_q, scale);
+template <typename T, bool kWide, int kGroup, int kChunks>
+maxsim_status launch_quantize_group(const QuantizeArgs& a, const HostDevice& dev, cudaStream_t st) {
+    constexpr int kThreads = quantize_threads(kGroup);
+    const unsigned grid = grid_of(a.rows, kThreads / kGroup, int64_t(dev.num_sms) * (2048 / kThreads));
+    quantize_rows_kernel<T, kWide, kGroup, kChunks><<<grid, kThreads, 0, st>>>(a);
     return launched();
 }
 
-maxsim_status run_dropout(const DropoutArgs& a, maxsim_dtype dtype, cudaStream_t st) {
+// The smallest group that holds a row: short rows then share a warp (fewer
+// shuffle steps for a row, several rows' loads in flight), long ones take a
+// block.
+template <typename T, bool kWide>
+maxsim_status launch_quantize(const QuantizeArgs& a, const HostDevice& dev, cudaStream_t st) {
+    const int64_t chunks = (a.cols + Chunk<T, kWide>::kVec - 1) / Chunk<T, kWide>::kVec;
+    if (chunks <= 8) return launch_quantize_group<T, kWide, 8, 1>(a, dev, st);
+    if (chunks <= 16) return launch_quantize_group<T, kWide, 8, 2>(a, dev, st);
+    if (chunks <= 32) return launch_quantize_group<T, kWide, 8, 4>(a, dev, st);
+    if (chunks <= 64) return launch_quantize_group<T, kWide, 8, 8>(a, dev, st);
+    if (chunks <= 128) return launch_quantize_group<T, kWide, 32, 4>(a, dev, st);
+    if (chunks <= 256) return launch_quantize_group<T, kWide, 32, 8>(a, dev, st);
+    if (chunks <= 512) return launch_quantize_group<T, kWide, 128, 4>(a, dev, st);
+    if (chunks <= 1024) return launch_quantize_group<T, kWide, 128, 8>(a, dev, st);
+    if (chunks <= 4096) return launch_quantize_group<T, kWide, 512, 8>(a, dev, st);
+    quantize_long_rows_kernel<T, kWide><<<grid_of(a.rows, 1, int64_t(dev.num_sms) * 4), 512, 0, st>>>(a);
+    return launched();
+}
+
+template <typename T>
+maxsim_status launch_quantize_any(const QuantizeArgs& a, const HostDevice& dev, cudaStream_t st) {
+    constexpr int kVec = Chunk<T, true>::kVec;
+    const bool wide = a.cols % kVec == 0 && a.ld_x % kVec == 0 && a.ld_q % kVec == 0 && ptr_aligned(a.x, 16) &&
+                      ptr_aligned(a.q, kVec);
+    return wide ? launch_quantize<T, true>(a, dev, st) : launch_quantize<T, false>(a, dev, st);
+}
+
+// The multiplier and shift that divide 0 <= i < 2^31 by d (round-up method: with l = ceil(log2 d),
+// ceil(2^(31 + l) / d) < 2^32 is exact for i < 2^31).
+void set_div(DropoutArgs* a, uint32_t d) {
+    if (d == 1) {
+        a->div_mul = 0;
+        a->div_shift = 0xffffffffu;
+        return;
+    }
+    uint32_t l = 0;
+    while ((uint64_t(1) << l) < d) ++l;
+    a->div_mul = static_cast<uint32_t>(((uint64_t(1) << (31 + l)) + d - 1) / d);
+    a->div_shift = l - 1;
+}
+
+template <typename T>
+maxsim_status launch_dropout(DropoutArgs& a, const HostDevice& dev, cudaStream_t st) {
+    const bool res = a.residual != nullptr;
+    const bool bases = ptr_aligned(a.x, 16) && ptr_aligned(a.y, 16) && ptr_aligned(a.residual, 16);
+    const bool one_run = a.rows == 1 || (a.ld_x == a.cols && a.ld_y == a.cols && (!res || a.ld_r == a.cols));
+    constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+    const bool rows_wide = a.cols % 8 == 0 && a.ld_x % kVec == 0 && a.ld_y % kVec == 0 && (!res || a.ld_r % kVec == 0);
+    const int64_t most = int64_t(dev.num_sms) * 8;
+    if (bases && one_run) {
+        const unsigned grid = grid_of(a.n / 8, 256, most);
+        if (res) dropout_wide_kernel<T, true, true><<<grid, 256, 0, st>>>(a);
+        else dropout_wide_kernel<T, true, false><<<grid, 256, 0, st>>>(a);
+    } else if (bases && rows_wide) {
+        set_div(&a, static_cast<uint32_t>(a.cols / 8));
+        const unsigned grid = grid_of(a.n / 8, 256, most);
+        if (res) dropout_wide_kernel<T, false, true><<<grid, 256, 0, st>>>(a);
+        else dropout_wide_kernel<T, false, false><<<grid, 256, 0, st>>>(a);
+    } else {
+        set_div(&a, static_cast<uint32_t>(a.cols));
+        const unsigned grid = grid_of(a.n, 8 * 256, most);
+        if (res) dropout_any_kernel<T, true><<<grid, 256, 0, st>>>(a);
+        else dropout_any_kernel<T, false><<<grid, 256, 0, st>>>(a);
+    }
+    return launched();
+}
+
+maxsim_status run_dropout(DropoutArgs& a, maxsim_dtype dtype, cudaStream_t st) {
     HostDevice dev;
     const maxsim_status rc = host_device(&dev);
     if (rc != MAXSIM_OK) return rc;
-    const int64_t blocks = (a.rows * a.cols + 7) / 8;
-    const unsigned grid = grid_of(blocks, 256, int64_t(dev.num_sms) * 8);
-    if (dtype == MAXSIM_F16) dropout_kernel<__half><<<grid, 256, 0, st>>>(a);
-    else if (dtype == MAXSIM_BF16) dropout_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a);
-    else dropout_kernel<float><<<grid, 256, 0, st>>>(a);
-    return launched();
+    if (dtype == MAXSIM_F16) return launch_dropout<__half>(a, dev, st);
+    if (dtype == MAXSIM_BF16) return launch_dropout<__nv_bfloat16>(a, dev, st);
+    return launch_dropout<float>(a, dev, st);
 }
 
 // Fills drop and scale from p; false where p is no probability.
@@ -61,12 +127,180 @@ bool dropout_rate(double p, DropoutArgs* a) {
     return true;
 }
 
+// ---------------------------------------------------------------- INT8 linear
+
+constexpr int64_t kFewTokens = 32;      // up to here linear_few_kernel
+constexpr int64_t kPairs = 76;          // CTA pairs of a GB300 (152 SMs): plans do not depend on the device
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+
+// Whether the kernels can read rows of K bytes, ld apart, where they are (from
+// a 16-byte aligned base): whole 16-byte pieces, and a stride that a TMA
+// descriptor can hold.
+inline bool rows_direct(int64_t K, int64_t ld) { return K % 16 == 0 && ld % 16 == 0 && ld < (int64_t(1) << 40); }
+
+struct LinearPlan {
+    bool few = false;
+    int tn = 256;
+    int64_t tiles = 0, tiles_n = 0;
+    int32_t kb = 0, slices = 1, kb_slice = 0;
+    int64_t k_pad = 0;
+    size_t off_x = 0, off_w = 0, off_partial = 0, bytes = 0;
+};
+
+LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool x_direct, bool w_direct) {
+    LinearPlan p;
+    if (M == 0 || N == 0 || K == 0) return p;
+    p.k_pad = (K + 15) / 16 * 16;
+    p.few = M <= kFewTokens;
+    size_t off = 0;
+    if (!x_direct) {
+        p.off_x = off;
+        off = bytes_round_up(off + static_cast<size_t>(M) * p.k_pad, 256);
+    }
+    if (!w_direct) {
+        p.off_w = off;
+        off = bytes_round_up(off + static_cast<size_t>(N) * p.k_pad, 256);
+    }
+    if (!p.few) {
+        // Tile width and slices of K by the time they should take, in cycles:
+        // the items of the busiest pair, each its blocks and a start and end,
+        // and for slices the kernel that joins them.
+        p.kb = static_cast<int32_t>((K + kTileK - 1) / kTileK);
+        double best = 0.0;
+        for (int tn = 256; tn >= 128; tn -= 128) {
+            const int64_t tiles_n = (N + tn - 1) / tn, tiles = (M + kTileM - 1) / kTileM * tiles_n;
+            const double block = tn == 256 ? 1024.0 : 640.0, ends = tn == 256 ? 3000.0 : 2000.0;
+            for (int32_t slices = 1; slices <= std::min(p.kb, 16); ++slices) {
+                const int32_t kb_slice = (p.kb + slices - 1) / slices;
+                if (slices > 1 && (tiles * slices > 2 * kPairs || (p.kb + kb_slice - 1) / kb_slice != slices)) continue;
+                double cost = static_cast<double>((tiles * slices + kPairs - 1) / kPairs) * (kb_slice * block + ends);
+                if (slices > 1) cost += 5000.0 + static_cast<double>(M) * N * slices * 4.0 / 1500.0;
+                if (best == 0.0 || cost < best) {
+                    best = cost;
+                    p.tn = tn;
+                    p.tiles = tiles;
+                    p.tiles_n = tiles_n;
+                    p.slices = slices;
+                    p.kb_slice = kb_slice;
+                }
+            }
+        }
+        if (p.slices > 1) {
+            p.off_partial = off;
+            off = bytes_round_up(off + static_cast<size_t>(p.slices) * M * N * 4, 256);
+        }
+    }
+    p.bytes = off;
+    return p;
+}
+
+bool encode_i8_rows(EncodeTiledFn encode, CUtensorMap* map, const void* base, int64_t K, int64_t rows, int64_t ld,
+                    uint32_t box_rows) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
+    const cuuint32_t box[2] = {kTileK, box_rows}, estr[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int kTiles>
+maxsim_status launch_few(const LinearArgs& a, cudaStream_t st) {
+    const int64_t chunks = (static_cast<int64_t>(a.K) + 63) / 64;
+    const unsigned threads = 32u * static_cast<unsigned>(std::min<int64_t>(kFewWarps, std::max<int64_t>(chunks, 1)));
+    linear_few_kernel<T, kTiles><<<static_cast<unsigned>((static_cast<int64_t>(a.N) + 15) / 16), threads, 0, st>>>(a);
+    return launched();
+}
+
+template <typename T, int kTN>
+maxsim_status launch_tile(const LinearPlan& p, const LinearArgs& l, int32_t* partial, const HostDevice& dev,
+                          cudaStream_t st) {
+    auto kern = linear_tile_kernel<T, kTN>;
+    constexpr size_t kSmem = tile_smem_bytes<kTN>();
+    static std::atomic<uint64_t> prepared{0};  // devices whose shared-memory limit is raised
+    const uint64_t bit = uint64_t(1) << dev.index;
+    if (!(prepared.load(std::memory_order_acquire) & bit)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem)) != cudaSuccess)
+            return MAXSIM_ERR_CUDA;
+        prepared.fetch_or(bit, std::memory_order_release);
+    }
+    CUtensorMap tx, tw;
+    if (!encode_i8_rows(dev.encode, &tx, l.x, l.K, l.M, l.ld_x, 128) ||
+        !encode_i8_rows(dev.encode, &tw, l.w, l.K, l.N, l.ld_w, TileCfg<kTN>::kBRows))
+        return MAXSIM_ERR_CUDA;
+    TileArgs a{};
+    a.l = l;
+    a.partial = partial;
+    a.items = p.tiles * p.slices;
+    a.tiles_n = static_cast<int32_t>(p.tiles_n);
+    a.slices = p.slices;
+    a.kb = p.kb;
+    a.kb_slice = p.kb_slice;
+    a.vec_out = ptr_aligned(l.out, 16) && l.ld_out * static_cast<int64_t>(sizeof(T)) % 16 == 0;
+    a.vec_scale = ptr_aligned(l.w_scale, 16) && ptr_aligned(l.bias, 16);
+    a.status = dev.status;
+    a.timeout_ns = kTimeoutNs;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(a.items, std::max(1, dev.num_sms / 2))));
+    cfg.blockDim = dim3(kTileThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, tx, tw, a) != cudaSuccess) return MAXSIM_ERR_CUDA;
+    return launched();
+}
+
+template <typename T>
+maxsim_status run_linear(const LinearPlan& p, LinearArgs l, bool x_direct, bool w_direct, uint8_t* ws,
+                         const HostDevice& dev, cudaStream_t st) {
+    const int64_t most = int64_t(dev.num_sms) * 8;
+    const unsigned join_grid = grid_of(static_cast<int64_t>(l.M) * l.N, 256, most);
+    if (l.K == 0) {  // no products: the bias
+        linear_join_kernel<T><<<join_grid, 256, 0, st>>>(l, nullptr, 0);
+        return launched();
+    }
+    const int32_t k_pad = static_cast<int32_t>(p.k_pad);
+    if (!x_direct) {
+        int8_t* to = reinterpret_cast<int8_t*>(ws + p.off_x);
+        repack_rows_kernel<<<grid_of(static_cast<int64_t>(l.M) * (k_pad / 16), 256, most), 256, 0, st>>>(
+            l.x, l.M, l.K, l.ld_x, to, k_pad);
+        l.x = to;
+        l.ld_x = k_pad;
+    }
+    if (!w_direct) {
+        int8_t* to = reinterpret_cast<int8_t*>(ws + p.off_w);
+        repack_rows_kernel<<<grid_of(static_cast<int64_t>(l.N) * (k_pad / 16), 256, most), 256, 0, st>>>(
+            l.w, l.N, l.K, l.ld_w, to, k_pad);
+        l.w = to;
+        l.ld_w = k_pad;
+    }
+    l.K = k_pad;  // an operand read where it is has K % 16 == 0 already; repacked tails are zero
+    maxsim_status rc = launched();
+    if (rc != MAXSIM_OK) return rc;
+    if (p.few) {
+        if (l.M <= 8) return launch_few<T, 1>(l, st);
+        if (l.M <= 16) return launch_few<T, 2>(l, st);
+        return launch_few<T, 4>(l, st);
+    }
+    int32_t* partial = reinterpret_cast<int32_t*>(ws + p.off_partial);
+    rc = p.tn == 256 ? launch_tile<T, 256>(p, l, partial, dev, st) : launch_tile<T, 128>(p, l, partial, dev, st);
+    if (rc != MAXSIM_OK || p.slices == 1) return rc;
+    linear_join_kernel<T><<<join_grid, 256, 0, st>>>(l, partial, p.slices);
+    return launched();
+}
+
 }  // namespace
 
 size_t linear_int8_ws_bytes(int64_t M, int64_t N, int64_t K, int64_t ld_x, int64_t ld_w) {
-    if (M < 0 || N < 0 || K < 0 || ld_x < 0 || ld_w < 0 || M > kI32Max || N > kI32Max || K > kLinearMaxK)
+    if (M < 0 || N < 0 || K < 0 || ld_x < 0 || ld_w < 0 || M > kLinearMaxRows || N > kLinearMaxRows || K > kLinearMaxK)
         return static_cast<size_t>(-1);
-    return 0;
+    return plan_linear(M, N, K, rows_direct(K, ld_x), rows_direct(K, ld_w)).bytes;
 }
 
 }  // namespace maxsim
@@ -87,10 +321,10 @@ maxsim_status maxsim_quantize_rows(const void* x, maxsim_dtype dtype, int64_t ro
     const maxsim_status rc = host_device(&dev);
     if (rc != MAXSIM_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (dtype == MAXSIM_F16) return launch_quantize<__half>(x, rows, cols, ld_x, normalize, q, ld_q, scale, dev, st);
-    if (dtype == MAXSIM_BF16)
-        return launch_quantize<__nv_bfloat16>(x, rows, cols, ld_x, normalize, q, ld_q, scale, dev, st);
-    return launch_quantize<float>(x, rows, cols, ld_x, normalize, q, ld_q, scale, dev, st);
+    const QuantizeArgs a{x, q, scale, rows, ld_x, ld_q, static_cast<int32_t>(cols), normalize != 0};
+    if (dtype == MAXSIM_F16) return launch_quantize_any<__half>(a, dev, st);
+    if (dtype == MAXSIM_BF16) return launch_quantize_any<__nv_bfloat16>(a, dev, st);
+    return launch_quantize_any<float>(a, dev, st);
 }
 
 maxsim_status maxsim_linear_int8(const int8_t* x, int64_t ld_x, const float* x_scale, const int8_t* w, int64_t ld_w,
@@ -99,23 +333,26 @@ maxsim_status maxsim_linear_int8(const int8_t* x, int64_t ld_x, const float* x_s
                                  size_t workspace_bytes, void* stream) {
     if (!any_dtype(out_dtype) || M < 0 || N < 0 || K < 0) return MAXSIM_ERR_INVALID_ARG;
     if (!rows_fit(M, K, ld_x) || !rows_fit(N, K, ld_w) || !rows_fit(M, N, ld_out)) return MAXSIM_ERR_INVALID_ARG;
-    if (M > kI32Max || N > kI32Max || K > kLinearMaxK) return MAXSIM_ERR_UNSUPPORTED;
+    if (M > kLinearMaxRows || N > kLinearMaxRows || K > kLinearMaxK) return MAXSIM_ERR_UNSUPPORTED;
     if (M == 0 || N == 0) return MAXSIM_OK;
     if (!out || !ptr_aligned(out, elem_bytes(out_dtype))) return MAXSIM_ERR_INVALID_ARG;
     if (!x_scale || !w_scale || !ptr_aligned(x_scale, 4) || !ptr_aligned(w_scale, 4) || !ptr_aligned(bias, 4))
         return MAXSIM_ERR_INVALID_ARG;
     if (K > 0 && (!x || !w)) return MAXSIM_ERR_INVALID_ARG;
+    const bool x_direct = rows_direct(K, ld_x) && ptr_aligned(x, 16), w_direct = rows_direct(K, ld_w) && ptr_aligned(w, 16);
+    const LinearPlan p = plan_linear(M, N, K, x_direct, w_direct);
+    if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes || !ptr_aligned(workspace, 256)))
+        return MAXSIM_ERR_WORKSPACE;
     HostDevice dev;
     const maxsim_status rc = host_device(&dev);
     if (rc != MAXSIM_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    LinearArgs a{x, w, ld_x, ld_w, ld_out, x_scale, w_scale, bias, out,
-                 static_cast<int32_t>(M), static_cast<int32_t>(N), static_cast<int32_t>(K)};
-    const unsigned grid = grid_of(((M + 15) / 16) * ((N + 15) / 16), 1, int64_t(dev.num_sms) * 8);
-    if (out_dtype == MAXSIM_F16) linear_simple_kernel<__half><<<grid, 256, 0, st>>>(a);
-    else if (out_dtype == MAXSIM_BF16) linear_simple_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a);
-    else linear_simple_kernel<float><<<grid, 256, 0, st>>>(a);
-    return launched();
+    uint8_t* ws8 = static_cast<uint8_t*>(workspace);
+    const LinearArgs l{x, w, ld_x, ld_w, ld_out, x_scale, w_scale, bias, out,
+                       static_cast<int32_t>(M), static_cast<int32_t>(N), static_cast<int32_t>(K)};
+    if (out_dtype == MAXSIM_F16) return run_linear<__half>(p, l, x_direct, w_direct, ws8, dev, st);
+    if (out_dtype == MAXSIM_BF16) return run_linear<__nv_bfloat16>(p, l, x_direct, w_direct, ws8, dev, st);
+    return run_linear<float>(p, l, x_direct, w_direct, ws8, dev, st);
 }
 
 maxsim_status maxsim_dropout_fwd(const void* x, maxsim_dtype dtype, int64_t rows, int64_t cols, int64_t ld_x,
@@ -138,8 +375,11 @@ maxsim_status maxsim_dropout_fwd(const void* x, maxsim_dtype dtype, int64_t rows
     a.ld_x = ld_x;
     a.ld_r = ld_residual;
     a.ld_y = ld_y;
-    a.seed = seed;
-    a.offset = offset;
+    a.n = rows * cols;
+    a.key0 = static_cast<uint32_t>(seed);
+    a.key1 = static_cast<uint32_t>(seed >> 32);
+    a.off0 = static_cast<uint32_t>(offset);
+    a.off1 = static_cast<uint32_t>(offset >> 32);
     return run_dropout(a, dtype, static_cast<cudaStream_t>(stream));
 }
 

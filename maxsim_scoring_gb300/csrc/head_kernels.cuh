@@ -7,6 +7,7 @@
 
 #include <cfloat>
 #include <cstdint>
+#include <type_traits>
 
 namespace maxsim {
 
@@ -29,42 +30,253 @@ template <>
 __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 
 // ---------------------------------------------------------------- row quantisation
+//
+// scale = max |x| / 127 needs the whole row before the first code, so a row
+// is held in registers between the two: one read of x, one write of q. A row
+// belongs to a group of 8, 32, 128 or 512 threads, each holding up to
+// kChunks 16-byte chunks (or kChunks single elements where the rows do not
+// start on 16-byte boundaries); only rows beyond 512 x 8 chunks are read
+// twice. Bound by HBM.
 
-// One block per row, two passes over it.
+// Maximum of two pairs of unsigned 16-bit values.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// One chunk of a row: kVec elements, 16 bytes or a single one.
+template <typename T, bool kWide>
+struct Chunk;
+
 template <typename T>
-__global__ void quantize_rows_kernel(const T* __restrict__ x, int64_t rows, int32_t cols, int64_t ld_x, int normalize,
-                                     int8_t* __restrict__ q, int64_t ld_q, float* __restrict__ scale) {
-    __shared__ uint32_t s_max[32];
-    __shared__ float s_sum[32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-        const T* xr = x + r * ld_x;
-        // |x| as bits: ordered as the values, with infinities and NaN on top
+struct Chunk<T, true> {
+    static constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+    uint4 v;
+    __device__ __forceinline__ void load(const T* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void clear() { v = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ float get(int i) const {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        if constexpr (sizeof(T) == 4) {
+            return __uint_as_float(w[i]);
+        } else {
+            const unsigned short h = static_cast<unsigned short>((i & 1) ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu);
+            if constexpr (std::is_same_v<T, __half>) return __half2float(__ushort_as_half(h));
+            else return __uint_as_float(static_cast<uint32_t>(h) << 16);
+        }
+    }
+    // max |.| so far, as bit patterns (ordered as the values; infinities and NaN on top)
+    __device__ __forceinline__ uint32_t fold_max(uint32_t m) const {
+        if constexpr (sizeof(T) == 4) {
+            return max(max(m, max(v.x & 0x7fffffffu, v.y & 0x7fffffffu)),
+                       max(v.z & 0x7fffffffu, v.w & 0x7fffffffu));
+        } else {
+            return max_u16x2(max_u16x2(m, max_u16x2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu)),
+                             max_u16x2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+        }
+    }
+    static __device__ __forceinline__ uint32_t max_bits(uint32_t m) {
+        return sizeof(T) == 4 ? m : max(m >> 16, m & 0xffffu);
+    }
+    static __device__ __forceinline__ void store(int8_t* q, const uint32_t* w) {
+        if constexpr (sizeof(T) == 4) *reinterpret_cast<uint32_t*>(q) = w[0];
+        else *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+    }
+};
+
+template <typename T>
+struct Chunk<T, false> {
+    static constexpr int kVec = 1;
+    T v;
+    __device__ __forceinline__ void load(const T* p) { v = *p; }
+    __device__ __forceinline__ void clear() { v = from_f32<T>(0.f); }
+    __device__ __forceinline__ float get(int) const { return to_f32(v); }
+    __device__ __forceinline__ uint32_t bits() const {
+        if constexpr (sizeof(T) == 4) return __float_as_uint(v) & 0x7fffffffu;
+        else return *reinterpret_cast<const unsigned short*>(&v) & 0x7fffu;
+    }
+    __device__ __forceinline__ uint32_t fold_max(uint32_t m) const { return max(m, bits()); }
+    static __device__ __forceinline__ uint32_t max_bits(uint32_t m) { return m; }
+    static __device__ __forceinline__ void store(int8_t* q, const uint32_t* w) { *q = static_cast<int8_t>(w[0]); }
+};
+
+// From the largest |x| of a row (bits of T): whether the row is finite, and s = max(a / 127, 2^-126).
+template <typename T>
+__device__ __forceinline__ bool row_step(uint32_t bits, float* s) {
+    float a;
+    bool finite;
+    if constexpr (sizeof(T) == 4) {
+        finite = bits < 0x7f800000u;
+        a = __uint_as_float(bits);
+    } else if constexpr (std::is_same_v<T, __half>) {
+        finite = bits < 0x7c00u;
+        a = __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
+    } else {
+        finite = bits < 0x7f80u;
+        a = __uint_as_float(bits << 16);
+    }
+    *s = finite ? fmaxf(__fdiv_rn(a, 127.f), FLT_MIN) : 1.f;
+    return finite;
+}
+
+// The codes of one chunk, packed in w, and its sum of squares of x / s.
+// rint(x / s) wants an IEEE division per element. x * inv, inv = 1 / s, is at
+// most 1.2e-5 away from the rounded quotient (|x / s| <= 127: 2^-24 relative
+// from inv, half a unit of the last place from the division), so only
+// products within 3e-5 of a half-integer can round to another code, and only
+// chunks that hold such a product divide. The product is rounded to an integer
+// by adding 1.5 * 2^23 in the same fma; the sum's low byte is the code.
+template <typename T, bool kWide>
+__device__ __forceinline__ float code_chunk(const Chunk<T, kWide>& c, float s, float inv, uint32_t keep, uint32_t* w) {
+    constexpr float kMagic = 12582912.f;
+    constexpr int kVec = Chunk<T, kWide>::kVec;
+    uint32_t m[kVec];
+    float sum = 0.f, off = 0.f;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+        const float x = c.get(i);
+        const float r = __fmaf_rn(x, inv, kMagic);
+        off = fmaxf(off, fabsf(__fmaf_rn(x, inv, -(r - kMagic))));
+        m[i] = __float_as_uint(r);
+        const float y = x * inv;
+        sum = __fmaf_rn(y, y, sum);
+    }
+    if (off > 0.49997f) {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) m[i] = __float_as_uint(__fdiv_rn(c.get(i), s) + kMagic);
+    }
+    if constexpr (kVec == 1) {
+        w[0] = m[0] & keep;
+    } else {
+#pragma unroll
+        for (int i = 0; i < kVec / 4; ++i) {
+            const uint32_t lo = __byte_perm(m[4 * i], m[4 * i + 1], 0x0040), hi = __byte_perm(m[4 * i + 2], m[4 * i + 3], 0x0040);
+            w[i] = __byte_perm(lo, hi, 0x5410) & keep;
+        }
+    }
+    return sum;
+}
+
+__device__ __forceinline__ float row_scale(bool finite, int normalize, float s, float sum) {
+    float out = s;
+    if (normalize) out = sum > 0.f ? __fdiv_rn(1.f, __fsqrt_rn(sum)) : FLT_MIN;
+    return finite ? out : __uint_as_float(0x7fffffffu);
+}
+
+// Sum and maximum over a group of kGroup threads, the same in all of them.
+// Groups above a warp are blocks; `slot` is shared memory for one value per
+// warp and must not be in use (two alternate).
+template <int kGroup>
+__device__ __forceinline__ uint32_t group_max(uint32_t v, uint32_t* slot) {
+    if constexpr (kGroup >= 32) v = __reduce_max_sync(0xffffffffu, v);
+    else
+#pragma unroll
+        for (int o = kGroup / 2; o; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if constexpr (kGroup > 32) {
+        if ((threadIdx.x & 31) == 0) slot[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = __reduce_max_sync(0xffffffffu, slot[(threadIdx.x & 31) % (kGroup / 32)]);
+    }
+    return v;
+}
+
+template <int kGroup>
+__device__ __forceinline__ float group_sum(float v, float* slot) {
+#pragma unroll
+    for (int o = (kGroup < 32 ? kGroup : 32) / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if constexpr (kGroup > 32) {
+        if ((threadIdx.x & 31) == 0) slot[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = 0.f;
+#pragma unroll
+        for (int i = 0; i < kGroup / 32; ++i) v += slot[i];
+    }
+    return v;
+}
+
+struct QuantizeArgs {
+    const void* x;
+    int8_t* q;
+    float* scale;
+    int64_t rows, ld_x, ld_q;
+    int32_t cols;
+    int normalize;
+};
+
+__host__ __device__ constexpr int quantize_threads(int group) { return group > 128 ? group : 128; }
+
+template <typename T, bool kWide, int kGroup, int kChunks>
+__global__ void __launch_bounds__(quantize_threads(kGroup)) quantize_rows_kernel(const QuantizeArgs a) {
+    using C = Chunk<T, kWide>;
+    constexpr int kThreads = quantize_threads(kGroup), kPerBlock = kThreads / kGroup;
+    __shared__ uint32_t s_max[16];
+    __shared__ float s_sum[16];
+    const int g = threadIdx.x / kGroup, t = threadIdx.x % kGroup;
+    // every thread of the block walks the same number of rows: the groups reduce with full-warp shuffles
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kPerBlock; r0 < a.rows;
+         r0 += static_cast<int64_t>(gridDim.x) * kPerBlock) {
+        const int64_t r = r0 + g;
+        const bool real = r < a.rows;
+        const T* xr = static_cast<const T*>(a.x) + (real ? r : r0) * a.ld_x;
+        C c[kChunks];
+#pragma unroll
+        for (int j = 0; j < kChunks; ++j) {
+            const int32_t col = (j * kGroup + t) * C::kVec;
+            if (col < a.cols) c[j].load(xr + col);
+            else c[j].clear();
+        }
         uint32_t m = 0;
-        for (int32_t c = threadIdx.x; c < cols; c += blockDim.x)
-            m = max(m, __float_as_uint(to_f32(xr[c])) & 0x7fffffffu);
-        m = __reduce_max_sync(0xffffffffu, m);
-        if (lane == 0) s_max[warp] = m;
-        __syncthreads();
-        m = __reduce_max_sync(0xffffffffu, lane < warps ? s_max[lane] : 0u);
-        const bool finite = m < 0x7f800000u;
-        const float s = fmaxf(__fdiv_rn(__uint_as_float(m), 127.f), FLT_MIN);
+#pragma unroll
+        for (int j = 0; j < kChunks; ++j) m = c[j].fold_max(m);
+        m = group_max<kGroup>(C::max_bits(m), s_max);
+        float s;
+        const bool finite = row_step<T>(m, &s);
+        const float inv = __frcp_rn(s);
         float sum = 0.f;
-        for (int32_t c = threadIdx.x; c < cols; c += blockDim.x) {
-            const float y = finite ? __fdiv_rn(to_f32(xr[c]), s) : 0.f;
-            sum += y * y;
-            q[r * ld_q + c] = static_cast<int8_t>(fminf(fmaxf(rintf(y), -127.f), 127.f));
+#pragma unroll
+        for (int j = 0; j < kChunks; ++j) {
+            const int32_t col = (j * kGroup + t) * C::kVec;
+            uint32_t w[2];
+            const float part = code_chunk<T, kWide>(c[j], s, inv, finite ? 0xffffffffu : 0u, w);
+            sum += part;
+            if (real && col < a.cols) C::store(a.q + r * a.ld_q + col, w);
         }
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) s_sum[warp] = sum;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            float total = 0.f;
-            for (int w = 0; w < warps; ++w) total += s_sum[w];
-            float out = s;
-            if (normalize) out = total > 0.f ? __fdiv_rn(1.f, __fsqrt_rn(total)) : FLT_MIN;
-            scale[r] = finite ? out : __uint_as_float(0x7fffffffu);
+        if (a.normalize) sum = group_sum<kGroup>(sum, s_sum);
+        if (real && t == 0) a.scale[r] = row_scale(finite, a.normalize, s, sum);
+        if constexpr (kGroup > 32) __syncthreads();  // the slots are free again
+    }
+}
+
+// Rows too long for the registers of a block: read once for the maximum, once for the codes.
+template <typename T, bool kWide>
+__global__ void __launch_bounds__(512) quantize_long_rows_kernel(const QuantizeArgs a) {
+    using C = Chunk<T, kWide>;
+    __shared__ uint32_t s_max[16];
+    __shared__ float s_sum[16];
+    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+        const T* xr = static_cast<const T*>(a.x) + r * a.ld_x;
+        uint32_t m = 0;
+#pragma unroll 4
+        for (int64_t col = threadIdx.x * C::kVec; col < a.cols; col += 512 * C::kVec) {
+            C c;
+            c.load(xr + col);
+            m = c.fold_max(m);
         }
+        m = group_max<512>(C::max_bits(m), s_max);
+        float s;
+        const bool finite = row_step<T>(m, &s);
+        const float inv = __frcp_rn(s);
+        float sum = 0.f;
+#pragma unroll 4
+        for (int64_t col = threadIdx.x * C::kVec; col < a.cols; col += 512 * C::kVec) {
+            C c;
+            c.load(xr + col);
+            uint32_t w[2];
+            sum += code_chunk<T, kWide>(c, s, inv, finite ? 0xffffffffu : 0u, w);
+            C::store(a.q + r * a.ld_q + col, w);
+        }
+        if (a.normalize) sum = group_sum<512>(sum, s_sum);
+        if (threadIdx.x == 0) a.scale[r] = row_scale(finite, a.normalize, s, sum);
         __syncthreads();
     }
 }
@@ -90,41 +302,145 @@ struct DropoutArgs {
     const void* residual;  // NULL = none
     void* y;
     int64_t rows, ld_x, ld_r, ld_y;
+    int64_t n;              // rows * cols
     int32_t cols;
-    uint32_t drop;  // T: elements that draw less than this are dropped
+    uint32_t drop;          // T: elements that draw less than this are dropped
     float scale;
-    uint64_t seed, offset;
+    uint32_t key0, key1, off0, off1;
+    uint32_t div_mul, div_shift;  // i / d = (i * div_mul) >> (32 + div_shift) for i < 2^31 (d: see the kernels)
 };
 
-// One thread per counter value: eight elements of the row-major matrix.
+// i / d by a product (d's reciprocal rounded up to 32 bits), for 0 <= i < 2^31.
+__device__ __forceinline__ uint32_t fast_div(uint32_t i, uint32_t mul, uint32_t shift) {
+    return shift == 0xffffffffu ? i : __umulhi(i, mul) >> shift;
+}
+
+__device__ __forceinline__ uint4 draw_block(const DropoutArgs& a, int64_t b) {
+    return philox4x32_10(make_uint4(static_cast<uint32_t>(b), static_cast<uint32_t>(static_cast<uint64_t>(b) >> 32),
+                                    a.off0, a.off1),
+                         a.key0, a.key1);
+}
+
 template <typename T>
-__global__ void dropout_kernel(const DropoutArgs a) {
-    const int64_t n = a.rows * a.cols;
-    const int64_t blocks = (n + 7) >> 3;
+struct Eight {  // eight consecutive elements
+    uint4 v[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
+    }
+    __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) reinterpret_cast<uint4*>(p)[i] = v[i];
+    }
+    __device__ __forceinline__ T& at(int i) { return reinterpret_cast<T*>(v)[i]; }
+};
+
+// Dropout where every eight elements that share a counter are one 16-byte
+// (f32: 32-byte) piece of a row: the rows are contiguous, or cols is a
+// multiple of 8 and rows start on 16-byte boundaries. One read, one write and
+// ten rounds of Philox per eight elements; two pieces per thread in flight
+// so that the loads cover the memory latency. Bound by HBM; the generator's
+// integer work is about half of what the SMs could issue meanwhile.
+// kFlat: one run of n elements (the last piece may be short); otherwise
+// fast_div divides the piece's number by the pieces of a row.
+template <typename T, bool kFlat, bool kRes>
+__global__ void __launch_bounds__(256) dropout_wide_kernel(const DropoutArgs a) {
+    constexpr int kPieces = 2;
     const T* x = static_cast<const T*>(a.x);
     const T* res = static_cast<const T*>(a.residual);
     T* y = static_cast<T*>(a.y);
-    for (int64_t b = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; b < blocks;
-         b += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const uint4 u = philox4x32_10(
-            make_uint4(static_cast<uint32_t>(b), static_cast<uint32_t>(static_cast<uint64_t>(b) >> 32),
-                       static_cast<uint32_t>(a.offset), static_cast<uint32_t>(a.offset >> 32)),
-            static_cast<uint32_t>(a.seed), static_cast<uint32_t>(a.seed >> 32));
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-        int64_t row = (b << 3) / a.cols;
-        int32_t col = static_cast<int32_t>((b << 3) - row * a.cols);
+    const int64_t blocks = a.n >> 3;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    const int64_t first = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
+    for (int64_t b0 = first; b0 < blocks; b0 += kPieces * step) {
+        Eight<T> xv[kPieces], rv[kPieces];
+        int64_t at_y[kPieces];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if ((b << 3) + e >= n) break;
-            const uint32_t bits = (e & 1) ? w[e >> 1] >> 16 : w[e >> 1] & 0xffffu;
-            float v = bits >= a.drop ? to_f32(x[row * a.ld_x + col]) * a.scale : 0.f;
-            if (res) v += to_f32(res[row * a.ld_r + col]);
-            y[row * a.ld_y + col] = from_f32<T>(v);
-            if (++col == a.cols) {
-                col = 0;
-                ++row;
+        for (int j = 0; j < kPieces; ++j) {
+            const int64_t b = b0 + j * step;
+            if (b >= blocks) break;
+            int64_t at_x = b << 3, at_r = at_x;
+            at_y[j] = at_x;
+            if constexpr (!kFlat) {
+                const int32_t per_row = a.cols >> 3;
+                const int64_t row = b < 0x80000000ll ? fast_div(static_cast<uint32_t>(b), a.div_mul, a.div_shift) : b / per_row;
+                const int64_t col = (b - row * per_row) << 3;
+                at_x = row * a.ld_x + col;
+                at_r = row * a.ld_r + col;
+                at_y[j] = row * a.ld_y + col;
+            }
+            xv[j].load(x + at_x);
+            if constexpr (kRes) rv[j].load(res + at_r);
+        }
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+            const int64_t b = b0 + j * step;
+            if (b >= blocks) break;
+            const uint4 u = draw_block(a, b);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t bits = (e & 1) ? w[e >> 1] >> 16 : w[e >> 1] & 0xffffu;
+                float v = bits >= a.drop ? to_f32(xv[j].at(e)) * a.scale : 0.f;
+                if constexpr (kRes) v += to_f32(rv[j].at(e));
+                xv[j].at(e) = from_f32<T>(v);
+            }
+            xv[j].store(y + at_y[j]);
+        }
+    }
+    if (kFlat && first == 0 && (a.n & 7)) {  // the short last piece
+        const uint4 u = draw_block(a, blocks);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        for (int e = 0; e < static_cast<int>(a.n & 7); ++e) {
+            const int64_t i = (blocks << 3) + e;
+            const uint32_t word = e < 2 ? w[0] : e < 4 ? w[1] : e < 6 ? w[2] : w[3];
+            const uint32_t bits = (e & 1) ? word >> 16 : word & 0xffffu;
+            float v = bits >= a.drop ? to_f32(x[i]) * a.scale : 0.f;
+            if constexpr (kRes) v += to_f32(res[i]);
+            y[i] = from_f32<T>(v);
+        }
+    }
+}
+
+// Dropout for every other layout (odd widths, rows off their 16-byte
+// boundaries). A warp takes 256 consecutive elements: its lanes draw one
+// counter each, pass the bits through shared memory, and then take every
+// 32nd element, so that loads and stores of single elements are coalesced.
+// fast_div divides an element's index by cols.
+template <typename T, bool kRes>
+__global__ void __launch_bounds__(256) dropout_any_kernel(const DropoutArgs a) {
+    __shared__ uint4 s_bits[8][32];
+    const T* x = static_cast<const T*>(a.x);
+    const T* res = static_cast<const T*>(a.residual);
+    T* y = static_cast<T*>(a.y);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned short* bits = reinterpret_cast<const unsigned short*>(s_bits[warp]);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * 8 * 256;
+    for (int64_t i0 = (static_cast<int64_t>(blockIdx.x) * 8 + warp) * 256; i0 < a.n; i0 += step) {
+        int64_t at_y[8];
+        T xv[8], rv[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int64_t i = i0 + j * 32 + lane;
+            if (i < a.n) {
+                const int64_t row = i < 0x80000000ll ? fast_div(static_cast<uint32_t>(i), a.div_mul, a.div_shift) : i / a.cols;
+                const int64_t col = i - row * a.cols;
+                xv[j] = x[row * a.ld_x + col];
+                if constexpr (kRes) rv[j] = res[row * a.ld_r + col];
+                at_y[j] = row * a.ld_y + col;
             }
         }
+        s_bits[warp][lane] = draw_block(a, (i0 >> 3) + lane);
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (i0 + j * 32 + lane < a.n) {
+                float v = bits[j * 32 + lane] >= a.drop ? to_f32(xv[j]) * a.scale : 0.f;
+                if constexpr (kRes) v += to_f32(rv[j]);
+                y[at_y[j]] = from_f32<T>(v);
+            }
+        }
+        __syncwarp();
     }
 }
 

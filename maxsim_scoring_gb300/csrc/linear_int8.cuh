@@ -1,10 +1,23 @@
 // out[m, n] = (sum_k x[m, k] w[n, k]) * x_scale[m] * w_scale[n] + bias[n] for
 // 8-bit integers x [M, K] and w [N, K].
+//
+// sm_103a has no 8-bit integer kind among its tcgen05 MMAs, and mma.sync's
+// 8-bit integer form was measured at 150 TOP/s, a quarter of the f16 form's
+// 605 TFLOP/s. So both kernels widen the integers to binary16 on the SM, next
+// to the tensor cores: |v| <= 128 is exact there, a product of two is exact in
+// fp32, and a sum of up to 1,024 products (2^24) is too. Device memory is read
+// as 8-bit values only.
+//
+//  * linear_few_kernel (few tokens): bound by the bytes of w, each read once.
+//  * linear_tile_kernel (many tokens): tcgen05 MMAs of 256 x 256 or 256 x 128
+//    tiles on CTA pairs, bound by the tensor pipe, or by the bytes of x where
+//    w is narrow.
 #pragma once
 
 #include <cstdint>
 
 #include "head_kernels.cuh"
+#include "ptx.cuh"
 
 namespace maxsim {
 
@@ -19,35 +32,534 @@ struct LinearArgs {
     int32_t M, N, K;
 };
 
-// 16 x 16 outputs per block, operands through shared memory.
-template <typename T>
-__global__ void linear_simple_kernel(const LinearArgs a) {
-    __shared__ int8_t sx[16][68], sw[16][68];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int64_t tiles_n = (static_cast<int64_t>(a.N) + 15) / 16;
-    const int64_t tiles = tiles_n * ((static_cast<int64_t>(a.M) + 15) / 16);
-    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-        const int64_t m0 = t / tiles_n * 16, n0 = t % tiles_n * 16;
-        int32_t acc = 0;
-        for (int32_t k0 = 0; k0 < a.K; k0 += 64) {
-            for (int i = threadIdx.x; i < 16 * 64; i += blockDim.x) {
-                const int r = i >> 6, k = i & 63;
-                const bool in = k0 + k < a.K;
-                sx[r][k] = in && m0 + r < a.M ? a.x[(m0 + r) * a.ld_x + k0 + k] : static_cast<int8_t>(0);
-                sw[r][k] = in && n0 + r < a.N ? a.w[(n0 + r) * a.ld_w + k0 + k] : static_cast<int8_t>(0);
-            }
-            __syncthreads();
+// Rows of K bytes into rows of ld_dst bytes (a multiple of 16, the tail zero):
+// operands whose rows do not start on 16-byte boundaries are laid out once.
+__global__ void __launch_bounds__(256) repack_rows_kernel(const int8_t* __restrict__ src, int64_t rows, int32_t K,
+                                                          int64_t ld_src, int8_t* __restrict__ dst, int32_t ld_dst) {
+    const int32_t per_row = ld_dst >> 4;
+    const int64_t n = rows * per_row;
+    for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n;
+         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        const int64_t r = i / per_row;
+        const int32_t k = static_cast<int32_t>(i - r * per_row) << 4;
+        const uint8_t* p = reinterpret_cast<const uint8_t*>(src) + r * ld_src + k;
+        uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-            for (int k = 0; k < 64; k += 4)
-                acc = __dp4a(*reinterpret_cast<const int*>(&sx[ty][k]), *reinterpret_cast<const int*>(&sw[tx][k]), acc);
-            __syncthreads();
+        for (int e = 0; e < 16; ++e)
+            if (k + e < K) w[e >> 2] |= static_cast<uint32_t>(p[e]) << ((e & 3) * 8);
+        *reinterpret_cast<uint4*>(dst + r * ld_dst + k) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// ---------------------------------------------------------------- few tokens
+
+__device__ __forceinline__ void mma_m16n8k16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 16 bytes to 16 halves: h[i] holds elements 2i and 2i + 1.
+__device__ __forceinline__ void widen16(uint4 v, uint32_t (&h)[8]) {
+    const uint4 lo = i8x8_to_f16x8(v.x, v.y), hi = i8x8_to_f16x8(v.z, v.w);
+    h[0] = lo.x; h[1] = lo.y; h[2] = lo.z; h[3] = lo.w;
+    h[4] = hi.x; h[5] = hi.y; h[6] = hi.z; h[7] = hi.w;
+}
+
+constexpr int kFewWarps = 16;  // most warps of a block
+
+// A block owns 16 channels and all M <= 8 * kTiles tokens; its warps take
+// 64-wide chunks of K in turn. A lane reads 16 consecutive bytes of two
+// channels (w is the MMA's 16-row operand) and of one token of each 8-token
+// tile: lane t of a row then holds k = 16 t .. 16 t + 15 instead of the
+// fragment's own columns, in both operands alike, so the sum over k is the
+// same and every load is 16 bytes wide. After 16 chunks of a warp (1,024
+// products, exact in fp32) the sums move to 32-bit integers, and the warps'
+// sums are added as integers in shared memory: exact, in any order.
+template <typename T, int kTiles>
+__global__ void __launch_bounds__(kFewWarps * 32) linear_few_kernel(const LinearArgs a) {
+    constexpr int kAhead = kTiles <= 2 ? 4 : 2;  // chunks whose loads are in flight
+    __shared__ int s_sum[16][8 * kTiles + 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
+    for (int i = threadIdx.x; i < 16 * (8 * kTiles + 1); i += blockDim.x) (&s_sum[0][0])[i] = 0;
+    __syncthreads();
+    // rows past the ends read the last row; what they give is not stored
+    const int8_t* w0 = a.w + min(n0 + g, static_cast<int64_t>(a.N) - 1) * a.ld_w + 16 * t;
+    const int8_t* w1 = a.w + min(n0 + g + 8, static_cast<int64_t>(a.N) - 1) * a.ld_w + 16 * t;
+    const int8_t* xr[kTiles];
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) xr[j] = a.x + static_cast<int64_t>(min(8 * j + g, a.M - 1)) * a.ld_x + 16 * t;
+    const int32_t chunks = (a.K + 63) >> 6;
+    int sum[kTiles][4] = {};
+    for (int32_t c0 = warp; c0 < chunks; c0 += 16 * warps) {
+        float acc[kTiles][4] = {};
+#pragma unroll 1
+        for (int i0 = 0; i0 < 16 && c0 + i0 * warps < chunks; i0 += kAhead) {
+            uint4 wv[kAhead][2], xv[kAhead][kTiles];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int32_t k = (c0 + (i0 + i) * warps) << 6;
+                const bool in = k + 16 * t < a.K;
+                const uint4 zero = make_uint4(0, 0, 0, 0);
+                wv[i][0] = in ? __ldg(reinterpret_cast<const uint4*>(w0 + k)) : zero;
+                wv[i][1] = in ? __ldg(reinterpret_cast<const uint4*>(w1 + k)) : zero;
+#pragma unroll
+                for (int j = 0; j < kTiles; ++j) xv[i][j] = in ? __ldg(reinterpret_cast<const uint4*>(xr[j] + k)) : zero;
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                uint32_t wa[8], wb[8];
+                widen16(wv[i][0], wa);
+                widen16(wv[i][1], wb);
+#pragma unroll
+                for (int j = 0; j < kTiles; ++j) {
+                    uint32_t xb[8];
+                    widen16(xv[i][j], xb);
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        mma_m16n8k16(acc[j], wa[2 * s], wb[2 * s], wa[2 * s + 1], wb[2 * s + 1], xb[2 * s], xb[2 * s + 1]);
+                }
+            }
         }
-        const int64_t m = m0 + ty, n = n0 + tx;
-        if (m < a.M && n < a.N) {
-            float v = static_cast<float>(acc) * a.x_scale[m] * a.w_scale[n];
-            if (a.bias) v += a.bias[n];
-            static_cast<T*>(a.out)[m * a.ld_out + n] = from_f32<T>(v);
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[j][e] += __float2int_rn(acc[j][e]);
+    }
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) atomicAdd(&s_sum[g + (e & 2) * 4][8 * j + 2 * t + (e & 1)], sum[j][e]);
+    __syncthreads();
+    for (int i = threadIdx.x; i < 16 * a.M; i += blockDim.x) {
+        const int m = i >> 4, n = i & 15;
+        if (n0 + n < a.N) {
+            float v = static_cast<float>(s_sum[n][m]) * a.x_scale[m] * a.w_scale[n0 + n];
+            if (a.bias) v += a.bias[n0 + n];
+            static_cast<T*>(a.out)[m * a.ld_out + n0 + n] = from_f32<T>(v);
         }
+    }
+}
+
+// ---------------------------------------------------------------- many tokens
+
+constexpr int kTileM = 256;            // tokens per tile: 128 on each CTA of a pair
+constexpr int kTileK = 128;            // bytes of K per block
+constexpr int kTileMaxRing = 4;
+constexpr int kWidenWarp0 = 4, kTileEpiWarp0 = 12;
+constexpr int kTileThreads = 640;      // warp 0 TMA, warp 1 MMA, warps 4-11 widen, warps 12-19 epilogue
+constexpr int kTileMaxStages8 = 6;
+constexpr uint32_t kTileACol = 256;    // tensor memory: accumulators in columns 0-255, widened A blocks above
+constexpr int kTileStatusTimeout = 4;  // MAXSIM_ERR_TIMEOUT
+
+template <int kTN>
+struct TileCfg {
+    static constexpr int kBRows = kTN / 2;                         // channels per CTA
+    static constexpr int kA8 = 128 * kTileK, kB8 = kBRows * kTileK;  // 8-bit block
+    static constexpr int kStage8 = kA8 + kB8;
+    static constexpr int kBAtom = kBRows * 128;                    // 64 halves of every row
+    static constexpr int kB16 = 2 * kBAtom;
+    // Depth of the 8-bit ring (even: each widening warpgroup then always meets
+    // the same stages, and sees every phase of their barriers) and of the ring of
+    // widened blocks (A in tensor memory, B in shared memory).
+    static constexpr int kStages8 = kTN == 256 ? 4 : 6;
+    static constexpr int kRing = kTN == 256 ? 3 : 4;
+    static constexpr int kAcc = 256 / kTN;                         // accumulator buffers
+};
+
+struct TileArgs {
+    LinearArgs l;
+    int32_t* partial;   // [slices, M, N] integer sums when slices > 1
+    int64_t items;      // tiles * slices
+    int32_t tiles_n;
+    int32_t slices;     // parts of K
+    int32_t kb;         // blocks of K
+    int32_t kb_slice;   // blocks per slice
+    int vec_out;        // rows of out start on 16-byte boundaries
+    int vec_scale;      // w_scale and bias start on 16-byte boundaries
+    int* status;
+    uint64_t timeout_ns;
+};
+
+struct alignas(16) TileCtl {
+    uint64_t full8[kTileMaxStages8], empty8[kTileMaxStages8];
+    uint64_t ready[kTileMaxRing], freed[kTileMaxRing];
+    uint64_t acc_full[2], acc_empty[2];
+    uint64_t mma_done;
+    uint32_t tmem_base;
+    volatile int32_t abort;
+};
+
+template <int kTN>
+constexpr size_t tile_smem_bytes() {
+    using C = TileCfg<kTN>;
+    return 1024 + static_cast<size_t>(C::kStages8) * C::kStage8 + C::kRing * C::kB16 + sizeof(TileCtl);
+}
+
+// Bounded wait of a thread: gives up after the limit (recorded in the device
+// status word) or when another role of the CTA has.
+template <bool kCluster = false>
+__device__ __forceinline__ bool tile_wait(const TileArgs& a, TileCtl* ctl, uint64_t* bar_ptr, uint32_t parity) {
+    const uint32_t bar = smem_u32(bar_ptr);
+    if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+        if ((it & 63u) == 0) {
+            if (ctl->abort) return false;
+            if (global_timer_ns() - t0 > a.timeout_ns) {
+                ctl->abort = 1;
+                atomicCAS(a.status, 0, kTileStatusTimeout);
+                return false;
+            }
+        }
+    }
+}
+
+template <bool kCluster = false>
+__device__ __forceinline__ bool tile_wait_warp(const TileArgs& a, TileCtl* ctl, uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, tile_wait<kCluster>(a, ctl, bar, parity));
+}
+
+// 32 registers into 32 consecutive columns of this thread's tensor-memory lane.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+        "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Four K = 16 steps into d with A in tensor memory (8 columns a step) and B in
+// shared memory (K-major, 128-byte swizzle: 32 bytes a step), from the elected
+// lane. The first step accumulates only if `accumulate` is nonzero.
+__device__ __forceinline__ void mma_chain4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred e, p0, pt;\n\t.reg .b64 b1, b2, b3;\n\t.reg .b32 a1, a2, a3;\n\t"
+        "setp.ne.b32 p0, %4, 0;\n\t"
+        "setp.eq.b32 pt, %4, %4;\n\t"
+        "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
+        "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a1], b1, %3, pt;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a2], b2, %3, pt;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a3], b3, %3, pt;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+struct TileItem {
+    int64_t m0, n0;  // this CTA's first token, the tile's first channel
+    int32_t kb0, kb1;
+    int32_t slice;
+};
+
+template <int kTN>
+__device__ __forceinline__ TileItem tile_item(const TileArgs& a, int64_t item, uint32_t rank) {
+    TileItem t;
+    const int64_t tile = a.slices == 1 ? item : item / a.slices;
+    t.slice = static_cast<int32_t>(item - tile * a.slices);
+    const int64_t tm = tile / a.tiles_n;
+    t.m0 = tm * kTileM + rank * 128;
+    t.n0 = (tile - tm * a.tiles_n) * kTN;
+    t.kb0 = t.slice * a.kb_slice;
+    t.kb1 = min(a.kb, t.kb0 + a.kb_slice);
+    return t;
+}
+
+// 32 consecutive outputs of row m from column n on.
+template <typename T>
+__device__ __forceinline__ void store_row32(const TileArgs& a, int64_t m, int64_t n, float xs, const float (&v)[32]) {
+    const LinearArgs& l = a.l;
+    T* out = static_cast<T*>(l.out) + m * l.ld_out + n;
+    if (n + 32 <= l.N && a.vec_out && a.vec_scale) {
+        constexpr int kPer = 16 / static_cast<int>(sizeof(T));  // outputs per 16-byte store
+#pragma unroll
+        for (int i = 0; i < 32; i += kPer) {
+            alignas(16) T o[kPer];
+#pragma unroll
+            for (int j = 0; j < kPer; j += 4) {
+                const float4 ws = __ldg(reinterpret_cast<const float4*>(l.w_scale + n + i + j));
+                const float4 b = l.bias ? __ldg(reinterpret_cast<const float4*>(l.bias + n + i + j))
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+                o[j + 0] = from_f32<T>(__fmaf_rn(v[i + j + 0] * xs, ws.x, b.x));
+                o[j + 1] = from_f32<T>(__fmaf_rn(v[i + j + 1] * xs, ws.y, b.y));
+                o[j + 2] = from_f32<T>(__fmaf_rn(v[i + j + 2] * xs, ws.z, b.z));
+                o[j + 3] = from_f32<T>(__fmaf_rn(v[i + j + 3] * xs, ws.w, b.w));
+            }
+            *reinterpret_cast<uint4*>(out + i) = *reinterpret_cast<const uint4*>(o);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            if (n + i < l.N)
+                out[i] = from_f32<T>(__fmaf_rn(v[i] * xs, __ldg(l.w_scale + n + i), l.bias ? __ldg(l.bias + n + i) : 0.f));
+        }
+    }
+}
+
+// One tile is 256 tokens (128 on each CTA of a pair) x kTN channels (each CTA
+// loads and widens half of them; the pair's MMA reads both halves):
+//  * TMA brings 128-byte-wide blocks of x and w rows into a ring of 8-bit
+//    stages (128-byte swizzle, rows and columns past the ends read as 0);
+//  * eight widening warps, alternating blocks by warpgroup, turn a block's x
+//    rows into halves in tensor memory (a thread owns a row, as an MMA with A
+//    in tensor memory wants it) and its w rows into the swizzled K-major layout
+//    in shared memory. With x in shared memory too, the widened writes and the
+//    MMA's operand reads would together take more shared-memory bandwidth than
+//    the MMA takes time;
+//  * one warp of the even CTA issues tcgen05.mma.cta_group::2 (M = 256, N =
+//    kTN, K = 16);
+//  * eight epilogue warps scale, add the bias, round once and store.
+// A tile's K may be cut into slices (few tiles, long K): each slice then
+// writes its integer sums, and linear_join_kernel adds them.
+template <typename T, int kTN>
+__global__ void __launch_bounds__(kTileThreads, 1)
+linear_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const TileArgs a) {
+    using C = TileCfg<kTN>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t* s8 = smem;
+    uint8_t* s16 = smem + C::kStages8 * C::kStage8;
+    TileCtl* ctl = reinterpret_cast<TileCtl*>(s16 + C::kRing * C::kB16);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::kStages8; ++s) {
+            mbar_init(smem_u32(&ctl->full8[s]), 1);
+            mbar_init(smem_u32(&ctl->empty8[s]), 4);
+        }
+        for (int r = 0; r < C::kRing; ++r) {
+            mbar_init(smem_u32(&ctl->ready[r]), 8);  // four warps of each CTA
+            mbar_init(smem_u32(&ctl->freed[r]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&ctl->acc_full[b]), 1);
+            mbar_init(smem_u32(&ctl->acc_empty[b]), 16);  // eight warps of each CTA
+        }
+        mbar_init(smem_u32(&ctl->mma_done), 1);
+        ctl->abort = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&tm_x);
+        tma_prefetch_desc(&tm_w);
+    }
+    if (warp == 1) {
+        tmem_alloc<2>(smem_u32(&ctl->tmem_base), 512);
+        tmem_relinquish<2>();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // barriers of both CTAs exist before any remote arrival
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem_base;
+    const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA
+        if (lane == 0) {
+            int32_t stage = 0;
+            uint32_t phase = 0;
+            int64_t issued = 0;
+            bool ok = true;
+            for (int64_t it = first; it < a.items && ok; it += step) {
+                const TileItem t = tile_item<kTN>(a, it, rank);
+                for (int32_t kb = t.kb0; kb < t.kb1; ++kb) {
+                    if (!tile_wait(a, ctl, &ctl->empty8[stage], phase ^ 1u)) { ok = false; break; }
+                    const uint32_t bar = smem_u32(&ctl->full8[stage]);
+                    uint8_t* dst = s8 + stage * C::kStage8;
+                    mbar_arrive_expect_tx(bar, C::kStage8);
+                    tma_load_2d(smem_u32(dst), &tm_x, bar, kb * kTileK, static_cast<int32_t>(t.m0));
+                    tma_load_2d(smem_u32(dst + C::kA8), &tm_w, bar, kb * kTileK,
+                                static_cast<int32_t>(t.n0) + static_cast<int32_t>(rank) * C::kBRows);
+                    ++issued;
+                    if (++stage == C::kStages8) { stage = 0; phase ^= 1u; }
+                }
+            }
+            if (ctl->abort) {  // the copies still in flight land before the CTA leaves
+                const int64_t n = issued < C::kStages8 ? issued : C::kStages8;
+                for (int64_t i = 0; i < n; ++i) {
+                    if (--stage < 0) { stage = C::kStages8 - 1; phase ^= 1u; }
+                    const uint64_t t0 = global_timer_ns();
+                    while (!mbar_try_wait(smem_u32(&ctl->full8[stage]), phase) && global_timer_ns() - t0 < a.timeout_ns) {}
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA (even CTA)
+        if (rank == 0) {
+            constexpr uint32_t idesc = idesc_f16_f32(0, kTileM, kTN);
+            const uint64_t b0 = sdesc_k_sw128(smem_u32(s16));
+            int32_t ring = 0;
+            uint32_t ring_phase = 0;
+            int32_t buf = 0;
+            uint32_t buf_phase = 0;
+            bool ok = true;
+            for (int64_t it = first; it < a.items && ok; it += step) {
+                const TileItem t = tile_item<kTN>(a, it, rank);
+                if (!tile_wait_warp<true>(a, ctl, &ctl->acc_empty[buf], buf_phase ^ 1u)) break;
+                tc_fence_after();
+                const uint32_t d = tmem + static_cast<uint32_t>(buf * kTN);
+                for (int32_t kb = t.kb0; kb < t.kb1; ++kb) {
+                    if (!tile_wait_warp<true>(a, ctl, &ctl->ready[ring], ring_phase)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t at = tmem + kTileACol + static_cast<uint32_t>(ring * 64);
+                    const uint64_t b = b0 + static_cast<uint64_t>((ring * C::kB16) >> 4);
+                    mma_chain4_ts(d, at, b, idesc, kb > t.kb0 ? 1u : 0u);
+                    mma_chain4_ts(d, at + 32, b + (C::kBAtom >> 4), idesc, 1u);
+                    mma_commit_elect<2>(smem_u32(&ctl->freed[ring]));
+                    if (++ring == C::kRing) { ring = 0; ring_phase ^= 1u; }
+                }
+                if (!ok) break;
+                mma_commit_elect<2>(smem_u32(&ctl->acc_full[buf]));
+                if (++buf == C::kAcc) { buf = 0; buf_phase ^= 1u; }
+            }
+            // every MMA issued above completes before the CTA leaves
+            mma_commit_elect<2>(smem_u32(&ctl->mma_done), 1);
+            if (lane == 0) {
+                const uint64_t t0 = global_timer_ns();
+                while (!mbar_try_wait(smem_u32(&ctl->mma_done), 0) && global_timer_ns() - t0 < a.timeout_ns) {}
+            }
+            __syncwarp();
+        }
+    } else if (warp >= kWidenWarp0 && warp < kTileEpiWarp0) {
+        // ------------------------------------------------------------ widening
+        const int wg = (warp - kWidenWarp0) >> 2, q = warp & 3;
+        const int row = q * 32 + lane;
+        const uint32_t a_lane = tmem + (static_cast<uint32_t>(q * 32) << 16) + kTileACol;
+        // this thread's w row, and the first of its 16-byte chunks
+        constexpr int kBChunks = 8 * C::kBRows / 128;
+        const int b_row = row % C::kBRows, b_chunk = (row / C::kBRows) * kBChunks;
+        int32_t stage = 0, ring = 0;
+        uint32_t phase = 0, ring_phase = 0;
+        int turn = 0;
+        bool ok = true;
+        for (int64_t it = first; it < a.items && ok; it += step) {
+            const TileItem t = tile_item<kTN>(a, it, rank);
+            for (int32_t kb = t.kb0; kb < t.kb1; ++kb) {
+                if (turn == wg) {
+                    if (!tile_wait_warp(a, ctl, &ctl->full8[stage], phase) ||
+                        !tile_wait_warp(a, ctl, &ctl->freed[ring], ring_phase ^ 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint8_t* src = s8 + stage * C::kStage8;
+                    const uint8_t* xrow = src + row * kTileK;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint4 v[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            v[c] = *reinterpret_cast<const uint4*>(xrow + (((half * 4 + c) ^ (row & 7)) << 4));
+                        uint32_t h[32];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t e[8];
+                            widen16(v[c], e);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) h[c * 8 + i] = e[i];
+                        }
+                        tmem_st32(a_lane + static_cast<uint32_t>(ring * 64 + half * 32), h);
+                    }
+                    const uint8_t* wrow = src + C::kA8 + b_row * kTileK;
+                    uint8_t* dst = s16 + ring * C::kB16 + b_row * 128;
+#pragma unroll
+                    for (int c0 = 0; c0 < kBChunks; ++c0) {
+                        const int c = b_chunk + c0;
+                        const uint4 v = *reinterpret_cast<const uint4*>(wrow + ((c ^ (b_row & 7)) << 4));
+                        uint8_t* p = dst + (c >> 2) * C::kBAtom;
+                        const int c16 = (c & 3) * 2;
+                        *reinterpret_cast<uint4*>(p + ((c16 ^ (b_row & 7)) << 4)) = i8x8_to_f16x8(v.x, v.y);
+                        *reinterpret_cast<uint4*>(p + (((c16 + 1) ^ (b_row & 7)) << 4)) = i8x8_to_f16x8(v.z, v.w);
+                    }
+                    fence_proxy_async_smem();
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive_cluster(map_shared_rank(smem_u32(&ctl->ready[ring]), 0));
+                        mbar_arrive(smem_u32(&ctl->empty8[stage]));
+                    }
+                }
+                turn ^= 1;
+                if (++stage == C::kStages8) { stage = 0; phase ^= 1u; }
+                if (++ring == C::kRing) { ring = 0; ring_phase ^= 1u; }
+            }
+        }
+    } else if (warp >= kTileEpiWarp0) {
+        // ------------------------------------------------------------ epilogue
+        const int q = warp & 3, half = (warp - kTileEpiWarp0) >> 2;
+        constexpr int kCols = kTN / 2;  // columns per warp
+        int32_t buf = 0;
+        uint32_t buf_phase = 0;
+        for (int64_t it = first; it < a.items; it += step) {
+            const TileItem t = tile_item<kTN>(a, it, rank);
+            const int64_t m = t.m0 + q * 32 + lane;
+            const bool real = m < a.l.M;
+            const float xs = real && a.slices == 1 ? __ldg(a.l.x_scale + m) : 0.f;
+            if (!tile_wait_warp(a, ctl, &ctl->acc_full[buf], buf_phase)) break;
+            tc_fence_after();
+            const uint32_t src = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * kTN + half * kCols);
+#pragma unroll 1
+            for (int c = 0; c < kCols; c += 32) {
+                float v[32];
+                tmem_ld32(src + c, v);
+                tmem_wait_ld();
+                if (c + 32 == kCols) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote(map_shared_rank(smem_u32(&ctl->acc_empty[buf]), 0));
+                }
+                const int64_t n = t.n0 + half * kCols + c;
+                if (real && n < a.l.N) {
+                    if (a.slices == 1) {
+                        store_row32<T>(a, m, n, xs, v);
+                    } else {
+                        int32_t* p = a.partial + (static_cast<int64_t>(t.slice) * a.l.M + m) * a.l.N + n;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (n + i < a.l.N) p[i] = __float2int_rn(v[i]);
+                    }
+                }
+            }
+            if (++buf == C::kAcc) { buf = 0; buf_phase ^= 1u; }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // no CTA leaves while its pair may still touch it
+    tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        tmem_dealloc<2>(tmem, 512);
+    }
+}
+
+// Adds the slices' integer sums, scales, adds the bias and rounds once.
+template <typename T>
+__global__ void __launch_bounds__(256) linear_join_kernel(const LinearArgs l, const int32_t* __restrict__ partial,
+                                                          int32_t slices) {
+    const int64_t n_out = static_cast<int64_t>(l.M) * l.N;
+    for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n_out;
+         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        const int64_t m = i / l.N, n = i - m * l.N;
+        int32_t sum = 0;
+        for (int32_t s = 0; s < slices; ++s) sum += partial[s * n_out + i];
+        float v = static_cast<float>(sum) * l.x_scale[m] * l.w_scale[n];
+        if (l.bias) v += l.bias[n];
+        static_cast<T*>(l.out)[m * l.ld_out + n] = from_f32<T>(v);
     }
 }
 

@@ -413,6 +413,12 @@ def maxsim_fwd_varlen_streamed(Q: torch.Tensor, cu_seqlens_q: Optional[torch.Ten
     return scores
 
 
+# The handle of a device's current stream, without the Stream object of
+# torch.cuda.current_stream (2 us of a small call).
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _rows(t: torch.Tensor, name: str):
     """(tensor, rows, cols, row stride) of a CUDA tensor [..., cols] whose rows
     the library can read in place; copied where its strides do not allow it."""
@@ -431,10 +437,8 @@ def _rows(t: torch.Tensor, name: str):
     return t, (t.numel() // cols if cols else t.shape[:-1].numel()), cols, cols
 
 
-def _given(out: Optional[torch.Tensor], name: str, shape, dtype, device):
-    """The caller's output buffer, checked, or a new one: contiguous rows."""
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+def _given(out: torch.Tensor, name: str, shape, dtype, device):
+    """The caller's output buffer, checked."""
     if out.shape != shape or out.dtype != dtype or out.device != device or not out.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return out
@@ -450,10 +454,11 @@ def quantize_rows(x: torch.Tensor, *, normalize: bool = False, q: Optional[torch
         raise TypeError(f"x must be float16, bfloat16 or float32, got {x.dtype}")
     shape, dev = x.shape, x.device
     x, rows, cols, ld = _rows(x, "x")
-    q = _given(q, "q", shape, torch.int8, dev)
-    scale = _given(scale, "scale", shape[:-1], torch.float32, dev)
+    q = torch.empty(shape, dtype=torch.int8, device=dev) if q is None else _given(q, "q", shape, torch.int8, dev)
+    scale = (torch.empty(shape[:-1], dtype=torch.float32, device=dev) if scale is None
+             else _given(scale, "scale", shape[:-1], torch.float32, dev))
     rc = _native.lib().maxsim_quantize_rows(x.data_ptr(), dt, rows, cols, ld, 1 if normalize else 0, q.data_ptr(),
-                                            cols, scale.data_ptr(), _stream(dev))
+                                            cols, scale.data_ptr(), _raw_stream(dev.index))
     if rc:
         _native.check(rc, "maxsim_quantize_rows")
     return q, scale
@@ -480,14 +485,13 @@ def linear_int8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale
         raise ValueError("w must be [N, K] with x's K")
     if x_scale.shape != shape[:-1] or w_scale.shape != (N,) or (bias is not None and bias.shape != (N,)):
         raise ValueError("x_scale must have x's leading shape, w_scale and bias [N]")
+    if w.device != dev or x_scale.device != dev or w_scale.device != dev or (bias is not None and bias.device != dev):
+        raise ValueError("x, w, their scales and bias must be on one device")
     x_scale, w_scale = x_scale.contiguous(), w_scale.contiguous()
     if bias is not None:
         bias = bias.contiguous()
-        if bias.device != dev:
-            raise ValueError(f"bias is on {bias.device}, expected {dev}")
-    if w.device != dev or x_scale.device != dev or w_scale.device != dev:
-        raise ValueError("x, w and their scales must be on one device")
-    out = _given(out, "out", shape[:-1] + (N,), out_dtype, dev)
+    full = shape[:-1] + (N,)
+    out = torch.empty(full, dtype=out_dtype, device=dev) if out is None else _given(out, "out", full, out_dtype, dev)
     px, pw = x.data_ptr(), w.data_ptr()
     lib = _native.lib()
     need = lib.maxsim_workspace_size(_native.OP_LINEAR_INT8, M, N, K, ld_x if px % 16 == 0 else 1,
@@ -497,7 +501,7 @@ def linear_int8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale
     ws, nbytes = _workspace(need, dev, workspace)
     rc = lib.maxsim_linear_int8(px, ld_x, x_scale.data_ptr(), pw, ld_w, w_scale.data_ptr(),
                                 None if bias is None else bias.data_ptr(), M, N, K, dt, out.data_ptr(), N,
-                                None if ws is None else ws.data_ptr(), nbytes, _stream(dev))
+                                None if ws is None else ws.data_ptr(), nbytes, _raw_stream(dev.index))
     if rc:
         _native.check(rc, "maxsim_linear_int8")
     return out
@@ -521,9 +525,9 @@ def dropout_fwd(x: torch.Tensor, p: float, seed: int, offset: int = 0, residual:
     else:
         pr, ld_r = None, 0
     x, rows, cols, ld = _rows(x, "x")
-    out = _given(out, "out", shape, x.dtype, dev)
+    out = torch.empty(shape, dtype=x.dtype, device=dev) if out is None else _given(out, "out", shape, x.dtype, dev)
     rc = _native.lib().maxsim_dropout_fwd(x.data_ptr(), dt, rows, cols, ld, pr, ld_r, p, seed, offset, out.data_ptr(),
-                                          cols, _stream(dev))
+                                          cols, _raw_stream(dev.index))
     if rc:
         _native.check(rc, "maxsim_dropout_fwd")
     return out
@@ -538,9 +542,10 @@ def dropout_bwd(grad: torch.Tensor, p: float, seed: int, offset: int = 0, *,
         raise TypeError(f"grad must be float16, bfloat16 or float32, got {grad.dtype}")
     shape, dev = grad.shape, grad.device
     grad, rows, cols, ld = _rows(grad, "grad")
-    out = _given(out, "out", shape, grad.dtype, dev)
+    out = (torch.empty(shape, dtype=grad.dtype, device=dev) if out is None
+           else _given(out, "out", shape, grad.dtype, dev))
     rc = _native.lib().maxsim_dropout_bwd(grad.data_ptr(), dt, rows, cols, ld, p, seed, offset, out.data_ptr(), cols,
-                                          _stream(dev))
+                                          _raw_stream(dev.index))
     if rc:
         _native.check(rc, "maxsim_dropout_bwd")
     return out
