@@ -359,8 +359,8 @@ maxsim_status maxsim_fwd_varlen_streamed(const void *Q, const int32_t *cu_seqlen
  *   x      [rows, cols] f16 / bf16 / f32, rows ld_x elements apart
  *   q      [rows, cols] i8 (out), rows ld_q bytes apart
  *   scale  [rows] f32 (out)
- *   a = max |x|;  s = max(a / 127, 2^-126);  q = clamp(rint(x / s), -127, 127)
- * with fp32 division and ties to even. scale is s, so that q * scale is the
+ *   a = max |x|;  s = max(a * (1 / 127), 2^-126);  q = clamp(rint(x / s), -127, 127)
+ * in fp32 (1 / 127 as fp32, the division rounded), ties to even. scale is s, so that q * scale is the
  * quantised row; with `normalize` (nonzero) it is 1 / ||x / s||_2, so that
  * q * scale is the quantised row of unit length. A row of zeros gives q = 0
  * and scale = 2^-126 either way (the scoring wants a positive scale). A row

@@ -140,11 +140,12 @@ inline bool rows_direct(int64_t K, int64_t ld) { return K % 16 == 0 && ld % 16 =
 
 struct LinearPlan {
     bool few = false;
+    bool swap = false;   // A is w, B is x
     int tn = 256;
-    int64_t tiles = 0, tiles_n = 0;
+    int64_t tiles = 0, tiles_b = 0;
     int32_t kb = 0, slices = 1, kb_slice = 0;
     int64_t k_pad = 0;
-    size_t off_x = 0, off_w = 0, off_partial = 0, bytes = 0;
+    size_t off_x = 0, off_w = 0, off_b = 0, off_partial = 0, bytes = 0;
 };
 
 LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool x_direct, bool w_direct) {
@@ -152,24 +153,28 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool x_direct, bool w_di
     if (M == 0 || N == 0 || K == 0) return p;
     p.k_pad = (K + 15) / 16 * 16;
     p.few = M <= kFewTokens;
+    p.swap = !p.few && N > M;  // the tile kernel's A is the larger operand
     size_t off = 0;
-    if (!x_direct) {
+    if (!x_direct && (p.few || !p.swap)) {
         p.off_x = off;
         off = bytes_round_up(off + static_cast<size_t>(M) * p.k_pad, 256);
     }
-    if (!w_direct) {
+    if (!w_direct && (p.few || p.swap)) {
         p.off_w = off;
         off = bytes_round_up(off + static_cast<size_t>(N) * p.k_pad, 256);
     }
     if (!p.few) {
+        const int64_t rows_a = p.swap ? N : M, rows_b = p.swap ? M : N;
+        p.off_b = off;
+        off = bytes_round_up(off + static_cast<size_t>(rows_b) * p.k_pad * 2, 256);
         // Tile width and slices of K by the time they should take, in cycles:
         // the items of the busiest pair, each its blocks and a start and end,
         // and for slices the kernel that joins them.
         p.kb = static_cast<int32_t>((K + kTileK - 1) / kTileK);
         double best = 0.0;
-        for (int tn = 256; tn >= 128; tn -= 128) {
-            const int64_t tiles_n = (N + tn - 1) / tn, tiles = (M + kTileM - 1) / kTileM * tiles_n;
-            const double block = tn == 256 ? 1024.0 : 640.0, ends = tn == 256 ? 3000.0 : 2000.0;
+        for (int tn = 256; tn >= 64; tn /= 2) {
+            const int64_t tiles_b = (rows_b + tn - 1) / tn, tiles = (rows_a + kTileM - 1) / kTileM * tiles_b;
+            const double block = tn == 256 ? 1050.0 : tn == 128 ? 600.0 : 500.0, ends = tn == 256 ? 3000.0 : 2000.0;
             for (int32_t slices = 1; slices <= std::min(p.kb, 16); ++slices) {
                 const int32_t kb_slice = (p.kb + slices - 1) / slices;
                 if (slices > 1 && (tiles * slices > 2 * kPairs || (p.kb + kb_slice - 1) / kb_slice != slices)) continue;
@@ -179,7 +184,7 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool x_direct, bool w_di
                     best = cost;
                     p.tn = tn;
                     p.tiles = tiles;
-                    p.tiles_n = tiles_n;
+                    p.tiles_b = tiles_b;
                     p.slices = slices;
                     p.kb_slice = kb_slice;
                 }
@@ -194,13 +199,14 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool x_direct, bool w_di
     return p;
 }
 
-bool encode_i8_rows(EncodeTiledFn encode, CUtensorMap* map, const void* base, int64_t K, int64_t rows, int64_t ld,
-                    uint32_t box_rows) {
+// Rows of K elements, ld bytes apart, in boxes of 128 bytes x box_rows with the 128-byte swizzle.
+bool encode_k_rows(EncodeTiledFn encode, CUtensorMap* map, CUtensorMapDataType type, int elem, const void* base,
+                   int64_t K, int64_t rows, int64_t ld, uint32_t box_rows) {
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
-    const cuuint32_t box[2] = {kTileK, box_rows}, estr[2] = {1, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const cuuint32_t box[2] = {128u / static_cast<cuuint32_t>(elem), box_rows}, estr[2] = {1, 1};
+    return encode(map, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -212,11 +218,12 @@ maxsim_status launch_few(const LinearArgs& a, cudaStream_t st) {
     return launched();
 }
 
-template <typename T, int kTN>
-maxsim_status launch_tile(const LinearPlan& p, const LinearArgs& l, int32_t* partial, const HostDevice& dev,
-                          cudaStream_t st) {
-    auto kern = linear_tile_kernel<T, kTN>;
+template <typename T, int kTN, bool kSwap>
+maxsim_status launch_tile(const LinearPlan& p, const LinearArgs& l, const __half* b16, int32_t* partial,
+                          const HostDevice& dev, cudaStream_t st) {
+    auto kern = linear_tile_kernel<T, kTN, kSwap>;
     constexpr size_t kSmem = tile_smem_bytes<kTN>();
+    static_assert(kSmem <= 232448, "shared memory of one SM");
     static std::atomic<uint64_t> prepared{0};  // devices whose shared-memory limit is raised
     const uint64_t bit = uint64_t(1) << dev.index;
     if (!(prepared.load(std::memory_order_acquire) & bit)) {
@@ -224,22 +231,26 @@ maxsim_status launch_tile(const LinearPlan& p, const LinearArgs& l, int32_t* par
             return MAXSIM_ERR_CUDA;
         prepared.fetch_or(bit, std::memory_order_release);
     }
-    CUtensorMap tx, tw;
-    if (!encode_i8_rows(dev.encode, &tx, l.x, l.K, l.M, l.ld_x, 128) ||
-        !encode_i8_rows(dev.encode, &tw, l.w, l.K, l.N, l.ld_w, TileCfg<kTN>::kBRows))
-        return MAXSIM_ERR_CUDA;
     TileArgs a{};
     a.l = l;
     a.partial = partial;
     a.items = p.tiles * p.slices;
-    a.tiles_n = static_cast<int32_t>(p.tiles_n);
+    a.rows_a = kSwap ? l.N : l.M;
+    a.rows_b = kSwap ? l.M : l.N;
+    a.tiles_b = static_cast<int32_t>(p.tiles_b);
     a.slices = p.slices;
     a.kb = p.kb;
     a.kb_slice = p.kb_slice;
     a.vec_out = ptr_aligned(l.out, 16) && l.ld_out * static_cast<int64_t>(sizeof(T)) % 16 == 0;
-    a.vec_scale = ptr_aligned(l.w_scale, 16) && ptr_aligned(l.bias, 16);
+    a.vec_scale = kSwap ? ptr_aligned(l.x_scale, 16) : ptr_aligned(l.w_scale, 16) && ptr_aligned(l.bias, 16);
     a.status = dev.status;
     a.timeout_ns = kTimeoutNs;
+    CUtensorMap ta, tb;
+    if (!encode_k_rows(dev.encode, &ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, kSwap ? l.w : l.x, l.K, a.rows_a,
+                       kSwap ? l.ld_w : l.ld_x, 128) ||
+        !encode_k_rows(dev.encode, &tb, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, b16, p.k_pad, a.rows_b, p.k_pad * 2,
+                       TileCfg<kTN>::kBRows))
+        return MAXSIM_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(a.items, std::max(1, dev.num_sms / 2))));
     cfg.blockDim = dim3(kTileThreads);
@@ -252,8 +263,16 @@ maxsim_status launch_tile(const LinearPlan& p, const LinearArgs& l, int32_t* par
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kern, tx, tw, a) != cudaSuccess) return MAXSIM_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, kern, ta, tb, a) != cudaSuccess) return MAXSIM_ERR_CUDA;
     return launched();
+}
+
+template <typename T, bool kSwap>
+maxsim_status launch_tile_width(const LinearPlan& p, const LinearArgs& l, const __half* b16, int32_t* partial,
+                                const HostDevice& dev, cudaStream_t st) {
+    if (p.tn == 256) return launch_tile<T, 256, kSwap>(p, l, b16, partial, dev, st);
+    if (p.tn == 128) return launch_tile<T, 128, kSwap>(p, l, b16, partial, dev, st);
+    return launch_tile<T, 64, kSwap>(p, l, b16, partial, dev, st);
 }
 
 template <typename T>
@@ -266,14 +285,24 @@ maxsim_status run_linear(const LinearPlan& p, LinearArgs l, bool x_direct, bool 
         return launched();
     }
     const int32_t k_pad = static_cast<int32_t>(p.k_pad);
-    if (!x_direct) {
+    const __half* b16 = nullptr;
+    if (!p.few) {  // B: x when swapped, else w
+        __half* to = reinterpret_cast<__half*>(ws + p.off_b);
+        const int8_t* from = p.swap ? l.x : l.w;
+        const int64_t rows = p.swap ? l.M : l.N, ld = p.swap ? l.ld_x : l.ld_w;
+        const unsigned grid = grid_of(rows * (k_pad / 16), 256, most);
+        if (p.swap ? x_direct : w_direct) widen_rows_kernel<true><<<grid, 256, 0, st>>>(from, rows, l.K, ld, to, k_pad);
+        else widen_rows_kernel<false><<<grid, 256, 0, st>>>(from, rows, l.K, ld, to, k_pad);
+        b16 = to;
+    }
+    if (!x_direct && (p.few || !p.swap)) {
         int8_t* to = reinterpret_cast<int8_t*>(ws + p.off_x);
         repack_rows_kernel<<<grid_of(static_cast<int64_t>(l.M) * (k_pad / 16), 256, most), 256, 0, st>>>(
             l.x, l.M, l.K, l.ld_x, to, k_pad);
         l.x = to;
         l.ld_x = k_pad;
     }
-    if (!w_direct) {
+    if (!w_direct && (p.few || p.swap)) {
         int8_t* to = reinterpret_cast<int8_t*>(ws + p.off_w);
         repack_rows_kernel<<<grid_of(static_cast<int64_t>(l.N) * (k_pad / 16), 256, most), 256, 0, st>>>(
             l.w, l.N, l.K, l.ld_w, to, k_pad);
@@ -289,7 +318,8 @@ maxsim_status run_linear(const LinearPlan& p, LinearArgs l, bool x_direct, bool 
         return launch_few<T, 4>(l, st);
     }
     int32_t* partial = reinterpret_cast<int32_t*>(ws + p.off_partial);
-    rc = p.tn == 256 ? launch_tile<T, 256>(p, l, partial, dev, st) : launch_tile<T, 128>(p, l, partial, dev, st);
+    rc = p.swap ? launch_tile_width<T, true>(p, l, b16, partial, dev, st)
+                : launch_tile_width<T, false>(p, l, b16, partial, dev, st);
     if (rc != MAXSIM_OK || p.slices == 1) return rc;
     linear_join_kernel<T><<<join_grid, 256, 0, st>>>(l, partial, p.slices);
     return launched();

@@ -31,7 +31,7 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 
 // ---------------------------------------------------------------- row quantisation
 //
-// scale = max |x| / 127 needs the whole row before the first code, so a row
+// The scale, a 127th of max |x|, needs the whole row before the first code, so a row
 // is held in registers between the two: one read of x, one write of q. A row
 // belongs to a group of 8, 32, 128 or 512 threads, each holding up to
 // kChunks 16-byte chunks (or kChunks single elements where the rows do not
@@ -100,7 +100,7 @@ struct Chunk<T, false> {
     static __device__ __forceinline__ void store(int8_t* q, const uint32_t* w) { *q = static_cast<int8_t>(w[0]); }
 };
 
-// From the largest |x| of a row (bits of T): whether the row is finite, and s = max(a / 127, 2^-126).
+// From the largest |x| of a row (bits of T): whether the row is finite, and s = max(a * (1 / 127), 2^-126).
 template <typename T>
 __device__ __forceinline__ bool row_step(uint32_t bits, float* s) {
     float a;
@@ -115,7 +115,7 @@ __device__ __forceinline__ bool row_step(uint32_t bits, float* s) {
         finite = bits < 0x7f80u;
         a = __uint_as_float(bits << 16);
     }
-    *s = finite ? fmaxf(__fdiv_rn(a, 127.f), FLT_MIN) : 1.f;
+    *s = finite ? fmaxf(__fmul_rn(a, 1.f / 127.f), FLT_MIN) : 1.f;
     return finite;
 }
 

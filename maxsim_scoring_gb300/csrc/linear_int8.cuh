@@ -5,13 +5,12 @@
 // 8-bit integer form was measured at 150 TOP/s, a quarter of the f16 form's
 // 605 TFLOP/s. So both kernels widen the integers to binary16 on the SM, next
 // to the tensor cores: |v| <= 128 is exact there, a product of two is exact in
-// fp32, and a sum of up to 1,024 products (2^24) is too. Device memory is read
-// as 8-bit values only.
+// fp32, and a sum of up to 1,024 products (2^24) is too.
 //
 //  * linear_few_kernel (few tokens): bound by the bytes of w, each read once.
-//  * linear_tile_kernel (many tokens): tcgen05 MMAs of 256 x 256 or 256 x 128
-//    tiles on CTA pairs, bound by the tensor pipe, or by the bytes of x where
-//    w is narrow.
+//  * linear_tile_kernel (many tokens): tcgen05 MMAs of 256-row tiles on CTA
+//    pairs, bound by the tensor pipe, or by the bytes of the larger operand
+//    where the other one is narrow.
 #pragma once
 
 #include <cstdint>
@@ -48,6 +47,34 @@ __global__ void __launch_bounds__(256) repack_rows_kernel(const int8_t* __restri
         for (int e = 0; e < 16; ++e)
             if (k + e < K) w[e >> 2] |= static_cast<uint32_t>(p[e]) << ((e & 3) * 8);
         *reinterpret_cast<uint4*>(dst + r * ld_dst + k) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// Rows of K bytes into rows of k_pad halves (a multiple of 16, the tail zero):
+// the tile kernel's smaller operand.
+template <bool kWide>
+__global__ void __launch_bounds__(256) widen_rows_kernel(const int8_t* __restrict__ src, int64_t rows, int32_t K,
+                                                         int64_t ld_src, __half* __restrict__ dst, int32_t k_pad) {
+    const int32_t per_row = k_pad >> 4;
+    const int64_t n = rows * per_row;
+    for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n;
+         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        const int64_t r = i / per_row;
+        const int32_t k = static_cast<int32_t>(i - r * per_row) << 4;
+        const uint8_t* p = reinterpret_cast<const uint8_t*>(src) + r * ld_src + k;
+        uint4 v;
+        if constexpr (kWide) {
+            v = __ldg(reinterpret_cast<const uint4*>(p));
+        } else {
+            uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (k + e < K) w[e >> 2] |= static_cast<uint32_t>(p[e]) << ((e & 3) * 8);
+            v = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        uint4* to = reinterpret_cast<uint4*>(dst + r * k_pad + k);
+        to[0] = i8x8_to_f16x8(v.x, v.y);
+        to[1] = i8x8_to_f16x8(v.z, v.w);
     }
 }
 
@@ -147,47 +174,46 @@ __global__ void __launch_bounds__(kFewWarps * 32) linear_few_kernel(const Linear
 
 // ---------------------------------------------------------------- many tokens
 
-constexpr int kTileM = 256;            // tokens per tile: 128 on each CTA of a pair
-constexpr int kTileK = 128;            // bytes of K per block
-constexpr int kTileMaxRing = 4;
-constexpr int kWidenWarp0 = 4, kTileEpiWarp0 = 12;
-constexpr int kTileThreads = 640;      // warp 0 TMA, warp 1 MMA, warps 4-11 widen, warps 12-19 epilogue
-constexpr int kTileMaxStages8 = 6;
-constexpr uint32_t kTileACol = 256;    // tensor memory: accumulators in columns 0-255, widened A blocks above
+constexpr int kTileM = 256;            // rows of A per tile: 128 on each CTA of a pair
+constexpr int kTileK = 128;            // values of K per block
+constexpr int kTileRing = 4;           // blocks ready for the MMA: A in tensor memory, B in shared memory
+constexpr int kTileBWarp = 2, kWidenWarp0 = 4, kTileEpiWarp0 = 12;
+constexpr int kTileThreads = 640;      // warp 0 TMA of A, warp 1 MMA, warp 2 TMA of B, warps 4-11 widen, 12-19 epilogue
+constexpr int kTileMaxStages8 = 8;
+constexpr uint32_t kTileACol = 256;    // tensor memory: accumulators in columns 0-255, the ring's A blocks above
 constexpr int kTileStatusTimeout = 4;  // MAXSIM_ERR_TIMEOUT
 
 template <int kTN>
 struct TileCfg {
-    static constexpr int kBRows = kTN / 2;                         // channels per CTA
-    static constexpr int kA8 = 128 * kTileK, kB8 = kBRows * kTileK;  // 8-bit block
-    static constexpr int kStage8 = kA8 + kB8;
-    static constexpr int kBAtom = kBRows * 128;                    // 64 halves of every row
+    static constexpr int kA8 = 128 * kTileK;           // 8-bit block of A: this CTA's 128 rows
+    static constexpr int kBRows = kTN / 2;             // rows of B per CTA
+    static constexpr int kBAtom = kBRows * 128;        // 64 halves of every row
     static constexpr int kB16 = 2 * kBAtom;
-    // Depth of the 8-bit ring (even: each widening warpgroup then always meets
-    // the same stages, and sees every phase of their barriers) and of the ring of
-    // widened blocks (A in tensor memory, B in shared memory).
-    static constexpr int kStages8 = kTN == 256 ? 4 : 6;
-    static constexpr int kRing = kTN == 256 ? 3 : 4;
-    static constexpr int kAcc = 256 / kTN;                         // accumulator buffers
+    // even: each widening warpgroup then always meets the same stages, and
+    // sees every phase of their barriers
+    static constexpr int kStages8 = kTN == 256 ? 6 : 8;
+    static constexpr int kAcc = kTN == 256 ? 1 : 2;    // accumulator buffers
 };
 
 struct TileArgs {
     LinearArgs l;
     int32_t* partial;   // [slices, M, N] integer sums when slices > 1
     int64_t items;      // tiles * slices
-    int32_t tiles_n;
+    int32_t rows_a;     // rows of A (tokens, or channels when swapped)
+    int32_t rows_b;
+    int32_t tiles_b;
     int32_t slices;     // parts of K
     int32_t kb;         // blocks of K
     int32_t kb_slice;   // blocks per slice
     int vec_out;        // rows of out start on 16-byte boundaries
-    int vec_scale;      // w_scale and bias start on 16-byte boundaries
+    int vec_scale;      // the scales (and bias) along B start on 16-byte boundaries
     int* status;
     uint64_t timeout_ns;
 };
 
 struct alignas(16) TileCtl {
     uint64_t full8[kTileMaxStages8], empty8[kTileMaxStages8];
-    uint64_t ready[kTileMaxRing], freed[kTileMaxRing];
+    uint64_t b_full[kTileRing], ready[kTileRing], freed[kTileRing];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t mma_done;
     uint32_t tmem_base;
@@ -197,7 +223,7 @@ struct alignas(16) TileCtl {
 template <int kTN>
 constexpr size_t tile_smem_bytes() {
     using C = TileCfg<kTN>;
-    return 1024 + static_cast<size_t>(C::kStages8) * C::kStage8 + C::kRing * C::kB16 + sizeof(TileCtl);
+    return 1024 + static_cast<size_t>(C::kStages8) * C::kA8 + kTileRing * C::kB16 + sizeof(TileCtl);
 }
 
 // Bounded wait of a thread: gives up after the limit (recorded in the device
@@ -260,7 +286,7 @@ __device__ __forceinline__ void mma_chain4_ts(uint32_t d, uint32_t a, uint64_t b
 }
 
 struct TileItem {
-    int64_t m0, n0;  // this CTA's first token, the tile's first channel
+    int64_t a0, b0;  // this CTA's first row of A, the tile's first row of B
     int32_t kb0, kb1;
     int32_t slice;
 };
@@ -270,15 +296,15 @@ __device__ __forceinline__ TileItem tile_item(const TileArgs& a, int64_t item, u
     TileItem t;
     const int64_t tile = a.slices == 1 ? item : item / a.slices;
     t.slice = static_cast<int32_t>(item - tile * a.slices);
-    const int64_t tm = tile / a.tiles_n;
-    t.m0 = tm * kTileM + rank * 128;
-    t.n0 = (tile - tm * a.tiles_n) * kTN;
+    const int64_t ta = tile / a.tiles_b;
+    t.a0 = ta * kTileM + rank * 128;
+    t.b0 = (tile - ta * a.tiles_b) * kTN;
     t.kb0 = t.slice * a.kb_slice;
     t.kb1 = min(a.kb, t.kb0 + a.kb_slice);
     return t;
 }
 
-// 32 consecutive outputs of row m from column n on.
+// 32 consecutive outputs of token m from channel n on.
 template <typename T>
 __device__ __forceinline__ void store_row32(const TileArgs& a, int64_t m, int64_t n, float xs, const float (&v)[32]) {
     const LinearArgs& l = a.l;
@@ -309,30 +335,59 @@ __device__ __forceinline__ void store_row32(const TileArgs& a, int64_t m, int64_
     }
 }
 
-// One tile is 256 tokens (128 on each CTA of a pair) x kTN channels (each CTA
-// loads and widens half of them; the pair's MMA reads both halves):
-//  * TMA brings 128-byte-wide blocks of x and w rows into a ring of 8-bit
-//    stages (128-byte swizzle, rows and columns past the ends read as 0);
-//  * eight widening warps, alternating blocks by warpgroup, turn a block's x
-//    rows into halves in tensor memory (a thread owns a row, as an MMA with A
-//    in tensor memory wants it) and its w rows into the swizzled K-major layout
-//    in shared memory. With x in shared memory too, the widened writes and the
-//    MMA's operand reads would together take more shared-memory bandwidth than
-//    the MMA takes time;
+// Channel n of 32 consecutive tokens from m on (lanes hold consecutive
+// channels: each store of a warp is one run).
+template <typename T>
+__device__ __forceinline__ void store_col32(const TileArgs& a, int64_t m, int64_t n, float ws, float bias,
+                                            const float (&v)[32]) {
+    const LinearArgs& l = a.l;
+    T* out = static_cast<T*>(l.out) + m * l.ld_out + n;
+    if (m + 32 <= l.M && a.vec_scale) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            const float4 xs = __ldg(reinterpret_cast<const float4*>(l.x_scale + m + i));
+            out[(i + 0) * l.ld_out] = from_f32<T>(__fmaf_rn(v[i + 0] * xs.x, ws, bias));
+            out[(i + 1) * l.ld_out] = from_f32<T>(__fmaf_rn(v[i + 1] * xs.y, ws, bias));
+            out[(i + 2) * l.ld_out] = from_f32<T>(__fmaf_rn(v[i + 2] * xs.z, ws, bias));
+            out[(i + 3) * l.ld_out] = from_f32<T>(__fmaf_rn(v[i + 3] * xs.w, ws, bias));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (m + i < l.M) out[i * l.ld_out] = from_f32<T>(__fmaf_rn(v[i] * __ldg(l.x_scale + m + i), ws, bias));
+    }
+}
+
+// One tile is 256 rows of A (128 on each CTA of a pair) x kTN rows of B. A is
+// the larger operand (x, or w when kSwap) and stays 8-bit until it is on the
+// SM; B, the smaller one, was widened to halves in device memory once for all
+// tiles (widen_rows_kernel).
+//  * TMA brings 128-byte-wide blocks of A's rows into a ring of 8-bit stages
+//    and blocks of B (each CTA half of the tile's rows) into a ring of operand
+//    stages (128-byte swizzle; rows and columns past the ends read as 0);
+//  * eight widening warps, alternating blocks by warpgroup, turn A's rows into
+//    halves in tensor memory: a thread owns a row, as an MMA with A in tensor
+//    memory wants it. Widened into shared memory, A would be written and read
+//    there once more, which with B's traffic takes more time than the MMA;
 //  * one warp of the even CTA issues tcgen05.mma.cta_group::2 (M = 256, N =
 //    kTN, K = 16);
 //  * eight epilogue warps scale, add the bias, round once and store.
+// What a widening warp hands to the MMA is in tensor memory (ordered by
+// tcgen05.fence::before_thread_sync) or was written by TMA (observed on
+// b_full), so its arrival on the even CTA's barrier releases at CTA scope. A
+// cluster-scope release took the warp 800 to 2,000 cycles per block
+// (32768 x 4096 x 4096: 751 us, and 609 us without).
 // A tile's K may be cut into slices (few tiles, long K): each slice then
 // writes its integer sums, and linear_join_kernel adds them.
-template <typename T, int kTN>
+template <typename T, int kTN, bool kSwap>
 __global__ void __launch_bounds__(kTileThreads, 1)
-linear_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const TileArgs a) {
+linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const TileArgs a) {
     using C = TileCfg<kTN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t* s8 = smem;
-    uint8_t* s16 = smem + C::kStages8 * C::kStage8;
-    TileCtl* ctl = reinterpret_cast<TileCtl*>(s16 + C::kRing * C::kB16);
+    uint8_t* s16 = smem + C::kStages8 * C::kA8;
+    TileCtl* ctl = reinterpret_cast<TileCtl*>(s16 + kTileRing * C::kB16);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     if (threadIdx.x == 0) {
@@ -340,7 +395,8 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             mbar_init(smem_u32(&ctl->full8[s]), 1);
             mbar_init(smem_u32(&ctl->empty8[s]), 4);
         }
-        for (int r = 0; r < C::kRing; ++r) {
+        for (int r = 0; r < kTileRing; ++r) {
+            mbar_init(smem_u32(&ctl->b_full[r]), 1);
             mbar_init(smem_u32(&ctl->ready[r]), 8);  // four warps of each CTA
             mbar_init(smem_u32(&ctl->freed[r]), 1);
         }
@@ -351,8 +407,8 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         mbar_init(smem_u32(&ctl->mma_done), 1);
         ctl->abort = 0;
         fence_barrier_init();
-        tma_prefetch_desc(&tm_x);
-        tma_prefetch_desc(&tm_w);
+        tma_prefetch_desc(&tm_a);
+        tma_prefetch_desc(&tm_b);
     }
     if (warp == 1) {
         tmem_alloc<2>(smem_u32(&ctl->tmem_base), 512);
@@ -365,9 +421,13 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     const uint32_t tmem = ctl->tmem_base;
     const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
-    if (warp == 0) {
+    if (warp == 0 || warp == kTileBWarp) {
         // ------------------------------------------------------------ TMA
         if (lane == 0) {
+            const bool is_a = warp == 0;
+            const int depth = is_a ? C::kStages8 : kTileRing;
+            uint64_t* full = is_a ? ctl->full8 : ctl->b_full;
+            uint64_t* empty = is_a ? ctl->empty8 : ctl->freed;
             int32_t stage = 0;
             uint32_t phase = 0;
             int64_t issued = 0;
@@ -375,36 +435,41 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             for (int64_t it = first; it < a.items && ok; it += step) {
                 const TileItem t = tile_item<kTN>(a, it, rank);
                 for (int32_t kb = t.kb0; kb < t.kb1; ++kb) {
-                    if (!tile_wait(a, ctl, &ctl->empty8[stage], phase ^ 1u)) { ok = false; break; }
-                    const uint32_t bar = smem_u32(&ctl->full8[stage]);
-                    uint8_t* dst = s8 + stage * C::kStage8;
-                    mbar_arrive_expect_tx(bar, C::kStage8);
-                    tma_load_2d(smem_u32(dst), &tm_x, bar, kb * kTileK, static_cast<int32_t>(t.m0));
-                    tma_load_2d(smem_u32(dst + C::kA8), &tm_w, bar, kb * kTileK,
-                                static_cast<int32_t>(t.n0) + static_cast<int32_t>(rank) * C::kBRows);
+                    if (!tile_wait(a, ctl, &empty[stage], phase ^ 1u)) { ok = false; break; }
+                    const uint32_t bar = smem_u32(&full[stage]);
+                    if (is_a) {
+                        mbar_arrive_expect_tx(bar, C::kA8);
+                        tma_load_2d(smem_u32(s8 + stage * C::kA8), &tm_a, bar, kb * kTileK, static_cast<int32_t>(t.a0));
+                    } else {
+                        const int32_t row = static_cast<int32_t>(t.b0) + static_cast<int32_t>(rank) * C::kBRows;
+                        const uint32_t dst = smem_u32(s16 + stage * C::kB16);
+                        mbar_arrive_expect_tx(bar, C::kB16);
+                        tma_load_2d(dst, &tm_b, bar, kb * kTileK, row);
+                        tma_load_2d(dst + C::kBAtom, &tm_b, bar, kb * kTileK + 64, row);
+                    }
                     ++issued;
-                    if (++stage == C::kStages8) { stage = 0; phase ^= 1u; }
+                    if (++stage == depth) { stage = 0; phase ^= 1u; }
                 }
             }
             if (ctl->abort) {  // the copies still in flight land before the CTA leaves
-                const int64_t n = issued < C::kStages8 ? issued : C::kStages8;
+                const int64_t n = issued < depth ? issued : depth;
                 for (int64_t i = 0; i < n; ++i) {
-                    if (--stage < 0) { stage = C::kStages8 - 1; phase ^= 1u; }
+                    if (--stage < 0) { stage = depth - 1; phase ^= 1u; }
                     const uint64_t t0 = global_timer_ns();
-                    while (!mbar_try_wait(smem_u32(&ctl->full8[stage]), phase) && global_timer_ns() - t0 < a.timeout_ns) {}
+                    while (!mbar_try_wait(smem_u32(&full[stage]), phase) && global_timer_ns() - t0 < a.timeout_ns) {}
                 }
             }
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA (even CTA)
         if (rank == 0) {
-            constexpr uint32_t idesc = idesc_f16_f32(0, kTileM, kTN);
-            const uint64_t b0 = sdesc_k_sw128(smem_u32(s16));
             int32_t ring = 0;
             uint32_t ring_phase = 0;
+            bool ok = true;
+            constexpr uint32_t idesc = idesc_f16_f32(0, kTileM, kTN);
+            const uint64_t b0 = sdesc_k_sw128(smem_u32(s16));
             int32_t buf = 0;
             uint32_t buf_phase = 0;
-            bool ok = true;
             for (int64_t it = first; it < a.items && ok; it += step) {
                 const TileItem t = tile_item<kTN>(a, it, rank);
                 if (!tile_wait_warp<true>(a, ctl, &ctl->acc_empty[buf], buf_phase ^ 1u)) break;
@@ -418,7 +483,7 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                     mma_chain4_ts(d, at, b, idesc, kb > t.kb0 ? 1u : 0u);
                     mma_chain4_ts(d, at + 32, b + (C::kBAtom >> 4), idesc, 1u);
                     mma_commit_elect<2>(smem_u32(&ctl->freed[ring]));
-                    if (++ring == C::kRing) { ring = 0; ring_phase ^= 1u; }
+                    if (++ring == kTileRing) { ring = 0; ring_phase ^= 1u; }
                 }
                 if (!ok) break;
                 mma_commit_elect<2>(smem_u32(&ctl->acc_full[buf]));
@@ -437,9 +502,6 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         const int wg = (warp - kWidenWarp0) >> 2, q = warp & 3;
         const int row = q * 32 + lane;
         const uint32_t a_lane = tmem + (static_cast<uint32_t>(q * 32) << 16) + kTileACol;
-        // this thread's w row, and the first of its 16-byte chunks
-        constexpr int kBChunks = 8 * C::kBRows / 128;
-        const int b_row = row % C::kBRows, b_chunk = (row / C::kBRows) * kBChunks;
         int32_t stage = 0, ring = 0;
         uint32_t phase = 0, ring_phase = 0;
         int turn = 0;
@@ -454,47 +516,34 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                         break;
                     }
                     tc_fence_after();
-                    const uint8_t* src = s8 + stage * C::kStage8;
-                    const uint8_t* xrow = src + row * kTileK;
+                    const uint8_t* src = s8 + stage * C::kA8 + row * kTileK;
+                    uint4 v[8];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) v[c] = *reinterpret_cast<const uint4*>(src + ((c ^ (row & 7)) << 4));
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        uint4 v[4];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            v[c] = *reinterpret_cast<const uint4*>(xrow + (((half * 4 + c) ^ (row & 7)) << 4));
                         uint32_t h[32];
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             uint32_t e[8];
-                            widen16(v[c], e);
+                            widen16(v[half * 4 + c], e);
 #pragma unroll
                             for (int i = 0; i < 8; ++i) h[c * 8 + i] = e[i];
                         }
                         tmem_st32(a_lane + static_cast<uint32_t>(ring * 64 + half * 32), h);
                     }
-                    const uint8_t* wrow = src + C::kA8 + b_row * kTileK;
-                    uint8_t* dst = s16 + ring * C::kB16 + b_row * 128;
-#pragma unroll
-                    for (int c0 = 0; c0 < kBChunks; ++c0) {
-                        const int c = b_chunk + c0;
-                        const uint4 v = *reinterpret_cast<const uint4*>(wrow + ((c ^ (b_row & 7)) << 4));
-                        uint8_t* p = dst + (c >> 2) * C::kBAtom;
-                        const int c16 = (c & 3) * 2;
-                        *reinterpret_cast<uint4*>(p + ((c16 ^ (b_row & 7)) << 4)) = i8x8_to_f16x8(v.x, v.y);
-                        *reinterpret_cast<uint4*>(p + (((c16 + 1) ^ (b_row & 7)) << 4)) = i8x8_to_f16x8(v.z, v.w);
-                    }
-                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&ctl->empty8[stage]));
                     tmem_wait_st();
                     tc_fence_before();
+                    // the block is ready once its B has landed too
+                    if (!tile_wait_warp(a, ctl, &ctl->b_full[ring], ring_phase)) { ok = false; break; }
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive_cluster(map_shared_rank(smem_u32(&ctl->ready[ring]), 0));
-                        mbar_arrive(smem_u32(&ctl->empty8[stage]));
-                    }
+                    if (lane == 0) mbar_arrive_remote(map_shared_rank(smem_u32(&ctl->ready[ring]), 0));
                 }
                 turn ^= 1;
                 if (++stage == C::kStages8) { stage = 0; phase ^= 1u; }
-                if (++ring == C::kRing) { ring = 0; ring_phase ^= 1u; }
+                if (++ring == kTileRing) { ring = 0; ring_phase ^= 1u; }
             }
         }
     } else if (warp >= kTileEpiWarp0) {
@@ -505,9 +554,13 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         uint32_t buf_phase = 0;
         for (int64_t it = first; it < a.items; it += step) {
             const TileItem t = tile_item<kTN>(a, it, rank);
-            const int64_t m = t.m0 + q * 32 + lane;
-            const bool real = m < a.l.M;
-            const float xs = real && a.slices == 1 ? __ldg(a.l.x_scale + m) : 0.f;
+            const int64_t ra = t.a0 + q * 32 + lane;  // this thread's row of A
+            const bool real = ra < a.rows_a;
+            float sa = 0.f, bias = 0.f;
+            if (real && a.slices == 1) {
+                sa = __ldg((kSwap ? a.l.w_scale : a.l.x_scale) + ra);
+                if (kSwap && a.l.bias) bias = __ldg(a.l.bias + ra);
+            }
             if (!tile_wait_warp(a, ctl, &ctl->acc_full[buf], buf_phase)) break;
             tc_fence_after();
             const uint32_t src = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * kTN + half * kCols);
@@ -521,15 +574,19 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                     __syncwarp();
                     if (lane == 0) mbar_arrive_remote(map_shared_rank(smem_u32(&ctl->acc_empty[buf]), 0));
                 }
-                const int64_t n = t.n0 + half * kCols + c;
-                if (real && n < a.l.N) {
-                    if (a.slices == 1) {
-                        store_row32<T>(a, m, n, xs, v);
-                    } else {
-                        int32_t* p = a.partial + (static_cast<int64_t>(t.slice) * a.l.M + m) * a.l.N + n;
+                const int64_t rb = t.b0 + half * kCols + c;
+                if (real && rb < a.rows_b) {
+                    if (a.slices > 1) {
+                        int32_t* p = a.partial + static_cast<int64_t>(t.slice) * a.l.M * a.l.N +
+                                     (kSwap ? rb * a.l.N + ra : ra * a.l.N + rb);
+                        const int64_t ld = kSwap ? a.l.N : 1;
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (n + i < a.l.N) p[i] = __float2int_rn(v[i]);
+                            if (rb + i < a.rows_b) p[i * ld] = __float2int_rn(v[i]);
+                    } else if constexpr (kSwap) {
+                        store_col32<T>(a, rb, ra, sa, bias, v);
+                    } else {
+                        store_row32<T>(a, ra, rb, sa, v);
                     }
                 }
             }

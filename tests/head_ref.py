@@ -49,7 +49,7 @@ def quantize(x, normalize):
     bad = ~np.isfinite(x).all(axis=1)
     xf = np.where(bad[:, None], np.float32(0), x)
     a = np.abs(xf).max(axis=1) if cols else np.zeros(rows, np.float32)
-    s = np.maximum((a / np.float32(127)).astype(np.float32), FLT_MIN)
+    s = np.maximum((a * (np.float32(1) / np.float32(127))).astype(np.float32), FLT_MIN)
     y = (xf / s[:, None]).astype(np.float32)
     q = np.clip(np.rint(y), -127, 127).astype(np.int8)
     scale, rel = s.astype(np.float64), np.full(rows, 2 * U)

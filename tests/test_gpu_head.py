@@ -73,12 +73,12 @@ def test_quantize_halfway_codes():
     # quotients on and one unit around every half-integer: fp32 division and ties to even decide
     base = np.arange(-126.5, 127.0, 1.0, dtype=np.float32)
     for a in (127.0, 1.0, 3.0e-5, 0.7):
-        s = np.float32(a) / np.float32(127)
-        y = (base * s).astype(np.float32)
-        x = np.concatenate([[np.float32(a)], y, np.nextafter(y, np.float32(9e9)), np.nextafter(y, np.float32(-9e9))])
-        x = torch.from_numpy(x.astype(np.float32)[None]).cuda()
-        q, _ = ms.quantize_rows(x)
-        assert np.array_equal(q.cpu().numpy(), head_ref.quantize(f64(x), False)[0])
+        for s in (np.float32(a) / np.float32(127), np.float32(a) * (np.float32(1) / np.float32(127))):
+            y = (base * s).astype(np.float32)
+            x = np.concatenate([[np.float32(a)], y, np.nextafter(y, np.float32(9e9)), np.nextafter(y, np.float32(-9e9))])
+            x = torch.from_numpy(x.astype(np.float32)[None]).cuda()
+            q, _ = ms.quantize_rows(x)
+            assert np.array_equal(q.cpu().numpy(), head_ref.quantize(f64(x), False)[0])
 
 
 def test_quantize_empty_and_shapes():
