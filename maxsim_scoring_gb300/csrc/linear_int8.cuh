@@ -180,6 +180,7 @@ constexpr int kTileRing = 4;           // blocks ready for the MMA: A in tensor 
 constexpr int kTileBWarp = 2, kWidenWarp0 = 4, kTileEpiWarp0 = 12;
 constexpr int kTileThreads = 640;      // warp 0 TMA of A, warp 1 MMA, warp 2 TMA of B, warps 4-11 widen, 12-19 epilogue
 constexpr int kTileMaxStages8 = 8;
+constexpr int kTileStage = 4096;       // staging of an epilogue warp: 32 x 32 sums
 constexpr uint32_t kTileACol = 256;    // tensor memory: accumulators in columns 0-255, the ring's A blocks above
 constexpr int kTileStatusTimeout = 4;  // MAXSIM_ERR_TIMEOUT
 
@@ -191,7 +192,7 @@ struct TileCfg {
     static constexpr int kB16 = 2 * kBAtom;
     // even: each widening warpgroup then always meets the same stages, and
     // sees every phase of their barriers
-    static constexpr int kStages8 = kTN == 256 ? 6 : 8;
+    static constexpr int kStages8 = kTN == 256 ? 4 : 8;
     static constexpr int kAcc = kTN == 256 ? 1 : 2;    // accumulator buffers
 };
 
@@ -205,8 +206,7 @@ struct TileArgs {
     int32_t slices;     // parts of K
     int32_t kb;         // blocks of K
     int32_t kb_slice;   // blocks per slice
-    int vec_out;        // rows of out start on 16-byte boundaries
-    int vec_scale;      // the scales (and bias) along B start on 16-byte boundaries
+    int vec_out;        // four outputs (sums) can be stored at once
     int* status;
     uint64_t timeout_ns;
 };
@@ -223,7 +223,7 @@ struct alignas(16) TileCtl {
 template <int kTN>
 constexpr size_t tile_smem_bytes() {
     using C = TileCfg<kTN>;
-    return 1024 + static_cast<size_t>(C::kStages8) * C::kA8 + kTileRing * C::kB16 + sizeof(TileCtl);
+    return 1024 + static_cast<size_t>(C::kStages8) * C::kA8 + kTileRing * C::kB16 + 8 * kTileStage + sizeof(TileCtl);
 }
 
 // Bounded wait of a thread: gives up after the limit (recorded in the device
@@ -304,57 +304,31 @@ __device__ __forceinline__ TileItem tile_item(const TileArgs& a, int64_t item, u
     return t;
 }
 
-// 32 consecutive outputs of token m from channel n on.
-template <typename T>
-__device__ __forceinline__ void store_row32(const TileArgs& a, int64_t m, int64_t n, float xs, const float (&v)[32]) {
-    const LinearArgs& l = a.l;
-    T* out = static_cast<T*>(l.out) + m * l.ld_out + n;
-    if (n + 32 <= l.N && a.vec_out && a.vec_scale) {
-        constexpr int kPer = 16 / static_cast<int>(sizeof(T));  // outputs per 16-byte store
-#pragma unroll
-        for (int i = 0; i < 32; i += kPer) {
-            alignas(16) T o[kPer];
-#pragma unroll
-            for (int j = 0; j < kPer; j += 4) {
-                const float4 ws = __ldg(reinterpret_cast<const float4*>(l.w_scale + n + i + j));
-                const float4 b = l.bias ? __ldg(reinterpret_cast<const float4*>(l.bias + n + i + j))
-                                        : make_float4(0.f, 0.f, 0.f, 0.f);
-                o[j + 0] = from_f32<T>(__fmaf_rn(v[i + j + 0] * xs, ws.x, b.x));
-                o[j + 1] = from_f32<T>(__fmaf_rn(v[i + j + 1] * xs, ws.y, b.y));
-                o[j + 2] = from_f32<T>(__fmaf_rn(v[i + j + 2] * xs, ws.z, b.z));
-                o[j + 3] = from_f32<T>(__fmaf_rn(v[i + j + 3] * xs, ws.w, b.w));
-            }
-            *reinterpret_cast<uint4*>(out + i) = *reinterpret_cast<const uint4*>(o);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            if (n + i < l.N)
-                out[i] = from_f32<T>(__fmaf_rn(v[i] * xs, __ldg(l.w_scale + n + i), l.bias ? __ldg(l.bias + n + i) : 0.f));
-        }
-    }
-}
+// Sums that are exact integers, for the join.
+template <>
+__device__ __forceinline__ int32_t from_f32<int32_t>(float v) { return __float2int_rn(v); }
 
-// Channel n of 32 consecutive tokens from m on (lanes hold consecutive
-// channels: each store of a warp is one run).
+// Byte of the 16-byte piece c of row r in a warp's staging tile [32][32] of
+// 4-byte values: 32 lanes that write one piece each of their own row, or read
+// the eight pieces of four rows, meet no bank twice.
+__device__ __forceinline__ uint32_t staged(int r, int c) { return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+// Four consecutive elements from p on, of which the first n exist.
 template <typename T>
-__device__ __forceinline__ void store_col32(const TileArgs& a, int64_t m, int64_t n, float ws, float bias,
-                                            const float (&v)[32]) {
-    const LinearArgs& l = a.l;
-    T* out = static_cast<T*>(l.out) + m * l.ld_out + n;
-    if (m + 32 <= l.M && a.vec_scale) {
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-            const float4 xs = __ldg(reinterpret_cast<const float4*>(l.x_scale + m + i));
-            out[(i + 0) * l.ld_out] = from_f32<T>(__fmaf_rn(v[i + 0] * xs.x, ws, bias));
-            out[(i + 1) * l.ld_out] = from_f32<T>(__fmaf_rn(v[i + 1] * xs.y, ws, bias));
-            out[(i + 2) * l.ld_out] = from_f32<T>(__fmaf_rn(v[i + 2] * xs.z, ws, bias));
-            out[(i + 3) * l.ld_out] = from_f32<T>(__fmaf_rn(v[i + 3] * xs.w, ws, bias));
+__device__ __forceinline__ void store4(T* p, int n, bool vec, float a, float b, float c, float d) {
+    if (vec && n >= 4) {
+        if constexpr (sizeof(T) == 4) {
+            alignas(16) T o[4] = {from_f32<T>(a), from_f32<T>(b), from_f32<T>(c), from_f32<T>(d)};
+            *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(o);
+        } else {
+            alignas(8) T o[4] = {from_f32<T>(a), from_f32<T>(b), from_f32<T>(c), from_f32<T>(d)};
+            *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(o);
         }
     } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (m + i < l.M) out[i * l.ld_out] = from_f32<T>(__fmaf_rn(v[i] * __ldg(l.x_scale + m + i), ws, bias));
+        if (n > 0) p[0] = from_f32<T>(a);
+        if (n > 1) p[1] = from_f32<T>(b);
+        if (n > 2) p[2] = from_f32<T>(c);
+        if (n > 3) p[3] = from_f32<T>(d);
     }
 }
 
@@ -387,7 +361,8 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t* s8 = smem;
     uint8_t* s16 = smem + C::kStages8 * C::kA8;
-    TileCtl* ctl = reinterpret_cast<TileCtl*>(s16 + kTileRing * C::kB16);
+    uint8_t* s_out = s16 + kTileRing * C::kB16;
+    TileCtl* ctl = reinterpret_cast<TileCtl*>(s_out + 8 * kTileStage);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     if (threadIdx.x == 0) {
@@ -548,46 +523,95 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         }
     } else if (warp >= kTileEpiWarp0) {
         // ------------------------------------------------------------ epilogue
+        // A warp owns 32 rows of A and half of the tile's columns, 32 at a time.
+        // Swapped, its lanes hold consecutive channels and store straight to
+        // out. Otherwise a lane holds a token: the sums go through shared
+        // memory so that eight lanes hold 32 channels of a token, four each,
+        // and stores are whole runs. All scales are in registers before the
+        // accumulator is waited for (loaded per column in between, they took
+        // four fifths of the epilogue's time).
         const int q = warp & 3, half = (warp - kTileEpiWarp0) >> 2;
         constexpr int kCols = kTN / 2;  // columns per warp
+        uint8_t* stage = s_out + (warp - kTileEpiWarp0) * kTileStage;
+        const int64_t ld = a.slices > 1 ? a.l.N : a.l.ld_out;
         int32_t buf = 0;
         uint32_t buf_phase = 0;
         for (int64_t it = first; it < a.items; it += step) {
             const TileItem t = tile_item<kTN>(a, it, rank);
-            const int64_t ra = t.a0 + q * 32 + lane;  // this thread's row of A
-            const bool real = ra < a.rows_a;
-            float sa = 0.f, bias = 0.f;
-            if (real && a.slices == 1) {
-                sa = __ldg((kSwap ? a.l.w_scale : a.l.x_scale) + ra);
-                if (kSwap && a.l.bias) bias = __ldg(a.l.bias + ra);
+            const int64_t ra0 = t.a0 + q * 32, rb0 = t.b0 + half * kCols;
+            int32_t* part = a.partial + static_cast<int64_t>(t.slice) * a.l.M * a.l.N;  // used when slices > 1
+            // this lane's row of A, and its column of each 32 along B
+            const bool in_a = ra0 + lane < a.rows_a;
+            const float* scale_b = kSwap ? a.l.x_scale : a.l.w_scale;
+            const float sa = in_a ? __ldg((kSwap ? a.l.w_scale : a.l.x_scale) + ra0 + lane) : 0.f;
+            float bias[kSwap ? 1 : kCols / 32], sb[kCols / 32];
+            if constexpr (kSwap) bias[0] = a.l.bias && in_a ? __ldg(a.l.bias + ra0 + lane) : 0.f;
+#pragma unroll
+            for (int c = 0; c < kCols / 32; ++c) {
+                const int64_t i = rb0 + c * 32 + lane;
+                sb[c] = i < a.rows_b ? __ldg(scale_b + i) : 0.f;
+                if constexpr (!kSwap) bias[c] = a.l.bias && i < a.rows_b ? __ldg(a.l.bias + i) : 0.f;
             }
             if (!tile_wait_warp(a, ctl, &ctl->acc_full[buf], buf_phase)) break;
             tc_fence_after();
             const uint32_t src = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * kTN + half * kCols);
-#pragma unroll 1
-            for (int c = 0; c < kCols; c += 32) {
+#pragma unroll
+            for (int c = 0; c < kCols / 32; ++c) {
+                const int64_t rb = rb0 + c * 32;
                 float v[32];
-                tmem_ld32(src + c, v);
+                tmem_ld32(src + c * 32, v);
                 tmem_wait_ld();
-                if (c + 32 == kCols) {
+                if (c + 1 == kCols / 32) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_remote(map_shared_rank(smem_u32(&ctl->acc_empty[buf]), 0));
                 }
-                const int64_t rb = t.b0 + half * kCols + c;
-                if (real && rb < a.rows_b) {
+                if (ra0 >= a.rows_a || rb >= a.rows_b) continue;
+                if constexpr (kSwap) {
+                    const int n = static_cast<int>(min(static_cast<int64_t>(32), a.rows_b - rb));
+                    const bool real = ra0 + lane < a.rows_a;
                     if (a.slices > 1) {
-                        int32_t* p = a.partial + static_cast<int64_t>(t.slice) * a.l.M * a.l.N +
-                                     (kSwap ? rb * a.l.N + ra : ra * a.l.N + rb);
-                        const int64_t ld = kSwap ? a.l.N : 1;
+                        int32_t* p = part + rb * ld + ra0 + lane;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (rb + i < a.rows_b) p[i * ld] = __float2int_rn(v[i]);
-                    } else if constexpr (kSwap) {
-                        store_col32<T>(a, rb, ra, sa, bias, v);
+                        for (int i = 0; i < 32; ++i, p += ld)
+                            if (i < n && real) *p = __float2int_rn(v[i]);
                     } else {
-                        store_row32<T>(a, ra, rb, sa, v);
+                        T* p = static_cast<T*>(a.l.out) + rb * ld + ra0 + lane;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i, p += ld) {
+                            const T y = from_f32<T>(__fmaf_rn(v[i] * __shfl_sync(0xffffffffu, sb[c], i), sa, bias[0]));
+                            if (i < n && real) *p = y;
+                        }
                     }
+                } else {
+                    const float f = a.slices > 1 ? 1.f : sa;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<float4*>(stage + staged(lane, i)) =
+                            make_float4(v[4 * i] * f, v[4 * i + 1] * f, v[4 * i + 2] * f, v[4 * i + 3] * f);
+                    float ws[4], bs[4];  // this lane's four channels
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        ws[j] = __shfl_sync(0xffffffffu, sb[c], 4 * (lane & 7) + j);
+                        bs[j] = __shfl_sync(0xffffffffu, bias[c], 4 * (lane & 7) + j);
+                    }
+                    __syncwarp();
+                    const int64_t n0 = rb + 4 * (lane & 7);
+                    const int n = static_cast<int>(min(static_cast<int64_t>(4), a.rows_b - n0));
+                    const int rows = static_cast<int>(min(static_cast<int64_t>(32), a.rows_a - ra0));
+                    int64_t at = (ra0 + (lane >> 3)) * ld + n0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i, at += 4 * ld) {
+                        const float4 y = *reinterpret_cast<const float4*>(stage + staged(4 * i + (lane >> 3), lane & 7));
+                        if (4 * i + (lane >> 3) >= rows) continue;
+                        if (a.slices > 1) {
+                            store4(part + at, n, a.vec_out, y.x, y.y, y.z, y.w);
+                        } else {
+                            store4(static_cast<T*>(a.l.out) + at, n, a.vec_out, __fmaf_rn(y.x, ws[0], bs[0]),
+                                   __fmaf_rn(y.y, ws[1], bs[1]), __fmaf_rn(y.z, ws[2], bs[2]), __fmaf_rn(y.w, ws[3], bs[3]));
+                        }
+                    }
+                    __syncwarp();
                 }
             }
             if (++buf == C::kAcc) { buf = 0; buf_phase ^= 1u; }
