@@ -227,6 +227,10 @@ maxsim_status launch_tile(const LinearPlan& p, const LinearArgs& l, const __half
     static std::atomic<uint64_t> prepared{0};  // devices whose shared-memory limit is raised
     const uint64_t bit = uint64_t(1) << dev.index;
     if (!(prepared.load(std::memory_order_acquire) & bit)) {
+        // the register split adds up only if every thread is launched with kTileRegs
+        cudaFuncAttributes fa{};
+        if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return MAXSIM_ERR_CUDA;
+        if (fa.numRegs < kTileRegs) return MAXSIM_ERR_UNSUPPORTED;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem)) != cudaSuccess)
             return MAXSIM_ERR_CUDA;
         prepared.fetch_or(bit, std::memory_order_release);

@@ -180,6 +180,11 @@ constexpr int kTileRing = 4;           // blocks ready for the MMA: A in tensor 
 constexpr int kTileBWarp = 2, kWidenWarp0 = 4, kTileEpiWarp0 = 12;
 constexpr int kTileThreads = 640;      // warp 0 TMA of A, warp 1 MMA, warp 2 TMA of B, warps 4-11 widen, 12-19 epilogue
 constexpr int kTileMaxStages8 = 8;
+// Registers per thread: the launch gives every thread kTileRegs; warps 0-3 and
+// the widening warps hand registers to the epilogue warps, which hold a
+// tile's rounded outputs until they are stored.
+constexpr int kTileRegs = 96, kTileRegsCtl = 48, kTileRegsWiden = 80, kTileRegsEpi = 136;
+static_assert(kTileRegsCtl * 128 + (kTileRegsWiden + kTileRegsEpi) * 256 <= kTileRegs * kTileThreads, "register split");
 constexpr int kTileStage = 4096;       // staging of an epilogue warp: 32 x 32 sums
 constexpr uint32_t kTileACol = 256;    // tensor memory: accumulators in columns 0-255, the ring's A blocks above
 constexpr int kTileStatusTimeout = 4;  // MAXSIM_ERR_TIMEOUT
@@ -313,6 +318,23 @@ __device__ __forceinline__ int32_t from_f32<int32_t>(float v) { return __float2i
 // the eight pieces of four rows, meet no bank twice.
 __device__ __forceinline__ uint32_t staged(int r, int c) { return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4)); }
 
+// Two 16-bit values of T in a word, and one of them again.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    if constexpr (std::is_same_v<T, __half>) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+template <typename T>
+__device__ __forceinline__ T half_of(uint32_t w, int i) {
+    const unsigned short h = static_cast<unsigned short>(i ? w >> 16 : w);
+    return *reinterpret_cast<const T*>(&h);
+}
+
 // Four consecutive elements from p on, of which the first n exist.
 template <typename T>
 __device__ __forceinline__ void store4(T* p, int n, bool vec, float a, float b, float c, float d) {
@@ -347,10 +369,10 @@ __device__ __forceinline__ void store4(T* p, int n, bool vec, float a, float b, 
 //    kTN, K = 16);
 //  * eight epilogue warps scale, add the bias, round once and store.
 // What a widening warp hands to the MMA is in tensor memory (ordered by
-// tcgen05.fence::before_thread_sync) or was written by TMA (observed on
-// b_full), so its arrival on the even CTA's barrier releases at CTA scope. A
-// cluster-scope release took the warp 800 to 2,000 cycles per block
-// (32768 x 4096 x 4096: 751 us, and 609 us without).
+// tcgen05.fence::before_thread_sync), and what the odd CTA reports of B was
+// written by TMA (observed on b_full), so these arrivals on the even CTA's
+// barriers release at CTA scope. A cluster-scope release took a warp 800 to
+// 2,000 cycles per block (32768 x 4096 x 4096: 751 us, and 609 us without).
 // A tile's K may be cut into slices (few tiles, long K): each slice then
 // writes its integer sums, and linear_join_kernel adds them.
 template <typename T, int kTN, bool kSwap>
@@ -372,7 +394,8 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         }
         for (int r = 0; r < kTileRing; ++r) {
             mbar_init(smem_u32(&ctl->b_full[r]), 1);
-            mbar_init(smem_u32(&ctl->ready[r]), 8);  // four warps of each CTA
+            // even CTA: four widening warps of each CTA, its own TMA of B, the odd CTA's report of B
+            mbar_init(smem_u32(&ctl->ready[r]), 10);
             mbar_init(smem_u32(&ctl->freed[r]), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -396,12 +419,16 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     const uint32_t tmem = ctl->tmem_base;
     const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
+    // each branch runs under its own register budget
+    if (warp < kWidenWarp0) {
+    regs_release<kTileRegsCtl>();
     if (warp == 0 || warp == kTileBWarp) {
         // ------------------------------------------------------------ TMA
         if (lane == 0) {
             const bool is_a = warp == 0;
             const int depth = is_a ? C::kStages8 : kTileRing;
-            uint64_t* full = is_a ? ctl->full8 : ctl->b_full;
+            // the even CTA's B lands on the barrier that its MMA warp waits for
+            uint64_t* full = is_a ? ctl->full8 : rank == 0 ? ctl->ready : ctl->b_full;
             uint64_t* empty = is_a ? ctl->empty8 : ctl->freed;
             int32_t stage = 0;
             uint32_t phase = 0;
@@ -436,11 +463,11 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
             }
         }
     } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA (even CTA)
+        int32_t ring = 0;
+        uint32_t ring_phase = 0;
+        bool ok = true;
         if (rank == 0) {
-            int32_t ring = 0;
-            uint32_t ring_phase = 0;
-            bool ok = true;
+            // ------------------------------------------------------------ MMA (even CTA)
             constexpr uint32_t idesc = idesc_f16_f32(0, kTileM, kTN);
             const uint64_t b0 = sdesc_k_sw128(smem_u32(s16));
             int32_t buf = 0;
@@ -471,8 +498,20 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                 while (!mbar_try_wait(smem_u32(&ctl->mma_done), 0) && global_timer_ns() - t0 < a.timeout_ns) {}
             }
             __syncwarp();
+        } else {
+            // ------------------------------------------------------------ odd CTA: reports its half of B
+            for (int64_t it = first; it < a.items && ok; it += step) {
+                const TileItem t = tile_item<kTN>(a, it, rank);
+                for (int32_t kb = t.kb0; kb < t.kb1; ++kb) {
+                    if (!tile_wait_warp(a, ctl, &ctl->b_full[ring], ring_phase)) { ok = false; break; }
+                    if (lane == 0) mbar_arrive_remote(map_shared_rank(smem_u32(&ctl->ready[ring]), 0));
+                    if (++ring == kTileRing) { ring = 0; ring_phase ^= 1u; }
+                }
+            }
         }
-    } else if (warp >= kWidenWarp0 && warp < kTileEpiWarp0) {
+    }
+    } else if (warp < kTileEpiWarp0) {
+        regs_release<kTileRegsWiden>();
         // ------------------------------------------------------------ widening
         const int wg = (warp - kWidenWarp0) >> 2, q = warp & 3;
         const int row = q * 32 + lane;
@@ -485,16 +524,13 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
             const TileItem t = tile_item<kTN>(a, it, rank);
             for (int32_t kb = t.kb0; kb < t.kb1; ++kb) {
                 if (turn == wg) {
-                    if (!tile_wait_warp(a, ctl, &ctl->full8[stage], phase) ||
-                        !tile_wait_warp(a, ctl, &ctl->freed[ring], ring_phase ^ 1u)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
+                    if (!tile_wait_warp(a, ctl, &ctl->full8[stage], phase)) { ok = false; break; }
                     const uint8_t* src = s8 + stage * C::kA8 + row * kTileK;
                     uint4 v[8];
 #pragma unroll
                     for (int c = 0; c < 8; ++c) v[c] = *reinterpret_cast<const uint4*>(src + ((c ^ (row & 7)) << 4));
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&ctl->empty8[stage]));
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         uint32_t h[32];
@@ -505,14 +541,15 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
 #pragma unroll
                             for (int i = 0; i < 8; ++i) h[c * 8 + i] = e[i];
                         }
+                        if (half == 0) {  // the MMAs that read the slot's last block are done
+                            if (!tile_wait_warp(a, ctl, &ctl->freed[ring], ring_phase ^ 1u)) { ok = false; break; }
+                            tc_fence_after();
+                        }
                         tmem_st32(a_lane + static_cast<uint32_t>(ring * 64 + half * 32), h);
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&ctl->empty8[stage]));
+                    if (!ok) break;
                     tmem_wait_st();
                     tc_fence_before();
-                    // the block is ready once its B has landed too
-                    if (!tile_wait_warp(a, ctl, &ctl->b_full[ring], ring_phase)) { ok = false; break; }
                     __syncwarp();
                     if (lane == 0) mbar_arrive_remote(map_shared_rank(smem_u32(&ctl->ready[ring]), 0));
                 }
@@ -521,15 +558,18 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                 if (++ring == kTileRing) { ring = 0; ring_phase ^= 1u; }
             }
         }
-    } else if (warp >= kTileEpiWarp0) {
+    } else {
+        regs_claim<kTileRegsEpi>();
         // ------------------------------------------------------------ epilogue
         // A warp owns 32 rows of A and half of the tile's columns, 32 at a time.
         // Swapped, its lanes hold consecutive channels and store straight to
         // out. Otherwise a lane holds a token: the sums go through shared
         // memory so that eight lanes hold 32 channels of a token, four each,
         // and stores are whole runs. All scales are in registers before the
-        // accumulator is waited for (loaded per column in between, they took
-        // four fifths of the epilogue's time).
+        // accumulator is waited for. 16-bit outputs are held until the
+        // accumulator has been read and handed back: all SMs store a tile at
+        // about the same time, which takes 8,500 cycles at 256 x 256, and the
+        // next tile's MMAs then run beside it.
         const int q = warp & 3, half = (warp - kTileEpiWarp0) >> 2;
         constexpr int kCols = kTN / 2;  // columns per warp
         uint8_t* stage = s_out + (warp - kTileEpiWarp0) * kTileStage;
@@ -555,6 +595,9 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
             if (!tile_wait_warp(a, ctl, &ctl->acc_full[buf], buf_phase)) break;
             tc_fence_after();
             const uint32_t src = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * kTN + half * kCols);
+            constexpr bool kHold = sizeof(T) == 2;
+            uint32_t held[kHold ? kCols / 32 : 1][16];
+            const int row_n = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(32), a.rows_a - ra0)));
 #pragma unroll
             for (int c = 0; c < kCols / 32; ++c) {
                 const int64_t rb = rb0 + c * 32;
@@ -578,9 +621,17 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                     } else {
                         T* p = static_cast<T*>(a.l.out) + rb * ld + ra0 + lane;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i, p += ld) {
-                            const T y = from_f32<T>(__fmaf_rn(v[i] * __shfl_sync(0xffffffffu, sb[c], i), sa, bias[0]));
-                            if (i < n && real) *p = y;
+                        for (int i = 0; i < 32; i += 2) {
+                            const float y0 = __fmaf_rn(v[i] * __shfl_sync(0xffffffffu, sb[c], i), sa, bias[0]);
+                            const float y1 = __fmaf_rn(v[i + 1] * __shfl_sync(0xffffffffu, sb[c], i + 1), sa, bias[0]);
+                            if constexpr (kHold) {
+                                held[c][i / 2] = pack2<T>(y0, y1);
+                            } else {
+                                if (i < n && real) *p = y0;
+                                p += ld;
+                                if (i + 1 < n && real) *p = y1;
+                                p += ld;
+                            }
                         }
                     }
                 } else {
@@ -598,20 +649,58 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                     __syncwarp();
                     const int64_t n0 = rb + 4 * (lane & 7);
                     const int n = static_cast<int>(min(static_cast<int64_t>(4), a.rows_b - n0));
-                    const int rows = static_cast<int>(min(static_cast<int64_t>(32), a.rows_a - ra0));
                     int64_t at = (ra0 + (lane >> 3)) * ld + n0;
 #pragma unroll
                     for (int i = 0; i < 8; ++i, at += 4 * ld) {
                         const float4 y = *reinterpret_cast<const float4*>(stage + staged(4 * i + (lane >> 3), lane & 7));
-                        if (4 * i + (lane >> 3) >= rows) continue;
+                        const bool real = 4 * i + (lane >> 3) < row_n;
                         if (a.slices > 1) {
-                            store4(part + at, n, a.vec_out, y.x, y.y, y.z, y.w);
+                            if (real) store4(part + at, n, a.vec_out, y.x, y.y, y.z, y.w);
+                            continue;
+                        }
+                        const float o[4] = {__fmaf_rn(y.x, ws[0], bs[0]), __fmaf_rn(y.y, ws[1], bs[1]),
+                                            __fmaf_rn(y.z, ws[2], bs[2]), __fmaf_rn(y.w, ws[3], bs[3])};
+                        if constexpr (kHold) {
+                            held[c][2 * i] = pack2<T>(o[0], o[1]);
+                            held[c][2 * i + 1] = pack2<T>(o[2], o[3]);
                         } else {
-                            store4(static_cast<T*>(a.l.out) + at, n, a.vec_out, __fmaf_rn(y.x, ws[0], bs[0]),
-                                   __fmaf_rn(y.y, ws[1], bs[1]), __fmaf_rn(y.z, ws[2], bs[2]), __fmaf_rn(y.w, ws[3], bs[3]));
+                            if (real) store4(static_cast<T*>(a.l.out) + at, n, a.vec_out, o[0], o[1], o[2], o[3]);
                         }
                     }
                     __syncwarp();
+                }
+            }
+            if constexpr (kHold) {
+                if (a.slices == 1 && row_n > 0) {
+#pragma unroll
+                    for (int c = 0; c < kCols / 32; ++c) {
+                        const int64_t rb = rb0 + c * 32;
+                        if (rb >= a.rows_b) break;
+                        if constexpr (kSwap) {
+                            const int n = static_cast<int>(min(static_cast<int64_t>(32), a.rows_b - rb));
+                            T* p = static_cast<T*>(a.l.out) + rb * ld + ra0 + lane;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i, p += ld)
+                                if (i < n && lane < row_n) *p = half_of<T>(held[c][i / 2], i & 1);
+                        } else {
+                            const int64_t n0 = rb + 4 * (lane & 7);
+                            const int n = static_cast<int>(min(static_cast<int64_t>(4), a.rows_b - n0));
+                            T* p = static_cast<T*>(a.l.out) + (ra0 + (lane >> 3)) * ld + n0;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i, p += 4 * ld) {
+                                if (4 * i + (lane >> 3) >= row_n) break;
+                                const uint32_t lo = held[c][2 * i], hi = held[c][2 * i + 1];
+                                if (a.vec_out && n == 4) {
+                                    *reinterpret_cast<uint2*>(p) = make_uint2(lo, hi);
+                                } else {
+                                    if (n > 0) p[0] = half_of<T>(lo, 0);
+                                    if (n > 1) p[1] = half_of<T>(lo, 1);
+                                    if (n > 2) p[2] = half_of<T>(hi, 0);
+                                    if (n > 3) p[3] = half_of<T>(hi, 1);
+                                }
+                            }
+                        }
+                    }
                 }
             }
             if (++buf == C::kAcc) { buf = 0; buf_phase ^= 1u; }
