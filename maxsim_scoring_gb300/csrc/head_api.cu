@@ -83,29 +83,38 @@ void set_div(DropoutArgs* a, uint32_t d) {
     a->div_shift = l - 1;
 }
 
-template <typename T>
-maxsim_status launch_dropout(DropoutArgs& a, const HostDevice& dev, cudaStream_t st) {
-    const bool res = a.residual != nullptr;
-    const bool bases = ptr_aligned(a.x, 16) && ptr_aligned(a.y, 16) && ptr_aligned(a.residual, 16);
-    const bool one_run = a.rows == 1 || (a.ld_x == a.cols && a.ld_y == a.cols && (!res || a.ld_r == a.cols));
+template <typename T, int kX, bool kRes>
+void launch_dropout_wide(const DropoutArgs& a, int64_t most, cudaStream_t st) {
+    dropout_wide_kernel<T, kX, kRes><<<grid_of(a.n / 8, 256 * dropout_pieces<T, kX>(), most), 256, 0, st>>>(a);
+}
+
+template <typename T, bool kRes>
+void launch_dropout_layout(DropoutArgs& a, const HostDevice& dev, cudaStream_t st) {
     constexpr int kVec = 16 / static_cast<int>(sizeof(T));
-    const bool rows_wide = a.cols % 8 == 0 && a.ld_x % kVec == 0 && a.ld_y % kVec == 0 && (!res || a.ld_r % kVec == 0);
     const int64_t most = int64_t(dev.num_sms) * 8;
-    if (bases && one_run) {
-        const unsigned grid = grid_of(a.n / 8, 256, most);
-        if (res) dropout_wide_kernel<T, true, true><<<grid, 256, 0, st>>>(a);
-        else dropout_wide_kernel<T, true, false><<<grid, 256, 0, st>>>(a);
-    } else if (bases && rows_wide) {
+    const bool x16 = ptr_aligned(a.x, 16), out16 = ptr_aligned(a.y, 16) && ptr_aligned(a.residual, 16);
+    const bool x_run = a.rows == 1 || a.ld_x == a.cols;
+    const bool out_run = a.rows == 1 || (a.ld_y == a.cols && (!kRes || a.ld_r == a.cols));
+    if (out16 && out_run && x16 && x_run) {
+        launch_dropout_wide<T, kXFlat, kRes>(a, most, st);
+    } else if (out16 && x16 && a.cols % 8 == 0 && a.ld_x % kVec == 0 && a.ld_y % kVec == 0 && (!kRes || a.ld_r % kVec == 0)) {
         set_div(&a, static_cast<uint32_t>(a.cols / 8));
-        const unsigned grid = grid_of(a.n / 8, 256, most);
-        if (res) dropout_wide_kernel<T, false, true><<<grid, 256, 0, st>>>(a);
-        else dropout_wide_kernel<T, false, false><<<grid, 256, 0, st>>>(a);
+        launch_dropout_wide<T, kXRows, kRes>(a, most, st);
+    } else if (out16 && out_run && a.cols >= 8) {
+        set_div(&a, static_cast<uint32_t>(a.cols));
+        launch_dropout_wide<T, kXGather, kRes>(a, most, st);
     } else {
         set_div(&a, static_cast<uint32_t>(a.cols));
-        const unsigned grid = grid_of(a.n, 8 * 256, most);
-        if (res) dropout_any_kernel<T, true><<<grid, 256, 0, st>>>(a);
-        else dropout_any_kernel<T, false><<<grid, 256, 0, st>>>(a);
+        const unsigned any_grid = grid_of(a.n, 8 * 256, most);
+        if (a.cols >= 256) dropout_any_kernel<T, kRes, 256><<<any_grid, 256, 0, st>>>(a);
+        else dropout_any_kernel<T, kRes, 0><<<any_grid, 256, 0, st>>>(a);
     }
+}
+
+template <typename T>
+maxsim_status launch_dropout(DropoutArgs& a, const HostDevice& dev, cudaStream_t st) {
+    if (a.residual) launch_dropout_layout<T, true>(a, dev, st);
+    else launch_dropout_layout<T, false>(a, dev, st);
     return launched();
 }
 

@@ -321,123 +321,228 @@ __device__ __forceinline__ uint4 draw_block(const DropoutArgs& a, int64_t b) {
                          a.key0, a.key1);
 }
 
+// Two 16-bit values of T in a word, and one of them again.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    if constexpr (std::is_same_v<T, __half>) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+template <typename T>
+__device__ __forceinline__ T half_of(uint32_t w, int i) {
+    const unsigned short h = static_cast<unsigned short>(i ? w >> 16 : w);
+    return *reinterpret_cast<const T*>(&h);
+}
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+    if constexpr (std::is_same_v<T, __half>) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+    else return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
 template <typename T>
 struct Eight {  // eight consecutive elements
-    uint4 v[sizeof(T) / 2];
+    static constexpr int kWords = 4 * static_cast<int>(sizeof(T)) / 2;
+    uint32_t v[kWords];
     __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
+        for (int i = 0; i < kWords; i += 4) {
+            const uint4 w = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + i);
+            v[i] = w.x; v[i + 1] = w.y; v[i + 2] = w.z; v[i + 3] = w.w;
+        }
     }
     __device__ __forceinline__ void store(T* p) const {
 #pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) reinterpret_cast<uint4*>(p)[i] = v[i];
+        for (int i = 0; i < kWords; i += 4)
+            *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(p) + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
     }
-    __device__ __forceinline__ T& at(int i) { return reinterpret_cast<T*>(v)[i]; }
+    // element e: p[e], or past a row's end (e >= end) q[e]
+    __device__ __forceinline__ void gather(const T* p, const T* q, int end) {
+        T t[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = (i >= end ? q : p)[i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                v[i] = __float_as_uint(t[i]);
+            } else {
+                const uint32_t h = *reinterpret_cast<const unsigned short*>(&t[i]);
+                v[i / 2] = (i & 1) ? v[i / 2] | h << 16 : h;
+            }
+        }
+    }
+    __device__ __forceinline__ float2 pair(int i) const {
+        if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+        else return unpack2<T>(v[i]);
+    }
+    __device__ __forceinline__ void set_pair(int i, float a, float b) {
+        if constexpr (sizeof(T) == 4) {
+            v[2 * i] = __float_as_uint(a);
+            v[2 * i + 1] = __float_as_uint(b);
+        } else {
+            v[i] = pack2<T>(a, b);
+        }
+    }
 };
 
-// Dropout where every eight elements that share a counter are one 16-byte
-// (f32: 32-byte) piece of a row: the rows are contiguous, or cols is a
-// multiple of 8 and rows start on 16-byte boundaries. One read, one write and
-// ten rounds of Philox per eight elements; two pieces per thread in flight
-// so that the loads cover the memory latency. Bound by HBM; the generator's
-// integer work is about half of what the SMs could issue meanwhile.
-// kFlat: one run of n elements (the last piece may be short); otherwise
-// fast_div divides the piece's number by the pieces of a row.
-template <typename T, bool kFlat, bool kRes>
+enum { kXFlat = 0, kXRows = 1, kXGather = 2 };
+
+// Dropout by pieces of eight elements that share a counter, 16 bytes (f32: 32)
+// of y and the residual: one read, one write and ten rounds of Philox a piece.
+//  kXFlat: x, residual and y are each one run of n elements.
+//  kXRows: cols is a multiple of 8 and the rows of all three start on 16-byte
+//          boundaries; fast_div divides a piece's number by the pieces of a row.
+//  kXGather: residual and y are runs; x's rows lie apart or off their
+//          boundaries (cols >= 8), and its elements are loaded one by one;
+//          fast_div divides by cols. (Paths of their own for whole pieces and for
+//          4-byte aligned ones left 1023 columns at 26 us and took 101 from 139
+//          to 174.)
+// A warp takes 32 * kPieces neighbouring pieces at a time, so that several
+// loads of a thread are in flight and a warp's accesses stay close together
+// (262144 x 1024 f16 without residual: 183 us with a thread's two pieces a grid
+// apart, 172 with two neighbouring, 171 with four; with a bf16 residual 264, 247
+// and 238). Bound by HBM, if the arithmetic stays near 100 instructions a
+// piece (three rounds of Philox instead of ten: 163 us): the comparisons take
+// the drawn halves as they lie in their words, and results are rounded two at
+// a time.
+template <typename T, int kX>
+__host__ __device__ constexpr int dropout_pieces() { return sizeof(T) == 2 && kX != kXGather ? 4 : 2; }
+
+template <typename T, int kX, bool kRes>
 __global__ void __launch_bounds__(256) dropout_wide_kernel(const DropoutArgs a) {
-    constexpr int kPieces = 2;
+    constexpr int kPieces = dropout_pieces<T, kX>();
     const T* x = static_cast<const T*>(a.x);
     const T* res = static_cast<const T*>(a.residual);
     T* y = static_cast<T*>(a.y);
     const int64_t blocks = a.n >> 3;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    const int64_t first = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
-    for (int64_t b0 = first; b0 < blocks; b0 += kPieces * step) {
+    const int64_t step = static_cast<int64_t>(gridDim.x) * 256 * kPieces;
+    const int64_t first = blockIdx.x * static_cast<int64_t>(256 * kPieces) + (threadIdx.x >> 5) * (32 * kPieces) + (threadIdx.x & 31);
+    const bool some = a.drop < 65536u;                 // anything is kept
+    const uint32_t least = a.drop << 16;
+    for (int64_t b0 = first; b0 < blocks; b0 += step) {
         Eight<T> xv[kPieces], rv[kPieces];
         int64_t at_y[kPieces];
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) {
-            const int64_t b = b0 + j * step;
+            const int64_t b = b0 + j * 32;
             if (b >= blocks) break;
-            int64_t at_x = b << 3, at_r = at_x;
-            at_y[j] = at_x;
-            if constexpr (!kFlat) {
+            const int64_t i = b << 3;
+            int64_t at_r = i;
+            at_y[j] = i;
+            if constexpr (kX == kXFlat) {
+                xv[j].load(x + i);
+            } else if constexpr (kX == kXRows) {
                 const int32_t per_row = a.cols >> 3;
                 const int64_t row = b < 0x80000000ll ? fast_div(static_cast<uint32_t>(b), a.div_mul, a.div_shift) : b / per_row;
                 const int64_t col = (b - row * per_row) << 3;
-                at_x = row * a.ld_x + col;
+                xv[j].load(x + row * a.ld_x + col);
                 at_r = row * a.ld_r + col;
                 at_y[j] = row * a.ld_y + col;
+            } else {
+                const int64_t row = i < 0x80000000ll ? fast_div(static_cast<uint32_t>(i), a.div_mul, a.div_shift) : i / a.cols;
+                const int64_t gap = a.ld_x - a.cols;
+                const T* p = x + i + row * gap;
+                xv[j].gather(p, p + gap, static_cast<int>(min((row + 1) * a.cols - i, static_cast<int64_t>(8))));
             }
-            xv[j].load(x + at_x);
             if constexpr (kRes) rv[j].load(res + at_r);
         }
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) {
-            const int64_t b = b0 + j * step;
+            const int64_t b = b0 + j * 32;
             if (b >= blocks) break;
             const uint4 u = draw_block(a, b);
             const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t bits = (e & 1) ? w[e >> 1] >> 16 : w[e >> 1] & 0xffffu;
-                float v = bits >= a.drop ? to_f32(xv[j].at(e)) * a.scale : 0.f;
-                if constexpr (kRes) v += to_f32(rv[j].at(e));
-                xv[j].at(e) = from_f32<T>(v);
+            for (int e = 0; e < 4; ++e) {
+                // half u >= T exactly where u << 16 (with anything below) >= T << 16
+                const bool keep0 = some && (w[e] << 16) >= least, keep1 = some && w[e] >= least;
+                const float2 v = xv[j].pair(e);
+                float y0 = keep0 ? v.x * a.scale : 0.f, y1 = keep1 ? v.y * a.scale : 0.f;
+                if constexpr (kRes) {
+                    const float2 r = rv[j].pair(e);
+                    y0 += r.x;
+                    y1 += r.y;
+                }
+                xv[j].set_pair(e, y0, y1);
             }
             xv[j].store(y + at_y[j]);
         }
     }
-    if (kFlat && first == 0 && (a.n & 7)) {  // the short last piece
+    if (kX != kXRows && first == 0 && (a.n & 7)) {  // the short last piece
         const uint4 u = draw_block(a, blocks);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        const int64_t skip = kX == kXGather ? (a.rows - 1) * (a.ld_x - a.cols) : 0;  // it ends the last row
         for (int e = 0; e < static_cast<int>(a.n & 7); ++e) {
             const int64_t i = (blocks << 3) + e;
-            const uint32_t word = e < 2 ? w[0] : e < 4 ? w[1] : e < 6 ? w[2] : w[3];
+            const uint32_t word = e < 2 ? u.x : e < 4 ? u.y : e < 6 ? u.z : u.w;
             const uint32_t bits = (e & 1) ? word >> 16 : word & 0xffffu;
-            float v = bits >= a.drop ? to_f32(x[i]) * a.scale : 0.f;
+            float v = bits >= a.drop ? to_f32(x[i + skip]) * a.scale : 0.f;
             if constexpr (kRes) v += to_f32(res[i]);
             y[i] = from_f32<T>(v);
         }
     }
 }
 
-// Dropout for every other layout (odd widths, rows off their 16-byte
-// boundaries). A warp takes 256 consecutive elements: its lanes draw one
+// Dropout for every other layout (residual or y with rows apart and off their
+// 16-byte boundaries, or the narrowest rows). A warp takes 256 consecutive elements: its lanes draw one
 // counter each, pass the bits through shared memory, and then take every
 // 32nd element, so that loads and stores of single elements are coalesced.
-// fast_div divides an element's index by cols.
-template <typename T, bool kRes>
+// kWidth = 256: rows are at least as long as the run, which then crosses at
+// most one row's end, and one division (fast_div by cols) places it; 0: any
+// width, a division per element. Bound by instruction issue.
+template <typename T, bool kRes, int kWidth>
 __global__ void __launch_bounds__(256) dropout_any_kernel(const DropoutArgs a) {
     __shared__ uint4 s_bits[8][32];
     const T* x = static_cast<const T*>(a.x);
     const T* res = static_cast<const T*>(a.residual);
     T* y = static_cast<T*>(a.y);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const unsigned short* bits = reinterpret_cast<const unsigned short*>(s_bits[warp]);
+    const unsigned short* bits = reinterpret_cast<const unsigned short*>(s_bits[warp]) + lane;
     const int64_t step = static_cast<int64_t>(gridDim.x) * 8 * 256;
+    auto divide = [&](int64_t i) {
+        return i < 0x80000000ll ? static_cast<int64_t>(fast_div(static_cast<uint32_t>(i), a.div_mul, a.div_shift)) : i / a.cols;
+    };
     for (int64_t i0 = (static_cast<int64_t>(blockIdx.x) * 8 + warp) * 256; i0 < a.n; i0 += step) {
-        int64_t at_y[8];
+        const int left = static_cast<int>(min(a.n - i0, static_cast<int64_t>(256))) - lane;  // element 32 j exists while 32 j < left
+        const int64_t row0 = kWidth ? divide(i0) : 0;
+        // element c of row0 onward: at p[c], or past the row's end (c >= cols) at q[c]
+        const int32_t col0 = static_cast<int32_t>(i0 - row0 * a.cols) + lane;
+        const T* px = x + row0 * a.ld_x + col0;
+        const T* pr = res + row0 * a.ld_r + col0;
+        T* py = y + row0 * a.ld_y + col0;
+        const int64_t dx = a.ld_x - a.cols, dr = a.ld_r - a.cols, dy = a.ld_y - a.cols;
+        const int32_t end = a.cols - col0;  // 32 j >= end: the next row
         T xv[8], rv[8];
+        s_bits[warp][lane] = draw_block(a, (i0 >> 3) + lane);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int64_t i = i0 + j * 32 + lane;
-            if (i < a.n) {
-                const int64_t row = i < 0x80000000ll ? fast_div(static_cast<uint32_t>(i), a.div_mul, a.div_shift) : i / a.cols;
-                const int64_t col = i - row * a.cols;
-                xv[j] = x[row * a.ld_x + col];
-                if constexpr (kRes) rv[j] = res[row * a.ld_r + col];
-                at_y[j] = row * a.ld_y + col;
+            if (32 * j < left) {
+                if constexpr (kWidth) {
+                    xv[j] = (32 * j >= end ? px + dx : px)[32 * j];
+                    if constexpr (kRes) rv[j] = (32 * j >= end ? pr + dr : pr)[32 * j];
+                } else {
+                    const int64_t i = i0 + 32 * j + lane, row = divide(i);
+                    xv[j] = x[i + row * dx];
+                    if constexpr (kRes) rv[j] = res[i + row * dr];
+                }
             }
         }
-        s_bits[warp][lane] = draw_block(a, (i0 >> 3) + lane);
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            if (i0 + j * 32 + lane < a.n) {
-                float v = bits[j * 32 + lane] >= a.drop ? to_f32(xv[j]) * a.scale : 0.f;
+            if (32 * j < left) {
+                float v = bits[32 * j] >= a.drop ? to_f32(xv[j]) * a.scale : 0.f;
                 if constexpr (kRes) v += to_f32(rv[j]);
-                y[at_y[j]] = from_f32<T>(v);
+                T* to;
+                if constexpr (kWidth) {
+                    to = (32 * j >= end ? py + dy : py) + 32 * j;
+                } else {
+                    const int64_t i = i0 + 32 * j + lane;
+                    to = y + i + divide(i) * dy;
+                }
+                *to = from_f32<T>(v);
             }
         }
         __syncwarp();

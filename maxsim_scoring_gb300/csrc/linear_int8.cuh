@@ -318,23 +318,6 @@ __device__ __forceinline__ int32_t from_f32<int32_t>(float v) { return __float2i
 // the eight pieces of four rows, meet no bank twice.
 __device__ __forceinline__ uint32_t staged(int r, int c) { return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4)); }
 
-// Two 16-bit values of T in a word, and one of them again.
-template <typename T>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    if constexpr (std::is_same_v<T, __half>) {
-        const __half2 h = __floats2half2_rn(a, b);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    }
-}
-template <typename T>
-__device__ __forceinline__ T half_of(uint32_t w, int i) {
-    const unsigned short h = static_cast<unsigned short>(i ? w >> 16 : w);
-    return *reinterpret_cast<const T*>(&h);
-}
-
 // Four consecutive elements from p on, of which the first n exist.
 template <typename T>
 __device__ __forceinline__ void store4(T* p, int n, bool vec, float a, float b, float c, float d) {
