@@ -29,6 +29,7 @@ OP_FWD, OP_FWD_VARLEN, OP_BWD, OP_FWD_INT8, OP_SCORE_PAIRS = 0, 1, 2, 3, 4
 OP_CHAMFER_FWD, OP_CHAMFER_BWD, OP_TWO_STAGE, OP_FWD_STREAMED, OP_BWD_VARLEN = 5, 6, 7, 8, 9
 OP_FWD_VARLEN_STREAMED, OP_LINEAR_INT8 = 10, 11
 F16, BF16, F32 = 0, 1, 2
+ERR_WORKSPACE = 5
 
 # Every symbol the header declares, with its ctypes signature.
 _I64, _VP, _SZ, _I = ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int

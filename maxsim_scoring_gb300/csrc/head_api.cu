@@ -219,6 +219,32 @@ bool encode_k_rows(EncodeTiledFn encode, CUtensorMap* map, CUtensorMapDataType t
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A launch that may begin before the kernel in front of it has ended (the
+// kernel waits for it where it reads its results), in clusters of `cluster`.
+template <typename... Params, typename... Args>
+maxsim_status launch_after(void (*kern)(Params...), unsigned grid, unsigned threads, size_t smem, unsigned cluster,
+                           cudaStream_t st, const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) {
+        cudaGetLastError();
+        return MAXSIM_ERR_CUDA;
+    }
+    return MAXSIM_OK;
+}
+
 template <typename T, int kTiles>
 maxsim_status launch_few(const LinearArgs& a, cudaStream_t st) {
     const int64_t chunks = (static_cast<int64_t>(a.K) + 63) / 64;
@@ -228,7 +254,7 @@ maxsim_status launch_few(const LinearArgs& a, cudaStream_t st) {
 }
 
 template <typename T, int kTN, bool kSwap>
-maxsim_status launch_tile(const LinearPlan& p, const LinearArgs& l, const __half* b16, int32_t* partial,
+maxsim_status launch_tile(const LinearPlan& p, const LinearArgs& l, const __half* b16, bool a_prepared, int32_t* partial,
                           const HostDevice& dev, cudaStream_t st) {
     auto kern = linear_tile_kernel<T, kTN, kSwap>;
     constexpr size_t kSmem = tile_smem_bytes<kTN>();
@@ -255,6 +281,7 @@ maxsim_status launch_tile(const LinearPlan& p, const LinearArgs& l, const __half
     a.kb = p.kb;
     a.kb_slice = p.kb_slice;
     a.vec_out = p.slices > 1 ? l.N % 4 == 0 : ptr_aligned(l.out, 4 * sizeof(T)) && l.ld_out % 4 == 0;
+    a.a_prepared = a_prepared;
     a.status = dev.status;
     a.timeout_ns = kTimeoutNs;
     CUtensorMap ta, tb;
@@ -263,28 +290,16 @@ maxsim_status launch_tile(const LinearPlan& p, const LinearArgs& l, const __half
         !encode_k_rows(dev.encode, &tb, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, b16, p.k_pad, a.rows_b, p.k_pad * 2,
                        TileCfg<kTN>::kBRows))
         return MAXSIM_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(a.items, std::max(1, dev.num_sms / 2))));
-    cfg.blockDim = dim3(kTileThreads);
-    cfg.dynamicSmemBytes = kSmem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kern, ta, tb, a) != cudaSuccess) return MAXSIM_ERR_CUDA;
-    return launched();
+    return launch_after(kern, static_cast<unsigned>(2 * std::min<int64_t>(a.items, std::max(1, dev.num_sms / 2))), kTileThreads,
+                        kSmem, 2, st, ta, tb, a);
 }
 
 template <typename T, bool kSwap>
-maxsim_status launch_tile_width(const LinearPlan& p, const LinearArgs& l, const __half* b16, int32_t* partial,
+maxsim_status launch_tile_width(const LinearPlan& p, const LinearArgs& l, const __half* b16, bool a_prepared, int32_t* partial,
                                 const HostDevice& dev, cudaStream_t st) {
-    if (p.tn == 256) return launch_tile<T, 256, kSwap>(p, l, b16, partial, dev, st);
-    if (p.tn == 128) return launch_tile<T, 128, kSwap>(p, l, b16, partial, dev, st);
-    return launch_tile<T, 64, kSwap>(p, l, b16, partial, dev, st);
+    if (p.tn == 256) return launch_tile<T, 256, kSwap>(p, l, b16, a_prepared, partial, dev, st);
+    if (p.tn == 128) return launch_tile<T, 128, kSwap>(p, l, b16, a_prepared, partial, dev, st);
+    return launch_tile<T, 64, kSwap>(p, l, b16, a_prepared, partial, dev, st);
 }
 
 template <typename T>
@@ -298,27 +313,27 @@ maxsim_status run_linear(const LinearPlan& p, LinearArgs l, bool x_direct, bool 
     }
     const int32_t k_pad = static_cast<int32_t>(p.k_pad);
     const __half* b16 = nullptr;
-    if (!p.few) {  // B: x when swapped, else w
-        __half* to = reinterpret_cast<__half*>(ws + p.off_b);
-        const int8_t* from = p.swap ? l.x : l.w;
-        const int64_t rows = p.swap ? l.M : l.N, ld = p.swap ? l.ld_x : l.ld_w;
-        const unsigned grid = grid_of(rows * (k_pad / 16), 256, most);
-        if (p.swap ? x_direct : w_direct) widen_rows_kernel<true><<<grid, 256, 0, st>>>(from, rows, l.K, ld, to, k_pad);
-        else widen_rows_kernel<false><<<grid, 256, 0, st>>>(from, rows, l.K, ld, to, k_pad);
-        b16 = to;
+    const bool copy_x = !x_direct && (p.few || !p.swap), copy_w = !w_direct && (p.few || p.swap);
+    if (!p.few || copy_x || copy_w) {
+        PrepArgs a{};
+        a.K = l.K;
+        a.k_pad = k_pad;
+        if (!p.few) {  // B: x when swapped, else w
+            b16 = reinterpret_cast<const __half*>(ws + p.off_b);
+            a.widen = {p.swap ? l.x : l.w, ws + p.off_b, p.swap ? l.M : l.N, p.swap ? l.ld_x : l.ld_w,
+                       p.swap ? x_direct : w_direct};
+        }
+        if (copy_x) a.copy = {l.x, ws + p.off_x, l.M, l.ld_x, 0};
+        if (copy_w) a.copy2 = {l.w, ws + p.off_w, l.N, l.ld_w, 0};
+        const int64_t pieces = (a.widen.rows + a.copy.rows + a.copy2.rows) * (k_pad / 16);
+        linear_prep_kernel<<<grid_of(pieces, 256, most), 256, 0, st>>>(a);
     }
-    if (!x_direct && (p.few || !p.swap)) {
-        int8_t* to = reinterpret_cast<int8_t*>(ws + p.off_x);
-        repack_rows_kernel<<<grid_of(static_cast<int64_t>(l.M) * (k_pad / 16), 256, most), 256, 0, st>>>(
-            l.x, l.M, l.K, l.ld_x, to, k_pad);
-        l.x = to;
+    if (copy_x) {
+        l.x = reinterpret_cast<const int8_t*>(ws + p.off_x);
         l.ld_x = k_pad;
     }
-    if (!w_direct && (p.few || p.swap)) {
-        int8_t* to = reinterpret_cast<int8_t*>(ws + p.off_w);
-        repack_rows_kernel<<<grid_of(static_cast<int64_t>(l.N) * (k_pad / 16), 256, most), 256, 0, st>>>(
-            l.w, l.N, l.K, l.ld_w, to, k_pad);
-        l.w = to;
+    if (copy_w) {
+        l.w = reinterpret_cast<const int8_t*>(ws + p.off_w);
         l.ld_w = k_pad;
     }
     l.K = k_pad;  // an operand read where it is has K % 16 == 0 already; repacked tails are zero
@@ -330,11 +345,11 @@ maxsim_status run_linear(const LinearPlan& p, LinearArgs l, bool x_direct, bool 
         return launch_few<T, 4>(l, st);
     }
     int32_t* partial = reinterpret_cast<int32_t*>(ws + p.off_partial);
-    rc = p.swap ? launch_tile_width<T, true>(p, l, b16, partial, dev, st)
-                : launch_tile_width<T, false>(p, l, b16, partial, dev, st);
+    const bool prepared = copy_x || copy_w;
+    rc = p.swap ? launch_tile_width<T, true>(p, l, b16, prepared, partial, dev, st)
+                : launch_tile_width<T, false>(p, l, b16, prepared, partial, dev, st);
     if (rc != MAXSIM_OK || p.slices == 1) return rc;
-    linear_join_kernel<T><<<join_grid, 256, 0, st>>>(l, partial, p.slices);
-    return launched();
+    return launch_after(linear_join_kernel<T>, join_grid, 256, 0, 1, st, l, const_cast<const int32_t*>(partial), p.slices);
 }
 
 }  // namespace

@@ -31,50 +31,53 @@ struct LinearArgs {
     int32_t M, N, K;
 };
 
-// Rows of K bytes into rows of ld_dst bytes (a multiple of 16, the tail zero):
-// operands whose rows do not start on 16-byte boundaries are laid out once.
-__global__ void __launch_bounds__(256) repack_rows_kernel(const int8_t* __restrict__ src, int64_t rows, int32_t K,
-                                                          int64_t ld_src, int8_t* __restrict__ dst, int32_t ld_dst) {
-    const int32_t per_row = ld_dst >> 4;
-    const int64_t n = rows * per_row;
-    for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int64_t r = i / per_row;
-        const int32_t k = static_cast<int32_t>(i - r * per_row) << 4;
-        const uint8_t* p = reinterpret_cast<const uint8_t*>(src) + r * ld_src + k;
-        uint32_t w[4] = {0, 0, 0, 0};
+// A dependent launch may begin while the kernel before it still runs: it then
+// waits, where it reads that kernel's results, for all of it to be done.
+__device__ __forceinline__ void begin_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Operands laid out once for the kernels below.
+struct PrepJob {
+    const int8_t* src;
+    void* dst;
+    int64_t rows, ld_src;
+    int direct;  // rows are whole 16-byte pieces on 16-byte boundaries
+};
+struct PrepArgs {
+    PrepJob copy;   // to rows of k_pad bytes (rows off their 16-byte boundaries)
+    PrepJob copy2;
+    PrepJob widen;  // to rows of k_pad halves (the tile kernel's smaller operand)
+    int32_t K, k_pad;  // k_pad a multiple of 16: the tail is zero
+};
+
+__device__ __forceinline__ uint4 load_row16(const PrepJob& j, int64_t r, int32_t k, int32_t K) {
+    const uint8_t* p = reinterpret_cast<const uint8_t*>(j.src) + r * j.ld_src + k;
+    if (j.direct) return __ldg(reinterpret_cast<const uint4*>(p));
+    uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-            if (k + e < K) w[e >> 2] |= static_cast<uint32_t>(p[e]) << ((e & 3) * 8);
-        *reinterpret_cast<uint4*>(dst + r * ld_dst + k) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
+    for (int e = 0; e < 16; ++e)
+        if (k + e < K) w[e >> 2] |= static_cast<uint32_t>(p[e]) << ((e & 3) * 8);
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Rows of K bytes into rows of k_pad halves (a multiple of 16, the tail zero):
-// the tile kernel's smaller operand.
-template <bool kWide>
-__global__ void __launch_bounds__(256) widen_rows_kernel(const int8_t* __restrict__ src, int64_t rows, int32_t K,
-                                                         int64_t ld_src, __half* __restrict__ dst, int32_t k_pad) {
-    const int32_t per_row = k_pad >> 4;
-    const int64_t n = rows * per_row;
-    for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int64_t r = i / per_row;
-        const int32_t k = static_cast<int32_t>(i - r * per_row) << 4;
-        const uint8_t* p = reinterpret_cast<const uint8_t*>(src) + r * ld_src + k;
-        uint4 v;
-        if constexpr (kWide) {
-            v = __ldg(reinterpret_cast<const uint4*>(p));
+__global__ void __launch_bounds__(256) linear_prep_kernel(const PrepArgs a) {
+    begin_dependents();
+    const int32_t per_row = a.k_pad >> 4;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x, n1 = a.widen.rows * per_row,
+                  n2 = n1 + a.copy.rows * per_row, n3 = n2 + a.copy2.rows * per_row;
+    for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n3; i += step) {
+        const PrepJob& j = i < n1 ? a.widen : i < n2 ? a.copy : a.copy2;
+        const int64_t at = i < n1 ? i : i < n2 ? i - n1 : i - n2;
+        const int64_t r = at / per_row;
+        const int32_t k = static_cast<int32_t>(at - r * per_row) << 4;
+        const uint4 v = load_row16(j, r, k, a.K);
+        if (i < n1) {
+            uint4* to = reinterpret_cast<uint4*>(static_cast<__half*>(j.dst) + r * a.k_pad + k);
+            to[0] = i8x8_to_f16x8(v.x, v.y);
+            to[1] = i8x8_to_f16x8(v.z, v.w);
         } else {
-            uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                if (k + e < K) w[e >> 2] |= static_cast<uint32_t>(p[e]) << ((e & 3) * 8);
-            v = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(static_cast<int8_t*>(j.dst) + r * a.k_pad + k) = v;
         }
-        uint4* to = reinterpret_cast<uint4*>(dst + r * k_pad + k);
-        to[0] = i8x8_to_f16x8(v.x, v.y);
-        to[1] = i8x8_to_f16x8(v.z, v.w);
     }
 }
 
@@ -212,6 +215,7 @@ struct TileArgs {
     int32_t kb;         // blocks of K
     int32_t kb_slice;   // blocks per slice
     int vec_out;        // four outputs (sums) can be stored at once
+    int a_prepared;     // A too was laid out by linear_prep_kernel
     int* status;
     uint64_t timeout_ns;
 };
@@ -340,7 +344,7 @@ __device__ __forceinline__ void store4(T* p, int n, bool vec, float a, float b, 
 // One tile is 256 rows of A (128 on each CTA of a pair) x kTN rows of B. A is
 // the larger operand (x, or w when kSwap) and stays 8-bit until it is on the
 // SM; B, the smaller one, was widened to halves in device memory once for all
-// tiles (widen_rows_kernel).
+// tiles (linear_prep_kernel).
 //  * TMA brings 128-byte-wide blocks of A's rows into a ring of 8-bit stages
 //    and blocks of B (each CTA half of the tile's rows) into a ring of operand
 //    stages (128-byte swizzle; rows and columns past the ends read as 0);
@@ -370,6 +374,7 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     TileCtl* ctl = reinterpret_cast<TileCtl*>(s_out + 8 * kTileStage);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
+    if (a.slices > 1) begin_dependents();
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages8; ++s) {
             mbar_init(smem_u32(&ctl->full8[s]), 1);
@@ -409,6 +414,7 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         // ------------------------------------------------------------ TMA
         if (lane == 0) {
             const bool is_a = warp == 0;
+            if (!is_a || a.a_prepared) wait_for_previous();
             const int depth = is_a ? C::kStages8 : kTileRing;
             // the even CTA's B lands on the barrier that its MMA warp waits for
             uint64_t* full = is_a ? ctl->full8 : rank == 0 ? ctl->ready : ctl->b_full;
@@ -705,6 +711,7 @@ template <typename T>
 __global__ void __launch_bounds__(256) linear_join_kernel(const LinearArgs l, const int32_t* __restrict__ partial,
                                                           int32_t slices) {
     const int64_t n_out = static_cast<int64_t>(l.M) * l.N;
+    wait_for_previous();
     for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n_out;
          i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
         const int64_t m = i / l.N, n = i - m * l.N;

@@ -483,25 +483,37 @@ def linear_int8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale
     w, N, Kw, ld_w = _rows(w, "w")
     if w.dim() != 2 or Kw != K:
         raise ValueError("w must be [N, K] with x's K")
-    if x_scale.shape != shape[:-1] or w_scale.shape != (N,) or (bias is not None and bias.shape != (N,)):
+    lead = shape[:-1]
+    if x_scale.shape != lead or w_scale.shape != (N,) or (bias is not None and bias.shape != (N,)):
         raise ValueError("x_scale must have x's leading shape, w_scale and bias [N]")
-    if w.device != dev or x_scale.device != dev or w_scale.device != dev or (bias is not None and bias.device != dev):
+    index = dev.index
+    if w.get_device() != index or x_scale.get_device() != index or w_scale.get_device() != index or (
+            bias is not None and bias.get_device() != index):
         raise ValueError("x, w, their scales and bias must be on one device")
-    x_scale, w_scale = x_scale.contiguous(), w_scale.contiguous()
-    if bias is not None:
-        bias = bias.contiguous()
-    full = shape[:-1] + (N,)
+    if not x_scale.is_contiguous():
+        x_scale = x_scale.contiguous()
+    if not w_scale.is_contiguous():
+        w_scale = w_scale.contiguous()
+    if bias is None:
+        pb = None
+    else:
+        if not bias.is_contiguous():
+            bias = bias.contiguous()
+        pb = bias.data_ptr()
+    full = lead + (N,)
     out = torch.empty(full, dtype=out_dtype, device=dev) if out is None else _given(out, "out", full, out_dtype, dev)
-    px, pw = x.data_ptr(), w.data_ptr()
-    lib = _native.lib()
-    need = lib.maxsim_workspace_size(_native.OP_LINEAR_INT8, M, N, K, ld_x if px % 16 == 0 else 1,
-                                     max(ld_w, 1) if pw % 16 == 0 else 1)
-    if need == _SIZE_MAX:
-        _native.check(2, "maxsim_linear_int8")
-    ws, nbytes = _workspace(need, dev, workspace)
-    rc = lib.maxsim_linear_int8(px, ld_x, x_scale.data_ptr(), pw, ld_w, w_scale.data_ptr(),
-                                None if bias is None else bias.data_ptr(), M, N, K, dt, out.data_ptr(), N,
-                                None if ws is None else ws.data_ptr(), nbytes, _raw_stream(dev.index))
+    px, pw, lib = x.data_ptr(), w.data_ptr(), _native.lib()
+    args = (px, ld_x, x_scale.data_ptr(), pw, ld_w, w_scale.data_ptr(), pb, M, N, K, dt, out.data_ptr(), N)
+    stream = _raw_stream(index)
+    # few tokens mostly need no workspace: ask for its size only once a call says that it is missing
+    rc = lib.maxsim_linear_int8(*args, None, 0, stream) if M <= 32 else _native.ERR_WORKSPACE
+    if rc == _native.ERR_WORKSPACE:
+        need = lib.maxsim_workspace_size(_native.OP_LINEAR_INT8, M, N, K, ld_x if px % 16 == 0 else 1,
+                                         ld_w if ld_w and pw % 16 == 0 else 1)
+        if need == _SIZE_MAX:
+            _native.check(2, "maxsim_linear_int8")
+        ws, nbytes = _workspace(need, dev, workspace)
+        rc = lib.maxsim_linear_int8(*args, None if ws is None else ws.data_ptr(), nbytes, stream)
     if rc:
         _native.check(rc, "maxsim_linear_int8")
     return out
