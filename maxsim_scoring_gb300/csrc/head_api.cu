@@ -138,7 +138,6 @@ bool dropout_rate(double p, DropoutArgs* a) {
 
 // ---------------------------------------------------------------- INT8 linear
 
-constexpr int64_t kFewTokens = 32;      // up to here linear_few_kernel
 constexpr int64_t kPairs = 76;          // CTA pairs of a GB300 (152 SMs): plans do not depend on the device
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
@@ -146,6 +145,20 @@ constexpr uint64_t kTimeoutNs = 2000000000ull;
 // a 16-byte aligned base): whole 16-byte pieces, and a stride that a TMA
 // descriptor can hold.
 inline bool rows_direct(int64_t K, int64_t ld) { return K % 16 == 0 && ld % 16 == 0 && ld < (int64_t(1) << 40); }
+
+// linear_few_kernel or the tile kernel. The former takes any product in one
+// launch, but reads w once per 32 tokens. In units of 16 channels x 32 tokens x
+// 64 of K (measured, few / tile): 32 x 4096 x 4096, 16,384 units: 9.6 / 9.9 us;
+// more tokens: 128 x 1024 x 1024, 4,096 units: 6.8 / 8.2, 128 x 2048 x 1024,
+// 8,192 units: 12.3 / 8.2. Rows off their 16-byte boundaries take more instructions.
+constexpr int64_t kFewTokens = 32, kFewUnits = 16384;
+inline bool few_kernel(int64_t M, int64_t N, int64_t K, bool whole) {
+    if (M <= kFewTokens && whole) return true;
+    const int64_t groups = (M + 31) / 32, tiles = (N + 15) / 16, chunks = (K + 63) / 64;
+    const int64_t weight = (M <= kFewTokens ? 1 : 4) * (whole || M <= 8 ? 1 : 2);
+    return groups <= kFewUnits && tiles <= kFewUnits && groups * tiles <= kFewUnits &&
+           groups * tiles * chunks * weight <= kFewUnits;
+}
 
 struct LinearPlan {
     bool few = false;
@@ -161,48 +174,47 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool x_direct, bool w_di
     LinearPlan p;
     if (M == 0 || N == 0 || K == 0) return p;
     p.k_pad = (K + 15) / 16 * 16;
-    p.few = M <= kFewTokens;
-    p.swap = !p.few && N > M;  // the tile kernel's A is the larger operand
+    p.few = few_kernel(M, N, K, x_direct && w_direct);
+    if (p.few) return p;
+    p.swap = N > M;  // the tile kernel's A is the larger operand
     size_t off = 0;
-    if (!x_direct && (p.few || !p.swap)) {
+    if (!x_direct && !p.swap) {
         p.off_x = off;
         off = bytes_round_up(off + static_cast<size_t>(M) * p.k_pad, 256);
     }
-    if (!w_direct && (p.few || p.swap)) {
+    if (!w_direct && p.swap) {
         p.off_w = off;
         off = bytes_round_up(off + static_cast<size_t>(N) * p.k_pad, 256);
     }
-    if (!p.few) {
-        const int64_t rows_a = p.swap ? N : M, rows_b = p.swap ? M : N;
-        p.off_b = off;
-        off = bytes_round_up(off + static_cast<size_t>(rows_b) * p.k_pad * 2, 256);
-        // Tile width and slices of K by the time they should take, in cycles:
-        // the items of the busiest pair, each its blocks and a start and end,
-        // and for slices the kernel that joins them.
-        p.kb = static_cast<int32_t>((K + kTileK - 1) / kTileK);
-        double best = 0.0;
-        for (int tn = 256; tn >= 64; tn /= 2) {
-            const int64_t tiles_b = (rows_b + tn - 1) / tn, tiles = (rows_a + kTileM - 1) / kTileM * tiles_b;
-            const double block = tn == 256 ? 1050.0 : tn == 128 ? 600.0 : 500.0, ends = tn == 256 ? 3000.0 : 2000.0;
-            for (int32_t slices = 1; slices <= std::min(p.kb, 16); ++slices) {
-                const int32_t kb_slice = (p.kb + slices - 1) / slices;
-                if (slices > 1 && (tiles * slices > 2 * kPairs || (p.kb + kb_slice - 1) / kb_slice != slices)) continue;
-                double cost = static_cast<double>((tiles * slices + kPairs - 1) / kPairs) * (kb_slice * block + ends);
-                if (slices > 1) cost += 5000.0 + static_cast<double>(M) * N * slices * 4.0 / 1500.0;
-                if (best == 0.0 || cost < best) {
-                    best = cost;
-                    p.tn = tn;
-                    p.tiles = tiles;
-                    p.tiles_b = tiles_b;
-                    p.slices = slices;
-                    p.kb_slice = kb_slice;
-                }
+    const int64_t rows_a = p.swap ? N : M, rows_b = p.swap ? M : N;
+    p.off_b = off;
+    off = bytes_round_up(off + static_cast<size_t>(rows_b) * p.k_pad * 2, 256);
+    // Tile width and slices of K by the time they should take, in cycles:
+    // the items of the busiest pair, each its blocks and a start and end,
+    // and for slices the kernel that joins them.
+    p.kb = static_cast<int32_t>((K + kTileK - 1) / kTileK);
+    double best = 0.0;
+    for (int tn = 256; tn >= 64; tn /= 2) {
+        const int64_t tiles_b = (rows_b + tn - 1) / tn, tiles = (rows_a + kTileM - 1) / kTileM * tiles_b;
+        const double block = tn == 256 ? 1050.0 : tn == 128 ? 600.0 : 500.0, ends = tn == 256 ? 3000.0 : 2000.0;
+        for (int32_t slices = 1; slices <= std::min(p.kb, 16); ++slices) {
+            const int32_t kb_slice = (p.kb + slices - 1) / slices;
+            if (slices > 1 && (tiles * slices > 2 * kPairs || (p.kb + kb_slice - 1) / kb_slice != slices)) continue;
+            double cost = static_cast<double>((tiles * slices + kPairs - 1) / kPairs) * (kb_slice * block + ends);
+            if (slices > 1) cost += 5000.0 + static_cast<double>(M) * N * slices * 4.0 / 1500.0;
+            if (best == 0.0 || cost < best) {
+                best = cost;
+                p.tn = tn;
+                p.tiles = tiles;
+                p.tiles_b = tiles_b;
+                p.slices = slices;
+                p.kb_slice = kb_slice;
             }
         }
-        if (p.slices > 1) {
-            p.off_partial = off;
-            off = bytes_round_up(off + static_cast<size_t>(p.slices) * M * N * 4, 256);
-        }
+    }
+    if (p.slices > 1) {
+        p.off_partial = off;
+        off = bytes_round_up(off + static_cast<size_t>(p.slices) * M * N * 4, 256);
     }
     p.bytes = off;
     return p;
@@ -246,10 +258,13 @@ maxsim_status launch_after(void (*kern)(Params...), unsigned grid, unsigned thre
 }
 
 template <typename T, int kTiles>
-maxsim_status launch_few(const LinearArgs& a, cudaStream_t st) {
+maxsim_status launch_few(const LinearArgs& a, bool whole, cudaStream_t st) {
     const int64_t chunks = (static_cast<int64_t>(a.K) + 63) / 64;
     const unsigned threads = 32u * static_cast<unsigned>(std::min<int64_t>(kFewWarps, std::max<int64_t>(chunks, 1)));
-    linear_few_kernel<T, kTiles><<<static_cast<unsigned>((static_cast<int64_t>(a.N) + 15) / 16), threads, 0, st>>>(a);
+    const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.N) + 15) / 16),
+                    static_cast<unsigned>((static_cast<int64_t>(a.M) + 8 * kTiles - 1) / (8 * kTiles)));
+    if (whole) linear_few_kernel<T, kTiles, true><<<grid, threads, 0, st>>>(a);
+    else linear_few_kernel<T, kTiles, false><<<grid, threads, 0, st>>>(a);
     return launched();
 }
 
@@ -311,23 +326,23 @@ maxsim_status run_linear(const LinearPlan& p, LinearArgs l, bool x_direct, bool 
         linear_join_kernel<T><<<join_grid, 256, 0, st>>>(l, nullptr, 0);
         return launched();
     }
-    const int32_t k_pad = static_cast<int32_t>(p.k_pad);
-    const __half* b16 = nullptr;
-    const bool copy_x = !x_direct && (p.few || !p.swap), copy_w = !w_direct && (p.few || p.swap);
-    if (!p.few || copy_x || copy_w) {
-        PrepArgs a{};
-        a.K = l.K;
-        a.k_pad = k_pad;
-        if (!p.few) {  // B: x when swapped, else w
-            b16 = reinterpret_cast<const __half*>(ws + p.off_b);
-            a.widen = {p.swap ? l.x : l.w, ws + p.off_b, p.swap ? l.M : l.N, p.swap ? l.ld_x : l.ld_w,
-                       p.swap ? x_direct : w_direct};
-        }
-        if (copy_x) a.copy = {l.x, ws + p.off_x, l.M, l.ld_x, 0};
-        if (copy_w) a.copy2 = {l.w, ws + p.off_w, l.N, l.ld_w, 0};
-        const int64_t pieces = (a.widen.rows + a.copy.rows + a.copy2.rows) * (k_pad / 16);
-        linear_prep_kernel<<<grid_of(pieces, 256, most), 256, 0, st>>>(a);
+    if (p.few) {
+        const bool whole = x_direct && w_direct;
+        if (l.M <= 8) return launch_few<T, 1>(l, whole, st);
+        if (l.M <= 16) return launch_few<T, 2>(l, whole, st);
+        return launch_few<T, 4>(l, whole, st);
     }
+    const int32_t k_pad = static_cast<int32_t>(p.k_pad);
+    const __half* b16 = reinterpret_cast<const __half*>(ws + p.off_b);
+    const bool copy_x = !x_direct && !p.swap, copy_w = !w_direct && p.swap;
+    PrepArgs prep{};
+    prep.K = l.K;
+    prep.k_pad = k_pad;
+    prep.widen = {p.swap ? l.x : l.w, ws + p.off_b, p.swap ? l.M : l.N, p.swap ? l.ld_x : l.ld_w,
+                  p.swap ? x_direct : w_direct};
+    if (copy_x) prep.copy = {l.x, ws + p.off_x, l.M, l.ld_x, 0};
+    if (copy_w) prep.copy = {l.w, ws + p.off_w, l.N, l.ld_w, 0};
+    linear_prep_kernel<<<grid_of((prep.widen.rows + prep.copy.rows) * (k_pad / 16), 256, most), 256, 0, st>>>(prep);
     if (copy_x) {
         l.x = reinterpret_cast<const int8_t*>(ws + p.off_x);
         l.ld_x = k_pad;
@@ -339,11 +354,6 @@ maxsim_status run_linear(const LinearPlan& p, LinearArgs l, bool x_direct, bool 
     l.K = k_pad;  // an operand read where it is has K % 16 == 0 already; repacked tails are zero
     maxsim_status rc = launched();
     if (rc != MAXSIM_OK) return rc;
-    if (p.few) {
-        if (l.M <= 8) return launch_few<T, 1>(l, st);
-        if (l.M <= 16) return launch_few<T, 2>(l, st);
-        return launch_few<T, 4>(l, st);
-    }
     int32_t* partial = reinterpret_cast<int32_t*>(ws + p.off_partial);
     const bool prepared = copy_x || copy_w;
     rc = p.swap ? launch_tile_width<T, true>(p, l, b16, prepared, partial, dev, st)

@@ -7,8 +7,9 @@
 // to the tensor cores: |v| <= 128 is exact there, a product of two is exact in
 // fp32, and a sum of up to 1,024 products (2^24) is too.
 //
-//  * linear_few_kernel (few tokens): bound by the bytes of w, each read once.
-//  * linear_tile_kernel (many tokens): tcgen05 MMAs of 256-row tiles on CTA
+//  * linear_few_kernel (few tokens, and small products of any shape): bound by
+//    the bytes of w, each read once per 32 tokens, or by its launch.
+//  * linear_tile_kernel (everything else): tcgen05 MMAs of 256-row tiles on CTA
 //    pairs, bound by the tensor pipe, or by the bytes of the larger operand
 //    where the other one is narrow.
 #pragma once
@@ -36,7 +37,37 @@ struct LinearArgs {
 __device__ __forceinline__ void begin_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Operands laid out once for the kernels below.
+// 16 bytes of a row from k on, zero from K on, where rows start anywhere:
+// aligned words shifted into place. The words may hold bytes of neighbouring
+// rows, but none outside the operand's [base, end): its first and last bytes
+// are loaded one by one.
+__device__ __forceinline__ uint4 load16_any(const int8_t* row, int32_t k, int32_t K, const int8_t* base, const int8_t* end) {
+    uint32_t w[4] = {0, 0, 0, 0};
+    const int n = K - k;
+    if (n <= 0) return make_uint4(0, 0, 0, 0);
+    const int8_t* p = row + k;
+    const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 3);
+    const int8_t* first = p - shift;
+    if (first >= base && first + 20 <= end) {
+        const uint32_t* q = reinterpret_cast<const uint32_t*>(first);
+        uint32_t v[5];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) v[i] = __ldg(q + i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = __funnelshift_r(v[i], v[i + 1], shift * 8);
+            const int left = n - 4 * i;  // bytes of this word that exist
+            if (left < 4) w[i] &= left <= 0 ? 0u : 0xffffffffu >> (32 - 8 * left);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            if (e < n) w[e >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(__ldg(p + e))) << ((e & 3) * 8);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Operands laid out once for the tile kernel.
 struct PrepJob {
     const int8_t* src;
     void* dst;
@@ -44,30 +75,25 @@ struct PrepJob {
     int direct;  // rows are whole 16-byte pieces on 16-byte boundaries
 };
 struct PrepArgs {
-    PrepJob copy;   // to rows of k_pad bytes (rows off their 16-byte boundaries)
-    PrepJob copy2;
+    PrepJob copy;   // to rows of k_pad bytes (A, where its rows are off their 16-byte boundaries)
     PrepJob widen;  // to rows of k_pad halves (the tile kernel's smaller operand)
     int32_t K, k_pad;  // k_pad a multiple of 16: the tail is zero
 };
 
 __device__ __forceinline__ uint4 load_row16(const PrepJob& j, int64_t r, int32_t k, int32_t K) {
-    const uint8_t* p = reinterpret_cast<const uint8_t*>(j.src) + r * j.ld_src + k;
-    if (j.direct) return __ldg(reinterpret_cast<const uint4*>(p));
-    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int e = 0; e < 16; ++e)
-        if (k + e < K) w[e >> 2] |= static_cast<uint32_t>(p[e]) << ((e & 3) * 8);
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    const int8_t* row = j.src + r * j.ld_src;
+    if (j.direct) return __ldg(reinterpret_cast<const uint4*>(row + k));
+    return load16_any(row, k, K, j.src, j.src + (j.rows - 1) * j.ld_src + K);
 }
 
 __global__ void __launch_bounds__(256) linear_prep_kernel(const PrepArgs a) {
     begin_dependents();
     const int32_t per_row = a.k_pad >> 4;
     const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x, n1 = a.widen.rows * per_row,
-                  n2 = n1 + a.copy.rows * per_row, n3 = n2 + a.copy2.rows * per_row;
-    for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n3; i += step) {
-        const PrepJob& j = i < n1 ? a.widen : i < n2 ? a.copy : a.copy2;
-        const int64_t at = i < n1 ? i : i < n2 ? i - n1 : i - n2;
+                  n2 = n1 + a.copy.rows * per_row;
+    for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n2; i += step) {
+        const PrepJob& j = i < n1 ? a.widen : a.copy;
+        const int64_t at = i < n1 ? i : i - n1;
         const int64_t r = at / per_row;
         const int32_t k = static_cast<int32_t>(at - r * per_row) << 4;
         const uint4 v = load_row16(j, r, k, a.K);
@@ -81,7 +107,7 @@ __global__ void __launch_bounds__(256) linear_prep_kernel(const PrepArgs a) {
     }
 }
 
-// ---------------------------------------------------------------- few tokens
+// ---------------------------------------------------------------- few tokens, small products
 
 __device__ __forceinline__ void mma_m16n8k16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                              uint32_t b0, uint32_t b1) {
@@ -100,29 +126,38 @@ __device__ __forceinline__ void widen16(uint4 v, uint32_t (&h)[8]) {
 
 constexpr int kFewWarps = 16;  // most warps of a block
 
-// A block owns 16 channels and all M <= 8 * kTiles tokens; its warps take
-// 64-wide chunks of K in turn. A lane reads 16 consecutive bytes of two
+// kWhole: rows are whole 16-byte pieces on 16-byte boundaries.
+template <bool kWhole>
+__device__ __forceinline__ uint4 load16(const int8_t* row, int32_t k, int32_t K, const int8_t* base, const int8_t* end) {
+    if constexpr (kWhole) return k < K ? __ldg(reinterpret_cast<const uint4*>(row + k)) : make_uint4(0, 0, 0, 0);
+    else return load16_any(row, k, K, base, end);
+}
+
+// A block owns 16 channels and up to 8 * kTiles tokens (blockIdx.y); its warps
+// take 64-wide chunks of K in turn. A lane reads 16 consecutive bytes of two
 // channels (w is the MMA's 16-row operand) and of one token of each 8-token
 // tile: lane t of a row then holds k = 16 t .. 16 t + 15 instead of the
 // fragment's own columns, in both operands alike, so the sum over k is the
 // same and every load is 16 bytes wide. After 16 chunks of a warp (1,024
 // products, exact in fp32) the sums move to 32-bit integers, and the warps'
 // sums are added as integers in shared memory: exact, in any order.
-template <typename T, int kTiles>
+template <typename T, int kTiles, bool kWhole>
 __global__ void __launch_bounds__(kFewWarps * 32) linear_few_kernel(const LinearArgs a) {
-    constexpr int kAhead = kTiles <= 2 ? 4 : 2;  // chunks whose loads are in flight
+    constexpr int kAhead = !kWhole ? 1 : kTiles <= 2 ? 4 : 2;  // chunks whose loads are in flight
     __shared__ int s_sum[16][8 * kTiles + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     const int g = lane >> 2, t = lane & 3;
-    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
+    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16, m0 = static_cast<int64_t>(blockIdx.y) * (8 * kTiles);
     for (int i = threadIdx.x; i < 16 * (8 * kTiles + 1); i += blockDim.x) (&s_sum[0][0])[i] = 0;
     __syncthreads();
     // rows past the ends read the last row; what they give is not stored
-    const int8_t* w0 = a.w + min(n0 + g, static_cast<int64_t>(a.N) - 1) * a.ld_w + 16 * t;
-    const int8_t* w1 = a.w + min(n0 + g + 8, static_cast<int64_t>(a.N) - 1) * a.ld_w + 16 * t;
+    const int8_t* w0 = a.w + min(n0 + g, static_cast<int64_t>(a.N) - 1) * a.ld_w;
+    const int8_t* w1 = a.w + min(n0 + g + 8, static_cast<int64_t>(a.N) - 1) * a.ld_w;
     const int8_t* xr[kTiles];
 #pragma unroll
-    for (int j = 0; j < kTiles; ++j) xr[j] = a.x + static_cast<int64_t>(min(8 * j + g, a.M - 1)) * a.ld_x + 16 * t;
+    for (int j = 0; j < kTiles; ++j) xr[j] = a.x + min(m0 + 8 * j + g, static_cast<int64_t>(a.M) - 1) * a.ld_x;
+    const int8_t* x_end = a.x + (static_cast<int64_t>(a.M) - 1) * a.ld_x + a.K;
+    const int8_t* w_end = a.w + (static_cast<int64_t>(a.N) - 1) * a.ld_w + a.K;
     const int32_t chunks = (a.K + 63) >> 6;
     int sum[kTiles][4] = {};
     for (int32_t c0 = warp; c0 < chunks; c0 += 16 * warps) {
@@ -132,13 +167,11 @@ __global__ void __launch_bounds__(kFewWarps * 32) linear_few_kernel(const Linear
             uint4 wv[kAhead][2], xv[kAhead][kTiles];
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
-                const int32_t k = (c0 + (i0 + i) * warps) << 6;
-                const bool in = k + 16 * t < a.K;
-                const uint4 zero = make_uint4(0, 0, 0, 0);
-                wv[i][0] = in ? __ldg(reinterpret_cast<const uint4*>(w0 + k)) : zero;
-                wv[i][1] = in ? __ldg(reinterpret_cast<const uint4*>(w1 + k)) : zero;
+                const int32_t k = ((c0 + (i0 + i) * warps) << 6) + 16 * t;
+                wv[i][0] = load16<kWhole>(w0, k, a.K, a.w, w_end);
+                wv[i][1] = load16<kWhole>(w1, k, a.K, a.w, w_end);
 #pragma unroll
-                for (int j = 0; j < kTiles; ++j) xv[i][j] = in ? __ldg(reinterpret_cast<const uint4*>(xr[j] + k)) : zero;
+                for (int j = 0; j < kTiles; ++j) xv[i][j] = load16<kWhole>(xr[j], k, a.K, a.x, x_end);
             }
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
@@ -165,12 +198,13 @@ __global__ void __launch_bounds__(kFewWarps * 32) linear_few_kernel(const Linear
 #pragma unroll
         for (int e = 0; e < 4; ++e) atomicAdd(&s_sum[g + (e & 2) * 4][8 * j + 2 * t + (e & 1)], sum[j][e]);
     __syncthreads();
-    for (int i = threadIdx.x; i < 16 * a.M; i += blockDim.x) {
+    const int tokens = static_cast<int>(min(a.M - m0, static_cast<int64_t>(8 * kTiles)));
+    for (int i = threadIdx.x; i < 16 * tokens; i += blockDim.x) {
         const int m = i >> 4, n = i & 15;
         if (n0 + n < a.N) {
-            float v = static_cast<float>(s_sum[n][m]) * a.x_scale[m] * a.w_scale[n0 + n];
+            float v = static_cast<float>(s_sum[n][m]) * a.x_scale[m0 + m] * a.w_scale[n0 + n];
             if (a.bias) v += a.bias[n0 + n];
-            static_cast<T*>(a.out)[m * a.ld_out + n0 + n] = from_f32<T>(v);
+            static_cast<T*>(a.out)[(m0 + m) * a.ld_out + n0 + n] = from_f32<T>(v);
         }
     }
 }

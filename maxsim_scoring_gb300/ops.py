@@ -505,8 +505,9 @@ def linear_int8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale
     px, pw, lib = x.data_ptr(), w.data_ptr(), _native.lib()
     args = (px, ld_x, x_scale.data_ptr(), pw, ld_w, w_scale.data_ptr(), pb, M, N, K, dt, out.data_ptr(), N)
     stream = _raw_stream(index)
-    # few tokens mostly need no workspace: ask for its size only once a call says that it is missing
-    rc = lib.maxsim_linear_int8(*args, None, 0, stream) if M <= 32 else _native.ERR_WORKSPACE
+    # few tokens and small products need no workspace: its size is asked for once a call says that it is missing
+    rc = (lib.maxsim_linear_int8(*args, None, 0, stream) if M <= 32 or M * N * K <= 1 << 29
+          else _native.ERR_WORKSPACE)
     if rc == _native.ERR_WORKSPACE:
         need = lib.maxsim_workspace_size(_native.OP_LINEAR_INT8, M, N, K, ld_x if px % 16 == 0 else 1,
                                          ld_w if ld_w and pw % 16 == 0 else 1)
