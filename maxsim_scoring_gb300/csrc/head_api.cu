@@ -295,7 +295,8 @@ maxsim_status launch_tile(const LinearPlan& p, const LinearArgs& l, const __half
     a.slices = p.slices;
     a.kb = p.kb;
     a.kb_slice = p.kb_slice;
-    a.vec_out = p.slices > 1 ? l.N % 4 == 0 : ptr_aligned(l.out, 4 * sizeof(T)) && l.ld_out % 4 == 0;
+    a.vec_out = p.slices > 1 ? l.N % 4 == 0
+                             : ptr_aligned(l.out, 16) && l.ld_out * static_cast<int64_t>(sizeof(T)) % 16 == 0;
     a.a_prepared = a_prepared;
     a.status = dev.status;
     a.timeout_ns = kTimeoutNs;

@@ -248,7 +248,7 @@ struct TileArgs {
     int32_t slices;     // parts of K
     int32_t kb;         // blocks of K
     int32_t kb_slice;   // blocks per slice
-    int vec_out;        // four outputs (sums) can be stored at once
+    int vec_out;        // rows of out (of the sums) start on 16-byte boundaries
     int a_prepared;     // A too was laid out by linear_prep_kernel
     int* status;
     uint64_t timeout_ns;
@@ -356,17 +356,13 @@ __device__ __forceinline__ int32_t from_f32<int32_t>(float v) { return __float2i
 // the eight pieces of four rows, meet no bank twice.
 __device__ __forceinline__ uint32_t staged(int r, int c) { return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4)); }
 
-// Four consecutive elements from p on, of which the first n exist.
+// Four consecutive 32-bit elements from p on, of which the first n exist.
 template <typename T>
 __device__ __forceinline__ void store4(T* p, int n, bool vec, float a, float b, float c, float d) {
+    static_assert(sizeof(T) == 4, "one 16-byte store");
     if (vec && n >= 4) {
-        if constexpr (sizeof(T) == 4) {
-            alignas(16) T o[4] = {from_f32<T>(a), from_f32<T>(b), from_f32<T>(c), from_f32<T>(d)};
-            *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(o);
-        } else {
-            alignas(8) T o[4] = {from_f32<T>(a), from_f32<T>(b), from_f32<T>(c), from_f32<T>(d)};
-            *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(o);
-        }
+        alignas(16) T o[4] = {from_f32<T>(a), from_f32<T>(b), from_f32<T>(c), from_f32<T>(d)};
+        *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(o);
     } else {
         if (n > 0) p[0] = from_f32<T>(a);
         if (n > 1) p[1] = from_f32<T>(b);
@@ -584,77 +580,94 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     } else {
         regs_claim<kTileRegsEpi>();
         // ------------------------------------------------------------ epilogue
-        // A warp owns 32 rows of A and half of the tile's columns, 32 at a time.
-        // Swapped, its lanes hold consecutive channels and store straight to
-        // out. Otherwise a lane holds a token: the sums go through shared
-        // memory so that eight lanes hold 32 channels of a token, four each,
-        // and stores are whole runs. All scales are in registers before the
-        // accumulator is waited for. 16-bit outputs are held until the
-        // accumulator has been read and handed back: all SMs store a tile at
-        // about the same time, which takes 8,500 cycles at 256 x 256, and the
-        // next tile's MMAs then run beside it.
+        // A warp owns 32 rows of A and half of the tile's columns; in the
+        // accumulator a lane holds a row. 16-bit outputs are scaled, rounded and
+        // held in registers until the accumulator has been read and handed
+        // back, so that only this stands between a tile's MMAs and the next
+        // one's: all SMs store their tiles at about the same time, which
+        // takes longer (8,500 cycles at 256 x 256). The scales along B wait in
+        // shared memory, where a read serves the whole warp. Swapped, lanes are
+        // consecutive channels and store straight to out; otherwise rows pass
+        // through shared memory so that stores are whole 128-byte runs. 32-bit
+        // outputs, and the integer sums of slices, are stored 32 columns at a
+        // time as they are read.
         const int q = warp & 3, half = (warp - kTileEpiWarp0) >> 2;
-        constexpr int kCols = kTN / 2;  // columns per warp
+        constexpr int kCols = kTN / 2, kChunks = kCols / 32;  // columns per warp
+        constexpr bool kHold = sizeof(T) == 2;
         uint8_t* stage = s_out + (warp - kTileEpiWarp0) * kTileStage;
+        float* tab = reinterpret_cast<float*>(stage);  // kHold: scales of the kCols columns, then biases
         const int64_t ld = a.slices > 1 ? a.l.N : a.l.ld_out;
+        const bool hold = kHold && a.slices == 1;
         int32_t buf = 0;
         uint32_t buf_phase = 0;
         for (int64_t it = first; it < a.items; it += step) {
             const TileItem t = tile_item<kTN>(a, it, rank);
             const int64_t ra0 = t.a0 + q * 32, rb0 = t.b0 + half * kCols;
             int32_t* part = a.partial + static_cast<int64_t>(t.slice) * a.l.M * a.l.N;  // used when slices > 1
+            const int row_n = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(32), a.rows_a - ra0)));
             // this lane's row of A, and its column of each 32 along B
-            const bool in_a = ra0 + lane < a.rows_a;
+            const bool in_a = lane < row_n;
             const float* scale_b = kSwap ? a.l.x_scale : a.l.w_scale;
             const float sa = in_a ? __ldg((kSwap ? a.l.w_scale : a.l.x_scale) + ra0 + lane) : 0.f;
-            float bias[kSwap ? 1 : kCols / 32], sb[kCols / 32];
-            if constexpr (kSwap) bias[0] = a.l.bias && in_a ? __ldg(a.l.bias + ra0 + lane) : 0.f;
+            const float bias_a = kSwap && a.l.bias && in_a ? __ldg(a.l.bias + ra0 + lane) : 0.f;
+            float sb[kChunks], bias[kSwap ? 1 : kChunks];
 #pragma unroll
-            for (int c = 0; c < kCols / 32; ++c) {
+            for (int c = 0; c < kChunks; ++c) {
                 const int64_t i = rb0 + c * 32 + lane;
                 sb[c] = i < a.rows_b ? __ldg(scale_b + i) : 0.f;
                 if constexpr (!kSwap) bias[c] = a.l.bias && i < a.rows_b ? __ldg(a.l.bias + i) : 0.f;
             }
+            if (hold) {
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    tab[c * 32 + lane] = sb[c];
+                    if constexpr (!kSwap) tab[kCols + c * 32 + lane] = bias[c];
+                }
+                __syncwarp();
+            }
             if (!tile_wait_warp(a, ctl, &ctl->acc_full[buf], buf_phase)) break;
             tc_fence_after();
             const uint32_t src = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * kTN + half * kCols);
-            constexpr bool kHold = sizeof(T) == 2;
-            uint32_t held[kHold ? kCols / 32 : 1][16];
-            const int row_n = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(32), a.rows_a - ra0)));
+            uint32_t held[kHold ? kChunks : 1][16];
 #pragma unroll
-            for (int c = 0; c < kCols / 32; ++c) {
+            for (int c = 0; c < kChunks; ++c) {
                 const int64_t rb = rb0 + c * 32;
                 float v[32];
                 tmem_ld32(src + c * 32, v);
                 tmem_wait_ld();
-                if (c + 1 == kCols / 32) {
+                if (c + 1 == kChunks) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_remote(map_shared_rank(smem_u32(&ctl->acc_empty[buf]), 0));
                 }
-                if (ra0 >= a.rows_a || rb >= a.rows_b) continue;
+                if constexpr (kHold) {
+                    if (a.slices == 1) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            const float4 s4 = *reinterpret_cast<const float4*>(tab + c * 32 + i);
+                            const float4 b4 = kSwap ? make_float4(bias_a, bias_a, bias_a, bias_a)
+                                                    : *reinterpret_cast<const float4*>(tab + kCols + c * 32 + i);
+                            held[c][i / 2] = pack2<T>(__fmaf_rn(v[i] * sa, s4.x, b4.x), __fmaf_rn(v[i + 1] * sa, s4.y, b4.y));
+                            held[c][i / 2 + 1] =
+                                pack2<T>(__fmaf_rn(v[i + 2] * sa, s4.z, b4.z), __fmaf_rn(v[i + 3] * sa, s4.w, b4.w));
+                        }
+                        continue;
+                    }
+                }
+                if (row_n == 0 || rb >= a.rows_b) continue;
                 if constexpr (kSwap) {
                     const int n = static_cast<int>(min(static_cast<int64_t>(32), a.rows_b - rb));
-                    const bool real = ra0 + lane < a.rows_a;
                     if (a.slices > 1) {
                         int32_t* p = part + rb * ld + ra0 + lane;
 #pragma unroll
                         for (int i = 0; i < 32; ++i, p += ld)
-                            if (i < n && real) *p = __float2int_rn(v[i]);
-                    } else {
+                            if (i < n && in_a) *p = __float2int_rn(v[i]);
+                    } else if constexpr (!kHold) {
                         T* p = static_cast<T*>(a.l.out) + rb * ld + ra0 + lane;
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            const float y0 = __fmaf_rn(v[i] * __shfl_sync(0xffffffffu, sb[c], i), sa, bias[0]);
-                            const float y1 = __fmaf_rn(v[i + 1] * __shfl_sync(0xffffffffu, sb[c], i + 1), sa, bias[0]);
-                            if constexpr (kHold) {
-                                held[c][i / 2] = pack2<T>(y0, y1);
-                            } else {
-                                if (i < n && real) *p = y0;
-                                p += ld;
-                                if (i + 1 < n && real) *p = y1;
-                                p += ld;
-                            }
+                        for (int i = 0; i < 32; ++i, p += ld) {
+                            const T y = from_f32<T>(__fmaf_rn(v[i] * __shfl_sync(0xffffffffu, sb[c], i), sa, bias_a));
+                            if (i < n && in_a) *p = y;
                         }
                     }
                 } else {
@@ -676,52 +689,59 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
 #pragma unroll
                     for (int i = 0; i < 8; ++i, at += 4 * ld) {
                         const float4 y = *reinterpret_cast<const float4*>(stage + staged(4 * i + (lane >> 3), lane & 7));
-                        const bool real = 4 * i + (lane >> 3) < row_n;
+                        if (4 * i + (lane >> 3) >= row_n) continue;
                         if (a.slices > 1) {
-                            if (real) store4(part + at, n, a.vec_out, y.x, y.y, y.z, y.w);
-                            continue;
-                        }
-                        const float o[4] = {__fmaf_rn(y.x, ws[0], bs[0]), __fmaf_rn(y.y, ws[1], bs[1]),
-                                            __fmaf_rn(y.z, ws[2], bs[2]), __fmaf_rn(y.w, ws[3], bs[3])};
-                        if constexpr (kHold) {
-                            held[c][2 * i] = pack2<T>(o[0], o[1]);
-                            held[c][2 * i + 1] = pack2<T>(o[2], o[3]);
-                        } else {
-                            if (real) store4(static_cast<T*>(a.l.out) + at, n, a.vec_out, o[0], o[1], o[2], o[3]);
+                            store4(part + at, n, a.vec_out, y.x, y.y, y.z, y.w);
+                        } else if constexpr (!kHold) {
+                            store4(static_cast<T*>(a.l.out) + at, n, a.vec_out, __fmaf_rn(y.x, ws[0], bs[0]),
+                                   __fmaf_rn(y.y, ws[1], bs[1]), __fmaf_rn(y.z, ws[2], bs[2]), __fmaf_rn(y.w, ws[3], bs[3]));
                         }
                     }
                     __syncwarp();
                 }
             }
             if constexpr (kHold) {
-                if (a.slices == 1 && row_n > 0) {
+                if (hold && row_n > 0) {
+                    __syncwarp();  // the table is done with
+                    if constexpr (kSwap) {
 #pragma unroll
-                    for (int c = 0; c < kCols / 32; ++c) {
-                        const int64_t rb = rb0 + c * 32;
-                        if (rb >= a.rows_b) break;
-                        if constexpr (kSwap) {
+                        for (int c = 0; c < kChunks; ++c) {
+                            const int64_t rb = rb0 + c * 32;
                             const int n = static_cast<int>(min(static_cast<int64_t>(32), a.rows_b - rb));
                             T* p = static_cast<T*>(a.l.out) + rb * ld + ra0 + lane;
 #pragma unroll
                             for (int i = 0; i < 32; ++i, p += ld)
-                                if (i < n && lane < row_n) *p = half_of<T>(held[c][i / 2], i & 1);
-                        } else {
-                            const int64_t n0 = rb + 4 * (lane & 7);
-                            const int n = static_cast<int>(min(static_cast<int64_t>(4), a.rows_b - n0));
-                            T* p = static_cast<T*>(a.l.out) + (ra0 + (lane >> 3)) * ld + n0;
+                                if (i < n && in_a) *p = half_of<T>(held[c][i / 2], i & 1);
+                        }
+                    } else {
+                        constexpr int kJoin = kChunks < 2 ? 1 : 2;         // chunks whose rows are staged together
+                        constexpr int kLanes = 4 * kJoin, kRows = 32 / kLanes;  // lanes of a row, rows of a store
 #pragma unroll
-                            for (int i = 0; i < 8; ++i, p += 4 * ld) {
-                                if (4 * i + (lane >> 3) >= row_n) break;
-                                const uint32_t lo = held[c][2 * i], hi = held[c][2 * i + 1];
-                                if (a.vec_out && n == 4) {
-                                    *reinterpret_cast<uint2*>(p) = make_uint2(lo, hi);
+                        for (int c = 0; c < kChunks; c += kJoin) {
+                            const int64_t n0 = rb0 + c * 32 + 8 * (lane % kLanes);
+                            const int n = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(8), a.rows_b - n0)));
+#pragma unroll
+                            for (int j = 0; j < kLanes; ++j)
+                                *reinterpret_cast<uint4*>(stage + staged(lane, j)) =
+                                    make_uint4(held[c + j / 4][(j % 4) * 4], held[c + j / 4][(j % 4) * 4 + 1],
+                                               held[c + j / 4][(j % 4) * 4 + 2], held[c + j / 4][(j % 4) * 4 + 3]);
+                            __syncwarp();
+                            T* p = static_cast<T*>(a.l.out) + (ra0 + lane / kLanes) * ld + n0;
+#pragma unroll
+                            for (int i = 0; i < kLanes; ++i, p += kRows * ld) {
+                                const int r = i * kRows + lane / kLanes;
+                                const uint4 y = *reinterpret_cast<const uint4*>(stage + staged(r, lane % kLanes));
+                                if (r >= row_n) continue;
+                                if (a.vec_out && n == 8) {
+                                    *reinterpret_cast<uint4*>(p) = y;
                                 } else {
-                                    if (n > 0) p[0] = half_of<T>(lo, 0);
-                                    if (n > 1) p[1] = half_of<T>(lo, 1);
-                                    if (n > 2) p[2] = half_of<T>(hi, 0);
-                                    if (n > 3) p[3] = half_of<T>(hi, 1);
+                                    const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e)
+                                        if (e < n) p[e] = half_of<T>(w[e / 2], e & 1);
                                 }
                             }
+                            __syncwarp();
                         }
                     }
                 }
