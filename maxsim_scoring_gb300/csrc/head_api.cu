@@ -34,39 +34,41 @@ inline bool rows_fit(int64_t rows, int64_t cols, int64_t ld) {
     return ld >= cols && (rows <= 1 || ld <= (int64_t(1) << 60) / std::max<int64_t>(rows, 1));
 }
 
-template <typename T, bool kWide, int kGroup, int kChunks>
+template <typename T, bool kWide, bool kNorm, int kGroup, int kChunks>
 maxsim_status launch_quantize_group(const QuantizeArgs& a, const HostDevice& dev, cudaStream_t st) {
     constexpr int kThreads = quantize_threads(kGroup);
     const unsigned grid = grid_of(a.rows, kThreads / kGroup, int64_t(dev.num_sms) * (2048 / kThreads));
-    quantize_rows_kernel<T, kWide, kGroup, kChunks><<<grid, kThreads, 0, st>>>(a);
+    quantize_rows_kernel<T, kWide, kNorm, kGroup, kChunks><<<grid, kThreads, 0, st>>>(a);
     return launched();
 }
 
 // The smallest group that holds a row: short rows then share a warp (fewer
 // shuffle steps for a row, several rows' loads in flight), long ones take a
 // block.
-template <typename T, bool kWide>
+template <typename T, bool kWide, bool kNorm>
 maxsim_status launch_quantize(const QuantizeArgs& a, const HostDevice& dev, cudaStream_t st) {
     const int64_t chunks = (a.cols + Chunk<T, kWide>::kVec - 1) / Chunk<T, kWide>::kVec;
-    if (chunks <= 8) return launch_quantize_group<T, kWide, 8, 1>(a, dev, st);
-    if (chunks <= 16) return launch_quantize_group<T, kWide, 8, 2>(a, dev, st);
-    if (chunks <= 32) return launch_quantize_group<T, kWide, 8, 4>(a, dev, st);
-    if (chunks <= 64) return launch_quantize_group<T, kWide, 8, 8>(a, dev, st);
-    if (chunks <= 128) return launch_quantize_group<T, kWide, 32, 4>(a, dev, st);
-    if (chunks <= 256) return launch_quantize_group<T, kWide, 32, 8>(a, dev, st);
-    if (chunks <= 512) return launch_quantize_group<T, kWide, 128, 4>(a, dev, st);
-    if (chunks <= 1024) return launch_quantize_group<T, kWide, 128, 8>(a, dev, st);
-    if (chunks <= 4096) return launch_quantize_group<T, kWide, 512, 8>(a, dev, st);
-    quantize_long_rows_kernel<T, kWide><<<grid_of(a.rows, 1, int64_t(dev.num_sms) * 4), 512, 0, st>>>(a);
+    if (chunks <= 8) return launch_quantize_group<T, kWide, kNorm, 8, 1>(a, dev, st);
+    if (chunks <= 16) return launch_quantize_group<T, kWide, kNorm, 8, 2>(a, dev, st);
+    if (chunks <= 32) return launch_quantize_group<T, kWide, kNorm, 8, 4>(a, dev, st);
+    if (chunks <= 64) return launch_quantize_group<T, kWide, kNorm, 8, 8>(a, dev, st);
+    if (chunks <= 128) return launch_quantize_group<T, kWide, kNorm, 32, 4>(a, dev, st);
+    if (chunks <= 256) return launch_quantize_group<T, kWide, kNorm, 32, 8>(a, dev, st);
+    if (chunks <= 512) return launch_quantize_group<T, kWide, kNorm, 128, 4>(a, dev, st);
+    if (chunks <= 1024) return launch_quantize_group<T, kWide, kNorm, 128, 8>(a, dev, st);
+    if (chunks <= 2048) return launch_quantize_group<T, kWide, kNorm, 512, 4>(a, dev, st);
+    if (chunks <= 4096) return launch_quantize_group<T, kWide, kNorm, 512, 8>(a, dev, st);
+    quantize_long_rows_kernel<T, kWide, kNorm><<<grid_of(a.rows, 1, int64_t(dev.num_sms) * 4), 512, 0, st>>>(a);
     return launched();
 }
 
 template <typename T>
-maxsim_status launch_quantize_any(const QuantizeArgs& a, const HostDevice& dev, cudaStream_t st) {
+maxsim_status launch_quantize_any(const QuantizeArgs& a, bool normalize, const HostDevice& dev, cudaStream_t st) {
     constexpr int kVec = Chunk<T, true>::kVec;
     const bool wide = a.cols % kVec == 0 && a.ld_x % kVec == 0 && a.ld_q % kVec == 0 && ptr_aligned(a.x, 16) &&
                       ptr_aligned(a.q, kVec);
-    return wide ? launch_quantize<T, true>(a, dev, st) : launch_quantize<T, false>(a, dev, st);
+    if (normalize) return wide ? launch_quantize<T, true, true>(a, dev, st) : launch_quantize<T, false, true>(a, dev, st);
+    return wide ? launch_quantize<T, true, false>(a, dev, st) : launch_quantize<T, false, false>(a, dev, st);
 }
 
 // The multiplier and shift that divide 0 <= i < 2^31 by d (round-up method: with l = ceil(log2 d),
@@ -389,10 +391,10 @@ maxsim_status maxsim_quantize_rows(const void* x, maxsim_dtype dtype, int64_t ro
     const maxsim_status rc = host_device(&dev);
     if (rc != MAXSIM_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const QuantizeArgs a{x, q, scale, rows, ld_x, ld_q, static_cast<int32_t>(cols), normalize != 0};
-    if (dtype == MAXSIM_F16) return launch_quantize_any<__half>(a, dev, st);
-    if (dtype == MAXSIM_BF16) return launch_quantize_any<__nv_bfloat16>(a, dev, st);
-    return launch_quantize_any<float>(a, dev, st);
+    const QuantizeArgs a{x, q, scale, rows, ld_x, ld_q, static_cast<int32_t>(cols)};
+    if (dtype == MAXSIM_F16) return launch_quantize_any<__half>(a, normalize != 0, dev, st);
+    if (dtype == MAXSIM_BF16) return launch_quantize_any<__nv_bfloat16>(a, normalize != 0, dev, st);
+    return launch_quantize_any<float>(a, normalize != 0, dev, st);
 }
 
 maxsim_status maxsim_linear_int8(const int8_t* x, int64_t ld_x, const float* x_scale, const int8_t* w, int64_t ld_w,

@@ -119,14 +119,14 @@ __device__ __forceinline__ bool row_step(uint32_t bits, float* s) {
     return finite;
 }
 
-// The codes of one chunk, packed in w, and its sum of squares of x / s.
+// The codes of one chunk, packed in w, and with kNorm its sum of squares of x / s.
 // rint(x / s) wants an IEEE division per element. x * inv, inv = 1 / s, is at
 // most 1.2e-5 away from the rounded quotient (|x / s| <= 127: 2^-24 relative
 // from inv, half a unit of the last place from the division), so only
 // products within 3e-5 of a half-integer can round to another code, and only
 // chunks that hold such a product divide. The product is rounded to an integer
 // by adding 1.5 * 2^23 in the same fma; the sum's low byte is the code.
-template <typename T, bool kWide>
+template <typename T, bool kWide, bool kNorm>
 __device__ __forceinline__ float code_chunk(const Chunk<T, kWide>& c, float s, float inv, uint32_t keep, uint32_t* w) {
     constexpr float kMagic = 12582912.f;
     constexpr int kVec = Chunk<T, kWide>::kVec;
@@ -138,8 +138,10 @@ __device__ __forceinline__ float code_chunk(const Chunk<T, kWide>& c, float s, f
         const float r = __fmaf_rn(x, inv, kMagic);
         off = fmaxf(off, fabsf(__fmaf_rn(x, inv, -(r - kMagic))));
         m[i] = __float_as_uint(r);
-        const float y = x * inv;
-        sum = __fmaf_rn(y, y, sum);
+        if constexpr (kNorm) {
+            const float y = x * inv;
+            sum = __fmaf_rn(y, y, sum);
+        }
     }
     if (off > 0.49997f) {
 #pragma unroll
@@ -157,9 +159,10 @@ __device__ __forceinline__ float code_chunk(const Chunk<T, kWide>& c, float s, f
     return sum;
 }
 
-__device__ __forceinline__ float row_scale(bool finite, int normalize, float s, float sum) {
+template <bool kNorm>
+__device__ __forceinline__ float row_scale(bool finite, float s, float sum) {
     float out = s;
-    if (normalize) out = sum > 0.f ? __fdiv_rn(1.f, __fsqrt_rn(sum)) : FLT_MIN;
+    if constexpr (kNorm) out = sum > 0.f ? rsqrtf(sum) : FLT_MIN;
     return finite ? out : __uint_as_float(0x7fffffffu);
 }
 
@@ -200,12 +203,11 @@ struct QuantizeArgs {
     float* scale;
     int64_t rows, ld_x, ld_q;
     int32_t cols;
-    int normalize;
 };
 
 __host__ __device__ constexpr int quantize_threads(int group) { return group > 128 ? group : 128; }
 
-template <typename T, bool kWide, int kGroup, int kChunks>
+template <typename T, bool kWide, bool kNorm, int kGroup, int kChunks>
 __global__ void __launch_bounds__(quantize_threads(kGroup)) quantize_rows_kernel(const QuantizeArgs a) {
     using C = Chunk<T, kWide>;
     constexpr int kThreads = quantize_threads(kGroup), kPerBlock = kThreads / kGroup;
@@ -237,18 +239,17 @@ __global__ void __launch_bounds__(quantize_threads(kGroup)) quantize_rows_kernel
         for (int j = 0; j < kChunks; ++j) {
             const int32_t col = (j * kGroup + t) * C::kVec;
             uint32_t w[2];
-            const float part = code_chunk<T, kWide>(c[j], s, inv, finite ? 0xffffffffu : 0u, w);
-            sum += part;
+            sum += code_chunk<T, kWide, kNorm>(c[j], s, inv, finite ? 0xffffffffu : 0u, w);
             if (real && col < a.cols) C::store(a.q + r * a.ld_q + col, w);
         }
-        if (a.normalize) sum = group_sum<kGroup>(sum, s_sum);
-        if (real && t == 0) a.scale[r] = row_scale(finite, a.normalize, s, sum);
+        if constexpr (kNorm) sum = group_sum<kGroup>(sum, s_sum);
+        if (real && t == 0) a.scale[r] = row_scale<kNorm>(finite, s, sum);
         if constexpr (kGroup > 32) __syncthreads();  // the slots are free again
     }
 }
 
 // Rows too long for the registers of a block: read once for the maximum, once for the codes.
-template <typename T, bool kWide>
+template <typename T, bool kWide, bool kNorm>
 __global__ void __launch_bounds__(512) quantize_long_rows_kernel(const QuantizeArgs a) {
     using C = Chunk<T, kWide>;
     __shared__ uint32_t s_max[16];
@@ -272,11 +273,11 @@ __global__ void __launch_bounds__(512) quantize_long_rows_kernel(const QuantizeA
             C c;
             c.load(xr + col);
             uint32_t w[2];
-            sum += code_chunk<T, kWide>(c, s, inv, finite ? 0xffffffffu : 0u, w);
+            sum += code_chunk<T, kWide, kNorm>(c, s, inv, finite ? 0xffffffffu : 0u, w);
             C::store(a.q + r * a.ld_q + col, w);
         }
-        if (a.normalize) sum = group_sum<512>(sum, s_sum);
-        if (threadIdx.x == 0) a.scale[r] = row_scale(finite, a.normalize, s, sum);
+        if constexpr (kNorm) sum = group_sum<512>(sum, s_sum);
+        if (threadIdx.x == 0) a.scale[r] = row_scale<kNorm>(finite, s, sum);
         __syncthreads();
     }
 }
