@@ -165,6 +165,7 @@ inline bool few_kernel(int64_t M, int64_t N, int64_t K, bool whole) {
 struct LinearPlan {
     bool few = false;
     bool swap = false;   // A is w, B is x
+    bool keep_b = false; // B stays in shared memory
     int tn = 256;
     int64_t tiles = 0, tiles_b = 0;
     int32_t kb = 0, slices = 1, kb_slice = 0;
@@ -214,6 +215,9 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool x_direct, bool w_di
             }
         }
     }
+    // a single tile of B for several tiles of A on every pair
+    p.keep_b = !p.swap && p.slices == 1 && p.tiles_b == 1 && p.tiles > kPairs &&
+               ((p.tn == 128 && p.kb <= TileCfg<128, true>::kStagesB) || (p.tn == 64 && p.kb <= TileCfg<64, true>::kStagesB));
     if (p.slices > 1) {
         p.off_partial = off;
         off = bytes_round_up(off + static_cast<size_t>(p.slices) * M * N * 4, 256);
@@ -270,11 +274,11 @@ maxsim_status launch_few(const LinearArgs& a, bool whole, cudaStream_t st) {
     return launched();
 }
 
-template <typename T, int kTN, bool kSwap>
+template <typename T, int kTN, bool kSwap, bool kKeepB>
 maxsim_status launch_tile(const LinearPlan& p, const LinearArgs& l, const __half* b16, bool a_prepared, int32_t* partial,
                           const HostDevice& dev, cudaStream_t st) {
-    auto kern = linear_tile_kernel<T, kTN, kSwap>;
-    constexpr size_t kSmem = tile_smem_bytes<kTN>();
+    auto kern = linear_tile_kernel<T, kTN, kSwap, kKeepB>;
+    constexpr size_t kSmem = tile_smem_bytes<kTN, kKeepB>();
     static_assert(kSmem <= 232448, "shared memory of one SM");
     static std::atomic<uint64_t> prepared{0};  // devices whose shared-memory limit is raised
     const uint64_t bit = uint64_t(1) << dev.index;
@@ -306,7 +310,7 @@ maxsim_status launch_tile(const LinearPlan& p, const LinearArgs& l, const __half
     if (!encode_k_rows(dev.encode, &ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, kSwap ? l.w : l.x, l.K, a.rows_a,
                        kSwap ? l.ld_w : l.ld_x, 128) ||
         !encode_k_rows(dev.encode, &tb, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, b16, p.k_pad, a.rows_b, p.k_pad * 2,
-                       TileCfg<kTN>::kBRows))
+                       TileCfg<kTN, kKeepB>::kBRows))
         return MAXSIM_ERR_CUDA;
     return launch_after(kern, static_cast<unsigned>(2 * std::min<int64_t>(a.items, std::max(1, dev.num_sms / 2))), kTileThreads,
                         kSmem, 2, st, ta, tb, a);
@@ -315,9 +319,13 @@ maxsim_status launch_tile(const LinearPlan& p, const LinearArgs& l, const __half
 template <typename T, bool kSwap>
 maxsim_status launch_tile_width(const LinearPlan& p, const LinearArgs& l, const __half* b16, bool a_prepared, int32_t* partial,
                                 const HostDevice& dev, cudaStream_t st) {
-    if (p.tn == 256) return launch_tile<T, 256, kSwap>(p, l, b16, a_prepared, partial, dev, st);
-    if (p.tn == 128) return launch_tile<T, 128, kSwap>(p, l, b16, a_prepared, partial, dev, st);
-    return launch_tile<T, 64, kSwap>(p, l, b16, a_prepared, partial, dev, st);
+    if constexpr (!kSwap) {
+        if (p.keep_b && p.tn == 128) return launch_tile<T, 128, false, true>(p, l, b16, a_prepared, partial, dev, st);
+        if (p.keep_b) return launch_tile<T, 64, false, true>(p, l, b16, a_prepared, partial, dev, st);
+    }
+    if (p.tn == 256) return launch_tile<T, 256, kSwap, false>(p, l, b16, a_prepared, partial, dev, st);
+    if (p.tn == 128) return launch_tile<T, 128, kSwap, false>(p, l, b16, a_prepared, partial, dev, st);
+    return launch_tile<T, 64, kSwap, false>(p, l, b16, a_prepared, partial, dev, st);
 }
 
 template <typename T>

@@ -226,7 +226,8 @@ constexpr int kTileStage = 4096;       // staging of an epilogue warp: 32 x 32 s
 constexpr uint32_t kTileACol = 256;    // tensor memory: accumulators in columns 0-255, the ring's A blocks above
 constexpr int kTileStatusTimeout = 4;  // MAXSIM_ERR_TIMEOUT
 
-template <int kTN>
+// kKeepB: B is one tile of rows for all tiles of A, and its blocks stay in shared memory.
+template <int kTN, bool kKeepB>
 struct TileCfg {
     static constexpr int kA8 = 128 * kTileK;           // 8-bit block of A: this CTA's 128 rows
     static constexpr int kBRows = kTN / 2;             // rows of B per CTA
@@ -234,7 +235,8 @@ struct TileCfg {
     static constexpr int kB16 = 2 * kBAtom;
     // even: each widening warpgroup then always meets the same stages, and
     // sees every phase of their barriers
-    static constexpr int kStages8 = kTN == 256 ? 4 : 8;
+    static constexpr int kStages8 = kTN == 256 || kKeepB ? 4 : 8;
+    static constexpr int kStagesB = !kKeepB ? kTileRing : kTN == 128 ? 8 : 16;  // kKeepB: the most blocks of K
     static constexpr int kAcc = kTN == 256 ? 1 : 2;    // accumulator buffers
 };
 
@@ -263,10 +265,10 @@ struct alignas(16) TileCtl {
     volatile int32_t abort;
 };
 
-template <int kTN>
+template <int kTN, bool kKeepB>
 constexpr size_t tile_smem_bytes() {
-    using C = TileCfg<kTN>;
-    return 1024 + static_cast<size_t>(C::kStages8) * C::kA8 + kTileRing * C::kB16 + 8 * kTileStage + sizeof(TileCtl);
+    using C = TileCfg<kTN, kKeepB>;
+    return 1024 + static_cast<size_t>(C::kStages8) * C::kA8 + C::kStagesB * C::kB16 + 8 * kTileStage + sizeof(TileCtl);
 }
 
 // Bounded wait of a thread: gives up after the limit (recorded in the device
@@ -390,17 +392,21 @@ __device__ __forceinline__ void store4(T* p, int n, bool vec, float a, float b, 
 // written by TMA (observed on b_full), so these arrivals on the even CTA's
 // barriers release at CTA scope. A cluster-scope release took a warp 800 to
 // 2,000 cycles per block (32768 x 4096 x 4096: 751 us, and 609 us without).
+// Narrow tiles are bound by what the SMs read from L2 (16384 x 128 x 4096: a
+// block of A and of B in 650 cycles, 11 TB/s over all SMs, whatever the MMAs and
+// the widening took). Where B is a single tile of rows and fits, as a head's
+// weights do, it is loaded once and kept (kKeepB).
 // A tile's K may be cut into slices (few tiles, long K): each slice then
 // writes its integer sums, and linear_join_kernel adds them.
-template <typename T, int kTN, bool kSwap>
+template <typename T, int kTN, bool kSwap, bool kKeepB>
 __global__ void __launch_bounds__(kTileThreads, 1)
 linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const TileArgs a) {
-    using C = TileCfg<kTN>;
+    using C = TileCfg<kTN, kKeepB>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t* s8 = smem;
     uint8_t* s16 = smem + C::kStages8 * C::kA8;
-    uint8_t* s_out = s16 + kTileRing * C::kB16;
+    uint8_t* s_out = s16 + C::kStagesB * C::kB16;
     TileCtl* ctl = reinterpret_cast<TileCtl*>(s_out + 8 * kTileStage);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -411,9 +417,10 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
             mbar_init(smem_u32(&ctl->empty8[s]), 4);
         }
         for (int r = 0; r < kTileRing; ++r) {
-            mbar_init(smem_u32(&ctl->b_full[r]), 1);
+            // its own TMA; kKeepB, even CTA: and the odd CTA's report
+            mbar_init(smem_u32(&ctl->b_full[r]), kKeepB && rank == 0 ? 2 : 1);
             // even CTA: four widening warps of each CTA, its own TMA of B, the odd CTA's report of B
-            mbar_init(smem_u32(&ctl->ready[r]), 10);
+            mbar_init(smem_u32(&ctl->ready[r]), kKeepB ? 8 : 10);
             mbar_init(smem_u32(&ctl->freed[r]), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -447,13 +454,24 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
             if (!is_a || a.a_prepared) wait_for_previous();
             const int depth = is_a ? C::kStages8 : kTileRing;
             // the even CTA's B lands on the barrier that its MMA warp waits for
-            uint64_t* full = is_a ? ctl->full8 : rank == 0 ? ctl->ready : ctl->b_full;
+            uint64_t* full = is_a ? ctl->full8 : rank == 0 && !kKeepB ? ctl->ready : ctl->b_full;
             uint64_t* empty = is_a ? ctl->empty8 : ctl->freed;
             int32_t stage = 0;
             uint32_t phase = 0;
             int64_t issued = 0;
             bool ok = true;
-            for (int64_t it = first; it < a.items && ok; it += step) {
+            if (kKeepB && !is_a && first < a.items) {  // every block once
+                const uint32_t bar = smem_u32(&ctl->b_full[0]);
+                mbar_arrive_expect_tx(bar, static_cast<uint32_t>(a.kb * C::kB16));
+                for (int32_t kb = 0; kb < a.kb; ++kb) {
+                    const uint32_t dst = smem_u32(s16 + kb * C::kB16);
+                    tma_load_2d(dst, &tm_b, bar, kb * kTileK, static_cast<int32_t>(rank) * C::kBRows);
+                    tma_load_2d(dst + C::kBAtom, &tm_b, bar, kb * kTileK + 64, static_cast<int32_t>(rank) * C::kBRows);
+                }
+                ++issued;
+                stage = 1;
+            }
+            for (int64_t it = first; it < a.items && ok && (is_a || !kKeepB); it += step) {
                 const TileItem t = tile_item<kTN>(a, it, rank);
                 for (int32_t kb = t.kb0; kb < t.kb1; ++kb) {
                     if (!tile_wait(a, ctl, &empty[stage], phase ^ 1u)) { ok = false; break; }
@@ -491,6 +509,7 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
             const uint64_t b0 = sdesc_k_sw128(smem_u32(s16));
             int32_t buf = 0;
             uint32_t buf_phase = 0;
+            if (kKeepB && first < a.items) ok = tile_wait_warp<true>(a, ctl, &ctl->b_full[0], 0);
             for (int64_t it = first; it < a.items && ok; it += step) {
                 const TileItem t = tile_item<kTN>(a, it, rank);
                 if (!tile_wait_warp<true>(a, ctl, &ctl->acc_empty[buf], buf_phase ^ 1u)) break;
@@ -500,7 +519,7 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                     if (!tile_wait_warp<true>(a, ctl, &ctl->ready[ring], ring_phase)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t at = tmem + kTileACol + static_cast<uint32_t>(ring * 64);
-                    const uint64_t b = b0 + static_cast<uint64_t>((ring * C::kB16) >> 4);
+                    const uint64_t b = b0 + static_cast<uint64_t>(((kKeepB ? kb : ring) * C::kB16) >> 4);
                     mma_chain4_ts(d, at, b, idesc, kb > t.kb0 ? 1u : 0u);
                     mma_chain4_ts(d, at + 32, b + (C::kBAtom >> 4), idesc, 1u);
                     mma_commit_elect<2>(smem_u32(&ctl->freed[ring]));
@@ -519,7 +538,9 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
             __syncwarp();
         } else {
             // ------------------------------------------------------------ odd CTA: reports its half of B
-            for (int64_t it = first; it < a.items && ok; it += step) {
+            if (kKeepB && first < a.items && tile_wait_warp(a, ctl, &ctl->b_full[0], 0) && lane == 0)
+                mbar_arrive_remote(map_shared_rank(smem_u32(&ctl->b_full[0]), 0));
+            for (int64_t it = first; it < a.items && ok && !kKeepB; it += step) {
                 const TileItem t = tile_item<kTN>(a, it, rank);
                 for (int32_t kb = t.kb0; kb < t.kb1; ++kb) {
                     if (!tile_wait_warp(a, ctl, &ctl->b_full[ring], ring_phase)) { ok = false; break; }

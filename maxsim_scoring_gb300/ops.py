@@ -473,34 +473,36 @@ def linear_int8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale
     dt = _DT_ANY.get(out_dtype)
     if dt is None:
         raise TypeError(f"out_dtype must be float16, bfloat16 or float32, got {out_dtype}")
-    if x.dtype != torch.int8 or w.dtype != torch.int8:
+    if x.dtype is not torch.int8 or w.dtype is not torch.int8:
         raise TypeError("x and w must be int8")
-    if x_scale.dtype != torch.float32 or w_scale.dtype != torch.float32 or (
-            bias is not None and bias.dtype != torch.float32):
+    if x_scale.dtype is not torch.float32 or w_scale.dtype is not torch.float32:
         raise TypeError("x_scale, w_scale and bias must be float32")
     shape, dev = x.shape, x.device
+    lead, channels, index = shape[:-1], w.shape[:1], dev.index
     x, M, K, ld_x = _rows(x, "x")
     w, N, Kw, ld_w = _rows(w, "w")
     if w.dim() != 2 or Kw != K:
         raise ValueError("w must be [N, K] with x's K")
-    lead = shape[:-1]
-    if x_scale.shape != lead or w_scale.shape != (N,) or (bias is not None and bias.shape != (N,)):
+    if x_scale.shape != lead or w_scale.shape != channels:
         raise ValueError("x_scale must have x's leading shape, w_scale and bias [N]")
-    index = dev.index
-    if w.get_device() != index or x_scale.get_device() != index or w_scale.get_device() != index or (
-            bias is not None and bias.get_device() != index):
+    if w.get_device() != index or x_scale.get_device() != index or w_scale.get_device() != index:
         raise ValueError("x, w, their scales and bias must be on one device")
     if not x_scale.is_contiguous():
         x_scale = x_scale.contiguous()
     if not w_scale.is_contiguous():
         w_scale = w_scale.contiguous()
-    if bias is None:
-        pb = None
-    else:
+    pb = None
+    if bias is not None:
+        if bias.dtype is not torch.float32:
+            raise TypeError("x_scale, w_scale and bias must be float32")
+        if bias.shape != channels:
+            raise ValueError("x_scale must have x's leading shape, w_scale and bias [N]")
+        if bias.get_device() != index:
+            raise ValueError("x, w, their scales and bias must be on one device")
         if not bias.is_contiguous():
             bias = bias.contiguous()
         pb = bias.data_ptr()
-    full = lead + (N,)
+    full = lead + channels
     out = torch.empty(full, dtype=out_dtype, device=dev) if out is None else _given(out, "out", full, out_dtype, dev)
     px, pw, lib = x.data_ptr(), w.data_ptr(), _native.lib()
     args = (px, ld_x, x_scale.data_ptr(), pw, ld_w, w_scale.data_ptr(), pb, M, N, K, dt, out.data_ptr(), N)

@@ -149,12 +149,30 @@ def test_linear_int8(M, N, K, dtype, bias):
     check_linear(codes(rng, M, K), codes(rng, N, K, low=-128), dtype, bias, rng)
 
 
+# several tiles for every pair of SMs: each width and orientation, weights kept in shared memory, K cut into slices
+@pytest.mark.parametrize("M,N,K,dtype", [
+    (20001, 128, 1024, "f16"), (19500, 100, 1008, "f32"), (30011, 64, 2048, "bf16"), (40000, 33, 176, "f32"),
+    (20000, 128, 1040, "bf16"), (6100, 2050, 272, "bf16"), (6000, 2001, 144, "f32"), (1500, 8100, 128, "f16"),
+    (700, 16000, 80, "f32"), (5000, 700, 512, "f16"), (90, 20000, 96, "bf16"), (150, 300, 9000, "bf16"),
+    (300, 120, 8000, "f32"), (40, 1000, 16000, "f16"), (20003, 120, 333, "bf16")])
+def test_linear_int8_many_tiles(M, N, K, dtype):
+    rng = np.random.default_rng(M + N + K)
+    check_linear(codes(rng, M, K), codes(rng, N, K), dtype, True, rng)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 5, 3), (7, 40, 33), (40, 130, 1111), (64, 31, 97), (70, 50, 1), (129, 300, 515),
                                    (600, 200, 77)])
 @pytest.mark.parametrize("pad,shift", [(0, 0), (5, 0), (16, 3), (0, 16)])
 def test_linear_int8_odd_rows(M, N, K, pad, shift):
     rng = np.random.default_rng(M + N + K + pad + shift)
     check_linear(codes(rng, M, K, pad, shift), codes(rng, N, K, 0, shift), "f16", True, rng)
+
+
+@pytest.mark.parametrize("M,N,K", [(3000, 200, 301), (200, 3000, 301), (5000, 600, 257), (600, 5000, 250), (20000, 70, 99)])
+@pytest.mark.parametrize("pad,shift", [(0, 0), (5, 1), (16, 3), (0, 16)])
+def test_linear_int8_odd_rows_of_large_products(M, N, K, pad, shift):
+    rng = np.random.default_rng(M + N + K + pad + shift)
+    check_linear(codes(rng, M, K, pad, shift), codes(rng, N, K, 0, shift), "bf16", True, rng)
 
 
 def test_linear_int8_extreme_sums():
@@ -169,6 +187,15 @@ def test_linear_int8_extreme_sums():
             check_linear(x, w, "f32", False, rng)
 
 
+@pytest.mark.parametrize("M,N,K", [(20, 100, 16384), (700, 300, 16384), (300, 1500, 6000), (2500, 600, 3000)])
+def test_linear_int8_one_signed_sums(M, N, K):
+    # sums that grow past 2^24 and stay there: the fp32 accumulator rounds, within its bound
+    rng = np.random.default_rng(M)
+    x = torch.from_numpy(rng.integers(90, 128, size=(M, K)).astype(np.int8)).cuda()
+    w = torch.from_numpy(rng.integers(90, 128, size=(N, K)).astype(np.int8)).cuda()
+    check_linear(x, w, "f32", False, rng)
+
+
 def test_linear_int8_longest_sum():
     K = 131071                                                     # the largest K, for both kernels
     rng = np.random.default_rng(5)
@@ -181,12 +208,12 @@ def test_linear_int8_longest_sum():
 
 def test_linear_int8_nonfinite_scales_stay_in_their_rows():
     rng = np.random.default_rng(6)
-    for M in (6, 200):
-        x, w = codes(rng, M, 256), codes(rng, 96, 256)
+    for M, N in ((6, 96), (200, 96), (8000, 96), (20000, 96), (300, 9000), (4000, 1000)):
+        x, w = codes(rng, M, 256), codes(rng, N, 256)
         xs = rng.uniform(0.01, 0.05, M).astype(np.float32)
         xs[2], xs[4], xs[5] = np.nan, np.inf, 0.0
         x[2] = 0
-        ws = rng.uniform(0.001, 0.002, 96).astype(np.float32)
+        ws = rng.uniform(0.001, 0.002, N).astype(np.float32)
         got = f64(ms.linear_int8(x, torch.from_numpy(xs).cuda(), w, torch.from_numpy(ws).cuda(), out_dtype=torch.float32))
         assert np.isnan(got[2]).all() and (got[5] == 0).all()
         fine = [r for r in range(M) if r not in (2, 4)]
@@ -213,8 +240,11 @@ def test_linear_int8_empty():
 def test_linear_int8_rows_of_a_wider_output():
     rng = np.random.default_rng(8)
     lib = _native.lib()
-    for M in (3, 150):
-        for N, ld, off in ((70, 77, 3), (64, 96, 0), (300, 301, 1)):
+    for M, shapes in ((3, ((70, 77, 3), (64, 96, 0), (300, 301, 1))), (150, ((70, 77, 3), (64, 96, 0), (300, 301, 1))),
+                      (9000, ((300, 301, 1), (304, 312, 0))), (300, ((9000, 9001, 3), (9000, 9008, 0))),
+                      (20000, ((70, 77, 3), (128, 136, 0), (50, 56, 8))), (2000, ((4100, 4101, 0),)),
+                      (4100, ((2000, 2008, 0), (1999, 2000, 8)))):
+        for N, ld, off in shapes:
             x, w = codes(rng, M, 128), codes(rng, N, 128)
             xs, ws = torch.rand(M, device="cuda"), torch.rand(N, device="cuda")
             for name, dt in DT.items():
@@ -232,7 +262,8 @@ def test_linear_int8_rows_of_a_wider_output():
 
 def test_linear_int8_repeats_and_other_streams():
     rng = np.random.default_rng(9)
-    for M, N, K in ((5, 300, 2048), (48, 1000, 1000), (300, 500, 4096), (129, 140, 1111)):
+    for M, N, K in ((5, 300, 2048), (48, 1000, 1000), (300, 500, 4096), (129, 140, 1111), (20000, 128, 512),
+                    (500, 9000, 256), (5000, 2000, 272)):
         x, w = codes(rng, M, K), codes(rng, N, K)
         xs, ws = torch.rand(M, device="cuda"), torch.rand(N, device="cuda")
         first = ms.linear_int8(x, xs, w, ws)
