@@ -149,17 +149,21 @@ constexpr uint64_t kTimeoutNs = 2000000000ull;
 inline bool rows_direct(int64_t K, int64_t ld) { return K % 16 == 0 && ld % 16 == 0 && ld < (int64_t(1) << 40); }
 
 // linear_few_kernel or the tile kernel. The former takes any product in one
-// launch, but reads w once per 32 tokens. In units of 16 channels x 32 tokens x
-// 64 of K (measured, few / tile): 32 x 4096 x 4096, 16,384 units: 9.6 / 9.9 us;
-// more tokens: 128 x 1024 x 1024, 4,096 units: 6.8 / 8.2, 128 x 2048 x 1024,
-// 8,192 units: 12.3 / 8.2. Rows off their 16-byte boundaries take more instructions.
-constexpr int64_t kFewTokens = 32, kFewUnits = 16384;
+// launch, but reads w once per 32 tokens; a block of it is 16 channels x 32
+// tokens. Measured, few / tile, in us: 16 x 16384 x 16384 52 / 55, 8 x 8192 x 8191
+// 34 / 45; beyond that by units of a block x 64 of K, and blocks: 32 x 4096 x 4096
+// (16,384 units, 256 blocks) 8.3 / 10.1, 128 x 2048 x 2048 (16,384, 512) 8.7 / 10.5,
+// 256 x 2048 x 1024 (16,384, 1,024) 9.8 / 8.0, 1024 x 1024 x 512 (16,384, 2,048)
+// 12.9 / 7.5, 32 x 16384 x 4096 (65,536, 1,024) 24 / 18. Rows off their 16-byte
+// boundaries cost about three times as much: 128 x 1024 x 1023 7.9 / 8.4,
+// 3000 x 200 x 301 12.6 / 7.8. The tile kernel's second launch is a further 3 us
+// of the caller's time.
+constexpr int64_t kFewCost = 20480;
 inline bool few_kernel(int64_t M, int64_t N, int64_t K, bool whole) {
-    if (M <= kFewTokens && whole) return true;
+    if (M <= 8 || (M <= 16 && whole)) return true;
     const int64_t groups = (M + 31) / 32, tiles = (N + 15) / 16, chunks = (K + 63) / 64;
-    const int64_t weight = (M <= kFewTokens ? 1 : 4) * (whole || M <= 8 ? 1 : 2);
-    return groups <= kFewUnits && tiles <= kFewUnits && groups * tiles <= kFewUnits &&
-           groups * tiles * chunks * weight <= kFewUnits;
+    if (groups > kFewCost || tiles > kFewCost) return false;
+    return groups * tiles * (chunks * (whole ? 1 : 3) + 4) <= kFewCost;
 }
 
 struct LinearPlan {
@@ -266,7 +270,15 @@ maxsim_status launch_after(void (*kern)(Params...), unsigned grid, unsigned thre
 template <typename T, int kTiles>
 maxsim_status launch_few(const LinearArgs& a, bool whole, cudaStream_t st) {
     const int64_t chunks = (static_cast<int64_t>(a.K) + 63) / 64;
-    const unsigned threads = 32u * static_cast<unsigned>(std::min<int64_t>(kFewWarps, std::max<int64_t>(chunks, 1)));
+    const int64_t blocks = (static_cast<int64_t>(a.N) + 15) / 16 * ((static_cast<int64_t>(a.M) + 8 * kTiles - 1) / (8 * kTiles));
+    int64_t warps = std::min<int64_t>(kFewWarps, std::max<int64_t>(chunks, 1));
+    // Fewer warps with longer runs of K once there are enough blocks: a block
+    // starts and joins its warps' sums once. Measured with at most 4,096 and
+    // 2,048 warps in all: 1 x 4096 x 16384 14.4 and 18.3 us, but
+    // 32 x 4096 x 4096 10.2 and 8.3 us (more registers a warp).
+    const int64_t most_warps = kTiles == 1 ? 4096 : 2048;
+    while (warps > 4 && blocks * warps > most_warps) warps = (warps + 1) / 2;
+    const unsigned threads = 32u * static_cast<unsigned>(warps);
     const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.N) + 15) / 16),
                     static_cast<unsigned>((static_cast<int64_t>(a.M) + 8 * kTiles - 1) / (8 * kTiles)));
     if (whole) linear_few_kernel<T, kTiles, true><<<grid, threads, 0, st>>>(a);

@@ -134,16 +134,17 @@ __device__ __forceinline__ uint4 load16(const int8_t* row, int32_t k, int32_t K,
 }
 
 // A block owns 16 channels and up to 8 * kTiles tokens (blockIdx.y); its warps
-// take 64-wide chunks of K in turn. A lane reads 16 consecutive bytes of two
+// take runs of 64-wide chunks of K. A lane reads 16 consecutive bytes of two
 // channels (w is the MMA's 16-row operand) and of one token of each 8-token
 // tile: lane t of a row then holds k = 16 t .. 16 t + 15 instead of the
 // fragment's own columns, in both operands alike, so the sum over k is the
-// same and every load is 16 bytes wide. After 16 chunks of a warp (1,024
+// same and every load is 16 bytes wide; the loads of the next chunks are in
+// flight while one is widened. After 16 chunks of a warp (1,024
 // products, exact in fp32) the sums move to 32-bit integers, and the warps'
 // sums are added as integers in shared memory: exact, in any order.
 template <typename T, int kTiles, bool kWhole>
 __global__ void __launch_bounds__(kFewWarps * 32) linear_few_kernel(const LinearArgs a) {
-    constexpr int kAhead = !kWhole ? 1 : kTiles <= 2 ? 4 : 2;  // chunks whose loads are in flight
+    constexpr int kAhead = !kWhole ? 1 : kTiles == 2 ? 4 : 2;  // chunks whose loads are in flight
     __shared__ int s_sum[16][8 * kTiles + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     const int g = lane >> 2, t = lane & 3;
@@ -158,40 +159,47 @@ __global__ void __launch_bounds__(kFewWarps * 32) linear_few_kernel(const Linear
     for (int j = 0; j < kTiles; ++j) xr[j] = a.x + min(m0 + 8 * j + g, static_cast<int64_t>(a.M) - 1) * a.ld_x;
     const int8_t* x_end = a.x + (static_cast<int64_t>(a.M) - 1) * a.ld_x + a.K;
     const int8_t* w_end = a.w + (static_cast<int64_t>(a.N) - 1) * a.ld_w + a.K;
-    const int32_t chunks = (a.K + 63) >> 6;
+    // this warp's run of chunks, and where its values end
+    const int32_t chunks = (a.K + 63) >> 6, run = (chunks + warps - 1) / warps;
+    const int32_t c0 = warp * run, c1 = min(chunks, c0 + run), k_end = min(a.K, c1 << 6);
+    uint4 wv[kAhead][2], xv[kAhead][kTiles];
+    auto load = [&](int slot, int32_t chunk) {
+        const int32_t k = (chunk << 6) + 16 * t;
+        wv[slot][0] = load16<kWhole>(w0, k, k_end, a.w, w_end);
+        wv[slot][1] = load16<kWhole>(w1, k, k_end, a.w, w_end);
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) xv[slot][j] = load16<kWhole>(xr[j], k, k_end, a.x, x_end);
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load(i, c0 + i);
     int sum[kTiles][4] = {};
-    for (int32_t c0 = warp; c0 < chunks; c0 += 16 * warps) {
-        float acc[kTiles][4] = {};
+    float acc[kTiles][4] = {};
 #pragma unroll 1
-        for (int i0 = 0; i0 < 16 && c0 + i0 * warps < chunks; i0 += kAhead) {
-            uint4 wv[kAhead][2], xv[kAhead][kTiles];
+    for (int32_t c = c0; c < c1; c += kAhead) {
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const int32_t k = ((c0 + (i0 + i) * warps) << 6) + 16 * t;
-                wv[i][0] = load16<kWhole>(w0, k, a.K, a.w, w_end);
-                wv[i][1] = load16<kWhole>(w1, k, a.K, a.w, w_end);
+        for (int i = 0; i < kAhead; ++i) {
+            uint32_t wa[8], wb[8];
+            widen16(wv[i][0], wa);
+            widen16(wv[i][1], wb);
 #pragma unroll
-                for (int j = 0; j < kTiles; ++j) xv[i][j] = load16<kWhole>(xr[j], k, a.K, a.x, x_end);
+            for (int j = 0; j < kTiles; ++j) {
+                uint32_t xb[8];
+                widen16(xv[i][j], xb);
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    mma_m16n8k16(acc[j], wa[2 * s], wb[2 * s], wa[2 * s + 1], wb[2 * s + 1], xb[2 * s], xb[2 * s + 1]);
             }
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                uint32_t wa[8], wb[8];
-                widen16(wv[i][0], wa);
-                widen16(wv[i][1], wb);
-#pragma unroll
-                for (int j = 0; j < kTiles; ++j) {
-                    uint32_t xb[8];
-                    widen16(xv[i][j], xb);
-#pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        mma_m16n8k16(acc[j], wa[2 * s], wb[2 * s], wa[2 * s + 1], wb[2 * s + 1], xb[2 * s], xb[2 * s + 1]);
-                }
-            }
+            load(i, c + i + kAhead);
         }
+        if (((c - c0 + kAhead) & 15) == 0 || c + kAhead >= c1) {
 #pragma unroll
-        for (int j = 0; j < kTiles; ++j)
+            for (int j = 0; j < kTiles; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sum[j][e] += __float2int_rn(acc[j][e]);
+                for (int e = 0; e < 4; ++e) {
+                    sum[j][e] += __float2int_rn(acc[j][e]);
+                    acc[j][e] = 0.f;
+                }
+        }
     }
 #pragma unroll
     for (int j = 0; j < kTiles; ++j)
