@@ -399,8 +399,8 @@ enum { kXFlat = 0, kXRows = 1, kXGather = 2 };
 //  kXGather: residual and y are runs; x's rows lie apart or off their
 //          boundaries (cols >= 8), and its elements are loaded one by one;
 //          fast_div divides by cols. (Paths of their own for whole pieces and for
-//          4-byte aligned ones left 1023 columns at 26 us and took 101 from 139
-//          to 174.)
+//          4-byte aligned ones left 16384 x 1023 at 26 us and took 1000000 x 101
+//          from 139 to 174; one piece a thread instead of two: 22 and 121.)
 // A warp takes 32 * kPieces neighbouring pieces at a time, so that several
 // loads of a thread are in flight and a warp's accesses stay close together
 // (262144 x 1024 f16 without residual: 183 us with a thread's two pieces a grid
@@ -410,7 +410,7 @@ enum { kXFlat = 0, kXRows = 1, kXGather = 2 };
 // the drawn halves as they lie in their words, and results are rounded two at
 // a time.
 template <typename T, int kX>
-__host__ __device__ constexpr int dropout_pieces() { return sizeof(T) == 2 && kX != kXGather ? 4 : 2; }
+__host__ __device__ constexpr int dropout_pieces() { return kX == kXGather ? 1 : sizeof(T) == 2 ? 4 : 2; }
 
 template <typename T, int kX, bool kRes>
 __global__ void __launch_bounds__(256) dropout_wide_kernel(const DropoutArgs a) {
