@@ -376,13 +376,15 @@ maxsim_status maxsim_quantize_rows(const void *x, maxsim_dtype dtype, int64_t ro
  *   x [M, K] i8, rows ld_x apart;  x_scale [M] f32
  *   w [N, K] i8, rows ld_w apart;  w_scale [N] f32;  bias [N] f32 or NULL
  *   out [M, N] f16 / bf16 / f32 (out_dtype), rows ld_out elements apart
- * All of [-128, 127] is taken. Up to 32 tokens the sum is an exact 32-bit
- * integer; beyond, the tensor cores sum exact products in fp32 (exact while
- * the partial sums stay below 2^24). K = 0 gives the bias. Scales and bias need
- * 4-byte alignment. 0 <= M, N < 2^31 - 1023, K <= 131071.
- * An operand whose pointer, row stride or K is not a multiple of 16 is copied
- * into the workspace first. Workspace: maxsim_workspace_size(
- * MAXSIM_OP_LINEAR_INT8, M, N, K, ld_x, ld_w), with 1 in the place of the
+ * All of [-128, 127] is taken. Few tokens and small products are summed
+ * exactly in 32-bit integers; larger ones by the tensor cores in fp32, where
+ * products are exact and sums are while they stay below 2^24 (always for
+ * K <= 1024). The same call on the same inputs gives the same bits. K = 0 gives
+ * the bias. Scales and bias need 4-byte alignment. 0 <= M, N < 2^31 - 1023,
+ * K <= 131071.
+ * Operands may start anywhere; larger products copy one whose pointer, row
+ * stride or K is not a multiple of 16 into the workspace first. Workspace: maxsim_workspace_size(
+ * MAXSIM_OP_LINEAR_INT8, M, N, K, ld_x, ld_w), ld_w > 0, with 1 in the place of the
  * stride of an operand whose pointer is not 16-byte aligned; 256-byte aligned.
  */
 maxsim_status maxsim_linear_int8(const int8_t *x, int64_t ld_x, const float *x_scale, const int8_t *w, int64_t ld_w,

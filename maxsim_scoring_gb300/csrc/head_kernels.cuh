@@ -31,12 +31,16 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 
 // ---------------------------------------------------------------- row quantisation
 //
-// The scale, a 127th of max |x|, needs the whole row before the first code, so a row
-// is held in registers between the two: one read of x, one write of q. A row
-// belongs to a group of 8, 32, 128 or 512 threads, each holding up to
-// kChunks 16-byte chunks (or kChunks single elements where the rows do not
-// start on 16-byte boundaries); only rows beyond 512 x 8 chunks are read
-// twice. Bound by HBM.
+// The scale, a 127th of max |x|, needs the whole row before the first code, so a
+// row is held in registers between the two: one read of x, one write of q. A
+// row belongs to a group of 8, 32, 128 or 512 threads, each holding up to kChunks
+// 16-byte chunks (or single elements where the rows do not start on 16-byte
+// boundaries); only rows beyond that are read twice. Several short rows share a
+// warp: fewer shuffle steps for a row, and their loads are in flight together.
+// Bound by HBM: 5,000,000 x 128 f32 in 480 us (6.7 TB/s), 65536 x 4096 bf16 in
+// 121 us (6.6 TB/s); 16-bit rows of 128 with the norm in 220 us for 3,000,000 (5.3
+// TB/s, 70 % of the issue slots), odd widths by their single-element accesses
+// (100000 x 1023 bf16 in 106 us, 2.9 TB/s).
 
 // Maximum of two pairs of unsigned 16-bit values.
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
@@ -492,7 +496,8 @@ __global__ void __launch_bounds__(256) dropout_wide_kernel(const DropoutArgs a) 
 // 32nd element, so that loads and stores of single elements are coalesced.
 // kWidth = 256: rows are at least as long as the run, which then crosses at
 // most one row's end, and one division (fast_div by cols) places it; 0: any
-// width, a division per element. Bound by instruction issue.
+// width, a division per element. Bound by instruction issue (16384 x 1023 bf16
+// with a residual, all rows apart: 28 us, 3.6 TB/s).
 template <typename T, bool kRes, int kWidth>
 __global__ void __launch_bounds__(256) dropout_any_kernel(const DropoutArgs a) {
     __shared__ uint4 s_bits[8][32];
