@@ -420,21 +420,31 @@ _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_get
 
 
 def _rows(t: torch.Tensor, name: str):
-    """(tensor, rows, cols, row stride) of a CUDA tensor [..., cols] whose rows
-    the library can read in place; copied where its strides do not allow it."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() == 0:
-        raise ValueError(f"{name} must have at least one dimension")
-    cols = t.shape[-1]
-    if not t.is_contiguous():
+    """(tensor, rows, row stride) of a CUDA tensor [..., cols] whose rows the
+    library can read in place; copied where its strides do not allow it."""
+    shape = t.shape
+    if t.is_contiguous():
+        if len(shape) == 2:
+            return t, shape[0], shape[1]
+    else:
         # rows one fixed stride apart (a slice of a wider buffer) are read where they are
-        ld = t.stride(-2) if t.dim() > 1 else cols
+        cols = shape[-1]
+        ld = t.stride(-2) if len(shape) > 1 else cols
         if cols and t.stride(-1) == 1 and ld >= cols and all(
-                t.stride(i) == t.stride(i + 1) * t.shape[i + 1] for i in range(t.dim() - 2)):
-            return t, t.numel() // cols, cols, ld
+                t.stride(i) == t.stride(i + 1) * shape[i + 1] for i in range(len(shape) - 2)):
+            return t, t.numel() // cols, ld
         t = t.contiguous()
-    return t, (t.numel() // cols if cols else t.shape[:-1].numel()), cols, cols
+    if not shape:
+        raise ValueError(f"{name} must have at least one dimension")
+    cols = shape[-1]
+    return t, (t.numel() // cols if cols else shape[:-1].numel()), cols
+
+
+def _device(t: torch.Tensor, name: str) -> int:
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return index
 
 
 def _given(out: torch.Tensor, name: str, shape, dtype, device):
@@ -452,13 +462,14 @@ def quantize_rows(x: torch.Tensor, *, normalize: bool = False, q: Optional[torch
     dt = _DT_ANY.get(x.dtype)
     if dt is None:
         raise TypeError(f"x must be float16, bfloat16 or float32, got {x.dtype}")
-    shape, dev = x.shape, x.device
-    x, rows, cols, ld = _rows(x, "x")
+    index, shape, dev = _device(x, "x"), x.shape, x.device
+    x, rows, ld = _rows(x, "x")
+    cols = shape[-1]
     q = torch.empty(shape, dtype=torch.int8, device=dev) if q is None else _given(q, "q", shape, torch.int8, dev)
     scale = (torch.empty(shape[:-1], dtype=torch.float32, device=dev) if scale is None
              else _given(scale, "scale", shape[:-1], torch.float32, dev))
     rc = _native.lib().maxsim_quantize_rows(x.data_ptr(), dt, rows, cols, ld, 1 if normalize else 0, q.data_ptr(),
-                                            cols, scale.data_ptr(), _raw_stream(dev.index))
+                                            cols, scale.data_ptr(), _raw_stream(index))
     if rc:
         _native.check(rc, "maxsim_quantize_rows")
     return q, scale
@@ -477,16 +488,16 @@ def linear_int8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale
         raise TypeError("x and w must be int8")
     if x_scale.dtype is not torch.float32 or w_scale.dtype is not torch.float32:
         raise TypeError("x_scale, w_scale and bias must be float32")
-    shape, dev = x.shape, x.device
-    lead, channels, index = shape[:-1], w.shape[:1], dev.index
-    x, M, K, ld_x = _rows(x, "x")
-    w, N, Kw, ld_w = _rows(w, "w")
-    if w.dim() != 2 or Kw != K:
-        raise ValueError("w must be [N, K] with x's K")
-    if x_scale.shape != lead or w_scale.shape != channels:
-        raise ValueError("x_scale must have x's leading shape, w_scale and bias [N]")
+    index, shape, channels = _device(x, "x"), x.shape, w.shape
     if w.get_device() != index or x_scale.get_device() != index or w_scale.get_device() != index:
         raise ValueError("x, w, their scales and bias must be on one device")
+    if len(channels) != 2 or not shape or shape[-1] != channels[1]:
+        raise ValueError("w must be [N, K] with x's K")
+    lead, (N, K), channels = shape[:-1], channels, channels[:1]
+    if x_scale.shape != lead or w_scale.shape != channels:
+        raise ValueError("x_scale must have x's leading shape, w_scale and bias [N]")
+    x, M, ld_x = _rows(x, "x")
+    w, _, ld_w = _rows(w, "w")
     if not x_scale.is_contiguous():
         x_scale = x_scale.contiguous()
     if not w_scale.is_contiguous():
@@ -495,28 +506,28 @@ def linear_int8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale
     if bias is not None:
         if bias.dtype is not torch.float32:
             raise TypeError("x_scale, w_scale and bias must be float32")
-        if bias.shape != channels:
-            raise ValueError("x_scale must have x's leading shape, w_scale and bias [N]")
         if bias.get_device() != index:
             raise ValueError("x, w, their scales and bias must be on one device")
+        if bias.shape != channels:
+            raise ValueError("x_scale must have x's leading shape, w_scale and bias [N]")
         if not bias.is_contiguous():
             bias = bias.contiguous()
         pb = bias.data_ptr()
-    full = lead + channels
+    full, dev = lead + channels, x.device
     out = torch.empty(full, dtype=out_dtype, device=dev) if out is None else _given(out, "out", full, out_dtype, dev)
-    px, pw, lib = x.data_ptr(), w.data_ptr(), _native.lib()
-    args = (px, ld_x, x_scale.data_ptr(), pw, ld_w, w_scale.data_ptr(), pb, M, N, K, dt, out.data_ptr(), N)
-    stream = _raw_stream(index)
+    px, pw, lib, stream = x.data_ptr(), w.data_ptr(), _native.lib(), _raw_stream(index)
+    px_scale, pw_scale, p_out = x_scale.data_ptr(), w_scale.data_ptr(), out.data_ptr()
     # few tokens and small products need no workspace: its size is asked for once a call says that it is missing
-    rc = (lib.maxsim_linear_int8(*args, None, 0, stream) if M <= 32 or M * N * K <= 1 << 29
-          else _native.ERR_WORKSPACE)
+    rc = (lib.maxsim_linear_int8(px, ld_x, px_scale, pw, ld_w, pw_scale, pb, M, N, K, dt, p_out, N, None, 0, stream)
+          if M <= 32 or M * N * K <= 1 << 29 else _native.ERR_WORKSPACE)
     if rc == _native.ERR_WORKSPACE:
         need = lib.maxsim_workspace_size(_native.OP_LINEAR_INT8, M, N, K, ld_x if px % 16 == 0 else 1,
                                          ld_w if ld_w and pw % 16 == 0 else 1)
         if need == _SIZE_MAX:
             _native.check(2, "maxsim_linear_int8")
         ws, nbytes = _workspace(need, dev, workspace)
-        rc = lib.maxsim_linear_int8(*args, None if ws is None else ws.data_ptr(), nbytes, stream)
+        rc = lib.maxsim_linear_int8(px, ld_x, px_scale, pw, ld_w, pw_scale, pb, M, N, K, dt, p_out, N,
+                                    None if ws is None else ws.data_ptr(), nbytes, stream)
     if rc:
         _native.check(rc, "maxsim_linear_int8")
     return out
@@ -531,18 +542,18 @@ def dropout_fwd(x: torch.Tensor, p: float, seed: int, offset: int = 0, residual:
     dt = _DT_ANY.get(x.dtype)
     if dt is None:
         raise TypeError(f"x must be float16, bfloat16 or float32, got {x.dtype}")
-    shape, dev = x.shape, x.device
+    index, shape, dev = _device(x, "x"), x.shape, x.device
+    pr, ld_r = None, 0
     if residual is not None:
-        if residual.shape != shape or residual.dtype != x.dtype or residual.device != dev:
+        if residual.shape != shape or residual.dtype is not x.dtype or residual.get_device() != index:
             raise ValueError("residual must have x's shape, dtype and device")
-        residual, _, _, ld_r = _rows(residual, "residual")
+        residual, _, ld_r = _rows(residual, "residual")
         pr = residual.data_ptr()
-    else:
-        pr, ld_r = None, 0
-    x, rows, cols, ld = _rows(x, "x")
+    x, rows, ld = _rows(x, "x")
+    cols = shape[-1]
     out = torch.empty(shape, dtype=x.dtype, device=dev) if out is None else _given(out, "out", shape, x.dtype, dev)
     rc = _native.lib().maxsim_dropout_fwd(x.data_ptr(), dt, rows, cols, ld, pr, ld_r, p, seed, offset, out.data_ptr(),
-                                          cols, _raw_stream(dev.index))
+                                          cols, _raw_stream(index))
     if rc:
         _native.check(rc, "maxsim_dropout_fwd")
     return out
@@ -555,12 +566,13 @@ def dropout_bwd(grad: torch.Tensor, p: float, seed: int, offset: int = 0, *,
     dt = _DT_ANY.get(grad.dtype)
     if dt is None:
         raise TypeError(f"grad must be float16, bfloat16 or float32, got {grad.dtype}")
-    shape, dev = grad.shape, grad.device
-    grad, rows, cols, ld = _rows(grad, "grad")
+    index, shape, dev = _device(grad, "grad"), grad.shape, grad.device
+    grad, rows, ld = _rows(grad, "grad")
+    cols = shape[-1]
     out = (torch.empty(shape, dtype=grad.dtype, device=dev) if out is None
            else _given(out, "out", shape, grad.dtype, dev))
     rc = _native.lib().maxsim_dropout_bwd(grad.data_ptr(), dt, rows, cols, ld, p, seed, offset, out.data_ptr(), cols,
-                                          _raw_stream(dev.index))
+                                          _raw_stream(index))
     if rc:
         _native.check(rc, "maxsim_dropout_bwd")
     return out
