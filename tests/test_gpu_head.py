@@ -154,7 +154,9 @@ def test_linear_int8(M, N, K, dtype, bias):
     (20001, 128, 1024, "f16"), (19500, 100, 1008, "f32"), (30011, 64, 2048, "bf16"), (40000, 33, 176, "f32"),
     (20000, 128, 1040, "bf16"), (6100, 2050, 272, "bf16"), (6000, 2001, 144, "f32"), (1500, 8100, 128, "f16"),
     (700, 16000, 80, "f32"), (5000, 700, 512, "f16"), (90, 20000, 96, "bf16"), (150, 300, 9000, "bf16"),
-    (300, 120, 8000, "f32"), (40, 1000, 16000, "f16"), (20003, 120, 333, "bf16")])
+    (300, 120, 8000, "f32"), (40, 1000, 16000, "f16"), (20003, 120, 333, "bf16"),
+    (20000, 48, 640, "f16"), (400, 9000, 640, "f32"), (9000, 400, 640, "f16"), (130, 9000, 640, "f16"), (9000, 130, 640, "f32"),
+    (60, 16000, 640, "f32"), (16000, 60, 2112, "bf16"), (16000, 60, 2112, "f32")])
 def test_linear_int8_many_tiles(M, N, K, dtype):
     rng = np.random.default_rng(M + N + K)
     check_linear(codes(rng, M, K), codes(rng, N, K), dtype, True, rng)
