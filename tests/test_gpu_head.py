@@ -277,6 +277,24 @@ def test_linear_int8_repeats_and_other_streams():
         assert all(torch.equal(first, a) for a in again)
 
 
+@pytest.mark.parametrize("M,N,K", [(4, 300, 512), (700, 1100, 640), (150, 300, 9000), (20000, 64, 256)])
+def test_linear_int8_in_a_cuda_graph(M, N, K):
+    # the call only enqueues: captured with its dependent launches and replayed on new values
+    rng = np.random.default_rng(K)
+    x, w = codes(rng, M, K), codes(rng, N, K)
+    xs, ws = torch.rand(M, device="cuda"), torch.rand(N, device="cuda")
+    ms.linear_int8(x, xs, w, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = ms.linear_int8(x, xs, w, ws)
+    for _ in range(3):
+        x.copy_(codes(rng, M, K))
+        graph.replay()
+        assert torch.equal(out, ms.linear_int8(x, xs, w, ws))
+    assert ms.device_status() == 0
+
+
 # ---------------------------------------------------------------- dropout
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
