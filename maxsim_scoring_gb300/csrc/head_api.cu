@@ -48,22 +48,32 @@ maxsim_status launch_quantize_group(const QuantizeArgs& a, const HostDevice& dev
 template <typename T, bool kWide, bool kNorm>
 maxsim_status launch_quantize(const QuantizeArgs& a, const HostDevice& dev, cudaStream_t st) {
     const int64_t chunks = (a.cols + Chunk<T, kWide>::kVec - 1) / Chunk<T, kWide>::kVec;
-    if (chunks <= 8) return launch_quantize_group<T, kWide, kNorm, 8, 1>(a, dev, st);
-    if (chunks <= 16) return launch_quantize_group<T, kWide, kNorm, 8, 2>(a, dev, st);
-    if (chunks <= 32) return launch_quantize_group<T, kWide, kNorm, 8, 4>(a, dev, st);
-    if (chunks <= 64) return launch_quantize_group<T, kWide, kNorm, 8, 8>(a, dev, st);
-    if (chunks <= 128) return launch_quantize_group<T, kWide, kNorm, 32, 4>(a, dev, st);
-    if (chunks <= 256) return launch_quantize_group<T, kWide, kNorm, 32, 8>(a, dev, st);
     if constexpr (kWide) {
+        if (chunks <= 8) return launch_quantize_group<T, kWide, kNorm, 8, 1>(a, dev, st);
+        if (chunks <= 16) return launch_quantize_group<T, kWide, kNorm, 8, 2>(a, dev, st);
+        if (chunks <= 32) return launch_quantize_group<T, kWide, kNorm, 8, 4>(a, dev, st);
+        if (chunks <= 64) return launch_quantize_group<T, kWide, kNorm, 8, 8>(a, dev, st);
+        if (chunks <= 128) return launch_quantize_group<T, kWide, kNorm, 32, 4>(a, dev, st);
+        if (chunks <= 256) return launch_quantize_group<T, kWide, kNorm, 32, 8>(a, dev, st);
         if (chunks <= 512) return launch_quantize_group<T, kWide, kNorm, 128, 4>(a, dev, st);
         if (chunks <= 1024) return launch_quantize_group<T, kWide, kNorm, 128, 8>(a, dev, st);
         if (chunks <= 2048) return launch_quantize_group<T, kWide, kNorm, 512, 4>(a, dev, st);
+        if (chunks <= 4096) return launch_quantize_group<T, kWide, kNorm, 512, 8>(a, dev, st);
     } else {  // single elements: more of them a thread
+        if (chunks <= kNarrow) {
+            quantize_narrow_rows_kernel<T, kNorm><<<grid_of(a.rows, 128, int64_t(dev.num_sms) * 16), 128, 0, st>>>(a);
+            return launched();
+        }
+        if (chunks <= 16) return launch_quantize_group<T, kWide, kNorm, 8, 2>(a, dev, st);
+        if (chunks <= 32) return launch_quantize_group<T, kWide, kNorm, 8, 4>(a, dev, st);
+        if (chunks <= 64) return launch_quantize_group<T, kWide, kNorm, 8, 8>(a, dev, st);
+        if (chunks <= 128) return launch_quantize_group<T, kWide, kNorm, 8, 16>(a, dev, st);
+        if (chunks <= 256) return launch_quantize_group<T, kWide, kNorm, 32, 8>(a, dev, st);
         if (chunks <= 512) return launch_quantize_group<T, kWide, kNorm, 32, 16>(a, dev, st);
         if (chunks <= 1024) return launch_quantize_group<T, kWide, kNorm, 32, 32>(a, dev, st);
         if (chunks <= 2048) return launch_quantize_group<T, kWide, kNorm, 128, 16>(a, dev, st);
+        if (chunks <= 4096) return launch_quantize_group<T, kWide, kNorm, 512, 8>(a, dev, st);
     }
-    if (chunks <= 4096) return launch_quantize_group<T, kWide, kNorm, 512, 8>(a, dev, st);
     quantize_long_rows_kernel<T, kWide, kNorm><<<grid_of(a.rows, 1, int64_t(dev.num_sms) * 4), 512, 0, st>>>(a);
     return launched();
 }

@@ -31,7 +31,8 @@ def f64(t):
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
 @pytest.mark.parametrize("rows,cols,pad,shift", [
     (1, 1, 0, 0), (3, 7, 0, 0), (32, 128, 0, 0), (33, 128, 8, 0), (5, 100, 3, 1), (2, 1024, 0, 1), (7, 1000, 24, 8),
-    (4, 2048, 0, 0), (3, 4104, 0, 0), (2, 8193, 0, 0), (2, 20000, 8, 0), (1, 70001, 0, 3), (1000, 16, 0, 0), (777, 24, 0, 0)])
+    (4, 2048, 0, 0), (3, 4104, 0, 0), (2, 8193, 0, 0), (2, 20000, 8, 0), (1, 70001, 0, 3), (1000, 16, 0, 0), (777, 24, 0, 0),
+    (300, 5, 0, 0), (301, 17, 2, 1), (50, 85, 0, 0), (40, 250, 1, 0), (9, 511, 0, 0), (9, 1500, 1, 1), (3, 5001, 0, 0)])
 @pytest.mark.parametrize("normalize", [False, True])
 def test_quantize_rows(dtype, rows, cols, pad, shift, normalize):
     x = rows_of(np.random.default_rng(rows + cols), rows, cols, dtype, pad, shift)
@@ -43,7 +44,7 @@ def test_quantize_rows(dtype, rows, cols, pad, shift, normalize):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
-@pytest.mark.parametrize("cols", [8, 129, 1024, 9000])
+@pytest.mark.parametrize("cols", [7, 8, 13, 100, 129, 1024, 3001, 9000])
 @pytest.mark.parametrize("normalize", [False, True])
 def test_quantize_special_rows(dtype, cols, normalize):
     rng = np.random.default_rng(cols)
