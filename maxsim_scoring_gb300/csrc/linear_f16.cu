@@ -1,0 +1,7 @@
+#include "linear_launch.cuh"
+
+namespace maxsim {
+
+template maxsim_status run_linear<__half>(const LinearPlan&, LinearArgs, bool, bool, uint8_t*, const HostDevice&, cudaStream_t);
+
+}  // namespace maxsim

@@ -87,7 +87,7 @@ __device__ __forceinline__ uint4 load_row16(const PrepJob& j, int64_t r, int32_t
 }
 
 // One pass, bound by its bytes: 4096 x 4096 widened in about 8 us.
-__global__ void __launch_bounds__(256) linear_prep_kernel(const PrepArgs a) {
+static __global__ void __launch_bounds__(256) linear_prep_kernel(const PrepArgs a) {
     begin_dependents();
     const int32_t per_row = a.k_pad >> 4;
     const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x, n1 = a.widen.rows * per_row,
@@ -256,14 +256,14 @@ struct TileCfg {
 struct TileArgs {
     LinearArgs l;
     int32_t* partial;   // [slices, M, N] integer sums when slices > 1
-    int64_t items;      // tiles * slices
+    int64_t items;      // tiles * slices, < 2^32 (the divisions of short items are worth 32 bits)
     int32_t rows_a;     // rows of A (tokens, or channels when swapped)
     int32_t rows_b;
     int32_t tiles_b;
     int32_t slices;     // parts of K
     int32_t kb;         // blocks of K
     int32_t kb_slice;   // blocks per slice
-    int vec_out;        // rows of out (of the sums) start on 16-byte boundaries
+    int words_out;      // rows of out start on 4-byte boundaries
     int a_prepared;     // A too was laid out by linear_prep_kernel
     int* status;
     uint64_t timeout_ns;
@@ -350,13 +350,12 @@ struct TileItem {
 };
 
 template <int kTN>
-__device__ __forceinline__ TileItem tile_item(const TileArgs& a, int64_t item, uint32_t rank) {
+__device__ __forceinline__ TileItem tile_item(const TileArgs& a, uint32_t item, uint32_t rank) {
     TileItem t;
-    const int64_t tile = a.slices == 1 ? item : item / a.slices;
-    t.slice = static_cast<int32_t>(item - tile * a.slices);
-    const int64_t ta = tile / a.tiles_b;
-    t.a0 = ta * kTileM + rank * 128;
-    t.b0 = (tile - ta * a.tiles_b) * kTN;
+    const uint32_t tile = item / static_cast<uint32_t>(a.slices), row = tile / static_cast<uint32_t>(a.tiles_b);
+    t.slice = static_cast<int32_t>(item - tile * static_cast<uint32_t>(a.slices));
+    t.a0 = static_cast<int64_t>(row) * kTileM + rank * 128;
+    t.b0 = static_cast<int64_t>(tile - row * static_cast<uint32_t>(a.tiles_b)) * kTN;
     t.kb0 = t.slice * a.kb_slice;
     t.kb1 = min(a.kb, t.kb0 + a.kb_slice);
     return t;
@@ -371,11 +370,11 @@ __device__ __forceinline__ int32_t from_f32<int32_t>(float v) { return __float2i
 // the eight pieces of four rows, meet no bank twice.
 __device__ __forceinline__ uint32_t staged(int r, int c) { return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4)); }
 
-// Four consecutive 32-bit elements from p on, of which the first n exist.
+// Four consecutive 32-bit elements from p (16-byte aligned) on, of which the first n exist.
 template <typename T>
-__device__ __forceinline__ void store4(T* p, int n, bool vec, float a, float b, float c, float d) {
+__device__ __forceinline__ void store4(T* p, int n, float a, float b, float c, float d) {
     static_assert(sizeof(T) == 4, "one 16-byte store");
-    if (vec && n >= 4) {
+    if (n >= 4) {
         alignas(16) T o[4] = {from_f32<T>(a), from_f32<T>(b), from_f32<T>(c), from_f32<T>(d)};
         *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(o);
     } else {
@@ -409,13 +408,15 @@ __device__ __forceinline__ void store4(T* p, int n, bool vec, float a, float b, 
 // block of A and of B in 650 cycles, 11 TB/s over all SMs, whatever the MMAs and
 // the widening took). Where B is a single tile of rows and fits, as a head's
 // weights do, it is loaded once and kept (kKeepB).
+// kRows16: rows of out (of the sums) start on 16-byte boundaries. (Both ways of
+// storing in one kernel cost the other one 3 to 8 %.)
 // A tile's K may be cut into slices (few tiles, long K): each slice then
 // writes its integer sums, and linear_join_kernel adds them.
 // Measured with the preparation: 32768 x 4096 x 4096 in 536 us, 2.05 PFLOP/s
 // (tensor pipe 90 % active; 597 us, 1.84 PFLOP/s, once the power limit holds the
 // clock), 1048576 x 128 x 1024 in 213 us, 6.3 TB/s (HBM), 2048 x 4096 x 1024 in 19.7 us
 // (two rounds of tiles, the last one's stores).
-template <typename T, int kTN, bool kSwap, bool kKeepB>
+template <typename T, int kTN, bool kSwap, bool kKeepB, bool kRows16>
 __global__ void __launch_bounds__(kTileThreads, 1)
 linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const TileArgs a) {
     using C = TileCfg<kTN, kKeepB>;
@@ -638,31 +639,49 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         const bool hold = kHold && a.slices == 1;
         int32_t buf = 0;
         uint32_t buf_phase = 0;
+        // this lane's row of A, and its column of each 32 along B. Loaded an item
+        // ahead where registers are left for it (525402 x 960 x 64 f32 616 -> 569 us,
+        // 603311 x 64 x 64 bf16 56 -> 50), not beside the held outputs of wide tiles
+        // (202805 x 576 x 64 bf16 110, and 116 ahead; 1048576 x 128 x 1024 f16 216 and 221)
+        constexpr bool kAhead = !kHold || kTN == 64;
+        float next_sa = 0.f, next_bias_a = 0.f, next_sb[kChunks], next_bias[kSwap ? 1 : kChunks];
+        auto load_scales = [&](const TileItem& t) {
+            if (a.slices > 1) return;
+            const int64_t ra = t.a0 + q * 32 + lane;
+            const bool in = ra < a.rows_a;
+            next_sa = in ? __ldg((kSwap ? a.l.w_scale : a.l.x_scale) + ra) : 0.f;
+            if constexpr (kSwap) next_bias_a = a.l.bias && in ? __ldg(a.l.bias + ra) : 0.f;
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                const int64_t i = t.b0 + half * kCols + c * 32 + lane;
+                next_sb[c] = i < a.rows_b ? __ldg((kSwap ? a.l.x_scale : a.l.w_scale) + i) : 0.f;
+                if constexpr (!kSwap) next_bias[c] = a.l.bias && i < a.rows_b ? __ldg(a.l.bias + i) : 0.f;
+            }
+        };
+        if constexpr (kAhead) load_scales(tile_item<kTN>(a, first, rank));
         for (int64_t it = first; it < a.items; it += step) {
             const TileItem t = tile_item<kTN>(a, it, rank);
+            if constexpr (!kAhead) load_scales(t);
             const int64_t ra0 = t.a0 + q * 32, rb0 = t.b0 + half * kCols;
             int32_t* part = a.partial + static_cast<int64_t>(t.slice) * a.l.M * a.l.N;  // used when slices > 1
             const int row_n = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(32), a.rows_a - ra0)));
-            // this lane's row of A, and its column of each 32 along B
             const bool in_a = lane < row_n;
-            const float* scale_b = kSwap ? a.l.x_scale : a.l.w_scale;
-            const float sa = in_a ? __ldg((kSwap ? a.l.w_scale : a.l.x_scale) + ra0 + lane) : 0.f;
-            const float bias_a = kSwap && a.l.bias && in_a ? __ldg(a.l.bias + ra0 + lane) : 0.f;
-            float sb[kChunks], bias[kSwap ? 1 : kChunks];
+            const float sa = next_sa, bias_a = next_bias_a;
+            float sb[kHold ? 1 : kChunks], bias[kHold || kSwap ? 1 : kChunks];
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
-                const int64_t i = rb0 + c * 32 + lane;
-                sb[c] = i < a.rows_b ? __ldg(scale_b + i) : 0.f;
-                if constexpr (!kSwap) bias[c] = a.l.bias && i < a.rows_b ? __ldg(a.l.bias + i) : 0.f;
-            }
-            if (hold) {
-#pragma unroll
-                for (int c = 0; c < kChunks; ++c) {
-                    tab[c * 32 + lane] = sb[c];
-                    if constexpr (!kSwap) tab[kCols + c * 32 + lane] = bias[c];
+                if constexpr (kHold) {
+                    if (hold) {
+                        tab[c * 32 + lane] = next_sb[c];
+                        if constexpr (!kSwap) tab[kCols + c * 32 + lane] = next_bias[c];
+                    }
+                } else {
+                    sb[c] = next_sb[c];
+                    if constexpr (!kSwap) bias[c] = next_bias[c];
                 }
-                __syncwarp();
             }
+            __syncwarp();
+            if (kAhead && it + step < a.items) load_scales(tile_item<kTN>(a, it + step, rank));
             if (!tile_wait_warp(a, ctl, &ctl->acc_full[buf], buf_phase)) break;
             tc_fence_after();
             const uint32_t src = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * kTN + half * kCols);
@@ -714,25 +733,40 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                     for (int i = 0; i < 8; ++i)
                         *reinterpret_cast<float4*>(stage + staged(lane, i)) =
                             make_float4(v[4 * i] * f, v[4 * i + 1] * f, v[4 * i + 2] * f, v[4 * i + 3] * f);
-                    float ws[4], bs[4];  // this lane's four channels
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        ws[j] = __shfl_sync(0xffffffffu, sb[c], 4 * (lane & 7) + j);
-                        bs[j] = __shfl_sync(0xffffffffu, bias[c], 4 * (lane & 7) + j);
-                    }
                     __syncwarp();
-                    const int64_t n0 = rb + 4 * (lane & 7);
-                    const int n = static_cast<int>(min(static_cast<int64_t>(4), a.rows_b - n0));
-                    int64_t at = (ra0 + (lane >> 3)) * ld + n0;
+                    if constexpr (kRows16) {
+                        float ws[4] = {}, bs[4] = {};  // this lane's four channels
+                        if constexpr (!kHold) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i, at += 4 * ld) {
-                        const float4 y = *reinterpret_cast<const float4*>(stage + staged(4 * i + (lane >> 3), lane & 7));
-                        if (4 * i + (lane >> 3) >= row_n) continue;
-                        if (a.slices > 1) {
-                            store4(part + at, n, a.vec_out, y.x, y.y, y.z, y.w);
-                        } else if constexpr (!kHold) {
-                            store4(static_cast<T*>(a.l.out) + at, n, a.vec_out, __fmaf_rn(y.x, ws[0], bs[0]),
-                                   __fmaf_rn(y.y, ws[1], bs[1]), __fmaf_rn(y.z, ws[2], bs[2]), __fmaf_rn(y.w, ws[3], bs[3]));
+                            for (int j = 0; j < 4; ++j) {
+                                ws[j] = __shfl_sync(0xffffffffu, sb[c], 4 * (lane & 7) + j);
+                                bs[j] = __shfl_sync(0xffffffffu, bias[c], 4 * (lane & 7) + j);
+                            }
+                        }
+                        const int64_t n0 = rb + 4 * (lane & 7);
+                        const int n = static_cast<int>(min(static_cast<int64_t>(4), a.rows_b - n0));
+                        int64_t at = (ra0 + (lane >> 3)) * ld + n0;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i, at += 4 * ld) {
+                            const float4 y = *reinterpret_cast<const float4*>(stage + staged(4 * i + (lane >> 3), lane & 7));
+                            if (4 * i + (lane >> 3) >= row_n) continue;
+                            if (a.slices > 1) {
+                                store4(part + at, n, y.x, y.y, y.z, y.w);
+                            } else if constexpr (!kHold) {
+                                store4(static_cast<T*>(a.l.out) + at, n, __fmaf_rn(y.x, ws[0], bs[0]), __fmaf_rn(y.y, ws[1], bs[1]),
+                                       __fmaf_rn(y.z, ws[2], bs[2]), __fmaf_rn(y.w, ws[3], bs[3]));
+                            }
+                        }
+                    } else {  // rows off their 16-byte boundaries: a row at a time, a lane per column
+                        const bool in_b = rb + lane < a.rows_b;
+                        const uint8_t* from = stage + (lane & 3) * 4;
+                        int64_t at = ra0 * ld + rb + lane;
+#pragma unroll 8
+                        for (int r = 0; r < row_n; ++r, at += ld) {
+                            const float y = *reinterpret_cast<const float*>(from + staged(r, lane >> 2));
+                            if (!in_b) continue;
+                            if (a.slices > 1) part[at] = __float2int_rn(y);
+                            else if constexpr (!kHold) static_cast<T*>(a.l.out)[at] = __fmaf_rn(y, sb[c], bias[c]);
                         }
                     }
                     __syncwarp();
@@ -764,19 +798,42 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                                     make_uint4(held[c + j / 4][(j % 4) * 4], held[c + j / 4][(j % 4) * 4 + 1],
                                                held[c + j / 4][(j % 4) * 4 + 2], held[c + j / 4][(j % 4) * 4 + 3]);
                             __syncwarp();
-                            T* p = static_cast<T*>(a.l.out) + (ra0 + lane / kLanes) * ld + n0;
+                            if constexpr (kRows16) {
+                                T* p = static_cast<T*>(a.l.out) + (ra0 + lane / kLanes) * ld + n0;
 #pragma unroll
-                            for (int i = 0; i < kLanes; ++i, p += kRows * ld) {
-                                const int r = i * kRows + lane / kLanes;
-                                const uint4 y = *reinterpret_cast<const uint4*>(stage + staged(r, lane % kLanes));
-                                if (r >= row_n) continue;
-                                if (a.vec_out && n == 8) {
-                                    *reinterpret_cast<uint4*>(p) = y;
+                                for (int i = 0; i < kLanes; ++i, p += kRows * ld) {
+                                    const int r = i * kRows + lane / kLanes;
+                                    const uint4 y = *reinterpret_cast<const uint4*>(stage + staged(r, lane % kLanes));
+                                    if (r >= row_n) continue;
+                                    if (n == 8) {
+                                        *reinterpret_cast<uint4*>(p) = y;
+                                    } else {
+                                        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                                        for (int e = 0; e < 8; ++e)
+                                            if (e < n) p[e] = half_of<T>(w[e / 2], e & 1);
+                                    }
+                                }
+                            } else {  // rows off their 16-byte boundaries: runs of a row, a lane per column or two
+                                const int64_t left = a.rows_b - (rb0 + c * 32);
+                                T* p = static_cast<T*>(a.l.out) + ra0 * ld + rb0 + c * 32;
+                                if (a.words_out) {
+                                    constexpr int kWords = 16 * kJoin;  // words of a row
+                                    const int col = 2 * (lane % kWords);
+#pragma unroll 8
+                                    for (int r = lane / kWords; r < row_n; r += 32 / kWords) {
+                                        const uint32_t w = *reinterpret_cast<const uint32_t*>(stage + staged(r, col >> 3) + (col & 7) * 2);
+                                        if (col + 1 < left) *reinterpret_cast<uint32_t*>(p + r * ld + col) = w;
+                                        else if (col < left) p[r * ld + col] = half_of<T>(w, 0);
+                                    }
                                 } else {
-                                    const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll 4
+                                    for (int r = 0; r < row_n; ++r) {
 #pragma unroll
-                                    for (int e = 0; e < 8; ++e)
-                                        if (e < n) p[e] = half_of<T>(w[e / 2], e & 1);
+                                        for (int col = lane; col < 32 * kJoin; col += 32)
+                                            if (col < left)
+                                                p[r * ld + col] = *reinterpret_cast<const T*>(stage + staged(r, col >> 3) + (col & 7) * 2);
+                                    }
                                 }
                             }
                             __syncwarp();
