@@ -263,7 +263,6 @@ struct TileArgs {
     int32_t slices;     // parts of K
     int32_t kb;         // blocks of K
     int32_t kb_slice;   // blocks per slice
-    int words_out;      // rows of out start on 4-byte boundaries
     int a_prepared;     // A too was laid out by linear_prep_kernel
     int* status;
     uint64_t timeout_ns;
@@ -409,7 +408,7 @@ __device__ __forceinline__ void store4(T* p, int n, float a, float b, float c, f
 // the widening took). Where B is a single tile of rows and fits, as a head's
 // weights do, it is loaded once and kept (kKeepB).
 // kRows16: rows of out (of the sums) start on 16-byte boundaries. (Both ways of
-// storing in one kernel cost the other one 3 to 8 %.)
+// storing in one kernel cost this one 3 to 8 %.)
 // A tile's K may be cut into slices (few tiles, long K): each slice then
 // writes its integer sums, and linear_join_kernel adds them.
 // Measured with the preparation: 32768 x 4096 x 4096 in 536 us, 2.05 PFLOP/s
@@ -785,7 +784,7 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                             for (int i = 0; i < 32; ++i, p += ld)
                                 if (i < n && in_a) *p = half_of<T>(held[c][i / 2], i & 1);
                         }
-                    } else {
+                    } else if constexpr (kRows16) {
                         constexpr int kJoin = kChunks < 2 ? 1 : 2;         // chunks whose rows are staged together
                         constexpr int kLanes = 4 * kJoin, kRows = 32 / kLanes;  // lanes of a row, rows of a store
 #pragma unroll
@@ -798,42 +797,79 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                                     make_uint4(held[c + j / 4][(j % 4) * 4], held[c + j / 4][(j % 4) * 4 + 1],
                                                held[c + j / 4][(j % 4) * 4 + 2], held[c + j / 4][(j % 4) * 4 + 3]);
                             __syncwarp();
-                            if constexpr (kRows16) {
-                                T* p = static_cast<T*>(a.l.out) + (ra0 + lane / kLanes) * ld + n0;
+                            T* p = static_cast<T*>(a.l.out) + (ra0 + lane / kLanes) * ld + n0;
 #pragma unroll
-                                for (int i = 0; i < kLanes; ++i, p += kRows * ld) {
-                                    const int r = i * kRows + lane / kLanes;
-                                    const uint4 y = *reinterpret_cast<const uint4*>(stage + staged(r, lane % kLanes));
-                                    if (r >= row_n) continue;
-                                    if (n == 8) {
-                                        *reinterpret_cast<uint4*>(p) = y;
-                                    } else {
-                                        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                                        for (int e = 0; e < 8; ++e)
-                                            if (e < n) p[e] = half_of<T>(w[e / 2], e & 1);
-                                    }
-                                }
-                            } else {  // rows off their 16-byte boundaries: runs of a row, a lane per column or two
-                                const int64_t left = a.rows_b - (rb0 + c * 32);
-                                T* p = static_cast<T*>(a.l.out) + ra0 * ld + rb0 + c * 32;
-                                if (a.words_out) {
-                                    constexpr int kWords = 16 * kJoin;  // words of a row
-                                    const int col = 2 * (lane % kWords);
-#pragma unroll 8
-                                    for (int r = lane / kWords; r < row_n; r += 32 / kWords) {
-                                        const uint32_t w = *reinterpret_cast<const uint32_t*>(stage + staged(r, col >> 3) + (col & 7) * 2);
-                                        if (col + 1 < left) *reinterpret_cast<uint32_t*>(p + r * ld + col) = w;
-                                        else if (col < left) p[r * ld + col] = half_of<T>(w, 0);
-                                    }
+                            for (int i = 0; i < kLanes; ++i, p += kRows * ld) {
+                                const int r = i * kRows + lane / kLanes;
+                                const uint4 y = *reinterpret_cast<const uint4*>(stage + staged(r, lane % kLanes));
+                                if (r >= row_n) continue;
+                                if (n == 8) {
+                                    *reinterpret_cast<uint4*>(p) = y;
                                 } else {
-#pragma unroll 4
-                                    for (int r = 0; r < row_n; ++r) {
+                                    const uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                                        for (int col = lane; col < 32 * kJoin; col += 32)
-                                            if (col < left)
-                                                p[r * ld + col] = *reinterpret_cast<const T*>(stage + staged(r, col >> 3) + (col & 7) * 2);
-                                    }
+                                    for (int e = 0; e < 8; ++e)
+                                        if (e < n) p[e] = half_of<T>(w[e / 2], e & 1);
+                                }
+                            }
+                            __syncwarp();
+                        }
+                    } else {
+                        // Rows off their 16-byte boundaries. Every lane turns its row by the
+                        // phase of its address, so that staged pieces are pieces of out; the
+                        // first one holds the row's first elements and, wrapped around, its last
+                        // ones, which go out one by one. (139270 x 1861 x 176 bf16: 712 us with
+                        // single elements throughout, 427 joining pieces at the store.)
+                        constexpr int kJoin = kChunks < 2 ? 1 : 2;         // chunks whose rows are staged together
+                        constexpr int kRun = 32 * kJoin, kPieces = kRun / 8, kRows = 32 / kPieces;
+                        auto phase_of = [](const T* p) { return static_cast<int>(reinterpret_cast<uintptr_t>(p) >> 1) & 7; };
+                        const int k = lane % kPieces, r0 = lane / kPieces;
+#pragma unroll
+                        for (int c = 0; c < kChunks; c += kJoin) {
+                            const int64_t n0 = rb0 + c * 32;
+                            if (n0 >= a.rows_b) break;
+                            const int left = static_cast<int>(min(static_cast<int64_t>(kRun), a.rows_b - n0));
+                            T* const out0 = static_cast<T*>(a.l.out) + ra0 * ld + n0;
+                            const int turn = phase_of(out0 + lane * ld);
+                            uint32_t v[kRun / 2], u[kRun / 2];
+#pragma unroll
+                            for (int i = 0; i < kRun / 2; ++i) v[i] = held[c + i / 16][i % 16];
+#pragma unroll
+                            for (int i = 0; i < kRun / 2; ++i)
+                                u[i] = __funnelshift_l(v[(i + kRun / 2 - 1) % (kRun / 2)], v[i], (turn & 1) * 16);
+#pragma unroll
+                            for (int i = 0; i < kRun / 2; ++i) v[i] = turn & 2 ? u[(i + kRun / 2 - 1) % (kRun / 2)] : u[i];
+#pragma unroll
+                            for (int i = 0; i < kRun / 2; ++i) u[i] = turn & 4 ? v[(i + kRun / 2 - 2) % (kRun / 2)] : v[i];
+#pragma unroll
+                            for (int j = 0; j < kPieces; ++j)
+                                *reinterpret_cast<uint4*>(stage + staged(lane, j)) =
+                                    make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
+                            __syncwarp();
+                            T* p = out0 + r0 * ld;
+#pragma unroll
+                            for (int i = 0; i < kPieces; ++i, p += kRows * ld) {
+                                const int r = i * kRows + r0, ph = phase_of(p);
+                                const uint4 y = *reinterpret_cast<const uint4*>(stage + staged(r, k));
+                                if (r < row_n && (k > 0 || ph == 0) && 8 * k - ph + 8 <= left)
+                                    *reinterpret_cast<uint4*>(p + 8 * k - ph) = y;
+                            }
+                            p = out0 + (lane >> 3) * ld;
+                            const int e = lane & 7;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i, p += 4 * ld) {
+                                const int r = i * 4 + (lane >> 3), ph = phase_of(p), col = e < ph ? kRun - ph + e : e - ph;
+                                const T y = *reinterpret_cast<const T*>(stage + staged(r, 0) + e * 2);
+                                if (r < row_n && ph != 0 && col < left) p[col] = y;
+                            }
+                            if (left < kRun) {  // the last columns: the end of a row is not yet in its first piece
+                                p = out0 + (lane >> 3) * ld;
+#pragma unroll
+                                for (int i = 0; i < 8; ++i, p += 4 * ld) {
+                                    const int r = i * 4 + (lane >> 3), ph = phase_of(p), end = (left + ph) >> 3;
+                                    const T y = *reinterpret_cast<const T*>(stage + staged(r, end % kPieces) + e * 2);
+                                    if (r < row_n && e < ((left + ph) & 7) && end < kPieces && (end > 0 || ph == 0))
+                                        p[8 * end - ph + e] = y;
                                 }
                             }
                             __syncwarp();

@@ -111,7 +111,6 @@ maxsim_status launch_tile_rows(const LinearPlan& p, const LinearArgs& l, const _
     a.slices = p.slices;
     a.kb = p.kb;
     a.kb_slice = p.kb_slice;
-    a.words_out = ptr_aligned(l.out, 4) && l.ld_out * static_cast<int64_t>(sizeof(T)) % 4 == 0;
     a.a_prepared = a_prepared;
     a.status = dev.status;
     a.timeout_ns = kTimeoutNs;
