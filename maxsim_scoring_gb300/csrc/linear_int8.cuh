@@ -369,6 +369,14 @@ __device__ __forceinline__ int32_t from_f32<int32_t>(float v) { return __float2i
 // the eight pieces of four rows, meet no bank twice.
 __device__ __forceinline__ uint32_t staged(int r, int c) { return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4)); }
 
+// The same piece in the box of a TMA store of 32 rows x 32 * kJoin 16-bit values
+// (rows of 128 or 64 bytes, swizzled as wide): no bank twice either.
+template <int kJoin>
+__device__ __forceinline__ uint32_t boxed(int r, int c) {
+    if constexpr (kJoin == 2) return staged(r, c);
+    else return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+
 // Four consecutive 32-bit elements from p (16-byte aligned) on, of which the first n exist.
 template <typename T>
 __device__ __forceinline__ void store4(T* p, int n, float a, float b, float c, float d) {
@@ -407,7 +415,8 @@ __device__ __forceinline__ void store4(T* p, int n, float a, float b, float c, f
 // block of A and of B in 650 cycles, 11 TB/s over all SMs, whatever the MMAs and
 // the widening took). Where B is a single tile of rows and fits, as a head's
 // weights do, it is loaded once and kept (kKeepB).
-// kRows16: rows of out (of the sums) start on 16-byte boundaries. (Both ways of
+// kRows16: rows of out (of the sums) start on 16-byte boundaries, and those of
+// 16-bit outputs end there. (Both ways of
 // storing in one kernel cost this one 3 to 8 %.)
 // A tile's K may be cut into slices (few tiles, long K): each slice then
 // writes its integer sums, and linear_join_kernel adds them.
@@ -417,7 +426,8 @@ __device__ __forceinline__ void store4(T* p, int n, float a, float b, float c, f
 // (two rounds of tiles, the last one's stores).
 template <typename T, int kTN, bool kSwap, bool kKeepB, bool kRows16>
 __global__ void __launch_bounds__(kTileThreads, 1)
-linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const TileArgs a) {
+linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                   const __grid_constant__ CUtensorMap tm_out, const TileArgs a) {
     using C = TileCfg<kTN, kKeepB>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -622,16 +632,16 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         // accumulator a lane holds a row. 16-bit outputs are scaled, rounded and
         // held in registers until the accumulator has been read and handed
         // back, so that only this stands between a tile's MMAs and the next
-        // one's: all SMs store their tiles at about the same time, which
-        // takes longer (8,500 cycles at 256 x 256). The scales along B wait in
-        // shared memory, where a read serves the whole warp. Swapped, lanes are
-        // consecutive channels and store straight to out; otherwise rows pass
-        // through shared memory so that stores are whole 128-byte runs. 32-bit
-        // outputs, and the integer sums of slices, are stored 32 columns at a
-        // time as they are read.
+        // one's. The scales along B wait in shared memory, where a read serves
+        // the whole warp. Rows of 16-bit outputs then pass through shared memory
+        // to TMA stores (139270 x 1864 x 64 bf16: 148 us, and 209 with 16-byte
+        // stores of the warps, most of it their instructions). Swapped, lanes are
+        // consecutive channels and store straight to out. 32-bit outputs, and
+        // the integer sums of slices, are stored 32 columns at a time as they
+        // are read, through shared memory so that stores are whole 128-byte runs.
         const int q = warp & 3, half = (warp - kTileEpiWarp0) >> 2;
         constexpr int kCols = kTN / 2, kChunks = kCols / 32;  // columns per warp
-        constexpr bool kHold = sizeof(T) == 2;
+        constexpr bool kHold = sizeof(T) == 2, kTma = kHold && kRows16 && !kSwap;
         uint8_t* stage = s_out + (warp - kTileEpiWarp0) * kTileStage;
         float* tab = reinterpret_cast<float*>(stage);  // kHold: scales of the kCols columns, then biases
         const int64_t ld = a.slices > 1 ? a.l.N : a.l.ld_out;
@@ -667,6 +677,10 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
             const bool in_a = lane < row_n;
             const float sa = next_sa, bias_a = next_bias_a;
             float sb[kHold ? 1 : kChunks], bias[kHold || kSwap ? 1 : kChunks];
+            if constexpr (kTma) {  // the table is written where the last tile's stores read
+                if (lane == 0) bulk_wait_read();
+                __syncwarp();
+            }
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
                 if constexpr (kHold) {
@@ -784,35 +798,24 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                             for (int i = 0; i < 32; ++i, p += ld)
                                 if (i < n && in_a) *p = half_of<T>(held[c][i / 2], i & 1);
                         }
-                    } else if constexpr (kRows16) {
-                        constexpr int kJoin = kChunks < 2 ? 1 : 2;         // chunks whose rows are staged together
-                        constexpr int kLanes = 4 * kJoin, kRows = 32 / kLanes;  // lanes of a row, rows of a store
+                    } else if constexpr (kTma) {
+                        constexpr int kJoin = kChunks < 2 ? 1 : 2;  // chunks that are staged and stored together
 #pragma unroll
                         for (int c = 0; c < kChunks; c += kJoin) {
-                            const int64_t n0 = rb0 + c * 32 + 8 * (lane % kLanes);
-                            const int n = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(8), a.rows_b - n0)));
+                            const int64_t n0 = rb0 + c * 32;
+                            if (n0 >= a.rows_b) break;
+                            if (c > 0) {
+                                if (lane == 0) bulk_wait_read();
+                                __syncwarp();
+                            }
 #pragma unroll
-                            for (int j = 0; j < kLanes; ++j)
-                                *reinterpret_cast<uint4*>(stage + staged(lane, j)) =
+                            for (int j = 0; j < 4 * kJoin; ++j)
+                                *reinterpret_cast<uint4*>(stage + boxed<kJoin>(lane, j)) =
                                     make_uint4(held[c + j / 4][(j % 4) * 4], held[c + j / 4][(j % 4) * 4 + 1],
                                                held[c + j / 4][(j % 4) * 4 + 2], held[c + j / 4][(j % 4) * 4 + 3]);
+                            fence_proxy_async_smem();
                             __syncwarp();
-                            T* p = static_cast<T*>(a.l.out) + (ra0 + lane / kLanes) * ld + n0;
-#pragma unroll
-                            for (int i = 0; i < kLanes; ++i, p += kRows * ld) {
-                                const int r = i * kRows + lane / kLanes;
-                                const uint4 y = *reinterpret_cast<const uint4*>(stage + staged(r, lane % kLanes));
-                                if (r >= row_n) continue;
-                                if (n == 8) {
-                                    *reinterpret_cast<uint4*>(p) = y;
-                                } else {
-                                    const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                                    for (int e = 0; e < 8; ++e)
-                                        if (e < n) p[e] = half_of<T>(w[e / 2], e & 1);
-                                }
-                            }
-                            __syncwarp();
+                            if (lane == 0) tma_store_2d(&tm_out, smem_u32(stage), static_cast<int32_t>(n0), static_cast<int32_t>(ra0));
                         }
                     } else {
                         // Rows off their 16-byte boundaries. Every lane turns its row by the
@@ -879,6 +882,7 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
             }
             if (++buf == C::kAcc) { buf = 0; buf_phase ^= 1u; }
         }
+        if (kTma && lane == 0) bulk_wait();
     }
 
     tc_fence_before();

@@ -28,14 +28,14 @@ struct LinearPlan {
     size_t off_x = 0, off_w = 0, off_b = 0, off_partial = 0, bytes = 0;
 };
 
-// Rows of K elements, ld bytes apart, in boxes of 128 bytes x box_rows with the 128-byte swizzle.
+// Rows of K elements, ld bytes apart, in boxes of box_bytes (128 or 64) x box_rows, swizzled as wide.
 inline bool encode_k_rows(EncodeTiledFn encode, CUtensorMap* map, CUtensorMapDataType type, int elem, const void* base,
-                   int64_t K, int64_t rows, int64_t ld, uint32_t box_rows) {
+                   int64_t K, int64_t rows, int64_t ld, uint32_t box_rows, uint32_t box_bytes = 128) {
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
-    const cuuint32_t box[2] = {128u / static_cast<cuuint32_t>(elem), box_rows}, estr[2] = {1, 1};
+    const cuuint32_t box[2] = {box_bytes / static_cast<cuuint32_t>(elem), box_rows}, estr[2] = {1, 1};
     return encode(map, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -120,16 +120,24 @@ maxsim_status launch_tile_rows(const LinearPlan& p, const LinearArgs& l, const _
         !encode_k_rows(dev.encode, &tb, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, b16, p.k_pad, a.rows_b, p.k_pad * 2,
                        TileCfg<kTN, kKeepB>::kBRows))
         return MAXSIM_ERR_CUDA;
+    CUtensorMap tout = tb;  // used by 16-bit outputs that are stored by TMA alone
+    if constexpr (sizeof(T) == 2 && kRows16 && !kSwap) {
+        if (p.slices == 1 && !encode_k_rows(dev.encode, &tout, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, l.out, l.N, l.M,
+                                            l.ld_out * 2, 32, kTN == 64 ? 64 : 128))
+            return MAXSIM_ERR_CUDA;
+    }
     return launch_after(kern, static_cast<unsigned>(2 * std::min<int64_t>(a.items, std::max(1, dev.num_sms / 2))), kTileThreads,
-                        kSmem, 2, st, ta, tb, a);
+                        kSmem, 2, st, ta, tb, tout, a);
 }
 
 template <typename T, int kTN, bool kSwap, bool kKeepB>
 maxsim_status launch_tile(const LinearPlan& p, const LinearArgs& l, const __half* b16, bool a_prepared, int32_t* partial,
                           const HostDevice& dev, cudaStream_t st) {
     if constexpr (!kSwap) {  // swapped, a store is one channel per lane in any case
-        const bool rows16 = p.slices > 1 ? l.N % 4 == 0
-                                         : ptr_aligned(l.out, 16) && l.ld_out * static_cast<int64_t>(sizeof(T)) % 16 == 0;
+        // 16-bit outputs leave by TMA, which wants strides below 2^40 bytes and
+        // writes an odd row's last element with the one behind it
+        bool rows16 = p.slices > 1 ? l.N % 4 == 0 : ptr_aligned(l.out, 16) && l.ld_out * static_cast<int64_t>(sizeof(T)) % 16 == 0;
+        if (sizeof(T) == 2 && p.slices == 1) rows16 = rows16 && l.N % 8 == 0 && l.ld_out < (int64_t(1) << 38);
         if (!rows16) return launch_tile_rows<T, kTN, kSwap, kKeepB, false>(p, l, b16, a_prepared, partial, dev, st);
     }
     return launch_tile_rows<T, kTN, kSwap, kKeepB, true>(p, l, b16, a_prepared, partial, dev, st);
