@@ -232,9 +232,13 @@ constexpr int kTileThreads = 640;      // warp 0 TMA of A, warp 1 MMA, warp 2 TM
 constexpr int kTileMaxStages8 = 8;
 // Registers per thread: the launch gives every thread kTileRegs; warps 0-3 and
 // the widening warps hand registers to the epilogue warps, which hold a
-// tile's rounded outputs until they are stored.
-constexpr int kTileRegs = 96, kTileRegsCtl = 48, kTileRegsWiden = 80, kTileRegsEpi = 136;
-static_assert(kTileRegsCtl * 128 + (kTileRegsWiden + kTileRegsEpi) * 256 <= kTileRegs * kTileThreads, "register split");
+// tile's rounded outputs until they are stored. 16-bit outputs, which are held,
+// get 8 more than others (1048576 x 64 x 1024 f16 195 -> 189 us; f32 999 x 1537 x
+// 1111 would lose, 10.4 -> 11.2).
+constexpr int kTileRegs = 96, kTileRegsCtl = 48;
+__host__ __device__ constexpr int tile_regs_epi(bool held) { return held ? 144 : 136; }
+__host__ __device__ constexpr int tile_regs_widen(bool held) { return 216 - tile_regs_epi(held); }
+static_assert(kTileRegsCtl * 128 + 216 * 256 <= kTileRegs * kTileThreads, "register split");
 constexpr int kTileStage = 4096;       // staging of an epilogue warp: 32 x 32 sums
 constexpr uint32_t kTileACol = 256;    // tensor memory: accumulators in columns 0-255, the ring's A blocks above
 constexpr int kTileStatusTimeout = 4;  // MAXSIM_ERR_TIMEOUT
@@ -321,6 +325,24 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(taddr));
+}
+
+// Waits for this thread's tensor-memory loads; v, loaded by one of them, is not used before.
+__device__ __forceinline__ void tmem_wait_ld16(float (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+                 :
+                 : "memory");
+}
+
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Four K = 16 steps into d with A in tensor memory (8 columns a step) and B in
@@ -358,6 +380,19 @@ __device__ __forceinline__ TileItem tile_item(const TileArgs& a, uint32_t item, 
     t.kb0 = t.slice * a.kb_slice;
     t.kb1 = min(a.kb, t.kb0 + a.kb_slice);
     return t;
+}
+
+// a * b and a * b + c of two values in one instruction, each rounded once.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    mul2_rn(a.x, a.y, b.x, b.y);
+    return a;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
 }
 
 // Sums that are exact integers, for the join.
@@ -420,9 +455,9 @@ __device__ __forceinline__ void store4(T* p, int n, float a, float b, float c, f
 // storing in one kernel cost this one 3 to 8 %.)
 // A tile's K may be cut into slices (few tiles, long K): each slice then
 // writes its integer sums, and linear_join_kernel adds them.
-// Measured with the preparation: 32768 x 4096 x 4096 in 536 us, 2.05 PFLOP/s
+// Measured with the preparation: 32768 x 4096 x 4096 in 529 us, 2.08 PFLOP/s
 // (tensor pipe 90 % active; 597 us, 1.84 PFLOP/s, once the power limit holds the
-// clock), 1048576 x 128 x 1024 in 213 us, 6.3 TB/s (HBM), 2048 x 4096 x 1024 in 19.7 us
+// clock), 1048576 x 128 x 1024 in 215 us, 6.3 TB/s (HBM), 2048 x 4096 x 1024 in 18.4 us
 // (two rounds of tiles, the last one's stores).
 template <typename T, int kTN, bool kSwap, bool kKeepB, bool kRows16>
 __global__ void __launch_bounds__(kTileThreads, 1)
@@ -578,7 +613,7 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         }
     }
     } else if (warp < kTileEpiWarp0) {
-        regs_release<kTileRegsWiden>();
+        regs_release<tile_regs_widen(sizeof(T) == 2)>();
         // ------------------------------------------------------------ widening
         const int wg = (warp - kWidenWarp0) >> 2, q = warp & 3;
         const int row = q * 32 + lane;
@@ -626,7 +661,7 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
             }
         }
     } else {
-        regs_claim<kTileRegsEpi>();
+        regs_claim<tile_regs_epi(sizeof(T) == 2)>();
         // ------------------------------------------------------------ epilogue
         // A warp owns 32 rows of A and half of the tile's columns; in the
         // accumulator a lane holds a row. 16-bit outputs are scaled, rounded and
@@ -676,6 +711,7 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
             const int row_n = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(32), a.rows_a - ra0)));
             const bool in_a = lane < row_n;
             const float sa = next_sa, bias_a = next_bias_a;
+            const float2 sa2 = make_float2(sa, sa);
             float sb[kHold ? 1 : kChunks], bias[kHold || kSwap ? 1 : kChunks];
             if constexpr (kTma) {  // the table is written where the last tile's stores read
                 if (lane == 0) bulk_wait_read();
@@ -699,8 +735,37 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
             tc_fence_after();
             const uint32_t src = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * kTN + half * kCols);
             uint32_t held[kHold ? kChunks : 1][16];
+            if constexpr (kHold) {
+                if (hold) {
+                    constexpr int kParts = kCols / 16;  // one is in flight while another is worked on (2048 x 4096 x 1024 bf16 19.6 -> 18.7 us)
+                    float v[2][16];
+                    tmem_ld16(src, v[0]);
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
+                    for (int c = 0; c < kParts; ++c) {
+                        tmem_wait_ld16(v[c & 1]);
+                        if (c + 1 < kParts) {
+                            tmem_ld16(src + (c + 1) * 16, v[(c + 1) & 1]);
+                        } else {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive_remote(map_shared_rank(smem_u32(&ctl->acc_empty[buf]), 0));
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4) {
+                            const float4 s4 = *reinterpret_cast<const float4*>(tab + c * 16 + i);
+                            const float4 b4 = kSwap ? make_float4(bias_a, bias_a, bias_a, bias_a)
+                                                    : *reinterpret_cast<const float4*>(tab + kCols + c * 16 + i);
+                            const float* u = v[c & 1] + i;
+                            const float2 lo = fma2(mul2(make_float2(u[0], u[1]), sa2), make_float2(s4.x, s4.y), make_float2(b4.x, b4.y));
+                            const float2 hi = fma2(mul2(make_float2(u[2], u[3]), sa2), make_float2(s4.z, s4.w), make_float2(b4.z, b4.w));
+                            held[c / 2][(c & 1) * 8 + i / 2] = pack2<T>(lo.x, lo.y);
+                            held[c / 2][(c & 1) * 8 + i / 2 + 1] = pack2<T>(hi.x, hi.y);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < kChunks && !hold; ++c) {
                 const int64_t rb = rb0 + c * 32;
                 float v[32];
                 tmem_ld32(src + c * 32, v);
@@ -709,20 +774,6 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_remote(map_shared_rank(smem_u32(&ctl->acc_empty[buf]), 0));
-                }
-                if constexpr (kHold) {
-                    if (a.slices == 1) {
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            const float4 s4 = *reinterpret_cast<const float4*>(tab + c * 32 + i);
-                            const float4 b4 = kSwap ? make_float4(bias_a, bias_a, bias_a, bias_a)
-                                                    : *reinterpret_cast<const float4*>(tab + kCols + c * 32 + i);
-                            held[c][i / 2] = pack2<T>(__fmaf_rn(v[i] * sa, s4.x, b4.x), __fmaf_rn(v[i + 1] * sa, s4.y, b4.y));
-                            held[c][i / 2 + 1] =
-                                pack2<T>(__fmaf_rn(v[i + 2] * sa, s4.z, b4.z), __fmaf_rn(v[i + 3] * sa, s4.w, b4.w));
-                        }
-                        continue;
-                    }
                 }
                 if (row_n == 0 || rb >= a.rows_b) continue;
                 if constexpr (kSwap) {
