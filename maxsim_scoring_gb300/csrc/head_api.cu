@@ -15,57 +15,75 @@ namespace {
 
 constexpr int64_t kI32Max = 2147483647;
 
-template <typename T, bool kWide, bool kNorm, int kGroup, int kChunks>
+template <typename T, RowMode kMode, bool kNorm, int kGroup, int kChunks>
 maxsim_status launch_quantize_group(const QuantizeArgs& a, const HostDevice& dev, cudaStream_t st) {
     constexpr int kThreads = quantize_threads(kGroup);
     const unsigned grid = grid_of(a.rows, kThreads / kGroup, int64_t(dev.num_sms) * (2048 / kThreads));
-    quantize_rows_kernel<T, kWide, kNorm, kGroup, kChunks><<<grid, kThreads, 0, st>>>(a);
+    quantize_rows_kernel<T, kMode, kNorm, kGroup, kChunks><<<grid, kThreads, 0, st>>>(a);
     return launched();
 }
 
 // The smallest group that holds a row: short rows then share a warp (fewer
-// shuffle steps for a row, several rows' loads in flight), long ones take a
-// block.
-template <typename T, bool kWide, bool kNorm>
+// shuffle steps for a row, several rows' loads in flight), the shortest take a
+// thread each, long ones take a block.
+template <typename T, RowMode kMode, bool kNorm>
 maxsim_status launch_quantize(const QuantizeArgs& a, const HostDevice& dev, cudaStream_t st) {
-    const int64_t chunks = (a.cols + Chunk<T, kWide>::kVec - 1) / Chunk<T, kWide>::kVec;
-    if constexpr (kWide) {
-        if (chunks <= 8) return launch_quantize_group<T, kWide, kNorm, 8, 1>(a, dev, st);
-        if (chunks <= 16) return launch_quantize_group<T, kWide, kNorm, 8, 2>(a, dev, st);
-        if (chunks <= 32) return launch_quantize_group<T, kWide, kNorm, 8, 4>(a, dev, st);
-        if (chunks <= 64) return launch_quantize_group<T, kWide, kNorm, 8, 8>(a, dev, st);
-        if (chunks <= 128) return launch_quantize_group<T, kWide, kNorm, 32, 4>(a, dev, st);
-        if (chunks <= 256) return launch_quantize_group<T, kWide, kNorm, 32, 8>(a, dev, st);
-        if (chunks <= 512) return launch_quantize_group<T, kWide, kNorm, 128, 4>(a, dev, st);
-        if (chunks <= 1024) return launch_quantize_group<T, kWide, kNorm, 128, 8>(a, dev, st);
-        if (chunks <= 2048) return launch_quantize_group<T, kWide, kNorm, 512, 4>(a, dev, st);
-        if (chunks <= 4096) return launch_quantize_group<T, kWide, kNorm, 512, 8>(a, dev, st);
-    } else {  // single elements: more of them a thread
-        if (chunks <= kNarrow) {
-            quantize_narrow_rows_kernel<T, kNorm><<<grid_of(a.rows, 128, int64_t(dev.num_sms) * 16), 128, 0, st>>>(a);
-            return launched();
+    constexpr int kVec = QuantizeRow<T, kMode>::C::kVec;
+    const int64_t chunks = (a.cols + (kMode == kTouched ? 2 * kVec - 2 : kVec - 1)) / kVec;  // the most that a row touches
+    if constexpr (kMode != kSingle) {
+        if constexpr (kMode == kWhole) {  // measured, by single threads and by groups of 8: 3000000 x 16 bf16 32 and 133 us,
+            // 3000000 x 40 bf16 82 and 145, 3000000 x 32 f32 (eight chunks) 135 and 95
+            if (chunks <= 1) return launch_quantize_group<T, kMode, kNorm, 1, 1>(a, dev, st);
+            if (chunks <= 2) return launch_quantize_group<T, kMode, kNorm, 1, 2>(a, dev, st);
+            if (chunks <= 4) return launch_quantize_group<T, kMode, kNorm, 1, 4>(a, dev, st);
+            if (chunks <= 6) return launch_quantize_group<T, kMode, kNorm, 1, 6>(a, dev, st);
+            if (chunks <= 8) return launch_quantize_group<T, kMode, kNorm, 8, 1>(a, dev, st);
+            if (chunks <= 16) return launch_quantize_group<T, kMode, kNorm, 8, 2>(a, dev, st);
         }
-        if (chunks <= 16) return launch_quantize_group<T, kWide, kNorm, 8, 2>(a, dev, st);
-        if (chunks <= 32) return launch_quantize_group<T, kWide, kNorm, 8, 4>(a, dev, st);
-        if (chunks <= 64) return launch_quantize_group<T, kWide, kNorm, 8, 8>(a, dev, st);
-        if (chunks <= 128) return launch_quantize_group<T, kWide, kNorm, 8, 16>(a, dev, st);
-        if (chunks <= 256) return launch_quantize_group<T, kWide, kNorm, 32, 8>(a, dev, st);
-        if (chunks <= 512) return launch_quantize_group<T, kWide, kNorm, 32, 16>(a, dev, st);
-        if (chunks <= 1024) return launch_quantize_group<T, kWide, kNorm, 32, 32>(a, dev, st);
-        if (chunks <= 2048) return launch_quantize_group<T, kWide, kNorm, 128, 16>(a, dev, st);
-        if (chunks <= 4096) return launch_quantize_group<T, kWide, kNorm, 512, 8>(a, dev, st);
+        if (chunks <= 32) return launch_quantize_group<T, kMode, kNorm, 8, 4>(a, dev, st);
+        if (chunks <= 64) return launch_quantize_group<T, kMode, kNorm, 8, 8>(a, dev, st);
+        if (chunks <= 128) return launch_quantize_group<T, kMode, kNorm, 32, 4>(a, dev, st);
+        if constexpr (kMode == kTouched)
+            if (chunks <= 192) return launch_quantize_group<T, kMode, kNorm, 32, 6>(a, dev, st);
+        if (chunks <= 256) return launch_quantize_group<T, kMode, kNorm, 32, 8>(a, dev, st);
+        if (chunks <= 512) return launch_quantize_group<T, kMode, kNorm, kMode == kTouched ? 32 : 128, kMode == kTouched ? 16 : 4>(a, dev, st);
+        if (chunks <= 1024) return launch_quantize_group<T, kMode, kNorm, 128, 8>(a, dev, st);
+        if (chunks <= 2048) return launch_quantize_group<T, kMode, kNorm, 512, 4>(a, dev, st);
+        if (chunks <= 4096) return launch_quantize_group<T, kMode, kNorm, 512, 8>(a, dev, st);
+    } else {  // single elements: more of them a thread
+        if (chunks <= 12) return launch_quantize_group<T, kMode, kNorm, 1, 12>(a, dev, st);
+        if (chunks <= 16) return launch_quantize_group<T, kMode, kNorm, 8, 2>(a, dev, st);
+        if (chunks <= 32) return launch_quantize_group<T, kMode, kNorm, 8, 4>(a, dev, st);
+        if (chunks <= 64) return launch_quantize_group<T, kMode, kNorm, 8, 8>(a, dev, st);
+        if (chunks <= 128) return launch_quantize_group<T, kMode, kNorm, 8, 16>(a, dev, st);
+        if (chunks <= 256) return launch_quantize_group<T, kMode, kNorm, 32, 8>(a, dev, st);
+        if (chunks <= 512) return launch_quantize_group<T, kMode, kNorm, 32, 16>(a, dev, st);
+        if (chunks <= 1024) return launch_quantize_group<T, kMode, kNorm, 32, 32>(a, dev, st);
+        if (chunks <= 2048) return launch_quantize_group<T, kMode, kNorm, 128, 16>(a, dev, st);
+        if (chunks <= 4096) return launch_quantize_group<T, kMode, kNorm, 512, 8>(a, dev, st);
     }
-    quantize_long_rows_kernel<T, kWide, kNorm><<<grid_of(a.rows, 1, int64_t(dev.num_sms) * 4), 512, 0, st>>>(a);
+    quantize_long_rows_kernel<T, kMode, kNorm><<<grid_of(a.rows, 1, int64_t(dev.num_sms) * 4), 512, 0, st>>>(a);
     return launched();
+}
+
+template <typename T, bool kNorm>
+maxsim_status launch_quantize_mode(const QuantizeArgs& a, const HostDevice& dev, cudaStream_t st) {
+    constexpr int kVec = Chunk<T, true>::kVec;
+    if (a.cols % kVec == 0 && a.ld_x % kVec == 0 && a.ld_q % kVec == 0 && ptr_aligned(a.x, 16) && ptr_aligned(a.q, kVec))
+        return launch_quantize<T, kWhole, kNorm>(a, dev, st);
+    if constexpr (sizeof(T) == 2) {
+        // Measured, touched chunks and single elements: 608816 x 92 bf16 83 and 68 us, 500000 x 150 86 and 115,
+        // 6847 x 2505 23 and 38, 15875 x 7518 76 and 145; f32 60000 x 2001 126 and 104.
+        const uintptr_t phase = reinterpret_cast<uintptr_t>(a.x) / 2 - reinterpret_cast<uintptr_t>(a.q);
+        if (a.cols >= 128 && phase % kVec == 0 && (a.rows == 1 || (a.ld_x - a.ld_q) % kVec == 0))
+            return launch_quantize<T, kTouched, kNorm>(a, dev, st);
+    }
+    return launch_quantize<T, kSingle, kNorm>(a, dev, st);
 }
 
 template <typename T>
 maxsim_status launch_quantize_any(const QuantizeArgs& a, bool normalize, const HostDevice& dev, cudaStream_t st) {
-    constexpr int kVec = Chunk<T, true>::kVec;
-    const bool wide = a.cols % kVec == 0 && a.ld_x % kVec == 0 && a.ld_q % kVec == 0 && ptr_aligned(a.x, 16) &&
-                      ptr_aligned(a.q, kVec);
-    if (normalize) return wide ? launch_quantize<T, true, true>(a, dev, st) : launch_quantize<T, false, true>(a, dev, st);
-    return wide ? launch_quantize<T, true, false>(a, dev, st) : launch_quantize<T, false, false>(a, dev, st);
+    return normalize ? launch_quantize_mode<T, true>(a, dev, st) : launch_quantize_mode<T, false>(a, dev, st);
 }
 
 // The multiplier and shift that divide 0 <= i < 2^31 by d (round-up method: with l = ceil(log2 d),

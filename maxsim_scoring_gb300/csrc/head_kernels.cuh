@@ -33,14 +33,15 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 //
 // The scale, a 127th of max |x|, needs the whole row before the first code, so a
 // row is held in registers between the two: one read of x, one write of q. A
-// row belongs to a group of 8, 32, 128 or 512 threads, each holding up to kChunks
-// 16-byte chunks (or single elements where the rows do not start on 16-byte
-// boundaries); only rows beyond that are read twice. Several short rows share a
-// warp: fewer shuffle steps for a row, and their loads are in flight together.
+// row belongs to a group of 1, 8, 32, 128 or 512 threads, each holding up to
+// kChunks 16-byte chunks (or single elements, see RowMode); only rows beyond that
+// are read twice. Several short rows share a warp: fewer shuffle steps for a row,
+// and their loads are in flight together.
 // Bound by HBM: 5,000,000 x 128 f32 in 480 us (6.7 TB/s), 65536 x 4096 bf16 in
 // 121 us (6.6 TB/s); 16-bit rows of 128 with the norm in 220 us for 3,000,000 (5.3
-// TB/s, 70 % of the issue slots), odd widths by their single-element accesses
-// (100000 x 1023 bf16 in 106 us, 2.9 TB/s).
+// TB/s, 70 % of the issue slots), rows off their 16-byte boundaries by the
+// handling of their ends or by single elements (100000 x 1023 bf16 in 90 us, 3.4
+// TB/s, f32 in 110 us, 4.6 TB/s).
 
 // Maximum of two pairs of unsigned 16-bit values.
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
@@ -59,6 +60,25 @@ struct Chunk<T, true> {
     uint4 v;
     __device__ __forceinline__ void load(const T* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
     __device__ __forceinline__ void clear() { v = make_uint4(0, 0, 0, 0); }
+    // elements first .. last - 1 from p one by one, zeros around them
+    __device__ __forceinline__ void load_some(const T* p, int first, int last) {
+        alignas(16) T e[kVec];
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) e[i] = i >= first && i < last ? p[i] : from_f32<T>(0.f);
+        v = *reinterpret_cast<const uint4*>(e);
+    }
+    // zeros outside elements first .. last - 1
+    __device__ __forceinline__ void keep(int first, int last) {
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        constexpr int kPer = 4 / static_cast<int>(sizeof(T));  // elements of a word
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t m = i * kPer >= first && i * kPer < last ? (kPer == 1 ? 0xffffffffu : 0xffffu) : 0u;
+            if (kPer == 2 && i * 2 + 1 >= first && i * 2 + 1 < last) m |= 0xffff0000u;
+            w[i] &= m;
+        }
+        v = make_uint4(w[0], w[1], w[2], w[3]);
+    }
     __device__ __forceinline__ float get(int i) const {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         if constexpr (sizeof(T) == 4) {
@@ -209,11 +229,76 @@ struct QuantizeArgs {
     int32_t cols;
 };
 
+// How rows are read: element by element; in 16-byte chunks from their starts
+// (rows on 16-byte boundaries); or in the aligned chunks that they touch, whose
+// elements of other rows count as zeros and are not stored (rows anywhere, if
+// the codes of a chunk are an aligned piece of q too: the phases of x and q agree).
+enum RowMode { kSingle, kWhole, kTouched };
+
+template <typename T, RowMode kMode>
+struct QuantizeRow {
+    using C = Chunk<T, kMode != kSingle>;
+    const T* x;
+    int8_t* q;
+    int64_t before, after;  // elements of the operand in front of the row and from its start on
+    int32_t cols, skip;     // skip: elements of the first chunk that are not the row's
+
+    __device__ __forceinline__ QuantizeRow(const QuantizeArgs& a, int64_t r) {
+        before = r * a.ld_x;
+        after = (a.rows - 1 - r) * a.ld_x + a.cols;
+        x = static_cast<const T*>(a.x) + before;
+        q = a.q + r * a.ld_q;
+        cols = a.cols;
+        skip = kMode == kTouched ? static_cast<int32_t>(reinterpret_cast<uintptr_t>(x) / sizeof(T)) & (C::kVec - 1) : 0;
+    }
+    template <typename I>
+    __device__ __forceinline__ I col(I chunk) const { return chunk * C::kVec - skip; }
+    template <typename I>
+    __device__ __forceinline__ void load(C& c, I chunk, bool start) const {  // start: may hold the row's first element
+        const I at = col(chunk);
+        if (at >= cols) {
+            c.clear();
+        } else if constexpr (kMode != kTouched) {
+            c.load(x + at);
+        } else if ((!start || at >= 0) && at + C::kVec <= cols) {
+            c.load(x + at);
+        } else {
+            const int first = start && at < 0 ? static_cast<int>(-at) : 0, last = static_cast<int>(min(static_cast<I>(C::kVec), cols - at));
+            if (before + at >= 0 && at + C::kVec <= after) {
+                c.load(x + at);
+                c.keep(first, last);
+            } else {  // not past the operand's ends
+                c.load_some(x + at, first, last);
+            }
+        }
+    }
+    template <typename I>
+    __device__ __forceinline__ void store(const uint32_t* w, I chunk, bool start) const {
+        const I at = col(chunk);
+        if (at >= cols) return;
+        if constexpr (kMode != kTouched) {
+            C::store(q + at, w);
+        } else if ((!start || at >= 0) && at + C::kVec <= cols) {
+            C::store(q + at, w);
+        } else {
+#pragma unroll
+            for (int i = 0; i < C::kVec; ++i)
+                if ((!start || at + i >= 0) && at + i < cols) q[at + i] = static_cast<int8_t>(w[i / 4] >> (8 * (i % 4)));
+        }
+    }
+};
+
 __host__ __device__ constexpr int quantize_threads(int group) { return group > 128 ? group : 128; }
 
-template <typename T, bool kWide, bool kNorm, int kGroup, int kChunks>
-__global__ void __launch_bounds__(quantize_threads(kGroup)) quantize_rows_kernel(const QuantizeArgs a) {
-    using C = Chunk<T, kWide>;
+// Blocks of an SM that registers must leave room for: with few single elements a
+// thread, all of its threads (500000 x 30 f32 23.7 us, and 26 with 34 registers).
+// 0: none in particular.
+__host__ __device__ constexpr int quantize_blocks(RowMode mode, int chunks) { return mode == kSingle && chunks <= 4 ? 16 : 0; }
+
+template <typename T, RowMode kMode, bool kNorm, int kGroup, int kChunks>
+__global__ void __launch_bounds__(quantize_threads(kGroup), quantize_blocks(kMode, kChunks))
+quantize_rows_kernel(const QuantizeArgs a) {
+    using C = typename QuantizeRow<T, kMode>::C;
     constexpr int kThreads = quantize_threads(kGroup), kPerBlock = kThreads / kGroup;
     __shared__ uint32_t s_max[16];
     __shared__ float s_sum[16];
@@ -223,14 +308,10 @@ __global__ void __launch_bounds__(quantize_threads(kGroup)) quantize_rows_kernel
          r0 += static_cast<int64_t>(gridDim.x) * kPerBlock) {
         const int64_t r = r0 + g;
         const bool real = r < a.rows;
-        const T* xr = static_cast<const T*>(a.x) + (real ? r : r0) * a.ld_x;
+        const QuantizeRow<T, kMode> row(a, real ? r : r0);
         C c[kChunks];
 #pragma unroll
-        for (int j = 0; j < kChunks; ++j) {
-            const int32_t col = (j * kGroup + t) * C::kVec;
-            if (col < a.cols) c[j].load(xr + col);
-            else c[j].clear();
-        }
+        for (int j = 0; j < kChunks; ++j) row.load(c[j], j * kGroup + t, j == 0);
         uint32_t m = 0;
 #pragma unroll
         for (int j = 0; j < kChunks; ++j) m = c[j].fold_max(m);
@@ -241,10 +322,10 @@ __global__ void __launch_bounds__(quantize_threads(kGroup)) quantize_rows_kernel
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < kChunks; ++j) {
-            const int32_t col = (j * kGroup + t) * C::kVec;
+            if (kGroup == 1 && row.col(j) >= a.cols) continue;
             uint32_t w[2];
-            sum += code_chunk<T, kWide, kNorm>(c[j], s, inv, finite ? 0xffffffffu : 0u, w);
-            if (real && col < a.cols) C::store(a.q + r * a.ld_q + col, w);
+            sum += code_chunk<T, kMode != kSingle, kNorm>(c[j], s, inv, finite ? 0xffffffffu : 0u, w);
+            if (real) row.store(w, j * kGroup + t, j == 0);
         }
         if constexpr (kNorm) sum = group_sum<kGroup>(sum, s_sum);
         if (real && t == 0) a.scale[r] = row_scale<kNorm>(finite, s, sum);
@@ -252,54 +333,19 @@ __global__ void __launch_bounds__(quantize_threads(kGroup)) quantize_rows_kernel
     }
 }
 
-// Rows of up to kNarrow elements off their 16-byte boundaries, a thread each:
-// the work that a row costs besides its elements is then one lane's, not a
-// group's (1443119 x 5 f32: 13 us, and 42 by groups of eight threads; at 14
-// elements the groups are as fast).
-constexpr int kNarrow = 12;
-
-template <typename T, bool kNorm>
-__global__ void __launch_bounds__(128) quantize_narrow_rows_kernel(const QuantizeArgs a) {
-    using C = Chunk<T, false>;
-    for (int64_t r = blockIdx.x * 128ll + threadIdx.x; r < a.rows; r += gridDim.x * 128ll) {
-        const T* xr = static_cast<const T*>(a.x) + r * a.ld_x;
-        C c[kNarrow];
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < kNarrow; ++j) {
-            if (j < a.cols) c[j].load(xr + j);
-            else c[j].clear();
-            m = c[j].fold_max(m);
-        }
-        float s;
-        const bool finite = row_step<T>(m, &s);
-        const float inv = __frcp_rn(s);
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < kNarrow; ++j) {
-            if (j < a.cols) {
-                uint32_t w[1];
-                sum += code_chunk<T, false, kNorm>(c[j], s, inv, finite ? 0xffffffffu : 0u, w);
-                C::store(a.q + r * a.ld_q + j, w);
-            }
-        }
-        a.scale[r] = row_scale<kNorm>(finite, s, sum);
-    }
-}
-
 // Rows too long for the registers of a block: read once for the maximum, once for the codes.
-template <typename T, bool kWide, bool kNorm>
+template <typename T, RowMode kMode, bool kNorm>
 __global__ void __launch_bounds__(512) quantize_long_rows_kernel(const QuantizeArgs a) {
-    using C = Chunk<T, kWide>;
+    using C = typename QuantizeRow<T, kMode>::C;
     __shared__ uint32_t s_max[16];
     __shared__ float s_sum[16];
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        const T* xr = static_cast<const T*>(a.x) + r * a.ld_x;
+        const QuantizeRow<T, kMode> row(a, r);
         uint32_t m = 0;
 #pragma unroll 4
-        for (int64_t col = threadIdx.x * C::kVec; col < a.cols; col += 512 * C::kVec) {
+        for (int64_t i = threadIdx.x; row.col(i) < a.cols; i += 512) {
             C c;
-            c.load(xr + col);
+            row.load(c, i, true);
             m = c.fold_max(m);
         }
         m = group_max<512>(C::max_bits(m), s_max);
@@ -308,12 +354,12 @@ __global__ void __launch_bounds__(512) quantize_long_rows_kernel(const QuantizeA
         const float inv = __frcp_rn(s);
         float sum = 0.f;
 #pragma unroll 4
-        for (int64_t col = threadIdx.x * C::kVec; col < a.cols; col += 512 * C::kVec) {
+        for (int64_t i = threadIdx.x; row.col(i) < a.cols; i += 512) {
             C c;
-            c.load(xr + col);
+            row.load(c, i, true);
             uint32_t w[2];
-            sum += code_chunk<T, kWide, kNorm>(c, s, inv, finite ? 0xffffffffu : 0u, w);
-            C::store(a.q + r * a.ld_q + col, w);
+            sum += code_chunk<T, kMode != kSingle, kNorm>(c, s, inv, finite ? 0xffffffffu : 0u, w);
+            row.store(w, i, true);
         }
         if constexpr (kNorm) sum = group_sum<512>(sum, s_sum);
         if (threadIdx.x == 0) a.scale[r] = row_scale<kNorm>(finite, s, sum);

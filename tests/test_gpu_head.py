@@ -32,7 +32,9 @@ def f64(t):
 @pytest.mark.parametrize("rows,cols,pad,shift", [
     (1, 1, 0, 0), (3, 7, 0, 0), (32, 128, 0, 0), (33, 128, 8, 0), (5, 100, 3, 1), (2, 1024, 0, 1), (7, 1000, 24, 8),
     (4, 2048, 0, 0), (3, 4104, 0, 0), (2, 8193, 0, 0), (2, 20000, 8, 0), (1, 70001, 0, 3), (1000, 16, 0, 0), (777, 24, 0, 0),
-    (300, 5, 0, 0), (301, 17, 2, 1), (50, 85, 0, 0), (40, 250, 1, 0), (9, 511, 0, 0), (9, 1500, 1, 1), (3, 5001, 0, 0)])
+    (300, 5, 0, 0), (301, 17, 2, 1), (50, 85, 0, 0), (40, 250, 1, 0), (9, 511, 0, 0), (9, 1500, 1, 1), (3, 5001, 0, 0),
+    (500, 40, 0, 0), (200, 4, 0, 0), (70, 33, 0, 0), (41, 131, 0, 0), (40, 200, 8, 3), (33, 203, 16, 8), (17, 1039, 0, 0),
+    (13, 1100, 0, 4), (9, 1801, 8, 0), (5, 3003, 0, 0), (3, 33001, 0, 0), (2, 40003, 8, 0), (1, 129, 0, 8)])
 @pytest.mark.parametrize("normalize", [False, True])
 def test_quantize_rows(dtype, rows, cols, pad, shift, normalize):
     x = rows_of(np.random.default_rng(rows + cols), rows, cols, dtype, pad, shift)
@@ -44,7 +46,7 @@ def test_quantize_rows(dtype, rows, cols, pad, shift, normalize):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
-@pytest.mark.parametrize("cols", [7, 8, 13, 100, 129, 1024, 3001, 9000])
+@pytest.mark.parametrize("cols", [7, 8, 13, 40, 100, 129, 1024, 3001, 9000])
 @pytest.mark.parametrize("normalize", [False, True])
 def test_quantize_special_rows(dtype, cols, normalize):
     rng = np.random.default_rng(cols)
