@@ -84,6 +84,29 @@ def test_quantize_halfway_codes():
             assert np.array_equal(q.cpu().numpy(), head_ref.quantize(f64(x), False)[0])
 
 
+@pytest.mark.parametrize("cols,ld_x,ld_q,shift", [(131, 131, 131, 0), (131, 139, 147, 3), (200, 205, 205, 5), (1039, 1040, 1048, 7),
+                                                  (300, 301, 302, 1), (40, 48, 48, 8), (33001, 33009, 33001, 2)])
+def test_quantize_rows_leaves_what_is_not_theirs(cols, ld_x, ld_q, shift):
+    # codes between other bytes, values between NaN: neither the one nor the other may leak
+    lib = _native.lib()
+    rng = np.random.default_rng(cols)
+    rows = 7
+    for name, dt in DT.items():
+        x = torch.full((shift + rows * ld_x,), float("nan"), dtype=dt, device="cuda")
+        view = x[shift:].view(rows, ld_x)
+        view[:, :cols] = torch.from_numpy(rng.standard_normal((rows, cols)).astype(np.float32)).to("cuda", dt)
+        q = torch.full((shift + rows * ld_q,), 77, dtype=torch.int8, device="cuda")
+        codes_view = q[shift:].view(rows, ld_q)
+        scale = torch.empty(rows, device="cuda")
+        rc = lib.maxsim_quantize_rows(view.data_ptr(), ms.ops._DT_ANY[dt], rows, cols, ld_x, 0, codes_view.data_ptr(), ld_q,
+                                      scale.data_ptr(), torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        ref_q, ref_s, rel = head_ref.quantize(f64(view[:, :cols]), False)
+        assert np.array_equal(codes_view[:, :cols].cpu().numpy(), ref_q)
+        assert np.all(np.abs(f64(scale) - ref_s) <= rel * ref_s)
+        assert (codes_view[:, cols:] == 77).all() and (q[:shift] == 77).all()
+
+
 def test_quantize_empty_and_shapes():
     q, s = ms.quantize_rows(torch.empty((0, 16), device="cuda"))
     assert q.shape == (0, 16) and s.shape == (0,)
@@ -246,8 +269,8 @@ def test_linear_int8_rows_of_a_wider_output():
     rng = np.random.default_rng(8)
     lib = _native.lib()
     for M, shapes in ((3, ((70, 77, 3), (64, 96, 0), (300, 301, 1))), (150, ((70, 77, 3), (64, 96, 0), (300, 301, 1))),
-                      (9000, ((300, 301, 1), (304, 312, 0))), (300, ((9000, 9001, 3), (9000, 9008, 0))),
-                      (20000, ((70, 77, 3), (128, 136, 0), (50, 56, 8))), (2000, ((4100, 4101, 0),)),
+                      (9000, ((300, 301, 1), (304, 312, 0), (300, 302, 2), (606, 618, 4))), (300, ((9000, 9001, 3), (9000, 9008, 0))),
+                      (20000, ((70, 77, 3), (128, 136, 0), (50, 56, 8), (33, 34, 1))), (2000, ((4100, 4101, 0),)),
                       (4100, ((2000, 2008, 0), (1999, 2000, 8)))):
         for N, ld, off in shapes:
             x, w = codes(rng, M, 128), codes(rng, N, 128)
