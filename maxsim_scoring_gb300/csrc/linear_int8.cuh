@@ -451,8 +451,8 @@ __device__ __forceinline__ void store4(T* p, int n, float a, float b, float c, f
 // the widening took). Where B is a single tile of rows and fits, as a head's
 // weights do, it is loaded once and kept (kKeepB).
 // kRows16: rows of out (of the sums) start on 16-byte boundaries, and those of
-// 16-bit outputs end there. (Both ways of
-// storing in one kernel cost this one 3 to 8 %.)
+// 16-bit outputs end there. (Both ways of storing in one kernel cost this one
+// 3 to 8 %.)
 // A tile's K may be cut into slices (few tiles, long K): each slice then
 // writes its integer sums, and linear_join_kernel adds them.
 // Measured with the preparation: 32768 x 4096 x 4096 in 529 us, 2.08 PFLOP/s
@@ -737,7 +737,8 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
             uint32_t held[kHold ? kChunks : 1][16];
             if constexpr (kHold) {
                 if (hold) {
-                    constexpr int kParts = kCols / 16;  // one is in flight while another is worked on (2048 x 4096 x 1024 bf16 19.6 -> 18.7 us)
+                    // one part is in flight while another is worked on (2048 x 4096 x 1024 bf16 19.6 -> 18.7 us)
+                    constexpr int kParts = kCols / 16;
                     float v[2][16];
                     tmem_ld16(src, v[0]);
 #pragma unroll
