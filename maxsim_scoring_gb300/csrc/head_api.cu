@@ -23,13 +23,18 @@ maxsim_status launch_quantize_group(const QuantizeArgs& a, const HostDevice& dev
     return launched();
 }
 
+// The most chunks of vec elements that a row of cols touches. (In 64 bits: cols goes up to 2^31 - 1.)
+constexpr int64_t most_chunks(int64_t cols, int vec, RowMode mode) {
+    return (cols + (mode == kTouched ? 2 * vec - 2 : vec - 1)) / vec;
+}
+static_assert(most_chunks(int32_t{kI32Max}, 8, kTouched) == (int64_t{1} << 28) + 1, "the longest row");
+
 // The smallest group that holds a row: short rows then share a warp (fewer
 // shuffle steps for a row, several rows' loads in flight), the shortest take a
 // thread each, long ones take a block.
 template <typename T, RowMode kMode, bool kNorm>
 maxsim_status launch_quantize(const QuantizeArgs& a, const HostDevice& dev, cudaStream_t st) {
-    constexpr int kVec = QuantizeRow<T, kMode>::C::kVec;
-    const int64_t chunks = (a.cols + (kMode == kTouched ? 2 * kVec - 2 : kVec - 1)) / kVec;  // the most that a row touches
+    const int64_t chunks = most_chunks(a.cols, QuantizeRow<T, kMode>::C::kVec, kMode);
     if constexpr (kMode != kSingle) {
         if constexpr (kMode == kWhole) {  // measured, by single threads and by groups of 8: 3000000 x 16 bf16 32 and 133 us,
             // 3000000 x 40 bf16 82 and 145, 3000000 x 32 f32 (eight chunks) 135 and 95
