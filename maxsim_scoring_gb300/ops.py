@@ -2,12 +2,16 @@
 
 Every function here checks shapes / dtypes, allocates outputs and workspace
 with torch on the tensors' device, and calls the entry point of the same name
-in libmaxsim.so on the current CUDA stream. All arithmetic happens in the
-CUDA kernels behind that call.
+in libmaxsim.so on that device's current CUDA stream. All arithmetic happens in
+the CUDA kernels behind that call. The library launches on the calling thread's
+current device: where the tensors are on another one, the call is made with
+theirs current.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 from typing import Optional
 
 import torch
@@ -19,6 +23,30 @@ _DT_ANY = {**_DT, torch.float32: _native.F32}
 
 
 _SIZE_MAX = ctypes.c_size_t(-1).value
+
+# The calling thread's current device (without the initialisation check of
+# torch.cuda.current_device: asked only where a CUDA tensor is at hand).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _with_device(index: int, fn, *args, **kwargs):
+    """fn(...) with device `index` current."""
+    with torch.cuda.device(index):
+        return fn(*args, **kwargs)
+
+
+def _on_tensors_device(fn):
+    """fn, run with the device of its first argument current."""
+    first = next(iter(inspect.signature(fn).parameters))
+
+    @functools.wraps(fn)
+    def call(*args, **kwargs):
+        t = args[0] if args else kwargs.get(first)
+        index = t.get_device() if isinstance(t, torch.Tensor) else -1
+        if index >= 0 and index != _current_device():
+            return _with_device(index, fn, *args, **kwargs)
+        return fn(*args, **kwargs)
+    return call
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -71,6 +99,7 @@ def _workspace(nbytes: int, device, ws: Optional[torch.Tensor]):
     return t, nbytes
 
 
+@_on_tensors_device
 def maxsim_fwd(Q: torch.Tensor, D: torch.Tensor, q_mask=None, d_mask=None, *, want_argmax: bool = False,
                scores: Optional[torch.Tensor] = None, argmax: Optional[torch.Tensor] = None,
                workspace: Optional[torch.Tensor] = None):
@@ -95,6 +124,7 @@ def maxsim_fwd(Q: torch.Tensor, D: torch.Tensor, q_mask=None, d_mask=None, *, wa
     return scores, argmax
 
 
+@_on_tensors_device
 def maxsim_fwd_varlen(Q: torch.Tensor, cu_seqlens_q: Optional[torch.Tensor], max_lq: int, D: torch.Tensor,
                       cu_seqlens_d: torch.Tensor, q_mask=None, d_mask=None, *, want_argmax: bool = False,
                       scores: Optional[torch.Tensor] = None, argmax: Optional[torch.Tensor] = None,
@@ -131,6 +161,7 @@ def maxsim_fwd_varlen(Q: torch.Tensor, cu_seqlens_q: Optional[torch.Tensor], max
     return scores, argmax
 
 
+@_on_tensors_device
 def maxsim_score_pairs_packed(Q: torch.Tensor, cu_seqlens_q: Optional[torch.Tensor], max_lq: int, D: torch.Tensor,
                               cu_seqlens_d: torch.Tensor, pairs: torch.Tensor, q_mask=None, d_mask=None, *,
                               want_argmax: bool = False, scores: Optional[torch.Tensor] = None,
@@ -168,6 +199,7 @@ def maxsim_score_pairs_packed(Q: torch.Tensor, cu_seqlens_q: Optional[torch.Tens
     return scores, argmax
 
 
+@_on_tensors_device
 def maxsim_bwd(Q: torch.Tensor, D: torch.Tensor, argmax: torch.Tensor, grad_scores: torch.Tensor, q_mask=None, *,
                want_dq: bool = True, want_dd: bool = True, want_csr: bool = False,
                dQ: Optional[torch.Tensor] = None, dD: Optional[torch.Tensor] = None,
@@ -200,6 +232,7 @@ def maxsim_bwd(Q: torch.Tensor, D: torch.Tensor, argmax: torch.Tensor, grad_scor
     return dQ, dD, row_ptr, col
 
 
+@_on_tensors_device
 def maxsim_bwd_varlen(Q: torch.Tensor, cu_seqlens_q: Optional[torch.Tensor], max_lq: int, D: torch.Tensor,
                       cu_seqlens_d: torch.Tensor, max_ld: int, argmax: torch.Tensor, grad_scores: torch.Tensor,
                       q_mask=None, *, want_dq: bool = True, want_dd: bool = True, want_csr: bool = False,
@@ -233,6 +266,7 @@ def maxsim_bwd_varlen(Q: torch.Tensor, cu_seqlens_q: Optional[torch.Tensor], max
     return dQ, dD, row_ptr, col
 
 
+@_on_tensors_device
 def maxsim_fwd_int8(Q: torch.Tensor, q_scale: torch.Tensor, D: torch.Tensor, d_scale: torch.Tensor, q_mask=None,
                     d_mask=None, *, want_argmax: bool = False, want_win_dot: bool = False,
                     scores: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
@@ -263,6 +297,7 @@ def _points(P: torch.Tensor, Q: torch.Tensor):
     return _contig(P, "P", torch.float32), _contig(Q, "Q", torch.float32, dev), dev
 
 
+@_on_tensors_device
 def chamfer_fwd(P: torch.Tensor, Q: torch.Tensor, *, workspace: Optional[torch.Tensor] = None):
     """Chamfer distance of B pairs of point sets P [B,N,dim], Q [B,M,dim] (f32).
 
@@ -283,6 +318,7 @@ def chamfer_fwd(P: torch.Tensor, Q: torch.Tensor, *, workspace: Optional[torch.T
     return loss, dist_p, idx_p, dist_q, idx_q
 
 
+@_on_tensors_device
 def chamfer_bwd(P: torch.Tensor, Q: torch.Tensor, idx_p: torch.Tensor, idx_q: torch.Tensor, grad_loss: torch.Tensor,
                 *, dP: Optional[torch.Tensor] = None, dQ: Optional[torch.Tensor] = None,
                 workspace: Optional[torch.Tensor] = None):
@@ -309,6 +345,7 @@ def chamfer_bwd(P: torch.Tensor, Q: torch.Tensor, idx_p: torch.Tensor, idx_q: to
     return dP, dQ
 
 
+@_on_tensors_device
 def maxsim_topk(scores: torch.Tensor, k: int):
     """(values [R, k] f32, indices [R, k] i32): the k largest entries of every
     row of scores [R, n] (f32), descending, the lower index first among ties."""
@@ -323,6 +360,7 @@ def maxsim_topk(scores: torch.Tensor, k: int):
     return vals, idx
 
 
+@_on_tensors_device
 def maxsim_two_stage_topk(Q8: torch.Tensor, q_scale: torch.Tensor, D8: torch.Tensor, d_scale: torch.Tensor,
                           Q16: torch.Tensor, D16: torch.Tensor, k1: int, k: int, *, want_stage1: bool = False,
                           workspace: Optional[torch.Tensor] = None):
@@ -352,6 +390,7 @@ def maxsim_two_stage_topk(Q8: torch.Tensor, q_scale: torch.Tensor, D8: torch.Ten
     return top_idx, top_scores, s8, cand
 
 
+@_on_tensors_device
 def maxsim_fwd_streamed(Q: torch.Tensor, D_host: torch.Tensor, q_mask=None, *, block_docs: int = 20_000,
                         scores: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
     """Scores [Nq, Nd] of a device query batch Q [Nq,Lq,d] against a corpus
@@ -378,6 +417,7 @@ def maxsim_fwd_streamed(Q: torch.Tensor, D_host: torch.Tensor, q_mask=None, *, b
     return scores
 
 
+@_on_tensors_device
 def maxsim_fwd_varlen_streamed(Q: torch.Tensor, cu_seqlens_q: Optional[torch.Tensor], max_lq: int,
                                D_host: torch.Tensor, cu_seqlens_d_host: torch.Tensor, q_mask=None, *,
                                block_docs: int = 20_000, block_tokens: int = 1 << 22,
@@ -463,6 +503,8 @@ def quantize_rows(x: torch.Tensor, *, normalize: bool = False, q: Optional[torch
     if dt is None:
         raise TypeError(f"x must be float16, bfloat16 or float32, got {x.dtype}")
     index, shape, dev = _device(x, "x"), x.shape, x.device
+    if index != _current_device():
+        return _with_device(index, quantize_rows, x, normalize=normalize, q=q, scale=scale)
     x, rows, ld = _rows(x, "x")
     cols = shape[-1]
     q = torch.empty(shape, dtype=torch.int8, device=dev) if q is None else _given(q, "q", shape, torch.int8, dev)
@@ -489,6 +531,9 @@ def linear_int8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale
     if x_scale.dtype is not torch.float32 or w_scale.dtype is not torch.float32:
         raise TypeError("x_scale, w_scale and bias must be float32")
     index, shape, channels = _device(x, "x"), x.shape, w.shape
+    if index != _current_device():
+        return _with_device(index, linear_int8, x, x_scale, w, w_scale, bias, out_dtype=out_dtype, out=out,
+                            workspace=workspace)
     if w.get_device() != index or x_scale.get_device() != index or w_scale.get_device() != index:
         raise ValueError("x, w, their scales and bias must be on one device")
     if len(channels) != 2 or not shape or shape[-1] != channels[1]:
@@ -543,6 +588,8 @@ def dropout_fwd(x: torch.Tensor, p: float, seed: int, offset: int = 0, residual:
     if dt is None:
         raise TypeError(f"x must be float16, bfloat16 or float32, got {x.dtype}")
     index, shape, dev = _device(x, "x"), x.shape, x.device
+    if index != _current_device():
+        return _with_device(index, dropout_fwd, x, p, seed, offset, residual, out=out)
     pr, ld_r = None, 0
     if residual is not None:
         if residual.shape != shape or residual.dtype is not x.dtype or residual.get_device() != index:
@@ -567,6 +614,8 @@ def dropout_bwd(grad: torch.Tensor, p: float, seed: int, offset: int = 0, *,
     if dt is None:
         raise TypeError(f"grad must be float16, bfloat16 or float32, got {grad.dtype}")
     index, shape, dev = _device(grad, "grad"), grad.shape, grad.device
+    if index != _current_device():
+        return _with_device(index, dropout_bwd, grad, p, seed, offset, out=out)
     grad, rows, ld = _rows(grad, "grad")
     cols = shape[-1]
     out = (torch.empty(shape, dtype=grad.dtype, device=dev) if out is None
@@ -581,7 +630,8 @@ def dropout_bwd(grad: torch.Tensor, p: float, seed: int, offset: int = 0, *,
 def device_status(device=None) -> int:
     """Synchronise the current stream and return (and clear) the device status word."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    return int(_native.lib().maxsim_device_status(_stream(dev)))
+    with torch.cuda.device(dev):
+        return int(_native.lib().maxsim_device_status(_stream(dev)))
 
 
 def debug_inject_wait_timeout(limit_ns: int) -> None:
