@@ -92,6 +92,8 @@ def _workspace(nbytes: int, device, ws: Optional[torch.Tensor]):
     if nbytes == 0:
         return None, 0
     if ws is not None:
+        if ws.device != device or not ws.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {device}")
         if ws.numel() * ws.element_size() < nbytes:
             raise ValueError(f"workspace needs {nbytes} bytes")
         return ws, ws.numel() * ws.element_size()

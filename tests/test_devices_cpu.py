@@ -85,3 +85,13 @@ def test_other_entry_points_run_with_the_tensors_device_current(fake):
                ms.maxsim_fwd_int8, ms.chamfer_fwd, ms.chamfer_bwd, ms.maxsim_topk, ms.maxsim_two_stage_topk,
                ms.maxsim_fwd_streamed, ms.maxsim_fwd_varlen_streamed):
         assert fn.__wrapped__.__name__ == fn.__name__
+
+
+@pytest.mark.parametrize("workspace", [torch.zeros(64, dtype=torch.uint8), torch.zeros(64, 2, dtype=torch.uint8, device="meta")[:, 0]])
+def test_workspace_elsewhere_or_strided_is_refused(workspace):
+    # its bytes from data_ptr() on would not be the device's, or not the tensor's
+    with pytest.raises(ValueError):
+        ops._workspace(32, torch.device("meta"), workspace)
+    assert ops._workspace(32, torch.device("meta"), torch.zeros(64, dtype=torch.uint8, device="meta"))[1] == 64
+    with pytest.raises(ValueError):
+        ops._workspace(65, torch.device("meta"), torch.zeros(64, dtype=torch.uint8, device="meta"))
