@@ -89,11 +89,13 @@ class _Dropout(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad):
-        dx = ops.dropout_bwd(grad, *ctx.args) if ctx.needs_input_grad[0] else None
+        # for a mask the map is linear and its own transpose: dropout of the gradient, itself differentiable
+        dx = _Dropout.apply(grad, None, *ctx.args) if ctx.needs_input_grad[0] else None
         return dx, grad if ctx.needs_input_grad[1] else None, None, None, None
 
 
 def dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0, residual=None) -> torch.Tensor:
     """Differentiable dropout of x (plus `residual` where given): nothing is
-    saved but (p, seed, offset), from which the backward draws the mask again."""
+    saved but (p, seed, offset), from which the backward draws the mask again;
+    differentiable at every order."""
     return _Dropout.apply(x, residual, p, seed, offset)
