@@ -376,11 +376,13 @@ maxsim_status maxsim_quantize_rows(const void *x, maxsim_dtype dtype, int64_t ro
  *   x [M, K] i8, rows ld_x apart;  x_scale [M] f32
  *   w [N, K] i8, rows ld_w apart;  w_scale [N] f32;  bias [N] f32 or NULL
  *   out [M, N] f16 / bf16 / f32 (out_dtype), rows ld_out elements apart
- * All of [-128, 127] is taken. Few tokens and small products are summed
- * exactly in 32-bit integers; larger ones by the tensor cores in fp32, where
- * products are exact and sums are while they stay below 2^24 (always for
- * K <= 1024). The same call on the same inputs gives the same bits. K = 0 gives
- * the bias. Scales and bias need 4-byte alignment. 0 <= M, N < 2^31 - 1023,
+ * All of [-128, 127] is taken. The sum over k is exact and rounded once to
+ * fp32, the scales and the bias are applied in fp32: an f32 row has the same
+ * bits whatever rows are with it. Only 16-bit outputs of larger products (not
+ * few tokens, K > 1024) are summed in one fp32 accumulator: exact while its
+ * partial sums stay below 2^24, past that each step of 16 products may lose
+ * 2^-23 of the partial sum. The same call on the same inputs gives the same
+ * bits. K = 0 gives the bias (with finite scales). Scales and bias need 4-byte alignment. 0 <= M, N < 2^31 - 1023,
  * K <= 131071.
  * Operands may start anywhere; larger products copy one whose pointer, row
  * stride or K is not a multiple of 16 into the workspace first. Workspace: maxsim_workspace_size(

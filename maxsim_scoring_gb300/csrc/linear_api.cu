@@ -41,7 +41,7 @@ inline bool few_kernel(int64_t M, int64_t N, int64_t K, bool whole) {
     return groups * tiles * (chunks * (whole ? 1 : 3) + 4) <= kFewCost;
 }
 
-LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool x_direct, bool w_direct) {
+LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool x_direct, bool w_direct, bool out32) {
     LinearPlan p;
     if (M == 0 || N == 0 || K == 0) return p;
     p.k_pad = (K + 15) / 16 * 16;
@@ -71,6 +71,7 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool x_direct, bool w_di
         for (int32_t slices = 1; slices <= std::min(p.kb, 16); ++slices) {
             const int32_t kb_slice = (p.kb + slices - 1) / slices;
             if (slices > 1 && (tiles * slices > 2 * kPairs || (p.kb + kb_slice - 1) / kb_slice != slices)) continue;
+            if (tn == 256 && parts_needed(kb_slice) && (out32 || slices > 1)) continue;
             double cost = static_cast<double>((tiles * slices + kPairs - 1) / kPairs) * (kb_slice * block + ends);
             if (slices > 1) cost += 5000.0 + static_cast<double>(M) * N * slices * 4.0 / 1500.0;
             if (best == 0.0 || cost < best) {
@@ -99,7 +100,8 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool x_direct, bool w_di
 size_t linear_int8_ws_bytes(int64_t M, int64_t N, int64_t K, int64_t ld_x, int64_t ld_w) {
     if (M < 0 || N < 0 || K < 0 || ld_x < 0 || ld_w < 0 || M > kLinearMaxRows || N > kLinearMaxRows || K > kLinearMaxK)
         return static_cast<size_t>(-1);
-    return plan_linear(M, N, K, rows_direct(K, ld_x), rows_direct(K, ld_w)).bytes;
+    const bool x_direct = rows_direct(K, ld_x), w_direct = rows_direct(K, ld_w);
+    return std::max(plan_linear(M, N, K, x_direct, w_direct, false).bytes, plan_linear(M, N, K, x_direct, w_direct, true).bytes);
 }
 
 }  // namespace maxsim
@@ -121,7 +123,7 @@ maxsim_status maxsim_linear_int8(const int8_t* x, int64_t ld_x, const float* x_s
         return MAXSIM_ERR_INVALID_ARG;
     if (K > 0 && (!x || !w)) return MAXSIM_ERR_INVALID_ARG;
     const bool x_direct = rows_direct(K, ld_x) && ptr_aligned(x, 16), w_direct = rows_direct(K, ld_w) && ptr_aligned(w, 16);
-    const LinearPlan p = plan_linear(M, N, K, x_direct, w_direct);
+    const LinearPlan p = plan_linear(M, N, K, x_direct, w_direct, out_dtype == MAXSIM_F32);
     if (p.tiles * p.slices > kI32Max) return MAXSIM_ERR_UNSUPPORTED;
     if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes || !ptr_aligned(workspace, 256)))
         return MAXSIM_ERR_WORKSPACE;

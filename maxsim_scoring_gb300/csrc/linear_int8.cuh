@@ -5,7 +5,8 @@
 // 8-bit integer form was measured at 150 TOP/s, a quarter of the f16 form's
 // 605 TFLOP/s. So both kernels widen the integers to binary16 on the SM, next
 // to the tensor cores: |v| <= 128 is exact there, a product of two is exact in
-// fp32, and a sum of up to 1,024 products (2^24) is too.
+// fp32, and a sum of up to 1,024 products (2^24) is too; longer ones are added
+// as integers (16-bit outputs of the tile kernel apart, see parts_needed).
 //
 //  * linear_few_kernel (few tokens, and small products of any shape): bound by
 //    the bytes of w, each read once per 32 tokens, or by its launch.
@@ -226,6 +227,7 @@ __global__ void __launch_bounds__(kFewWarps * 32) linear_few_kernel(const Linear
 
 constexpr int kTileM = 256;            // rows of A per tile: 128 on each CTA of a pair
 constexpr int kTileK = 128;            // values of K per block
+constexpr int kExactBlocks = 8;        // blocks whose sums are exact in fp32: 1,024 products of at most 2^14
 constexpr int kTileRing = 4;           // blocks ready for the MMA: A in tensor memory, B in shared memory
 constexpr int kTileBWarp = 2, kWidenWarp0 = 4, kTileEpiWarp0 = 12;
 constexpr int kTileThreads = 640;      // warp 0 TMA of A, warp 1 MMA, warp 2 TMA of B, warps 4-11 widen, 12-19 epilogue
@@ -257,9 +259,21 @@ struct TileCfg {
     static constexpr int kAcc = kTN == 256 ? 1 : 2;    // accumulator buffers
 };
 
+// Whether 32-bit results (f32 outputs, and the integer sums of slices) of `blocks`
+// blocks of K are summed in parts. Past kExactBlocks an fp32 accumulator may
+// round; the epilogue then takes what it holds and adds the parts without loss,
+// as 32-bit integers, or two of them as floats (the one rounding of an exact
+// sum). Tiles of 256 columns have no registers for those sums: 32768 x 4096 x
+// 4096 f32 takes 700 us in tiles of 128, and 585 in one accumulator of 256
+// columns; shorter or narrower products lose 2 to 11 %. 16-bit outputs stay in one
+// accumulator (528 us; tiles of 128 columns without parts take 644): past 2^24
+// a step of 16 products may lose 2^-23 of the partial sum, for sums of one
+// sign up to K = 16,384 at most a quarter of an f16 output's rounding.
+constexpr bool parts_needed(int32_t blocks) { return blocks > kExactBlocks; }
+
 struct TileArgs {
     LinearArgs l;
-    int32_t* partial;   // [slices, M, N] integer sums when slices > 1
+    int32_t* partial;   // [slices, M, N] integer sums (T = int32_t)
     int64_t items;      // tiles * slices, < 2^32 (the divisions of short items are worth 32 bits)
     int32_t rows_a;     // rows of A (tokens, or channels when swapped)
     int32_t rows_b;
@@ -267,6 +281,7 @@ struct TileArgs {
     int32_t slices;     // parts of K
     int32_t kb;         // blocks of K
     int32_t kb_slice;   // blocks per slice
+    int32_t kb_part;    // kParts: blocks per part, of one size but for a slice's last one
     int a_prepared;     // A too was laid out by linear_prep_kernel
     int* status;
     uint64_t timeout_ns;
@@ -395,9 +410,9 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     return d;
 }
 
-// Sums that are exact integers, for the join.
+// Integer sums pass the epilogue as their bits.
 template <>
-__device__ __forceinline__ int32_t from_f32<int32_t>(float v) { return __float2int_rn(v); }
+__device__ __forceinline__ int32_t from_f32<int32_t>(float v) { return __float_as_int(v); }
 
 // Byte of the 16-byte piece c of row r in a warp's staging tile [32][32] of
 // 4-byte values: 32 lanes that write one piece each of their own row, or read
@@ -454,12 +469,13 @@ __device__ __forceinline__ void store4(T* p, int n, float a, float b, float c, f
 // 16-bit outputs end there. (Both ways of storing in one kernel cost this one
 // 3 to 8 %.)
 // A tile's K may be cut into slices (few tiles, long K): each slice then
-// writes its integer sums, and linear_join_kernel adds them.
+// writes its integer sums (T = int32_t), and linear_join_kernel adds them.
+// kParts: 32-bit results of more than kExactBlocks blocks of K (parts_needed).
 // Measured with the preparation: 32768 x 4096 x 4096 in 529 us, 2.08 PFLOP/s
 // (tensor pipe 90 % active; 597 us, 1.84 PFLOP/s, once the power limit holds the
 // clock), 1048576 x 128 x 1024 in 215 us, 6.3 TB/s (HBM), 2048 x 4096 x 1024 in 18.4 us
 // (two rounds of tiles, the last one's stores).
-template <typename T, int kTN, bool kSwap, bool kKeepB, bool kRows16>
+template <typename T, int kTN, bool kSwap, bool kKeepB, bool kRows16, bool kParts>
 __global__ void __launch_bounds__(kTileThreads, 1)
 linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                    const __grid_constant__ CUtensorMap tm_out, const TileArgs a) {
@@ -472,7 +488,9 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     TileCtl* ctl = reinterpret_cast<TileCtl*>(s_out + 8 * kTileStage);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
-    if (a.slices > 1) begin_dependents();
+    constexpr bool kSums = std::is_same_v<T, int32_t>;
+    static_assert(!kParts || (sizeof(T) == 4 && kTN <= 128), "registers for the parts' sums");
+    if constexpr (kSums) begin_dependents();
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages8; ++s) {
             mbar_init(smem_u32(&ctl->full8[s]), 1);
@@ -574,22 +592,27 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
             if (kKeepB && first < a.items) ok = tile_wait_warp<true>(a, ctl, &ctl->b_full[0], 0);
             for (int64_t it = first; it < a.items && ok; it += step) {
                 const TileItem t = tile_item<kTN>(a, it, rank);
-                if (!tile_wait_warp<true>(a, ctl, &ctl->acc_empty[buf], buf_phase ^ 1u)) break;
-                tc_fence_after();
-                const uint32_t d = tmem + static_cast<uint32_t>(buf * kTN);
-                for (int32_t kb = t.kb0; kb < t.kb1; ++kb) {
-                    if (!tile_wait_warp<true>(a, ctl, &ctl->ready[ring], ring_phase)) { ok = false; break; }
+                int32_t s0 = t.kb0;
+                do {  // a run of blocks that are summed in one accumulator
+                    const int32_t s1 = kParts ? min(t.kb1, s0 + a.kb_part) : t.kb1;
+                    if (!tile_wait_warp<true>(a, ctl, &ctl->acc_empty[buf], buf_phase ^ 1u)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t at = tmem + kTileACol + static_cast<uint32_t>(ring * 64);
-                    const uint64_t b = b0 + static_cast<uint64_t>(((kKeepB ? kb : ring) * C::kB16) >> 4);
-                    mma_chain4_ts(d, at, b, idesc, kb > t.kb0 ? 1u : 0u);
-                    mma_chain4_ts(d, at + 32, b + (C::kBAtom >> 4), idesc, 1u);
-                    mma_commit_elect<2>(smem_u32(&ctl->freed[ring]));
-                    if (++ring == kTileRing) { ring = 0; ring_phase ^= 1u; }
-                }
-                if (!ok) break;
-                mma_commit_elect<2>(smem_u32(&ctl->acc_full[buf]));
-                if (++buf == C::kAcc) { buf = 0; buf_phase ^= 1u; }
+                    const uint32_t d = tmem + static_cast<uint32_t>(buf * kTN);
+                    for (int32_t kb = s0; kb < s1; ++kb) {
+                        if (!tile_wait_warp<true>(a, ctl, &ctl->ready[ring], ring_phase)) { ok = false; break; }
+                        tc_fence_after();
+                        const uint32_t at = tmem + kTileACol + static_cast<uint32_t>(ring * 64);
+                        const uint64_t b = b0 + static_cast<uint64_t>(((kKeepB ? kb : ring) * C::kB16) >> 4);
+                        mma_chain4_ts(d, at, b, idesc, kb > s0 ? 1u : 0u);
+                        mma_chain4_ts(d, at + 32, b + (C::kBAtom >> 4), idesc, 1u);
+                        mma_commit_elect<2>(smem_u32(&ctl->freed[ring]));
+                        if (++ring == kTileRing) { ring = 0; ring_phase ^= 1u; }
+                    }
+                    if (!ok) break;
+                    mma_commit_elect<2>(smem_u32(&ctl->acc_full[buf]));
+                    if (++buf == C::kAcc) { buf = 0; buf_phase ^= 1u; }
+                    s0 = s1;
+                } while (kParts && s0 < t.kb1);
             }
             // every MMA issued above completes before the CTA leaves
             mma_commit_elect<2>(smem_u32(&ctl->mma_done), 1);
@@ -679,8 +702,7 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         constexpr bool kHold = sizeof(T) == 2, kTma = kHold && kRows16 && !kSwap;
         uint8_t* stage = s_out + (warp - kTileEpiWarp0) * kTileStage;
         float* tab = reinterpret_cast<float*>(stage);  // kHold: scales of the kCols columns, then biases
-        const int64_t ld = a.slices > 1 ? a.l.N : a.l.ld_out;
-        const bool hold = kHold && a.slices == 1;
+        const int64_t ld = kSums ? a.l.N : a.l.ld_out;
         int32_t buf = 0;
         uint32_t buf_phase = 0;
         // this lane's row of A, and its column of each 32 along B. Loaded an item
@@ -690,7 +712,7 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         constexpr bool kAhead = !kHold || kTN == 64;
         float next_sa = 0.f, next_bias_a = 0.f, next_sb[kChunks], next_bias[kSwap ? 1 : kChunks];
         auto load_scales = [&](const TileItem& t) {
-            if (a.slices > 1) return;
+            if constexpr (kSums) return;
             const int64_t ra = t.a0 + q * 32 + lane;
             const bool in = ra < a.rows_a;
             next_sa = in ? __ldg((kSwap ? a.l.w_scale : a.l.x_scale) + ra) : 0.f;
@@ -707,7 +729,8 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
             const TileItem t = tile_item<kTN>(a, it, rank);
             if constexpr (!kAhead) load_scales(t);
             const int64_t ra0 = t.a0 + q * 32, rb0 = t.b0 + half * kCols;
-            int32_t* part = a.partial + static_cast<int64_t>(t.slice) * a.l.M * a.l.N;  // used when slices > 1
+            T* out = static_cast<T*>(a.l.out);
+            if constexpr (kSums) out = a.partial + static_cast<int64_t>(t.slice) * a.l.M * a.l.N;
             const int row_n = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(32), a.rows_a - ra0)));
             const bool in_a = lane < row_n;
             const float sa = next_sa, bias_a = next_bias_a;
@@ -720,10 +743,8 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
                 if constexpr (kHold) {
-                    if (hold) {
-                        tab[c * 32 + lane] = next_sb[c];
-                        if constexpr (!kSwap) tab[kCols + c * 32 + lane] = next_bias[c];
-                    }
+                    tab[c * 32 + lane] = next_sb[c];
+                    if constexpr (!kSwap) tab[kCols + c * 32 + lane] = next_bias[c];
                 } else {
                     sb[c] = next_sb[c];
                     if constexpr (!kSwap) bias[c] = next_bias[c];
@@ -731,77 +752,120 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
             }
             __syncwarp();
             if (kAhead && it + step < a.items) load_scales(tile_item<kTN>(a, it + step, rank));
-            if (!tile_wait_warp(a, ctl, &ctl->acc_full[buf], buf_phase)) break;
-            tc_fence_after();
-            const uint32_t src = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * kTN + half * kCols);
-            uint32_t held[kHold ? kChunks : 1][16];
-            if constexpr (kHold) {
-                if (hold) {
-                    // one part is in flight while another is worked on (2048 x 4096 x 1024 bf16 19.6 -> 18.7 us)
-                    constexpr int kParts = kCols / 16;
+            const uint32_t src0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * kCols);
+            int32_t sum[kParts ? kCols : 1];
+            if constexpr (kParts) {  // two floats as such (conversions are slow): see parts_needed
+                bool ok = true;
+                const bool as_float = !kSums && t.kb1 - t.kb0 <= 2 * a.kb_part;
+                for (int32_t s0 = t.kb0; s0 < t.kb1; s0 += a.kb_part) {
+                    if (!(ok = tile_wait_warp(a, ctl, &ctl->acc_full[buf], buf_phase))) break;
+                    tc_fence_after();
                     float v[2][16];
-                    tmem_ld16(src, v[0]);
+                    const uint32_t from = src0 + static_cast<uint32_t>(buf * kTN);
+                    tmem_ld16(from, v[0]);
 #pragma unroll
-                    for (int c = 0; c < kParts; ++c) {
-                        tmem_wait_ld16(v[c & 1]);
-                        if (c + 1 < kParts) {
-                            tmem_ld16(src + (c + 1) * 16, v[(c + 1) & 1]);
+                    for (int c = 0; c < kCols; c += 16) {
+                        float (&u)[16] = v[(c / 16) & 1];
+                        tmem_wait_ld16(u);
+                        if (c + 16 < kCols) {
+                            tmem_ld16(from + c + 16, v[(c / 16 + 1) & 1]);
                         } else {
                             tc_fence_before();
                             __syncwarp();
                             if (lane == 0) mbar_arrive_remote(map_shared_rank(smem_u32(&ctl->acc_empty[buf]), 0));
                         }
+                        if (as_float) {
+                            const bool start = s0 == t.kb0;
 #pragma unroll
-                        for (int i = 0; i < 16; i += 4) {
-                            const float4 s4 = *reinterpret_cast<const float4*>(tab + c * 16 + i);
-                            const float4 b4 = kSwap ? make_float4(bias_a, bias_a, bias_a, bias_a)
-                                                    : *reinterpret_cast<const float4*>(tab + kCols + c * 16 + i);
-                            const float* u = v[c & 1] + i;
-                            const float2 lo = fma2(mul2(make_float2(u[0], u[1]), sa2), make_float2(s4.x, s4.y), make_float2(b4.x, b4.y));
-                            const float2 hi = fma2(mul2(make_float2(u[2], u[3]), sa2), make_float2(s4.z, s4.w), make_float2(b4.z, b4.w));
-                            held[c / 2][(c & 1) * 8 + i / 2] = pack2<T>(lo.x, lo.y);
-                            held[c / 2][(c & 1) * 8 + i / 2 + 1] = pack2<T>(hi.x, hi.y);
+                            for (int i = 0; i < 16; ++i)
+                                sum[c + i] = __float_as_int(start ? u[i] : __int_as_float(sum[c + i]) + u[i]);
+                        } else {
+                            const int32_t keep = s0 == t.kb0 ? 0 : -1;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) sum[c + i] = (sum[c + i] & keep) + __float2int_rn(u[i]);
                         }
+                    }
+                    if (s0 + a.kb_part < t.kb1 && ++buf == C::kAcc) { buf = 0; buf_phase ^= 1u; }
+                }
+                if (!ok) break;
+                if (!kSums && !as_float) {
+#pragma unroll
+                    for (int i = 0; i < kCols; ++i) sum[i] = __float_as_int(__int2float_rn(sum[i]));
+                }
+            } else {
+                if (!tile_wait_warp(a, ctl, &ctl->acc_full[buf], buf_phase)) break;
+                tc_fence_after();
+            }
+            const uint32_t src = src0 + static_cast<uint32_t>(buf * kTN);
+            uint32_t held[kHold ? kChunks : 1][16];
+            if constexpr (kHold) {
+                // one part is in flight while another is worked on (2048 x 4096 x 1024 bf16 19.6 -> 18.7 us)
+                constexpr int kLoads = kCols / 16;
+                float v[2][16];
+                tmem_ld16(src, v[0]);
+#pragma unroll
+                for (int c = 0; c < kLoads; ++c) {
+                    tmem_wait_ld16(v[c & 1]);
+                    if (c + 1 < kLoads) {
+                        tmem_ld16(src + (c + 1) * 16, v[(c + 1) & 1]);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_remote(map_shared_rank(smem_u32(&ctl->acc_empty[buf]), 0));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 s4 = *reinterpret_cast<const float4*>(tab + c * 16 + i);
+                        const float4 b4 = kSwap ? make_float4(bias_a, bias_a, bias_a, bias_a)
+                                                : *reinterpret_cast<const float4*>(tab + kCols + c * 16 + i);
+                        const float* u = v[c & 1] + i;
+                        const float2 lo = fma2(mul2(make_float2(u[0], u[1]), sa2), make_float2(s4.x, s4.y), make_float2(b4.x, b4.y));
+                        const float2 hi = fma2(mul2(make_float2(u[2], u[3]), sa2), make_float2(s4.z, s4.w), make_float2(b4.z, b4.w));
+                        held[c / 2][(c & 1) * 8 + i / 2] = pack2<T>(lo.x, lo.y);
+                        held[c / 2][(c & 1) * 8 + i / 2 + 1] = pack2<T>(hi.x, hi.y);
                     }
                 }
             }
 #pragma unroll
-            for (int c = 0; c < kChunks && !hold; ++c) {
+            for (int c = 0; c < kChunks && !kHold; ++c) {
                 const int64_t rb = rb0 + c * 32;
-                float v[32];
-                tmem_ld32(src + c * 32, v);
-                tmem_wait_ld();
-                if (c + 1 == kChunks) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_remote(map_shared_rank(smem_u32(&ctl->acc_empty[buf]), 0));
+                float v[32];  // kSums: integers as their bits
+                if constexpr (kParts) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = __int_as_float(sum[c * 32 + i]);
+                } else {
+                    tmem_ld32(src + c * 32, v);
+                    tmem_wait_ld();
+                    if (c + 1 == kChunks) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_remote(map_shared_rank(smem_u32(&ctl->acc_empty[buf]), 0));
+                    }
                 }
                 if (row_n == 0 || rb >= a.rows_b) continue;
+                if constexpr (kSums && !kParts) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = __int_as_float(__float2int_rn(v[i]));
+                }
                 if constexpr (kSwap) {
                     const int n = static_cast<int>(min(static_cast<int64_t>(32), a.rows_b - rb));
-                    if (a.slices > 1) {
-                        int32_t* p = part + rb * ld + ra0 + lane;
+                    T* p = out + rb * ld + ra0 + lane;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i, p += ld)
-                            if (i < n && in_a) *p = __float2int_rn(v[i]);
-                    } else if constexpr (!kHold) {
-                        T* p = static_cast<T*>(a.l.out) + rb * ld + ra0 + lane;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i, p += ld) {
-                            const T y = from_f32<T>(__fmaf_rn(v[i] * __shfl_sync(0xffffffffu, sb[c], i), sa, bias_a));
-                            if (i < n && in_a) *p = y;
-                        }
+                    for (int i = 0; i < 32; ++i, p += ld) {
+                        float y = v[i];
+                        if constexpr (!kSums) y = __fmaf_rn(y * __shfl_sync(0xffffffffu, sb[c], i), sa, bias_a);
+                        if (i < n && in_a) *p = from_f32<T>(y);
                     }
                 } else {
-                    const float f = a.slices > 1 ? 1.f : sa;
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         *reinterpret_cast<float4*>(stage + staged(lane, i)) =
-                            make_float4(v[4 * i] * f, v[4 * i + 1] * f, v[4 * i + 2] * f, v[4 * i + 3] * f);
+                            kSums ? make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3])
+                                  : make_float4(v[4 * i] * sa, v[4 * i + 1] * sa, v[4 * i + 2] * sa, v[4 * i + 3] * sa);
                     __syncwarp();
                     if constexpr (kRows16) {
                         float ws[4] = {}, bs[4] = {};  // this lane's four channels
-                        if constexpr (!kHold) {
+                        if constexpr (!kSums && !kHold) {
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 ws[j] = __shfl_sync(0xffffffffu, sb[c], 4 * (lane & 7) + j);
@@ -815,10 +879,10 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                         for (int i = 0; i < 8; ++i, at += 4 * ld) {
                             const float4 y = *reinterpret_cast<const float4*>(stage + staged(4 * i + (lane >> 3), lane & 7));
                             if (4 * i + (lane >> 3) >= row_n) continue;
-                            if (a.slices > 1) {
-                                store4(part + at, n, y.x, y.y, y.z, y.w);
+                            if constexpr (kSums) {
+                                store4(out + at, n, y.x, y.y, y.z, y.w);
                             } else if constexpr (!kHold) {
-                                store4(static_cast<T*>(a.l.out) + at, n, __fmaf_rn(y.x, ws[0], bs[0]), __fmaf_rn(y.y, ws[1], bs[1]),
+                                store4(out + at, n, __fmaf_rn(y.x, ws[0], bs[0]), __fmaf_rn(y.y, ws[1], bs[1]),
                                        __fmaf_rn(y.z, ws[2], bs[2]), __fmaf_rn(y.w, ws[3], bs[3]));
                             }
                         }
@@ -828,24 +892,23 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                         int64_t at = ra0 * ld + rb + lane;
 #pragma unroll 8
                         for (int r = 0; r < row_n; ++r, at += ld) {
-                            const float y = *reinterpret_cast<const float*>(from + staged(r, lane >> 2));
-                            if (!in_b) continue;
-                            if (a.slices > 1) part[at] = __float2int_rn(y);
-                            else if constexpr (!kHold) static_cast<T*>(a.l.out)[at] = __fmaf_rn(y, sb[c], bias[c]);
+                            float y = *reinterpret_cast<const float*>(from + staged(r, lane >> 2));
+                            if constexpr (!kSums && !kHold) y = __fmaf_rn(y, sb[c], bias[c]);
+                            if (in_b) out[at] = from_f32<T>(y);
                         }
                     }
                     __syncwarp();
                 }
             }
             if constexpr (kHold) {
-                if (hold && row_n > 0) {
+                if (row_n > 0) {
                     __syncwarp();  // the table is done with
                     if constexpr (kSwap) {
 #pragma unroll
                         for (int c = 0; c < kChunks; ++c) {
                             const int64_t rb = rb0 + c * 32;
                             const int n = static_cast<int>(min(static_cast<int64_t>(32), a.rows_b - rb));
-                            T* p = static_cast<T*>(a.l.out) + rb * ld + ra0 + lane;
+                            T* p = out + rb * ld + ra0 + lane;
 #pragma unroll
                             for (int i = 0; i < 32; ++i, p += ld)
                                 if (i < n && in_a) *p = half_of<T>(held[c][i / 2], i & 1);
@@ -884,7 +947,7 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                             const int64_t n0 = rb0 + c * 32;
                             if (n0 >= a.rows_b) break;
                             const int left = static_cast<int>(min(static_cast<int64_t>(kRun), a.rows_b - n0));
-                            T* const out0 = static_cast<T*>(a.l.out) + ra0 * ld + n0;
+                            T* const out0 = out + ra0 * ld + n0;
                             const int turn = phase_of(out0 + lane * ld);
                             uint32_t v[kRun / 2], u[kRun / 2];
 #pragma unroll

@@ -1,5 +1,6 @@
 // Launches of the INT8 linear, per output type (linear_f16.cu, linear_bf16.cu,
-// linear_f32.cu: most of the library's kernels, compiled side by side).
+// linear_f32.cu, linear_sums.cu for the sums of slices: most of the library's
+// kernels, compiled side by side).
 #pragma once
 
 #include <cuda.h>
@@ -8,6 +9,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
+#include <type_traits>
 
 #include "maxsim.h"
 #include "host_util.h"
@@ -84,10 +86,10 @@ maxsim_status launch_few(const LinearArgs& a, bool whole, cudaStream_t st) {
     return launched();
 }
 
-template <typename T, int kTN, bool kSwap, bool kKeepB, bool kRows16>
-maxsim_status launch_tile_rows(const LinearPlan& p, const LinearArgs& l, const __half* b16, bool a_prepared, int32_t* partial,
+template <typename T, int kTN, bool kSwap, bool kKeepB, bool kRows16, bool kParts>
+maxsim_status launch_tile_kernel(const LinearPlan& p, const LinearArgs& l, const __half* b16, bool a_prepared, int32_t* partial,
                           const HostDevice& dev, cudaStream_t st) {
-    auto kern = linear_tile_kernel<T, kTN, kSwap, kKeepB, kRows16>;
+    auto kern = linear_tile_kernel<T, kTN, kSwap, kKeepB, kRows16, kParts>;
     constexpr size_t kSmem = tile_smem_bytes<kTN, kKeepB>();
     static_assert(kSmem <= 232448, "shared memory of one SM");
     static std::atomic<uint64_t> prepared{0};  // devices whose shared-memory limit is raised
@@ -111,6 +113,8 @@ maxsim_status launch_tile_rows(const LinearPlan& p, const LinearArgs& l, const _
     a.slices = p.slices;
     a.kb = p.kb;
     a.kb_slice = p.kb_slice;
+    const int32_t parts = (p.kb_slice + kExactBlocks - 1) / kExactBlocks;
+    a.kb_part = (p.kb_slice + parts - 1) / parts;
     a.a_prepared = a_prepared;
     a.status = dev.status;
     a.timeout_ns = kTimeoutNs;
@@ -122,12 +126,22 @@ maxsim_status launch_tile_rows(const LinearPlan& p, const LinearArgs& l, const _
         return MAXSIM_ERR_CUDA;
     CUtensorMap tout = tb;  // used by 16-bit outputs that are stored by TMA alone
     if constexpr (sizeof(T) == 2 && kRows16 && !kSwap) {
-        if (p.slices == 1 && !encode_k_rows(dev.encode, &tout, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, l.out, l.N, l.M,
+        if (!encode_k_rows(dev.encode, &tout, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, l.out, l.N, l.M,
                                             l.ld_out * 2, 32, kTN == 64 ? 64 : 128))
             return MAXSIM_ERR_CUDA;
     }
     return launch_after(kern, static_cast<unsigned>(2 * std::min<int64_t>(a.items, std::max(1, dev.num_sms / 2))), kTileThreads,
                         kSmem, 2, st, ta, tb, tout, a);
+}
+
+template <typename T, int kTN, bool kSwap, bool kKeepB, bool kRows16>
+maxsim_status launch_tile_rows(const LinearPlan& p, const LinearArgs& l, const __half* b16, bool a_prepared, int32_t* partial,
+                               const HostDevice& dev, cudaStream_t st) {
+    if constexpr (sizeof(T) == 4 && kTN <= 128 && !(kKeepB && TileCfg<kTN, kKeepB>::kStagesB <= kExactBlocks)) {
+        if (parts_needed(p.kb_slice))
+            return launch_tile_kernel<T, kTN, kSwap, kKeepB, kRows16, true>(p, l, b16, a_prepared, partial, dev, st);
+    }
+    return launch_tile_kernel<T, kTN, kSwap, kKeepB, kRows16, false>(p, l, b16, a_prepared, partial, dev, st);
 }
 
 template <typename T, int kTN, bool kSwap, bool kKeepB>
@@ -136,8 +150,8 @@ maxsim_status launch_tile(const LinearPlan& p, const LinearArgs& l, const __half
     if constexpr (!kSwap) {  // swapped, a store is one channel per lane in any case
         // 16-bit outputs leave by TMA, which wants strides below 2^40 bytes and
         // writes an odd row's last element with the one behind it
-        bool rows16 = p.slices > 1 ? l.N % 4 == 0 : ptr_aligned(l.out, 16) && l.ld_out * static_cast<int64_t>(sizeof(T)) % 16 == 0;
-        if (sizeof(T) == 2 && p.slices == 1) rows16 = rows16 && l.N % 8 == 0 && l.ld_out < (int64_t(1) << 38);
+        bool rows16 = std::is_same_v<T, int32_t> ? l.N % 4 == 0 : ptr_aligned(l.out, 16) && l.ld_out * static_cast<int64_t>(sizeof(T)) % 16 == 0;
+        if (sizeof(T) == 2) rows16 = rows16 && l.N % 8 == 0 && l.ld_out < (int64_t(1) << 38);
         if (!rows16) return launch_tile_rows<T, kTN, kSwap, kKeepB, false>(p, l, b16, a_prepared, partial, dev, st);
     }
     return launch_tile_rows<T, kTN, kSwap, kKeepB, true>(p, l, b16, a_prepared, partial, dev, st);
@@ -146,7 +160,7 @@ maxsim_status launch_tile(const LinearPlan& p, const LinearArgs& l, const __half
 template <typename T, bool kSwap>
 maxsim_status launch_tile_width(const LinearPlan& p, const LinearArgs& l, const __half* b16, bool a_prepared, int32_t* partial,
                                 const HostDevice& dev, cudaStream_t st) {
-    if constexpr (!kSwap) {
+    if constexpr (!kSwap && !std::is_same_v<T, int32_t>) {
         if (p.keep_b && p.tn == 128) return launch_tile<T, 128, false, true>(p, l, b16, a_prepared, partial, dev, st);
         if (p.keep_b) return launch_tile<T, 64, false, true>(p, l, b16, a_prepared, partial, dev, st);
     }
@@ -154,6 +168,17 @@ maxsim_status launch_tile_width(const LinearPlan& p, const LinearArgs& l, const 
     if (p.tn == 128) return launch_tile<T, 128, kSwap, false>(p, l, b16, a_prepared, partial, dev, st);
     return launch_tile<T, 64, kSwap, false>(p, l, b16, a_prepared, partial, dev, st);
 }
+
+// The tile kernel for outputs of T, or for the integer sums of slices (int32_t).
+template <typename T>
+maxsim_status launch_tiles(const LinearPlan& p, const LinearArgs& l, const __half* b16, bool a_prepared, int32_t* partial,
+                           const HostDevice& dev, cudaStream_t st) {
+    return p.swap ? launch_tile_width<T, true>(p, l, b16, a_prepared, partial, dev, st)
+                  : launch_tile_width<T, false>(p, l, b16, a_prepared, partial, dev, st);
+}
+
+extern template maxsim_status launch_tiles<int32_t>(const LinearPlan&, const LinearArgs&, const __half*, bool, int32_t*,
+                                                    const HostDevice&, cudaStream_t);  // linear_sums.cu
 
 template <typename T>
 maxsim_status run_linear(const LinearPlan& p, LinearArgs l, bool x_direct, bool w_direct, uint8_t* ws,
@@ -194,9 +219,9 @@ maxsim_status run_linear(const LinearPlan& p, LinearArgs l, bool x_direct, bool 
     if (rc != MAXSIM_OK) return rc;
     int32_t* partial = reinterpret_cast<int32_t*>(ws + p.off_partial);
     const bool prepared = copy_x || copy_w;
-    rc = p.swap ? launch_tile_width<T, true>(p, l, b16, prepared, partial, dev, st)
-                : launch_tile_width<T, false>(p, l, b16, prepared, partial, dev, st);
-    if (rc != MAXSIM_OK || p.slices == 1) return rc;
+    if (p.slices == 1) return launch_tiles<T>(p, l, b16, prepared, partial, dev, st);
+    rc = launch_tiles<int32_t>(p, l, b16, prepared, partial, dev, st);
+    if (rc != MAXSIM_OK) return rc;
     return launch_after(linear_join_kernel<T>, join_grid, 256, 0, 1, st, l, const_cast<const int32_t*>(partial), p.slices);
 }
 
