@@ -75,3 +75,41 @@ def test_dropout_rows_of_almost_32_bits():
         for first in (0, cols // 3, cols - 2000):
             got = x[r, first:first + 2000].cpu().numpy()
             assert np.array_equal(got, np.where(keep_window(r * cols + first, 2000, 0.25, 21, 22), kept, np.float16(0)))
+
+
+LARGE = 4_300_001                                               # rows of about 1,000: more than 2^32 elements
+
+
+@pytest.mark.parametrize("cols,pad_x,pad_y", [(1000, 1, 0), (1000, 8, 8), (1000, 0, 1), (1001, 0, 0)])
+def test_dropout_beyond_32_bits_in_every_layout(cols, pad_x, pad_y):
+    # rows gathered into a run, rows of pieces, rows of single elements, a run
+    ld_x, ld_y = cols + pad_x, cols + pad_y
+    room(2 * LARGE * (ld_x + ld_y))
+    x = torch.ones((LARGE, ld_x), dtype=torch.float16, device="cuda")
+    y = torch.full((LARGE, ld_y), 5.0, dtype=torch.float16, device="cuda")
+    x[:, cols:] = float("nan")
+    rc = _native.lib().maxsim_dropout_fwd(x.data_ptr(), _native.F16, LARGE, cols, ld_x, None, 0, 0.25, 21, 22, y.data_ptr(), ld_y,
+                                          stream())
+    assert rc == 0
+    assert (y[:, cols:] == 5).all()
+    kept = np.float16(np.float32(65536 / 49152))
+    for row in (0, 2 ** 31 // cols - 1, 2 ** 31 // cols, 2 ** 31 // cols + 1, 2 ** 32 // cols - 1, 2 ** 32 // cols, LARGE - 1):
+        assert np.array_equal(y[row, :cols].cpu().numpy(),
+                              np.where(keep_window(row * cols, cols, 0.25, 21, 22), kept, np.float16(0)))
+    rate = torch.stack([(y[i:i + (1 << 16), :cols] != 0).sum() for i in range(0, LARGE, 1 << 16)]).sum().item() / (LARGE * cols)
+    assert abs(rate - 0.75) < 6 * (0.25 * 0.75 / (LARGE * cols)) ** 0.5
+
+
+@pytest.mark.parametrize("cols,dtype", [(1000, torch.bfloat16), (1001, torch.bfloat16), (1001, torch.float32)])
+def test_quantize_beyond_32_bits(cols, dtype):
+    # rows in whole chunks, in the chunks that they touch, in single elements
+    room(LARGE * cols * (dtype.itemsize + 1))
+    x = torch.empty((LARGE, cols), dtype=dtype, device="cuda")
+    for i in range(0, LARGE, 1 << 18):
+        x[i:i + (1 << 18)].normal_()
+    q, scale = ms.quantize_rows(x)
+    for i in range(0, LARGE, 1 << 18):
+        part = x[i:i + (1 << 18)].float()
+        s = (part.abs().amax(1) * (np.float32(1) / np.float32(127)).item()).clamp(min=2.0 ** -126)
+        assert torch.equal(scale[i:i + (1 << 18)], s)
+        assert torch.equal(q[i:i + (1 << 18)], torch.round(part / s[:, None]).clamp(-127, 127).to(torch.int8))
