@@ -25,14 +25,22 @@ inline bool rows_direct(int64_t K, int64_t ld) { return K % 16 == 0 && ld % 16 =
 
 // linear_few_kernel or the tile kernel. The former takes any product in one
 // launch, but reads w once per 32 tokens; a block of it is 16 channels x 32
-// tokens. Measured, few / tile, in us: 16 x 16384 x 16384 52 / 55, 8 x 8192 x 8191
-// 34 / 45; beyond that by units of a block x 64 of K, and blocks: 32 x 4096 x 4096
-// (16,384 units, 256 blocks) 8.3 / 10.1, 128 x 2048 x 2048 (16,384, 512) 8.7 / 10.5,
-// 256 x 2048 x 1024 (16,384, 1,024) 9.8 / 8.0, 1024 x 1024 x 512 (16,384, 2,048)
-// 12.9 / 7.5, 32 x 16384 x 4096 (65,536, 1,024) 24 / 18. Rows off their 16-byte
-// boundaries cost about three times as much: 128 x 1024 x 1023 7.9 / 8.4,
-// 3000 x 200 x 301 12.6 / 7.8. The tile kernel's second launch is a further 3 us
-// of the caller's time.
+// tokens. Up to 16 tokens it wins (few / tile, us on the GPU): 16 x 16384 x
+// 16384 52 / 55, 8 x 8192 x 8191 34 / 45. Beyond, by the cost below (blocks x
+// chunks of K, three times as much for rows off their 16-byte boundaries):
+//                       cost   GPU          call, one after another
+//   128 x 1024 x 1024    5120   4.5 /  7.7   12 / 22
+//   512 x 512 x 1024    10240   6.1 /  8.0   13 / 21
+//   900 x 900 x 256     13224  10.0 /  6.5   12 / 21
+//   2048 x 512 x 256    16384  12.0 /  6.0   14 / 22
+//   32 x 4096 x 4096    17408   8.2 /  9.7   12 / 24
+//   256 x 2048 x 1024   20480   9.5 /  7.8   13 / 22
+//   1024 x 1024 x 512   24576  12.7 /  6.8   15 / 21
+//   64 x 1000 x 4095    24696  11.8 /  9.7   14 / 24
+// The tile kernel's second launch and workspace are 7 to 9 us of an eager call,
+// so up to the limit a call is shorter through the few kernel even where its
+// GPU time, all that counts in a CUDA graph or a full queue, is up to 6 us
+// longer (many tokens, short K).
 constexpr int64_t kFewCost = 20480;
 inline bool few_kernel(int64_t M, int64_t N, int64_t K, bool whole) {
     if (M <= 8 || (M <= 16 && whole)) return true;
