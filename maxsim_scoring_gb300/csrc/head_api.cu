@@ -31,7 +31,16 @@ static_assert(most_chunks(int32_t{kI32Max}, 8, kTouched) == (int64_t{1} << 28) +
 
 // The smallest group that holds a row: short rows then share a warp (fewer
 // shuffle steps for a row, several rows' loads in flight), the shortest take a
-// thread each, long ones take a block.
+// thread each, long ones take a block. A step stays where the next one, which
+// would hold its rows too, is slower (us for 400 MB of rows at the step's
+// limit, by the step / by the next):
+//   whole chunks     1: 178 / 184 (bf16), 100 / 141 (f32)  2: 137 / 147  6: 141 / 235  8: 98 / 144 (f32)  16: 128 / 173
+//   of bf16         32: 106 / 160   64: 105 / 166  128: 101 / 152  256: 99 / 166  512: 107 / 159  1024: 106 / 193
+//                 2048: 124 / 159  4096: 105 / 132; at 4 within 3 % (f32 98 / 95)
+//   touched chunks  32: 165 / 270   64: 167 / 264  128: 151 / 192  192: 144 / 191  256: 155 / 217  512: 138 / 237
+//                 1024: 160 / 229  2048: 149 / 275  (4096: 182 / 177)
+//   single f32      16: 203 / 278   32: 137 / 192   64: 132 / 155  128: 142 / 178  256: 103 / 148  512: 86 / 178
+//                 1024: 100 / 143  2048: 87 / 201  4096: 121 / 133
 template <typename T, RowMode kMode, bool kNorm>
 maxsim_status launch_quantize(const QuantizeArgs& a, const HostDevice& dev, cudaStream_t st) {
     const int64_t chunks = most_chunks(a.cols, QuantizeRow<T, kMode>::C::kVec, kMode);
@@ -51,7 +60,7 @@ maxsim_status launch_quantize(const QuantizeArgs& a, const HostDevice& dev, cuda
         if constexpr (kMode == kTouched)
             if (chunks <= 192) return launch_quantize_group<T, kMode, kNorm, 32, 6>(a, dev, st);
         if (chunks <= 256) return launch_quantize_group<T, kMode, kNorm, 32, 8>(a, dev, st);
-        if (chunks <= 512) return launch_quantize_group<T, kMode, kNorm, kMode == kTouched ? 32 : 128, kMode == kTouched ? 16 : 4>(a, dev, st);
+        if (chunks <= 512) return launch_quantize_group<T, kMode, kNorm, 128, 4>(a, dev, st);
         if (chunks <= 1024) return launch_quantize_group<T, kMode, kNorm, 128, 8>(a, dev, st);
         if (chunks <= 2048) return launch_quantize_group<T, kMode, kNorm, 512, 4>(a, dev, st);
         if (chunks <= 4096) return launch_quantize_group<T, kMode, kNorm, 512, 8>(a, dev, st);
@@ -78,7 +87,7 @@ maxsim_status launch_quantize_mode(const QuantizeArgs& a, const HostDevice& dev,
         return launch_quantize<T, kWhole, kNorm>(a, dev, st);
     if constexpr (sizeof(T) == 2) {
         // Measured, touched chunks and single elements: 608816 x 92 bf16 83 and 68 us, 500000 x 150 86 and 115,
-        // 6847 x 2505 23 and 38, 15875 x 7518 76 and 145; f32 60000 x 2001 126 and 104.
+        // 6847 x 2505 17 and 38, 15875 x 7518 76 and 145; f32 60000 x 2001 126 and 104.
         const uintptr_t phase = reinterpret_cast<uintptr_t>(a.x) / 2 - reinterpret_cast<uintptr_t>(a.q);
         if (a.cols >= 128 && phase % kVec == 0 && (a.rows == 1 || (a.ld_x - a.ld_q) % kVec == 0))
             return launch_quantize<T, kTouched, kNorm>(a, dev, st);
