@@ -13,8 +13,6 @@
 namespace maxsim {
 namespace {
 
-constexpr int64_t kI32Max = 2147483647;
-
 template <typename T, RowMode kMode, bool kNorm, int kGroup, int kChunks>
 maxsim_status launch_quantize_group(const QuantizeArgs& a, const HostDevice& dev, cudaStream_t st) {
     constexpr int kThreads = quantize_threads(kGroup);

@@ -17,6 +17,10 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s bound on any single device-side wait
+constexpr size_t kSmemBudget = 232448;          // 227 KB: opt-in shared memory per block on sm_100 / sm_103
+constexpr int64_t kI32Max = 2147483647;
+
 struct HostDevice {
     int index = 0;
     int num_sms = 0;

@@ -13,7 +13,6 @@ extern template maxsim_status run_linear<float>(const LinearPlan&, LinearArgs, b
 
 namespace {
 
-constexpr int64_t kI32Max = 2147483647;
 constexpr int64_t kLinearMaxK = 131071;             // 131071 * 128 * 128 < 2^31
 constexpr int64_t kLinearMaxRows = kI32Max - 1023;  // a tile past the last row still has 32-bit coordinates
 constexpr int64_t kPairs = 76;          // CTA pairs of a GB300 (152 SMs): plans do not depend on the device

@@ -17,8 +17,6 @@
 
 namespace maxsim {
 
-constexpr uint64_t kTimeoutNs = 2000000000ull;
-
 struct LinearPlan {
     bool few = false;
     bool swap = false;   // A is w, B is x
@@ -91,7 +89,7 @@ maxsim_status launch_tile_kernel(const LinearPlan& p, const LinearArgs& l, const
                           const HostDevice& dev, cudaStream_t st) {
     auto kern = linear_tile_kernel<T, kTN, kSwap, kKeepB, kRows16, kParts>;
     constexpr size_t kSmem = tile_smem_bytes<kTN, kKeepB>();
-    static_assert(kSmem <= 232448, "shared memory of one SM");
+    static_assert(kSmem <= kSmemBudget, "shared memory of one SM");
     static std::atomic<uint64_t> prepared{0};  // devices whose shared-memory limit is raised
     const uint64_t bit = uint64_t(1) << dev.index;
     if (!(prepared.load(std::memory_order_acquire) & bit)) {

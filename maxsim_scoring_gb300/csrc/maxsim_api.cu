@@ -27,9 +27,7 @@ __device__ int g_device_status;
 
 namespace {
 
-constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s bound on any single device-side wait
 constexpr int kMaxDevices = 64;
-constexpr size_t kSmemBudget = 232448;          // 227 KB: opt-in shared memory per block on sm_100 / sm_103
 
 struct DeviceInfo {
     bool init = false;
@@ -636,7 +634,6 @@ maxsim_status check_dim(int64_t dim, int64_t multiple) {
     return MAXSIM_OK;
 }
 
-constexpr int64_t kI32Max = 2147483647;
 constexpr uint32_t kNaNPairF16 = 0x7E007E00u;
 constexpr uint32_t kNaNPairBF16 = 0x7FC07FC0u;
 
