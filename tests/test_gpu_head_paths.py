@@ -170,3 +170,16 @@ def test_linear_in_a_cuda_graph(M, N, K, dtype):
         graph.replay()
         assert torch.equal(out, ms.linear_int8(x, xs, w, ws, out_dtype=DT[dtype]))
     assert ms.device_status() == 0
+
+
+@pytest.mark.parametrize("N", [1, 3, 8, 16, 24])
+@pytest.mark.parametrize("swap", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_linear_narrower_than_a_tile(N, swap, dtype):
+    # boxes and tiles that reach past the smaller operand's last row; swapped: few tokens, too many for the other kernel
+    rng = np.random.default_rng(N)
+    M, N, K = (17 + N, 120000, 200) if swap else (120000, N, 200)
+    x, w = padded_codes(rng, M, K, 0), padded_codes(rng, N, K, 0)
+    y = ms.linear_int8(x, torch.ones(M, device="cuda"), w, torch.ones(N, device="cuda"), out_dtype=DT[dtype])
+    assert ms.device_status() == 0
+    assert torch.equal(y, (x.double() @ w.double().t()).float().to(DT[dtype]))
