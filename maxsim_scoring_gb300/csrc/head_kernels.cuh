@@ -595,12 +595,12 @@ __global__ void __launch_bounds__(256) dropout_any_kernel(const DropoutArgs a) {
         const int left = static_cast<int>(min(a.n - i0, static_cast<int64_t>(256))) - lane;  // element 32 j exists while 32 j < left
         const int64_t row0 = kWidth ? divide(i0) : 0;
         // element c of row0 onward: at p[c], or past the row's end (c >= cols) at q[c]
-        const int64_t col0 = i0 - row0 * a.cols + lane;  // may pass the row's end, and 32 bits with it
+        const uint32_t col0 = static_cast<uint32_t>(i0 - row0 * a.cols) + lane;  // unsigned: may reach 2^31
         const T* px = x + row0 * a.ld_x + col0;
         const T* pr = res + row0 * a.ld_r + col0;
         T* py = y + row0 * a.ld_y + col0;
         const int64_t dx = a.ld_x - a.cols, dr = a.ld_r - a.cols, dy = a.ld_y - a.cols;
-        const int end = static_cast<int>(min(a.cols - col0, static_cast<int64_t>(256)));  // 32 j >= end: the next row
+        const int32_t end = static_cast<int32_t>(a.cols - col0);  // 32 j >= end: the next row
         T xv[8], rv[8];
         s_bits[warp][lane] = draw_block(a, (i0 >> 3) + lane);
 #pragma unroll
