@@ -41,7 +41,7 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 // 121 us (6.6 TB/s); 16-bit rows of 128 with the norm in 220 us for 3,000,000 (5.3
 // TB/s, 70 % of the issue slots), rows off their 16-byte boundaries by the
 // handling of their ends or by single elements (100000 x 1023 bf16 in 90 us, 3.4
-// TB/s, f32 in 110 us, 4.6 TB/s).
+// TB/s, f32 in 102 us, 5.0 TB/s).
 
 // Maximum of two pairs of unsigned 16-bit values.
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(256) dropout_wide_kernel(const DropoutArgs a) 
 // kWidth = 256: rows are at least as long as the run, which then crosses at
 // most one row's end, and one division (fast_div by cols) places it; 0: any
 // width, a division per element. Bound by instruction issue (16384 x 1023 bf16
-// with a residual, all rows apart: 28 us, 3.6 TB/s).
+// with a residual, all rows apart: 33 us, 3.1 TB/s).
 template <typename T, bool kRes, int kWidth>
 __global__ void __launch_bounds__(256) dropout_any_kernel(const DropoutArgs a) {
     __shared__ uint4 s_bits[8][32];

@@ -235,8 +235,11 @@ constexpr int kTileMaxStages8 = 8;
 // Registers per thread: the launch gives every thread kTileRegs; warps 0-3 and
 // the widening warps hand registers to the epilogue warps, which hold a
 // tile's rounded outputs until they are stored. 16-bit outputs, which are held,
-// get 8 more than others (1048576 x 64 x 1024 f16 195 -> 189 us; f32 999 x 1537 x
-// 1111 would lose, 10.4 -> 11.2).
+// get 8 more than others (1048576 x 64 x 1024 f16 195 -> 189 us; f32 would lose a
+// little, 4096 x 4096 x 4096 102.5 -> 103.4). What is spilled, 44 to 76 bytes of
+// most variants, is the control and the widening warps' (compiled with 80
+// registers for the former, or 96 for the latter, half of it goes; with 200
+// for the epilogue, next to nothing).
 constexpr int kTileRegs = 96, kTileRegsCtl = 48;
 __host__ __device__ constexpr int tile_regs_epi(bool held) { return held ? 144 : 136; }
 __host__ __device__ constexpr int tile_regs_widen(bool held) { return 216 - tile_regs_epi(held); }
@@ -471,10 +474,10 @@ __device__ __forceinline__ void store4(T* p, int n, float a, float b, float c, f
 // A tile's K may be cut into slices (few tiles, long K): each slice then
 // writes its integer sums (T = int32_t), and linear_join_kernel adds them.
 // kParts: 32-bit results of more than kExactBlocks blocks of K (parts_needed).
-// Measured with the preparation: 32768 x 4096 x 4096 in 529 us, 2.08 PFLOP/s
-// (tensor pipe 90 % active; 597 us, 1.84 PFLOP/s, once the power limit holds the
-// clock), 1048576 x 128 x 1024 in 215 us, 6.3 TB/s (HBM), 2048 x 4096 x 1024 in 18.4 us
-// (two rounds of tiles, the last one's stores).
+// Measured with the preparation: 32768 x 4096 x 4096 in 525 us, 2.09 PFLOP/s
+// (tensor pipe 87 % active; 584 to 605 us, 1.8 to 1.9 PFLOP/s, once the power limit
+// holds the clock), 1048576 x 128 x 1024 in 210 us, 6.4 TB/s (HBM), 2048 x 4096 x 1024
+// in 18.1 us (two rounds of tiles, the last one's stores).
 template <typename T, int kTN, bool kSwap, bool kKeepB, bool kRows16, bool kParts>
 __global__ void __launch_bounds__(kTileThreads, 1)
 linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
@@ -692,8 +695,8 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         // back, so that only this stands between a tile's MMAs and the next
         // one's. The scales along B wait in shared memory, where a read serves
         // the whole warp. Rows of 16-bit outputs then pass through shared memory
-        // to TMA stores (139270 x 1864 x 64 bf16: 148 us, and 209 with 16-byte
-        // stores of the warps, most of it their instructions). Swapped, lanes are
+        // to TMA stores (139270 x 1864 x 64 bf16 209 -> 148 us from 16-byte
+        // stores of the warps, most of it their instructions; 135 now). Swapped, lanes are
         // consecutive channels and store straight to out. 32-bit outputs, and
         // the integer sums of slices, are stored 32 columns at a time as they
         // are read, through shared memory so that stores are whole 128-byte runs.
@@ -706,9 +709,10 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         int32_t buf = 0;
         uint32_t buf_phase = 0;
         // this lane's row of A, and its column of each 32 along B. Loaded an item
-        // ahead where registers are left for it (525402 x 960 x 64 f32 616 -> 569 us,
-        // 603311 x 64 x 64 bf16 56 -> 50), not beside the held outputs of wide tiles
-        // (202805 x 576 x 64 bf16 110, and 116 ahead; 1048576 x 128 x 1024 f16 216 and 221)
+        // ahead where registers are left for it (us ahead / not: 603311 x 64 x 64 bf16 36 / 44,
+        // 999 x 1537 x 1111 f32 11.4 / 12.0, 525402 x 960 x 64 f32 418 / 425, but 139270 x 1864 x
+        // 176 f32 262 / 248), not beside the held outputs of wide tiles (202805 x 576 x 64 bf16
+        // 80 / 73, 2048 x 4096 x 1024 bf16 18.5 / 18.1)
         constexpr bool kAhead = !kHold || kTN == 64;
         float next_sa = 0.f, next_bias_a = 0.f, next_sb[kChunks], next_bias[kSwap ? 1 : kChunks];
         auto load_scales = [&](const TileItem& t) {
@@ -937,7 +941,7 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
                         // phase of its address, so that staged pieces are pieces of out; the
                         // first one holds the row's first elements and, wrapped around, its last
                         // ones, which go out one by one. (139270 x 1861 x 176 bf16: 712 us with
-                        // single elements throughout, 427 joining pieces at the store.)
+                        // single elements throughout, 427 joining pieces at the store, 311 so; 244 now.)
                         constexpr int kJoin = kChunks < 2 ? 1 : 2;         // chunks whose rows are staged together
                         constexpr int kRun = 32 * kJoin, kPieces = kRun / 8, kRows = 32 / kPieces;
                         auto phase_of = [](const T* p) { return static_cast<int>(reinterpret_cast<uintptr_t>(p) >> 1) & 7; };
