@@ -78,7 +78,8 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool x_direct, bool w_di
         for (int32_t slices = 1; slices <= std::min(p.kb, 16); ++slices) {
             const int32_t kb_slice = (p.kb + slices - 1) / slices;
             if (slices > 1 && (tiles * slices > 2 * kPairs || (p.kb + kb_slice - 1) / kb_slice != slices)) continue;
-            if (tn == 256 && parts_needed(kb_slice) && (out32 || slices > 1)) continue;
+            // no parts in 256 columns; slices of few blocks, which could do without, are never the cheapest there
+            if (tn == 256 && (slices > 1 || (out32 && parts_needed(kb_slice)))) continue;
             double cost = static_cast<double>((tiles * slices + kPairs - 1) / kPairs) * (kb_slice * block + ends);
             if (slices > 1) cost += 5000.0 + static_cast<double>(M) * N * slices * 4.0 / 1500.0;
             if (best == 0.0 || cost < best) {

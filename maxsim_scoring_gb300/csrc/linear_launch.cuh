@@ -162,7 +162,9 @@ maxsim_status launch_tile_width(const LinearPlan& p, const LinearArgs& l, const 
         if (p.keep_b && p.tn == 128) return launch_tile<T, 128, false, true>(p, l, b16, a_prepared, partial, dev, st);
         if (p.keep_b) return launch_tile<T, 64, false, true>(p, l, b16, a_prepared, partial, dev, st);
     }
-    if (p.tn == 256) return launch_tile<T, 256, kSwap, false>(p, l, b16, a_prepared, partial, dev, st);
+    if constexpr (!std::is_same_v<T, int32_t>) {
+        if (p.tn == 256) return launch_tile<T, 256, kSwap, false>(p, l, b16, a_prepared, partial, dev, st);
+    }
     if (p.tn == 128) return launch_tile<T, 128, kSwap, false>(p, l, b16, a_prepared, partial, dev, st);
     return launch_tile<T, 64, kSwap, false>(p, l, b16, a_prepared, partial, dev, st);
 }
