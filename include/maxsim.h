@@ -420,6 +420,114 @@ maxsim_status maxsim_dropout_bwd(const void *grad, maxsim_dtype dtype, int64_t r
                                  double p, uint64_t seed, uint64_t offset, void *dx, int64_t ld_dx, void *stream);
 
 /*
+ * Rows of 4-bit floating-point values (E2M1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives) with a scale for every block of `block` consecutive values:
+ *   block 16: the scales are E4M3 bytes, and a row has a scale of its own (f32);
+ *   block 32: the scales are E8M0 bytes (2^(byte - 127), 255: NaN), no row scale.
+ * The layout is what the 4-bit tensor cores read. q holds two codes a byte, the
+ * lower column in the low half; a row is ceil(cols / 32) * 16 bytes (zeros
+ * behind its end), rows ld_q bytes apart, q and ld_q multiples of 16.
+ * block_scale is contiguous: with W = ceil(cols / (4 * block)), it has
+ * ceil(rows / 128) * W * 512 bytes, and the scale of row r's block b is byte
+ *   ((r / 128) * W + b / 4) * 512 + (r % 32) * 16 + (r / 32 % 4) * 4 + b % 4.
+ * Bytes of rows and blocks that do not exist are 0.
+ */
+
+/*
+ * Quantisation of rows to 4-bit floating point.
+ *   x            [rows, cols] f16 / bf16 / f32, rows ld_x elements apart
+ *   q, block_scale (out), 16-byte aligned;  scale [rows] f32 (out, block 16)
+ * block 16: a row's scale s is the smallest power of two, at least 2^-126,
+ * with max |row| <= 448 * 6 * s; a block's is b = max(e4m3(max |block| / (6 s)),
+ * 2^-9), and a code is e2m1(x / (s b)).
+ * block 32: b = 2^(floor(log2 max |block|) - 2), at least 2^-127, and a code is
+ * e2m1(x / b).
+ * Both roundings are to the nearest, ties to even, 6 at most, and act on the
+ * exact quotients; -0 keeps its sign. The value of a code is code * b (* s). A
+ * block of 32 that holds a NaN or an infinity gives codes 0 and the scale NaN;
+ * a row of block 16 that does gives codes 0 and the row scale NaN.
+ * 0 <= rows, cols < 2^31 - 127.
+ */
+maxsim_status maxsim_quantize_rows_fp4(const void *x, maxsim_dtype dtype, int64_t rows, int64_t cols, int64_t ld_x,
+                                       int block, uint8_t *q, int64_t ld_q, uint8_t *block_scale, float *scale,
+                                       void *stream);
+
+/*
+ * The rows that such codes stand for: y = code * b * scale, rounded once to
+ * f16 / bf16 / f32 (out_dtype), rows ld_y elements apart. scale [rows] may be
+ * NULL (1). Rows quantised with block 16 or 32 are exact in all three types
+ * wherever the type's exponents reach.
+ */
+maxsim_status maxsim_dequantize_rows_fp4(const uint8_t *q, int64_t ld_q, const uint8_t *block_scale, const float *scale,
+                                         int64_t rows, int64_t cols, int block, maxsim_dtype out_dtype, void *y,
+                                         int64_t ld_y, void *stream);
+
+/*
+ * Matrix product of 4-bit floating-point rows:
+ *   out[m, n] = (sum_k x[m, k] * w[n, k]) * x_scale[m] * w_scale[n] + bias[n]
+ * with x[m, k] and w[n, k] the codes times their block scales.
+ *   x [M, K], w [N, K]: rows ld_x / ld_w bytes apart, with their block scales;
+ *   x_scale [M], w_scale [N] f32 or NULL (1);  bias [N] f32 or NULL
+ *   out [M, N] f16 / bf16 / f32 (out_dtype), rows ld_out elements apart
+ * K counts what the rows hold, a multiple of 32 (codes behind a row's end are
+ * 0 and add nothing). The sum over k is accumulated in fp32, the scales and the
+ * bias are applied in fp32 and the result is rounded once. The same call on
+ * the same inputs gives the same bits. A NaN scale gives NaN in the outputs of
+ * its row or column. 0 <= M, N, K < 2^31 - 1023. No workspace.
+ */
+maxsim_status maxsim_linear_fp4(const uint8_t *x, int64_t ld_x, const uint8_t *x_block_scale, const float *x_scale,
+                                const uint8_t *w, int64_t ld_w, const uint8_t *w_block_scale, const float *w_scale,
+                                const float *bias, int64_t M, int64_t N, int64_t K, int block, maxsim_dtype out_dtype,
+                                void *out, int64_t ld_out, void *stream);
+
+/*
+ * Log probabilities of given columns of score (or logit) rows, with each row's
+ * entropy and its strongest columns. With y = scale * logits over the row's
+ * active columns and p = softmax(y):
+ *   logits       [rows, n] f16 / bf16 / f32, rows ld elements apart, n >= 1
+ *   targets      [rows, T] i64: columns, or -1 for none;  T <= 256
+ *   mask         u8 or NULL: [rows, n] rows ld_mask bytes apart, or [n] for all
+ *                rows with ld_mask = 0; nonzero = active. What an inactive
+ *                column holds has no effect.
+ *   logprob      [rows, T] f32 (out): log p of the targets; 0 for -1; minus
+ *                infinity for an inactive column or one of minus infinity
+ *   entropy      [rows] f32 (out): -sum p log p
+ *   top_idx      [rows, k] i32 (out): the k largest columns by descending value,
+ *                the lower index first among equal ones; k <= min(n, 64).
+ *                Inactive columns, minus infinity and NaN are not listed: -1
+ *                fills up what is left.
+ *   top_logprob  [rows, k] f32 (out): their log p; minus infinity beside a -1
+ *   stats        [rows, 2] f32 (out): the largest active logit M, and
+ *                log2 of sum 2^((logit - M) * scale * log2 e), which
+ *                maxsim_logprobs_bwd takes
+ * scale > 0 and finite (an inverse temperature). A row without active columns
+ * above minus infinity has entropy 0, log p = minus infinity throughout and no
+ * gradient. A row whose active columns hold a NaN or plus infinity gives NaN.
+ * A target that is neither -1 nor a column gives NaN and MAXSIM_ERR_DEVICE_INPUT
+ * in maxsim_device_status. One pass over the logits, in fp32. n < 2^31 - 1024.
+ */
+maxsim_status maxsim_logprobs_fwd(const void *logits, maxsim_dtype dtype, int64_t rows, int64_t n, int64_t ld,
+                                  const int64_t *targets, int64_t T, const uint8_t *mask, int64_t ld_mask, double scale,
+                                  int64_t k, float *logprob, float *entropy, int32_t *top_idx, float *top_logprob,
+                                  float *stats, void *stream);
+
+/*
+ * Its gradient in the logits, in their type, rows ld_dx elements apart:
+ *   dlogits[j] = scale * (sum_t g_t ([j = target_t] - p_j) + sum_i h_i ([j = top_i] - p_j)
+ *                         - g_entropy p_j (log p_j + entropy))
+ * from the forward's stats and entropy, with g = grad_logprob [rows, T],
+ * h = grad_top [rows, k] for top_idx, and grad_entropy [rows], all f32, each
+ * NULL for zero (k and top_idx are read with grad_top alone). A column given
+ * several times has its gradients added in order; targets of -1 and columns
+ * of probability zero (log p = minus infinity) pass none. Inactive columns get 0.
+ */
+maxsim_status maxsim_logprobs_bwd(const void *logits, maxsim_dtype dtype, int64_t rows, int64_t n, int64_t ld,
+                                  const int64_t *targets, int64_t T, const uint8_t *mask, int64_t ld_mask, double scale,
+                                  const float *stats, const float *entropy, const float *grad_logprob,
+                                  const float *grad_entropy, const int32_t *top_idx, const float *grad_top, int64_t k,
+                                  void *dlogits, int64_t ld_dx, void *stream);
+
+/*
  * Bytes of device workspace an operation needs for a shape (0 if none).
  *   MAXSIM_OP_FWD / MAXSIM_OP_FWD_INT8: (Nq, Lq, Nd, Ld, dim)
  *   MAXSIM_OP_FWD_VARLEN:              (Nq, max_lq, Nd, total_d, dim); assumes

@@ -60,6 +60,12 @@ SIGNATURES = {
     "maxsim_linear_int8": (_I, [_VP, _I64, _VP, _VP, _I64, _VP, _VP, _I64, _I64, _I64, _I, _VP, _I64, _VP, _SZ, _VP]),
     "maxsim_dropout_fwd": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _I64, _D, _U64, _U64, _VP, _I64, _VP]),
     "maxsim_dropout_bwd": (_I, [_VP, _I, _I64, _I64, _I64, _D, _U64, _U64, _VP, _I64, _VP]),
+    "maxsim_quantize_rows_fp4": (_I, [_VP, _I, _I64, _I64, _I64, _I, _VP, _I64, _VP, _VP, _VP]),
+    "maxsim_dequantize_rows_fp4": (_I, [_VP, _I64, _VP, _VP, _I64, _I64, _I, _I, _VP, _I64, _VP]),
+    "maxsim_linear_fp4": (_I, [_VP, _I64, _VP, _VP, _VP, _I64, _VP, _VP, _VP, _I64, _I64, _I64, _I, _I, _VP, _I64, _VP]),
+    "maxsim_logprobs_fwd": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _I64, _VP, _I64, _D, _I64, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "maxsim_logprobs_bwd": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _I64, _VP, _I64, _D, _VP, _VP, _VP, _VP, _VP, _VP, _I64,
+                                 _VP, _I64, _VP]),
     "maxsim_workspace_size": (_SZ, [_I, _I64, _I64, _I64, _I64, _I64]),
     "maxsim_status_string": (ctypes.c_char_p, [_I]),
     "maxsim_device_status": (_I, [_VP]),

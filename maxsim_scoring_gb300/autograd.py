@@ -99,3 +99,33 @@ def dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0, residual=None
     saved but (p, seed, offset), from which the backward draws the mask again;
     differentiable at every order."""
     return _Dropout.apply(x, residual, p, seed, offset)
+
+
+class _Logprobs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, targets, mask, scale, k):
+        logprob, entropy, top_idx, top_logprob, stats = ops.logprobs_fwd(logits, targets, mask, scale=scale, k=k)
+        ctx.save_for_backward(logits, targets, mask, stats, entropy, top_idx)
+        ctx.scale = scale
+        ctx.set_materialize_grads(False)
+        if top_idx is not None:
+            ctx.mark_non_differentiable(top_idx)
+        return logprob, entropy, top_idx, top_logprob
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g_logprob, g_entropy, _, g_top):
+        logits, targets, mask, stats, entropy, top_idx = ctx.saved_tensors
+        if g_logprob is None and g_entropy is None and g_top is None:
+            return None, None, None, None, None
+        dlogits = ops.logprobs_bwd(logits, targets, mask, stats, entropy, grad_logprob=g_logprob, grad_entropy=g_entropy,
+                                   top_idx=top_idx, grad_top=g_top, scale=ctx.scale)
+        return dlogits, None, None, None, None
+
+
+def logprobs(logits: torch.Tensor, targets, mask=None, *, scale: float = 1.0, k: int = 0):
+    """Differentiable (logprob, entropy, top_idx, top_logprob) of softmax(scale *
+    logits) over the active columns, as ops.logprobs_fwd gives them: the loss of a
+    contrastive step is -logprob.mean() with each query's document as its target.
+    The gradient is of first order."""
+    return _Logprobs.apply(logits, targets, mask, scale, k)

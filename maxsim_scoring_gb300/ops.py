@@ -629,6 +629,251 @@ def dropout_bwd(grad: torch.Tensor, p: float, seed: int, offset: int = 0, *,
     return out
 
 
+def _fp4_rows(q: torch.Tensor, block_scale: torch.Tensor, scale: Optional[torch.Tensor], name: str, block: int, index: int):
+    """(q, rows, row stride in bytes, block_scale, scale pointer, tensors to keep) of 4-bit rows, checked."""
+    if block not in (16, 32):
+        raise ValueError("block must be 16 or 32")
+    if q.dtype is not torch.uint8 or block_scale.dtype is not torch.uint8:
+        raise TypeError(f"{name} and its block scales must be uint8")
+    if q.get_device() != index or block_scale.get_device() != index or (scale is not None and scale.get_device() != index):
+        raise ValueError(f"{name} and its scales must be on one device with the other operands")
+    shape = q.shape
+    if not shape or shape[-1] % 16:
+        raise ValueError(f"{name} must have rows of whole 16-byte pieces")
+    q, rows, ld = _rows(q, name)
+    if q.data_ptr() % 16 or (rows > 1 and ld % 16):
+        q, ld = q.clone(memory_format=torch.contiguous_format), shape[-1]
+    words = (shape[-1] * 2 + 4 * block - 1) // (4 * block)
+    if block_scale.shape != ((rows + 127) // 128, words, 32, 4, 4):
+        raise ValueError(f"{name}'s block scales must be {((rows + 127) // 128, words, 32, 4, 4)}, got {tuple(block_scale.shape)}")
+    if not block_scale.is_contiguous() or block_scale.data_ptr() % 16:
+        block_scale = block_scale.clone(memory_format=torch.contiguous_format)
+    if scale is not None:
+        if scale.dtype is not torch.float32:
+            raise TypeError(f"{name}'s row scales must be float32")
+        if scale.shape != shape[:-1]:
+            raise ValueError(f"{name}'s row scales must have its leading shape")
+        if not scale.is_contiguous():
+            scale = scale.contiguous()
+    return q, rows, ld, block_scale, scale
+
+
+def quantize_rows_fp4(x: torch.Tensor, *, block: int = 16, q: Optional[torch.Tensor] = None,
+                      block_scale: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None):
+    """(q, block_scale, scale): rows of x [..., K] (f16 / bf16 / f32) as 4-bit
+    floating point (E2M1) with a scale for every `block` values: 16 (E4M3 scales,
+    and one f32 power of two for each row) or 32 (E8M0 scales; scale is None).
+    q is uint8 [..., ceil(K / 32) * 16], two codes a byte; block_scale is uint8
+    [row tiles, words, 32, 4, 4], laid out as the tensor cores read it."""
+    dt = _DT_ANY.get(x.dtype)
+    if dt is None:
+        raise TypeError(f"x must be float16, bfloat16 or float32, got {x.dtype}")
+    if block != 16 and block != 32:
+        raise ValueError("block must be 16 or 32")
+    if block == 32 and scale is not None:
+        raise ValueError("rows in blocks of 32 have no scale of their own")
+    index, shape, dev = _device(x, "x"), x.shape, x.device
+    if index != _current_device():
+        return _with_device(index, quantize_rows_fp4, x, block=block, q=q, block_scale=block_scale, scale=scale)
+    x, rows, ld = _rows(x, "x")
+    cols = shape[-1]
+    width, tiles = (cols + 31) // 32 * 16, ((rows + 127) // 128, (cols + 4 * block - 1) // (4 * block), 32, 4, 4)
+    q_shape = (*shape[:-1], width)
+    q = torch.empty(q_shape, dtype=torch.uint8, device=dev) if q is None else _given(q, "q", q_shape, torch.uint8, dev)
+    block_scale = (torch.empty(tiles, dtype=torch.uint8, device=dev) if block_scale is None
+                   else _given(block_scale, "block_scale", tiles, torch.uint8, dev))
+    ps = None
+    if block == 16:
+        scale = (torch.empty(shape[:-1], dtype=torch.float32, device=dev) if scale is None
+                 else _given(scale, "scale", shape[:-1], torch.float32, dev))
+        ps = scale.data_ptr()
+    rc = _native.lib().maxsim_quantize_rows_fp4(x.data_ptr(), dt, rows, cols, ld, block, q.data_ptr(), width,
+                                                block_scale.data_ptr(), ps, _raw_stream(index))
+    if rc:
+        _native.check(rc, "maxsim_quantize_rows_fp4")
+    return q, block_scale, scale
+
+
+def dequantize_rows_fp4(q: torch.Tensor, block_scale: torch.Tensor, scale: Optional[torch.Tensor] = None, *, block: int = 16,
+                        cols: Optional[int] = None, out_dtype: torch.dtype = torch.bfloat16,
+                        out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The rows [..., cols] in out_dtype that 4-bit rows (as quantize_rows_fp4
+    gives them) stand for; without `cols` all that q holds."""
+    dt = _DT_ANY.get(out_dtype)
+    if dt is None:
+        raise TypeError(f"out_dtype must be float16, bfloat16 or float32, got {out_dtype}")
+    index, shape, dev = _device(q, "q"), q.shape, q.device
+    if index != _current_device():
+        return _with_device(index, dequantize_rows_fp4, q, block_scale, scale, block=block, cols=cols, out_dtype=out_dtype, out=out)
+    q, rows, ld, block_scale, scale = _fp4_rows(q, block_scale, scale, "q", block, index)
+    if cols is None:
+        cols = 2 * shape[-1]
+    if not 0 <= cols <= 2 * shape[-1] or (cols + 31) // 32 * 16 != shape[-1]:
+        raise ValueError(f"rows of {shape[-1]} bytes do not hold {cols} columns")
+    full = (*shape[:-1], cols)
+    out = torch.empty(full, dtype=out_dtype, device=dev) if out is None else _given(out, "out", full, out_dtype, dev)
+    rc = _native.lib().maxsim_dequantize_rows_fp4(q.data_ptr(), ld, block_scale.data_ptr(), _ptr(scale), rows, cols, block, dt,
+                                                  out.data_ptr(), cols, _raw_stream(index))
+    if rc:
+        _native.check(rc, "maxsim_dequantize_rows_fp4")
+    return out
+
+
+def linear_fp4(x: torch.Tensor, x_block_scale: torch.Tensor, x_scale: Optional[torch.Tensor], w: torch.Tensor,
+               w_block_scale: torch.Tensor, w_scale: Optional[torch.Tensor], bias: Optional[torch.Tensor] = None, *,
+               block: int = 16, out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """[..., N] in out_dtype: x @ w.T + bias for 4-bit rows x [..., K] and w [N, K]
+    with their block scales and row scales (as quantize_rows_fp4 gives them, both
+    in blocks of `block`; a row scale of None is 1); bias [N] f32."""
+    dt = _DT_ANY.get(out_dtype)
+    if dt is None:
+        raise TypeError(f"out_dtype must be float16, bfloat16 or float32, got {out_dtype}")
+    index, shape, dev = _device(x, "x"), x.shape, x.device
+    if index != _current_device():
+        return _with_device(index, linear_fp4, x, x_block_scale, x_scale, w, w_block_scale, w_scale, bias, block=block,
+                            out_dtype=out_dtype, out=out)
+    if w.dim() != 2 or not shape or w.shape[1] != shape[-1]:
+        raise ValueError("w must be [N, bytes] with x's bytes a row")
+    N = w.shape[0]
+    x, M, ld_x, x_block_scale, x_scale = _fp4_rows(x, x_block_scale, x_scale, "x", block, index)
+    w, _, ld_w, w_block_scale, w_scale = _fp4_rows(w, w_block_scale, w_scale, "w", block, index)
+    if bias is not None:
+        if bias.dtype is not torch.float32:
+            raise TypeError("bias must be float32")
+        if bias.get_device() != index:
+            raise ValueError("bias must be on x's device")
+        if bias.shape != (N,):
+            raise ValueError("bias must be [N]")
+        if not bias.is_contiguous():
+            bias = bias.contiguous()
+    full = (*shape[:-1], N)
+    out = torch.empty(full, dtype=out_dtype, device=dev) if out is None else _given(out, "out", full, out_dtype, dev)
+    rc = _native.lib().maxsim_linear_fp4(x.data_ptr(), ld_x, x_block_scale.data_ptr(), _ptr(x_scale), w.data_ptr(), ld_w,
+                                         w_block_scale.data_ptr(), _ptr(w_scale), _ptr(bias), M, N, 2 * shape[-1], block, dt,
+                                         out.data_ptr(), N, _raw_stream(index))
+    if rc:
+        _native.check(rc, "maxsim_linear_fp4")
+    return out
+
+
+def _logprobs_rows(logits: torch.Tensor, targets: Optional[torch.Tensor], mask: Optional[torch.Tensor], index: int):
+    """(logits, rows, row stride, targets, T, mask, mask stride) of the log probabilities' operands, checked."""
+    shape = logits.shape
+    if not shape or not shape[-1]:
+        raise ValueError("logits must have at least one column")
+    lead = shape[:-1]
+    T = 0
+    if targets is not None:
+        if targets.dtype is torch.int32:
+            targets = targets.to(torch.int64)
+        if targets.dtype is not torch.int64:
+            raise TypeError(f"targets must be int64 or int32, got {targets.dtype}")
+        if targets.get_device() != index:
+            raise ValueError("targets must be on logits' device")
+        if targets.shape != lead and targets.shape[:-1] != lead:
+            raise ValueError("targets must have logits' leading shape, with one more dimension for several a row")
+        T = 1 if targets.shape == lead else targets.shape[-1]
+        if not targets.is_contiguous():
+            targets = targets.contiguous()
+    ld_mask = 0
+    if mask is not None:
+        if mask.dtype is torch.bool:
+            mask = mask.view(torch.uint8)
+        if mask.dtype is not torch.uint8:
+            raise TypeError(f"mask must be bool or uint8, got {mask.dtype}")
+        if mask.get_device() != index:
+            raise ValueError("mask must be on logits' device")
+        if mask.shape == shape[-1:]:
+            if not mask.is_contiguous():
+                mask = mask.contiguous()
+        elif mask.shape == shape:
+            mask, _, ld_mask = _rows(mask, "mask")
+        else:
+            raise ValueError("mask must have logits' shape, or be [n] for all rows")
+        if len(shape) == 1:
+            ld_mask = 0
+    logits, rows, ld = _rows(logits, "logits")
+    return logits, rows, ld, targets, T, mask, ld_mask
+
+
+def logprobs_fwd(logits: torch.Tensor, targets: Optional[torch.Tensor], mask: Optional[torch.Tensor] = None, *,
+                 scale: float = 1.0, k: int = 0):
+    """(logprob, entropy, top_idx, top_logprob, stats) of softmax(scale * logits) over
+    the active columns of logits [..., n] (f16 / bf16 / f32): the log probabilities
+    of `targets` ([...] or [..., T], -1 for none), each row's entropy, its k <= 64
+    largest columns (by descending value, the lower index first among equal ones;
+    -1 where there are fewer) with their log probabilities, and what logprobs_bwd
+    takes. mask: bool / uint8, logits' shape or [n]; nonzero = active. logprob is
+    None without targets; top_idx and top_logprob are None with k = 0."""
+    dt = _DT_ANY.get(logits.dtype)
+    if dt is None:
+        raise TypeError(f"logits must be float16, bfloat16 or float32, got {logits.dtype}")
+    index, shape, dev = _device(logits, "logits"), logits.shape, logits.device
+    if index != _current_device():
+        return _with_device(index, logprobs_fwd, logits, targets, mask, scale=scale, k=k)
+    logits, rows, ld, targets, T, mask, ld_mask = _logprobs_rows(logits, targets, mask, index)
+    lead, n = shape[:-1], shape[-1]
+    logprob = None if targets is None else torch.empty(targets.shape, dtype=torch.float32, device=dev)
+    entropy = torch.empty(lead, dtype=torch.float32, device=dev)
+    stats = torch.empty((*lead, 2), dtype=torch.float32, device=dev)
+    top_idx = top_logprob = None
+    if k:
+        top_idx = torch.empty((*lead, k), dtype=torch.int32, device=dev)
+        top_logprob = torch.empty((*lead, k), dtype=torch.float32, device=dev)
+    rc = _native.lib().maxsim_logprobs_fwd(logits.data_ptr(), dt, rows, n, ld, _ptr(targets), T, _ptr(mask), ld_mask, scale, k,
+                                           _ptr(logprob), entropy.data_ptr(), _ptr(top_idx), _ptr(top_logprob),
+                                           stats.data_ptr(), _raw_stream(index))
+    if rc:
+        _native.check(rc, "maxsim_logprobs_fwd")
+    return logprob, entropy, top_idx, top_logprob, stats
+
+
+def _grad(g: Optional[torch.Tensor], name: str, shape, index: int):
+    if g is None:
+        return None
+    if g.dtype is not torch.float32:
+        raise TypeError(f"{name} must be float32, got {g.dtype}")
+    if g.shape != shape or g.get_device() != index:
+        raise ValueError(f"{name} must be {tuple(shape)} on logits' device")
+    return g if g.is_contiguous() else g.contiguous()
+
+
+def logprobs_bwd(logits: torch.Tensor, targets: Optional[torch.Tensor], mask: Optional[torch.Tensor], stats: torch.Tensor,
+                 entropy: torch.Tensor, *, grad_logprob: Optional[torch.Tensor] = None,
+                 grad_entropy: Optional[torch.Tensor] = None, top_idx: Optional[torch.Tensor] = None,
+                 grad_top: Optional[torch.Tensor] = None, scale: float = 1.0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gradient in logits, in their type, of logprobs_fwd with the same
+    arguments, from its stats and entropy and the f32 gradients of its outputs
+    (None: zero; grad_top belongs to top_idx)."""
+    dt = _DT_ANY.get(logits.dtype)
+    if dt is None:
+        raise TypeError(f"logits must be float16, bfloat16 or float32, got {logits.dtype}")
+    index, shape, dev = _device(logits, "logits"), logits.shape, logits.device
+    if index != _current_device():
+        return _with_device(index, logprobs_bwd, logits, targets, mask, stats, entropy, grad_logprob=grad_logprob,
+                            grad_entropy=grad_entropy, top_idx=top_idx, grad_top=grad_top, scale=scale, out=out)
+    logits, rows, ld, targets, T, mask, ld_mask = _logprobs_rows(logits, targets, mask, index)
+    lead, n = shape[:-1], shape[-1]
+    stats, entropy = _grad(stats, "stats", (*lead, 2), index), _grad(entropy, "entropy", lead, index)
+    if grad_logprob is not None and targets is None:
+        raise ValueError("grad_logprob needs targets")
+    grad_logprob = _grad(grad_logprob, "grad_logprob", targets.shape if targets is not None else (), index)
+    grad_entropy = _grad(grad_entropy, "grad_entropy", lead, index)
+    k = 0
+    if grad_top is not None:
+        if top_idx is None or top_idx.dtype is not torch.int32 or top_idx.get_device() != index or top_idx.shape[:-1] != lead:
+            raise ValueError("grad_top needs the int32 top_idx of the forward")
+        grad_top = _grad(grad_top, "grad_top", top_idx.shape, index)
+        top_idx, k = top_idx.contiguous(), top_idx.shape[-1]
+    out = torch.empty(shape, dtype=logits.dtype, device=dev) if out is None else _given(out, "out", shape, logits.dtype, dev)
+    rc = _native.lib().maxsim_logprobs_bwd(logits.data_ptr(), dt, rows, n, ld, _ptr(targets), T, _ptr(mask), ld_mask, scale,
+                                           stats.data_ptr(), entropy.data_ptr(), _ptr(grad_logprob), _ptr(grad_entropy),
+                                           _ptr(top_idx), _ptr(grad_top), k, out.data_ptr(), n, _raw_stream(index))
+    if rc:
+        _native.check(rc, "maxsim_logprobs_bwd")
+    return out
+
+
 def device_status(device=None) -> int:
     """Synchronise the current stream and return (and clear) the device status word."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
