@@ -5,21 +5,46 @@
 #include <algorithm>
 #include <cstdint>
 
-#include "maxsim.h"
-#include "host_util.h"
-#include "linear_fp4.cuh"
+#include "linear_fp4_launch.cuh"
 
 namespace maxsim {
+
+extern template maxsim_status run_linear_fp4<__half>(const LinearFp4Plan&, const LinearFp4Args&, int, const HostDevice&, cudaStream_t);
+extern template maxsim_status run_linear_fp4<__nv_bfloat16>(const LinearFp4Plan&, const LinearFp4Args&, int, const HostDevice&, cudaStream_t);
+extern template maxsim_status run_linear_fp4<float>(const LinearFp4Plan&, const LinearFp4Args&, int, const HostDevice&, cudaStream_t);
+
 namespace {
 
 constexpr int64_t kMaxRows = kI32Max - 1023;  // a tile past the last row still has 32-bit coordinates
 
-template <typename T>
-maxsim_status run_linear_fp4(const LinearFp4Args& a, int block, const HostDevice& dev, cudaStream_t st) {
-    const unsigned grid = grid_of((int64_t(a.M) + 15) / 16 * ((int64_t(a.N) + 15) / 16), 1, int64_t(dev.num_sms) * 64);
-    if (block == 16) linear_fp4_simple_kernel<T, 16><<<grid, 256, 0, st>>>(a);
-    else linear_fp4_simple_kernel<T, 32><<<grid, 256, 0, st>>>(a);
-    return launched();
+constexpr int64_t kPairs = 76;                // CTA pairs of a GB300 (152 SMs): plans do not depend on the device
+
+// The tile's width, and the pairs that share its K where there are few tiles,
+// by the time they should take.
+LinearFp4Plan plan_linear_fp4(int64_t M, int64_t N, int64_t K, bool out32) {
+    LinearFp4Plan p;
+    p.swap = N > M;
+    p.kb = static_cast<int32_t>((K + kFp4TileK - 1) / kFp4TileK);
+    const int64_t rows_a = p.swap ? N : M, rows_b = p.swap ? M : N;
+    double best = 0.0;
+    for (int tn = out32 ? 128 : 256; tn >= 64; tn /= 2) {
+        const int64_t tiles_b = (rows_b + tn - 1) / tn, tiles = (rows_a + kFp4TileM - 1) / kFp4TileM * tiles_b;
+        const double stage = tn == 256 ? 900.0 : tn == 128 ? 650.0 : 500.0, ends = tn == 256 ? 3000.0 : tn == 128 ? 2000.0 : 1500.0;
+        for (int32_t splits = 1; splits <= kFp4MaxSplits; splits *= 2) {
+            const int32_t kb_split = (p.kb + splits - 1) / splits;
+            if (splits > 1 && (tn != 64 || tiles * splits > kPairs || kb_split * (splits - 1) >= p.kb)) continue;
+            const double cost = static_cast<double>((tiles * splits + kPairs - 1) / kPairs) * (kb_split * stage + ends) + (splits > 1 ? 2500.0 : 0.0);
+            if (best == 0.0 || cost < best) {
+                best = cost;
+                p.tn = tn;
+                p.tiles = tiles;
+                p.tiles_b = tiles_b;
+                p.splits = splits;
+                p.kb_split = kb_split;
+            }
+        }
+    }
+    return p;
 }
 
 }  // namespace
@@ -50,9 +75,11 @@ maxsim_status maxsim_linear_fp4(const uint8_t* x, int64_t ld_x, const uint8_t* x
     const LinearFp4Args a{x, w, x_block_scale, w_block_scale, ld_x, ld_w, ld_out, x_scale, w_scale, bias, out,
                           static_cast<int32_t>(M), static_cast<int32_t>(N), static_cast<int32_t>(K),
                           static_cast<int32_t>((K + 4 * block - 1) / (4 * block))};
-    if (out_dtype == MAXSIM_F16) return run_linear_fp4<__half>(a, block, dev, st);
-    if (out_dtype == MAXSIM_BF16) return run_linear_fp4<__nv_bfloat16>(a, block, dev, st);
-    return run_linear_fp4<float>(a, block, dev, st);
+    const LinearFp4Plan p = plan_linear_fp4(M, N, K, out_dtype == MAXSIM_F32);
+    if (p.tiles > kI32Max) return MAXSIM_ERR_UNSUPPORTED;
+    if (out_dtype == MAXSIM_F16) return run_linear_fp4<__half>(p, a, block, dev, st);
+    if (out_dtype == MAXSIM_BF16) return run_linear_fp4<__nv_bfloat16>(p, a, block, dev, st);
+    return run_linear_fp4<float>(p, a, block, dev, st);
 }
 
 }  // extern "C"
