@@ -12,6 +12,7 @@
 
 #include "head_kernels.cuh"
 #include "ptx.cuh"
+#include "tile_store.cuh"
 
 namespace maxsim {
 
@@ -45,73 +46,186 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN where eithe
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
     return d;
 }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {  // both sums in one instruction
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 z, x, y;\n\t"
+        "mov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
 __device__ __forceinline__ float minus_inf() { return __uint_as_float(0xff800000u); }
 
-// kVec elements (16 bytes) of a row.
+// Bytes of ones where the selected byte's high bit is set (a selector's digit: 8 + the byte).
+__device__ __forceinline__ uint32_t byte_signs(uint32_t w, uint32_t selector) {
+    uint32_t d;
+    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(d) : "r"(w), "r"(selector));
+    return d;
+}
+
+// ---------------------------------------------------------------- 16-byte pieces of a row
+
 template <typename T>
-struct Piece {
+struct PieceOf {
     static constexpr int kVec = 16 / static_cast<int>(sizeof(T));
-    float v[kVec];
-    __device__ __forceinline__ void set(uint4 u) {
+    // the type's minus infinity in every place of a word
+    static constexpr uint32_t kMinusInf = std::is_same_v<T, float> ? 0xff800000u : std::is_same_v<T, __half> ? 0xfc00fc00u : 0xff80ff80u;
+
+    // elements 2 i and 2 i + 1
+    static __device__ __forceinline__ float2 pair(const uint4& u, int i) {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        else return unpack2<T>(w[i]);
+    }
+    // the larger elements of two words, NaN where both are
+    static __device__ __forceinline__ uint32_t max_words(uint32_t a, uint32_t b) {
+        uint32_t d;
+        if constexpr (std::is_same_v<T, float>) asm("max.f32 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        else if constexpr (std::is_same_v<T, __half>) asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        else asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    }
+    // the smaller ones
+    static __device__ __forceinline__ uint32_t min_words(uint32_t a, uint32_t b) {
+        uint32_t d;
+        if constexpr (std::is_same_v<T, float>) asm("min.f32 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        else if constexpr (std::is_same_v<T, __half>) asm("min.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        else asm("min.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    }
+    static __device__ __forceinline__ uint32_t min_words(const uint4& u) { return min_words(min_words(u.x, u.y), min_words(u.z, u.w)); }
+    static __device__ __forceinline__ float word_min(uint32_t w) {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w);
+        const float2 v = unpack2<T>(w);
+        return fminf(v.x, v.y);
+    }
+    static __device__ __forceinline__ uint32_t max_words(const uint4& u) { return max_words(max_words(u.x, u.y), max_words(u.z, u.w)); }
+    static __device__ __forceinline__ float word_max(uint32_t w) {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w);
+        const float2 v = unpack2<T>(w);
+        return fmaxf(v.x, v.y);
+    }
+    // minus infinity where the high bit of the element's byte in m is clear
+    static __device__ __forceinline__ uint4 masked(uint4 u, const uint32_t (&m)[kVec / 4]) {
+        uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-            if constexpr (sizeof(T) == 4) {
-                v[i] = __uint_as_float(w[i]);
-            } else {
-                const uint32_t h = (i & 1) ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu;
-                if constexpr (std::is_same_v<T, __half>) v[i] = __half2float(__ushort_as_half(static_cast<unsigned short>(h)));
-                else v[i] = __uint_as_float(h << 16);
-            }
+        for (int i = 0; i < 4; ++i) {
+            // the sign of one byte (of two) in all bytes of its element
+            const uint32_t keep = sizeof(T) == 4 ? byte_signs(m[0], 0x8888 + 0x1111 * i) : byte_signs(m[i >> 1], (i & 1) ? 0xbbaa : 0x9988);
+            w[i] = (w[i] & keep) | (kMinusInf & ~keep);
         }
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
 };
 
+// High bits of the bytes of w that are not zero.
+__device__ __forceinline__ uint32_t nonzero_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x7f7f7f7fu) | w; }
+
 // A row seen as aligned 16-byte pieces: piece p holds columns p * kVec - skip
 // and on; the first and the last one may reach over the row's ends, and are
-// read element by element then.
+// read element by element then. Columns fit 32 bits.
 template <typename T>
 struct PiecedRow {
-    static constexpr int kVec = Piece<T>::kVec;
+    using P = PieceOf<T>;
+    static constexpr int kVec = P::kVec;
     const T* x;
     const uint8_t* mask;
-    int64_t n;
-    int32_t skip;
-    int32_t pieces;
+    int32_t n, skip, pieces;
 
-    __device__ __forceinline__ PiecedRow(const T* row, const uint8_t* m, int64_t cols) : x(row), mask(m), n(cols) {
-        skip = static_cast<int32_t>(reinterpret_cast<uintptr_t>(row) / sizeof(T)) & (kVec - 1);
-        pieces = static_cast<int32_t>((n + skip + kVec - 1) / kVec);
+    // `place`: pieces are those of the row that starts here (a multiple of T's size)
+    __device__ __forceinline__ PiecedRow(const T* row, const uint8_t* m, int64_t cols, const T* place)
+        : x(row), mask(m), n(static_cast<int32_t>(cols)) {
+        skip = static_cast<int32_t>(reinterpret_cast<uintptr_t>(place) / sizeof(T)) & (kVec - 1);
+        pieces = static_cast<int32_t>((cols + skip + kVec - 1) / kVec);
     }
-    __device__ __forceinline__ int64_t column(int32_t p) const { return static_cast<int64_t>(p) * kVec - skip; }
+    __device__ __forceinline__ int32_t column(int32_t p) const { return p * kVec - skip; }
     __device__ __forceinline__ bool whole(int32_t p) const { return column(p) >= 0 && column(p) + kVec <= n; }
-    // 16 bytes of piece p; what is not the row's is minus infinity
+    // whole piece p
+    __device__ __forceinline__ uint4 load_whole(int32_t p) const { return __ldg(reinterpret_cast<const uint4*>(x + column(p))); }
+    // piece p; what is not the row's is minus infinity. kShift: x's phase is not `place`'s.
+    template <bool kShift = false>
     __device__ __forceinline__ uint4 load(int32_t p) const {
-        const int64_t at = column(p);
-        if (at >= 0 && at + kVec <= n) return __ldg(reinterpret_cast<const uint4*>(x + at));
-        alignas(16) T e[kVec];
+        const int32_t at = column(p);
+        if constexpr (kShift) {
+            if (at >= kVec && at + 2 * kVec <= n) {  // the two aligned pieces that hold it are the row's
+                const uintptr_t from = reinterpret_cast<uintptr_t>(x + at);
+                const uint4 lo = __ldg(reinterpret_cast<const uint4*>(from & ~uintptr_t(15)));
+                const uint4 hi = __ldg(reinterpret_cast<const uint4*>((from & ~uintptr_t(15)) + 16));
+                uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                const uint32_t by = static_cast<uint32_t>(from) & 15u;
+                if (by & 8u) {
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) e[i] = at + i >= 0 && at + i < n ? x[at + i] : from_f32<T>(minus_inf());
-        return *reinterpret_cast<const uint4*>(e);
+                    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+                }
+                if (by & 4u) {
+#pragma unroll
+                    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+                }
+                const uint32_t bits = (by & 3u) * 8;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], bits);
+                return make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        } else {
+            if (at >= 0 && at + kVec <= n) return load_whole(p);
+        }
+        T e[kVec];  // all loads before the first use
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) e[i] = x[min(max(at + i, 0), n - 1)];
+        alignas(16) T o[kVec];
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) o[i] = at + i >= 0 && at + i < n ? e[i] : from_f32<T>(minus_inf());
+        return *reinterpret_cast<const uint4*>(o);
     }
-    // bit i: column i of piece p is active
-    __device__ __forceinline__ uint32_t active(int32_t p) const {
-        const int64_t at = column(p);
-        uint32_t bits = 0;
+    // the mask's bytes of piece p, a high bit for each active column
+    __device__ __forceinline__ void active(int32_t p, uint32_t (&m)[kVec / 4]) const {
+        const int32_t at = column(p);
+        if (at >= 4 && at + kVec + 4 <= n) {  // the words that hold them are the mask's own
+            const uintptr_t from = reinterpret_cast<uintptr_t>(mask + at);
+            if ((from & (kVec - 1)) == 0) {
+                if constexpr (kVec == 8) {
+                    const uint2 v = __ldg(reinterpret_cast<const uint2*>(from));
+                    m[0] = nonzero_bytes(v.x);
+                    m[1] = nonzero_bytes(v.y);
+                } else {
+                    m[0] = nonzero_bytes(__ldg(reinterpret_cast<const uint32_t*>(from)));
+                }
+                return;
+            }
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(from & ~uintptr_t(3));
+            const uint32_t bits = (static_cast<uint32_t>(from) & 3u) * 8;
+            uint32_t v[kVec / 4 + 1];
 #pragma unroll
-        for (int i = 0; i < kVec; ++i)
-            if (at + i >= 0 && at + i < n && mask[at + i]) bits |= 1u << i;
-        return bits;
-    }
-    template <bool kMask>
-    __device__ __forceinline__ void get(Piece<T>& e, uint4 u, uint32_t bits) const {
-        e.set(u);
-        if constexpr (kMask) {
+            for (int i = 0; i <= kVec / 4; ++i) v[i] = __ldg(w + i);
 #pragma unroll
-            for (int i = 0; i < kVec; ++i)
-                if (!(bits >> i & 1)) e.v[i] = minus_inf();
+            for (int i = 0; i < kVec / 4; ++i) m[i] = nonzero_bytes(__funnelshift_r(v[i], v[i + 1], bits));
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < kVec / 4; ++j) {
+            uint8_t b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[i] = mask[min(max(at + j * 4 + i, 0), n - 1)];
+            m[j] = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (at + j * 4 + i >= 0 && at + j * 4 + i < n && b[i]) m[j] |= 0x80u << (8 * i);
         }
     }
+    template <bool kMask>
+    __device__ __forceinline__ uint4 keep_active(uint4 u, int32_t p) const {
+        if constexpr (kMask) {
+            uint32_t m[kVec / 4];
+            active(p, m);
+            u = P::masked(u, m);
+        }
+        return u;
+    }
+    // piece p with minus infinity in inactive columns
+    template <bool kMask>
+    __device__ __forceinline__ uint4 get(int32_t p) const { return keep_active<kMask>(load(p), p); }
+    // one column as a key of the order of the strongest
+    template <bool kMask>
+    __device__ __forceinline__ uint64_t key(int32_t c) const;
 };
 
 // Running maximum, sum and weighted sum of what a thread (or a group) has seen.
@@ -131,55 +245,93 @@ struct Running {
     }
 };
 
-template <typename T>
-__device__ __forceinline__ float piece_max(const Piece<T>& e) {
-    float m = e.v[0];
-#pragma unroll
-    for (int i = 1; i + 1 < Piece<T>::kVec; i += 2) m = fmax3(m, e.v[i], e.v[i + 1]);
-    return fmaxf(m, e.v[Piece<T>::kVec - 1]);
-}
+// Two sums of a thread side by side (packed arithmetic).
+struct Pairwise {
+    float2 s = make_float2(0.f, 0.f), w = make_float2(0.f, 0.f);
+};
 
+// Adds a piece's exponentials: a subtraction, a product, a comparison (which
+// keeps 0 * infinity out of the weighted sum and lets NaN pass), an
+// exponential, a sum and an fma for each element.
 template <typename T>
-__device__ __forceinline__ void add_piece(Running& r, const Piece<T>& e, float ref, float c) {
+__device__ __forceinline__ void add_piece(Pairwise& r, const uint4& u, float2 minus_ref, float2 c) {
 #pragma unroll
-    for (int i = 0; i < Piece<T>::kVec; ++i) {
-        const float t = max_nan((e.v[i] - ref) * c, kNoExponent), y = exp2_fast(t);
-        r.s += y;
-        r.w = __fmaf_rn(y, t, r.w);
+    for (int i = 0; i < PieceOf<T>::kVec / 2; ++i) {
+        float2 t = mul2(add2(PieceOf<T>::pair(u, i), minus_ref), c);
+        t.x = max_nan(t.x, kNoExponent);
+        t.y = max_nan(t.y, kNoExponent);
+        const float2 e = make_float2(exp2_fast(t.x), exp2_fast(t.y));
+        r.s = add2(r.s, e);
+        r.w = fma2(e, t, r.w);
     }
 }
 
-constexpr int kLogprobsBatch = 4;  // pieces of a thread in flight
+constexpr int kLogprobsBatch = 4;  // pieces of a thread that are looked at together
+constexpr int kTopSlots = 8;       // parts of a thread's share whose maxima are kept
 
-// A thread's share of a row: pieces first, first + step, ... The column of the
-// piece that holds the maximum (the first of equal ones) goes to *best.
-template <typename T, bool kMask, bool kBest>
-__device__ __forceinline__ Running scan_row(const PiecedRow<T>& row, int32_t first, int32_t last, int32_t step, float c, int32_t* best) {
+// A thread's share of a row, pieces first, first + step, ..., in batches.
+// kTop: the piece that holds the maximum (the first of equal ones) goes to
+// *best, and the maxima of up to kTopSlots runs of `slot` batches to slots[i *
+// threads]. Loads of one batch are in flight together, and other warps' beside them:
+// registers for a second batch cost more warps than they bring.
+template <typename T, bool kMask, bool kTop>
+__device__ __forceinline__ Running scan_row(const PiecedRow<T>& row, int32_t first, int32_t last, int32_t step, float c, int32_t* best,
+                                            float* slots, int32_t slot, int32_t threads) {
+    using P = PieceOf<T>;
     Running r;
+    Pairwise sums;
+    const float2 c2 = make_float2(c, c);
+    const uint4 none = make_uint4(P::kMinusInf, P::kMinusInf, P::kMinusInf, P::kMinusInf);
+    float slot_max = minus_inf();
+    int32_t left = slot;
     for (int32_t p = first; p < last; p += step * kLogprobsBatch) {
         uint4 u[kLogprobsBatch];
-        uint32_t bits[kLogprobsBatch];
+        if (row.whole(p) && p + 3 * step < last && row.whole(p + 3 * step)) {
 #pragma unroll
-        for (int j = 0; j < kLogprobsBatch; ++j)
-            if (p + j * step < last) {
-                u[j] = row.load(p + j * step);
-                if constexpr (kMask) bits[j] = row.active(p + j * step);
-            }
+            for (int j = 0; j < kLogprobsBatch; ++j) u[j] = row.load_whole(p + j * step);
 #pragma unroll
-        for (int j = 0; j < kLogprobsBatch; ++j) {
-            if (p + j * step >= last) break;
-            Piece<T> e;
-            row.template get<kMask>(e, u[j], kMask ? bits[j] : 0u);
-            const float m = piece_max(e);
-            if (m > r.m) {
-                r.raise(m, c);
-                if constexpr (kBest) *best = p + j * step;
-            }
-            add_piece(r, e, r.reference(), c);
+            for (int j = 0; j < kLogprobsBatch; ++j) u[j] = row.template keep_active<kMask>(u[j], p + j * step);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kLogprobsBatch; ++j) u[j] = p + j * step < last ? row.template get<kMask>(p + j * step) : none;
         }
+        uint32_t w[kLogprobsBatch];
+#pragma unroll
+        for (int j = 0; j < kLogprobsBatch; ++j) w[j] = P::max_words(u[j]);
+        const float m = P::word_max(P::max_words(P::max_words(w[0], w[1]), P::max_words(w[2], w[3])));
+        if (m > r.m) {
+            if constexpr (kTop) {
+#pragma unroll
+                for (int j = kLogprobsBatch - 1; j >= 0; --j)
+                    if (P::word_max(w[j]) == m) *best = p + j * step;
+            }
+            const float d = max_nan((r.m - m) * c, kNoExponent), f = exp2_fast(d);  // as Running::raise
+            const float2 f2 = make_float2(f, f);
+            sums.w = mul2(fma2(make_float2(d, d), sums.s, sums.w), f2);
+            sums.s = mul2(sums.s, f2);
+            r.m = m;
+        }
+        if constexpr (kTop) {
+            if (slots) {
+                slot_max = fmaxf(slot_max, m);
+                if (--left == 0 || p + step * kLogprobsBatch >= last) {
+                    *slots = slot_max;
+                    slots += threads;
+                    slot_max = minus_inf();
+                    left = slot;
+                }
+            }
+        }
+        const float ref = -r.reference();
+        const float2 ref2 = make_float2(ref, ref);
+#pragma unroll
+        for (int j = 0; j < kLogprobsBatch; ++j) add_piece<T>(sums, u[j], ref2, c2);
     }
+    r.s = sums.s.x + sums.s.y;
+    r.w = sums.w.x + sums.w.y;
     return r;
 }
+static_assert(kLogprobsBatch == 4, "the maxima above");
 
 template <int kThreads>
 __device__ __forceinline__ Running reduce_warp(Running r, float c) {
@@ -212,53 +364,54 @@ struct RowStats {
     }
 };
 
-// The log probability of one column: minus infinity where it is not active. (Not by way of t_j, which overflows earlier.)
-template <typename T>
-__device__ __forceinline__ float column_logprob(const T* row, const uint8_t* mask, int64_t j, const RowStats& st, float scale) {
-    if (mask && !mask[j]) return minus_inf();
-    const float x = to_f32(row[j]);
-    if (x == minus_inf()) return x;
-    return (x - st.m) * scale - kLn2 * st.l;
+// The log probability of a column of value x. (Not by way of t_j, which overflows earlier.)
+__device__ __forceinline__ float value_logprob(float x, const RowStats& st, float scale) {
+    return x == minus_inf() ? x : (x - st.m) * scale - kLn2 * st.l;
 }
+
+// A target's value: minus infinity where its column is not active. `kind`: 0 a
+// column, 1 none (-1), 2 not a column.
+template <typename T>
+__device__ __forceinline__ float target_value(const LogprobsArgs& a, int64_t r, int i, const T* row, const uint8_t* mask, int* kind) {
+    const int64_t j = a.targets[r * a.T + i];
+    *kind = j >= 0 && j < a.n ? 0 : j == -1 ? 1 : 2;
+    if (*kind) return 0.f;
+    return mask && !mask[j] ? minus_inf() : to_f32(row[j]);
+}
+__device__ __forceinline__ void write_target(const LogprobsArgs& a, int64_t r, int i, float x, int kind, const RowStats& st) {
+    if (kind == 2) atomicCAS(a.status, 0, kDeviceInput);
+    a.logprob[r * a.T + i] = kind == 0 ? value_logprob(x, st, a.scale) : kind == 1 ? 0.f : __uint_as_float(0x7fffffffu);
+}
+
+// The target of thread t of the group that holds the row, read before the scan.
+struct Ahead {
+    float x = 0.f;
+    int kind = 1;
+    template <typename T>
+    __device__ __forceinline__ Ahead(const LogprobsArgs& a, int64_t r, const T* row, const uint8_t* mask, int t) {
+        if (t < a.T) x = target_value(a, r, t, row, mask, &kind);
+    }
+};
 
 // Writes what does not depend on the strongest columns; every thread of the
 // group that holds the row calls it (thread t of `threads`).
 template <typename T>
 __device__ __forceinline__ void write_row(const LogprobsArgs& a, int64_t r, const T* row, const uint8_t* mask, const RowStats& st,
-                                          int t, int threads) {
+                                          const Ahead& ahead, int t, int threads) {
     if (t == 0) {
         a.entropy[r] = st.h;
         a.stats[2 * r] = st.m;
         a.stats[2 * r + 1] = st.l;
     }
-    for (int i = t; i < a.T; i += threads) {
-        const int64_t j = a.targets[r * a.T + i];
-        float v = 0.f;
-        if (j >= 0 && j < a.n) {
-            v = column_logprob(row, mask, j, st, a.scale);
-        } else if (j != -1) {
-            atomicCAS(a.status, 0, kDeviceInput);
-            v = __uint_as_float(0x7fffffffu);
-        }
-        a.logprob[r * a.T + i] = v;
+    if (t < a.T) write_target(a, r, t, ahead.x, ahead.kind, st);
+    for (int i = t + threads; i < a.T; i += threads) {
+        int kind;
+        const float x = target_value(a, r, i, row, mask, &kind);
+        write_target(a, r, i, x, kind, st);
     }
 }
 
-// ---------------------------------------------------------------- short rows: a warp each
-
-template <typename T, bool kMask>
-__global__ void __launch_bounds__(256) logprobs_warp_kernel(const LogprobsArgs a) {
-    const int lane = threadIdx.x & 31;
-    for (int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); r < a.rows; r += static_cast<int64_t>(gridDim.x) * 8) {
-        const T* x = static_cast<const T*>(a.x) + r * a.ld;
-        const uint8_t* mask = kMask ? a.mask + r * a.ld_mask : nullptr;
-        const PiecedRow<T> row(x, mask, a.n);
-        const RowStats st(reduce_warp<32>(scan_row<T, kMask, false>(row, lane, row.pieces, 32, a.c, nullptr), a.c));
-        write_row(a, r, x, mask, st, lane, 32);
-    }
-}
-
-// ---------------------------------------------------------------- long rows: a block, or a cluster of blocks
+// ---------------------------------------------------------------- the strongest columns
 
 // A column's place in the order of the strongest: larger value, then lower
 // index, first. 0: not listed (inactive, minus infinity, NaN).
@@ -269,74 +422,264 @@ __device__ __forceinline__ uint64_t rank_key(float v, int32_t column) {
     b = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
     return static_cast<uint64_t>(b) << 32 | (0xffffffffu - static_cast<uint32_t>(column));
 }
+__device__ __forceinline__ float key_value(uint64_t key) {
+    const uint32_t b = static_cast<uint32_t>(key >> 32);
+    return __uint_as_float((b & 0x80000000u) ? b & 0x7fffffffu : ~b);
+}
 __device__ __forceinline__ int32_t key_column(uint64_t key) { return static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(key)); }
 
-constexpr int kTopBuffer = 1024;
+template <typename T>
+template <bool kMask>
+__device__ __forceinline__ uint64_t PiecedRow<T>::key(int32_t c) const {
+    if (c < 0 || c >= n || (kMask && !mask[c])) return 0;
+    return rank_key(to_f32(x[c]), c);
+}
 
+__device__ __forceinline__ uint64_t warp_max_key(uint64_t key) {
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(key >> 32));
+    const uint32_t lo = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(key >> 32) == hi ? static_cast<uint32_t>(key) : 0u);
+    return static_cast<uint64_t>(hi) << 32 | lo;
+}
+
+__device__ __forceinline__ void write_top(const LogprobsArgs& a, int64_t r, int i, uint64_t key, const RowStats& st) {
+    a.top_idx[r * a.k + i] = key ? key_column(key) : -1;
+    a.top_logprob[r * a.k + i] = key ? value_logprob(key_value(key), st, a.scale) : minus_inf();
+}
+
+// ---------------------------------------------------------------- short rows: a warp each
+
+// The strongest columns one after another: the largest of the lanes' own
+// maxima is next, and its lane's columns below it are searched, by the whole
+// warp, for that lane's next maximum.
+template <typename T, bool kMask>
+__device__ __forceinline__ void warp_top(const LogprobsArgs& a, int64_t r, const PiecedRow<T>& row, float m, int32_t best, const RowStats& st) {
+    constexpr int kVec = PieceOf<T>::kVec;
+    const int lane = threadIdx.x & 31;
+    uint64_t own = 0;
+    if (m > minus_inf()) {
+#pragma unroll
+        for (int j = kVec - 1; j >= 0; --j) own = max(own, row.template key<kMask>(row.column(best) + j));
+    }
+    uint64_t taken = 0;  // this lane's of the last 32
+    const int32_t per = (row.pieces + 31) / 32 * kVec;  // columns of a lane
+    for (int i = 0; i < a.k; ++i) {
+        const uint64_t key = warp_max_key(own);
+        if ((i & 31) == lane) taken = key;
+        if (key != 0) {
+            const uint32_t from = __ballot_sync(0xffffffffu, own == key);
+            const int owner = __ffs(from) - 1;
+            uint64_t next = 0;
+            for (int32_t e = lane; e < per; e += 32) {
+                const uint64_t k = row.template key<kMask>(row.column(owner + e / kVec * 32) + e % kVec);
+                if (k < key) next = max(next, k);
+            }
+            next = warp_max_key(next);
+            if (lane == owner) own = next;
+        }
+        if ((i & 31) == 31 || i + 1 == a.k) {
+            const int at = (i & ~31) + lane;
+            if (at <= i) write_top(a, r, at, taken, st);
+        }
+    }
+}
+
+template <typename T, bool kMask, bool kTop>
+__global__ void __launch_bounds__(256) logprobs_warp_kernel(const LogprobsArgs a) {
+    const int lane = threadIdx.x & 31;
+    const int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (r >= a.rows) return;
+    const T* x = static_cast<const T*>(a.x) + r * a.ld;
+    const uint8_t* mask = kMask ? a.mask + r * a.ld_mask : nullptr;
+    const PiecedRow<T> row(x, mask, a.n, x);
+    const Ahead ahead(a, r, x, mask, lane);
+    int32_t best = 0;
+    const Running mine = scan_row<T, kMask, kTop>(row, lane, row.pieces, 32, a.c, &best, nullptr, 0, 0);
+    const RowStats st(reduce_warp<32>(mine, a.c));
+    write_row(a, r, x, mask, st, ahead, lane, 32);
+    if constexpr (kTop) warp_top<T, kMask>(a, r, row, mine.m, best, st);
+}
+
+// ---------------------------------------------------------------- long rows: a block, or a cluster of blocks
+
+constexpr int kTopBuffer = 512;
+
+template <int kThreads>
 struct TopShared {
     uint64_t found[kTopBuffer];
     uint64_t best[kLogprobsMaxTop];
-    int32_t list[1024];
+    float slots[kTopSlots * kThreads];  // maxima of the threads' runs of batches
+    uint16_t list[kTopSlots * kThreads];
     int32_t listed, count;
-    uint64_t bound;
+    uint64_t bound, bounds[16];
 };
 
 // The k largest of found[0 .. count) into best, descending (0 where there are fewer).
 template <int kThreads>
-__device__ __forceinline__ void rank_found(TopShared* sh, int count, int k) {
+__device__ __forceinline__ void rank_found(TopShared<kThreads>* sh, int count, int k) {
     for (int i = threadIdx.x; i < k; i += kThreads) sh->best[i] = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < count; i += kThreads) {
         const uint64_t mine = sh->found[i];
         int rank = 0;
+#pragma unroll 4
         for (int j = 0; j < count; ++j) rank += sh->found[j] > mine;
         if (rank < k) sh->best[rank] = mine;
     }
     __syncthreads();
 }
 
-// The k strongest columns of pieces [0, last) with this block's stride.
-// A thread's own maximum says whether it can hold any of them: at least k
-// threads' maxima reach the bound that is searched for here, and only the
-// pieces of threads whose maximum reaches it are read again. Ties and rows
-// whose large columns all fall to one thread give more candidates than the
-// buffer takes: the k-th best of those found is then a higher bound.
-template <typename T, bool kMask, int kThreads>
-__device__ __forceinline__ void block_top(TopShared* sh, const PiecedRow<T>& row, int32_t first, int32_t last, int32_t step, float m,
-                                          int32_t best, int k) {
-    constexpr int kVec = Piece<T>::kVec;
-    // upper and lower end of what the maximum's piece holds
-    const uint64_t upper = m > minus_inf() ? rank_key(m, static_cast<int32_t>(max(row.column(best), static_cast<int64_t>(0)))) : 0;
-    const uint64_t lower = m > minus_inf() ? rank_key(m, static_cast<int32_t>(row.column(best) + kVec - 1)) : 0;
-    uint64_t lo = 1, hi = ~0ull;
-    if (__syncthreads_count(lower != 0) >= k) {
-        // the largest bound (or one reached by at most 2 k threads) that k threads reach
-        while (lo < hi) {
-            const uint64_t mid = lo + ((hi - lo) >> 1) + 1;
-            const int n = __syncthreads_count(lower >= mid);
-            if (n >= k) lo = mid;
-            else hi = mid - 1;
-            if (n >= k && n <= 2 * k) break;
+// The k largest of `lists` descending lists of k keys (0: none) into best: a
+// key's rank is its place in its own list and the number of larger keys in each
+// other one, found by halves.
+template <int kThreads>
+__device__ __forceinline__ void merge_lists(uint64_t* best, const uint64_t* all, int lists, int k) {
+    for (int i = threadIdx.x; i < k; i += kThreads) best[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < lists * k; i += kThreads) {
+        const uint64_t mine = all[i];
+        if (mine == 0) continue;
+        const int own = i / k;
+        int rank = i - own * k;
+        for (int l = 0; l < lists && rank < k; ++l) {
+            if (l == own) continue;
+            int lo = 0, hi = k;  // the first place whose key is not larger
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (all[l * k + mid] > mine) lo = mid + 1;
+                else hi = mid;
+            }
+            rank += lo;
+        }
+        if (rank < k) best[rank] = mine;
+    }
+    __syncthreads();
+}
+
+// Bounds that at least k of the threads' keys reach, and hardly more (1 where
+// there are fewer keys): thread t's keys are found[0 .. kThreads). One warp
+// searches by halves, among the values, and among the columns of one value only
+// where many are equal.
+template <int kThreads>
+__device__ __forceinline__ uint64_t search_bound(const uint64_t* found, int k) {
+    constexpr int kPer = kThreads / 32;
+    const int most = k + (k >> 2);
+    uint64_t mine[kPer];
+    uint32_t least = 0xffffffffu, largest = 0;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        mine[i] = found[i * 32 + (threadIdx.x & 31)];
+        const uint32_t v = static_cast<uint32_t>(mine[i] >> 32);
+        n += v != 0;
+        largest = max(largest, v);
+        if (v) least = min(least, v);
+    }
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (n < k) return 1;
+    uint32_t lo = __reduce_min_sync(0xffffffffu, least), hi = __reduce_max_sync(0xffffffffu, largest);
+    while (lo < hi && n > most) {
+        const uint32_t mid = lo + ((hi - lo) >> 1) + 1;
+        int count = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) count += static_cast<uint32_t>(mine[i] >> 32) >= mid;
+        count = __reduce_add_sync(0xffffffffu, count);
+        if (count >= k) {
+            lo = mid;
+            n = count;
+        } else {
+            hi = mid - 1;
         }
     }
-    uint64_t bound = lo;
-    for (;;) {
-        if (threadIdx.x == 0) sh->listed = sh->count = 0;
-        __syncthreads();
-        if (upper >= bound) sh->list[atomicAdd(&sh->listed, 1)] = threadIdx.x;
-        __syncthreads();
-        const int32_t per = (last - first + step - 1) / step, total = per * sh->listed;
-        for (int32_t i = threadIdx.x; i < total; i += kThreads) {
-            const int32_t p = first + sh->list[i / per] + (i % per) * step;
-            if (p >= last) continue;
-            Piece<T> e;
-            row.template get<kMask>(e, row.load(p), kMask ? row.active(p) : 0u);
+    uint64_t bound = static_cast<uint64_t>(lo) << 32;
+    if (n <= most) return bound;
+    uint32_t low = 0, high = 0xffffffffu;  // lo is the k-th value: columns decide
+    while (low < high && n > most) {
+        const uint32_t mid = low + ((high - low) >> 1) + 1;
+        int count = 0;
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                const uint64_t key = rank_key(e.v[j], static_cast<int32_t>(row.column(p) + j));
-                if (key >= bound) {
-                    const int at = atomicAdd(&sh->count, 1);
-                    if (at < kTopBuffer) sh->found[at] = key;
+        for (int i = 0; i < kPer; ++i) count += mine[i] >= (bound | mid);
+        count = __reduce_add_sync(0xffffffffu, count);
+        if (count >= k) {
+            low = mid;
+            n = count;
+        } else {
+            high = mid - 1;
+        }
+    }
+    return bound | low;
+}
+
+// The k strongest columns of pieces [first, last), which this block's threads
+// have seen with their stride. At least k threads' maxima reach the bound; only the
+// runs of batches whose maximum does are read again. Ties and rows whose large
+// columns all fall to few threads give more candidates than the buffer takes:
+// the k-th best of those found is then a higher bound.
+template <typename T, bool kMask, int kThreads>
+__device__ __noinline__ void block_top(TopShared<kThreads>* sh, const PiecedRow<T>& row, int32_t first, int32_t last, int32_t slot,
+                                       float m, int32_t best, int k, int blocks) {
+    constexpr int kVec = PieceOf<T>::kVec;
+    const int32_t per = slot * kLogprobsBatch;  // pieces of a run
+    // at most this key
+    auto upper = [&](float v, int32_t piece) { return v > minus_inf() ? rank_key(v, max(row.column(piece), 0)) : 0; };
+    const uint64_t lower = m > minus_inf() ? rank_key(m, row.column(best) + kVec - 1) : 0;
+    sh->found[threadIdx.x] = lower;
+    if (threadIdx.x == 0) sh->listed = sh->count = 0;
+    __syncthreads();
+    uint64_t bound = 1;
+    if (blocks > 1) {
+        // Every block has ceil(k / blocks) columns that reach its own bound for so
+        // many, so k of the row's reach the least of these.
+        if (threadIdx.x < 32) {
+            bound = search_bound<kThreads>(sh->found, (k + blocks - 1) / blocks);
+            if (threadIdx.x < blocks) {
+                const uint32_t at = map_shared_rank(smem_u32(&sh->bounds[cluster_ctarank()]), threadIdx.x);
+                asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(bound) : "memory");
+            }
+        }
+        cluster_sync_all();
+        bound = sh->bounds[0];
+        for (int i = 1; i < blocks; ++i) bound = min(bound, sh->bounds[i]);
+    }
+    if (bound <= 1) {
+        if (threadIdx.x < 32) {
+            bound = search_bound<kThreads>(sh->found, k);
+            if (threadIdx.x == 0) sh->bound = bound;
+        }
+        __syncthreads();
+        bound = sh->bound;
+    }
+    for (;;) {
+        if (upper(m, best) >= bound) {
+            for (int i = 0; i < kTopSlots; ++i) {
+                const int32_t p = first + threadIdx.x + i * per * kThreads;
+                if (p >= last) break;
+                if (upper(sh->slots[i * kThreads + threadIdx.x], p) >= bound)
+                    sh->list[atomicAdd(&sh->listed, 1)] = static_cast<uint16_t>(i * kThreads + threadIdx.x);
+            }
+        }
+        __syncthreads();
+        const int32_t total = per * sh->listed;
+        for (int32_t i0 = threadIdx.x; i0 < total; i0 += 4 * kThreads) {
+            uint4 u[4];
+            int32_t at[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int32_t i = i0 + j * kThreads, e = i < total ? sh->list[i / per] : 0;
+                at[j] = i < total ? first + e % kThreads + (e / kThreads * per + i % per) * kThreads : last;
+                if (at[j] < last) u[j] = row.template get<kMask>(at[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (at[j] >= last) continue;
+                if (upper(PieceOf<T>::word_max(PieceOf<T>::max_words(u[j])), at[j]) < bound) continue;
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) {
+                    const float2 v = PieceOf<T>::pair(u[j], e / 2);
+                    const uint64_t key = rank_key(e & 1 ? v.y : v.x, row.column(at[j]) + e);
+                    if (key >= bound) {
+                        const int to = atomicAdd(&sh->count, 1);
+                        if (to < kTopBuffer) sh->found[to] = key;
+                    }
                 }
             }
         }
@@ -345,85 +688,78 @@ __device__ __forceinline__ void block_top(TopShared* sh, const PiecedRow<T>& row
         rank_found<kThreads>(sh, min(count, kTopBuffer), k);
         if (count <= kTopBuffer) break;
         bound = sh->best[k - 1];
+        if (threadIdx.x == 0) sh->listed = sh->count = 0;
         __syncthreads();
     }
 }
 
 // kThreads threads of each of a cluster's blocks share a row.
 template <typename T, bool kMask, bool kTop, int kThreads>
-__global__ void __launch_bounds__(kThreads) logprobs_block_kernel(const LogprobsArgs a, int blocks) {
-    __shared__ float part[32][3];
+__global__ void __launch_bounds__(kThreads, (kMask ? 5 : 4) * 256 / kThreads) logprobs_block_kernel(const LogprobsArgs a, int blocks) {
+    __shared__ float part[kThreads / 32][3];
     __shared__ float gathered[16][3];
-    __shared__ uint64_t all_best[kTop ? 16 * kLogprobsMaxTop : 1];
-    __shared__ TopShared top;  // kTop
+    extern __shared__ uint64_t all_best[];  // kTop, blocks > 1: [blocks, k]
+    __shared__ TopShared<kThreads> top;  // kTop
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t rank = blocks > 1 ? cluster_ctarank() : 0;
     if (blocks > 1) cluster_sync_all();  // every block has started before its shared memory is written
-    for (int64_t r = blockIdx.x / blocks; r < a.rows; r += gridDim.x / blocks) {
-        const T* x = static_cast<const T*>(a.x) + r * a.ld;
-        const uint8_t* mask = kMask ? a.mask + r * a.ld_mask : nullptr;
-        const PiecedRow<T> row(x, mask, a.n);
-        const int32_t share = (row.pieces + blocks - 1) / blocks;
-        const int32_t p0 = min(row.pieces, static_cast<int32_t>(rank) * share), p1 = min(row.pieces, p0 + share);
-        int32_t best = 0;
-        Running mine = scan_row<T, kMask, kTop>(row, p0 + threadIdx.x, p1, kThreads, a.c, &best);
-        Running sum = reduce_warp<32>(mine, a.c);
-        if (lane == 0) {
-            part[warp][0] = sum.m;
-            part[warp][1] = sum.s;
-            part[warp][2] = sum.w;
+    const int64_t r = blockIdx.x / blocks;
+    const T* x = static_cast<const T*>(a.x) + r * a.ld;
+    const uint8_t* mask = kMask ? a.mask + r * a.ld_mask : nullptr;
+    const PiecedRow<T> row(x, mask, a.n, x);
+    const Ahead ahead(a, r, x, mask, rank == 0 ? threadIdx.x : a.T);
+    const int32_t share = (row.pieces + blocks - 1) / blocks;
+    const int32_t p0 = min(row.pieces, static_cast<int32_t>(rank) * share), p1 = min(row.pieces, p0 + share);
+    int32_t best = 0;
+    const int32_t per_thread = (share + kThreads * kLogprobsBatch - 1) / (kThreads * kLogprobsBatch);  // batches
+    const int32_t slot = max(1, (per_thread + kTopSlots - 1) / kTopSlots);
+    const Running mine = scan_row<T, kMask, kTop>(row, p0 + threadIdx.x, p1, kThreads, a.c, &best, kTop ? top.slots + threadIdx.x : nullptr,
+                                                  slot, kThreads);
+    const Running sum = reduce_warp<32>(mine, a.c);
+    if (lane == 0) {
+        part[warp][0] = sum.m;
+        part[warp][1] = sum.s;
+        part[warp][2] = sum.w;
+    }
+    __syncthreads();
+    Running all;
+    if (lane < kThreads / 32) {
+        all.m = part[lane][0];
+        all.s = part[lane][1];
+        all.w = part[lane][2];
+    }
+    all = reduce_warp<32>(all, a.c);
+    if constexpr (kTop) block_top<T, kMask, kThreads>(&top, row, p0, p1, slot, mine.m, best, a.k, blocks);
+    if (blocks > 1) {
+        // every block's sums and strongest columns to the first block's shared memory
+        if (threadIdx.x == 0) {
+            const uint32_t at = map_shared_rank(smem_u32(&gathered[rank][0]), 0);
+            asm volatile("st.shared::cluster.f32 [%0], %1;\n\tst.shared::cluster.f32 [%0+4], %2;\n\tst.shared::cluster.f32 [%0+8], %3;" ::"r"(at),
+                         "f"(all.m), "f"(all.s), "f"(all.w) : "memory");
         }
-        __syncthreads();
-        Running all;
-        if (lane < kThreads / 32) {
-            all.m = part[lane][0];
-            all.s = part[lane][1];
-            all.w = part[lane][2];
+        if constexpr (kTop) {
+            for (int i = threadIdx.x; i < a.k; i += kThreads) {
+                const uint32_t at = map_shared_rank(smem_u32(&all_best[rank * a.k + i]), 0);
+                asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(top.best[i]) : "memory");
+            }
+        }
+        cluster_sync_all();
+        if (rank != 0) return;
+        all = Running();
+        if (lane < blocks) {
+            all.m = gathered[lane][0];
+            all.s = gathered[lane][1];
+            all.w = gathered[lane][2];
         }
         all = reduce_warp<32>(all, a.c);
-        if constexpr (kTop) block_top<T, kMask, kThreads>(&top, row, p0, p1, kThreads, mine.m, best, a.k);
-        if (blocks > 1) {
-            // every block's sums and strongest columns to all blocks' shared memory
-            for (uint32_t to = threadIdx.x; to < static_cast<uint32_t>(blocks); to += kThreads) {
-                const uint32_t at = map_shared_rank(smem_u32(&gathered[rank][0]), to);
-                asm volatile("st.shared::cluster.f32 [%0], %1;\n\tst.shared::cluster.f32 [%0+4], %2;\n\tst.shared::cluster.f32 [%0+8], %3;" ::"r"(at),
-                             "f"(all.m), "f"(all.s), "f"(all.w) : "memory");
-            }
-            if constexpr (kTop) {
-                for (int i = threadIdx.x; i < a.k; i += kThreads) {
-                    const uint32_t at = map_shared_rank(smem_u32(&all_best[rank * a.k + i]), 0);
-                    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(top.best[i]) : "memory");
-                }
-            }
-            cluster_sync_all();
-            Running g;
-            if (lane < blocks) {
-                g.m = gathered[lane][0];
-                g.s = gathered[lane][1];
-                g.w = gathered[lane][2];
-            }
-            all = reduce_warp<32>(g, a.c);
+        if constexpr (kTop) {
+            merge_lists<kThreads>(top.best, all_best, blocks, a.k);
         }
-        const RowStats st(all);
-        if (rank == 0) {
-            write_row(a, r, x, mask, st, threadIdx.x, kThreads);
-            if constexpr (kTop) {
-                if (blocks > 1) {
-                    for (int i = threadIdx.x; i < blocks * a.k; i += kThreads) top.found[i] = all_best[i];
-                    __syncthreads();
-                    // keys of 0 rank last
-                    rank_found<kThreads>(&top, blocks * a.k, a.k);
-                }
-                for (int i = threadIdx.x; i < a.k; i += kThreads) {
-                    const uint64_t key = top.best[i];
-                    a.top_idx[r * a.k + i] = key ? key_column(key) : -1;
-                    a.top_logprob[r * a.k + i] = key ? column_logprob(x, mask, key_column(key), st, a.scale) : minus_inf();
-                }
-            }
-        }
-        if (blocks > 1) cluster_sync_all();
-        else __syncthreads();
     }
+    const RowStats st(all);
+    write_row(a, r, x, mask, st, ahead, threadIdx.x, kThreads);
+    if constexpr (kTop)
+        for (int i = threadIdx.x; i < a.k; i += kThreads) write_top(a, r, i, top.best[i], st);
 }
 
 // ---------------------------------------------------------------- gradient
@@ -448,7 +784,7 @@ struct LogprobsBwdArgs {
 // The i-th of a row's T + k columns with a gradient of their own: its column
 // (-1: none) and gradient.
 template <typename T>
-__device__ __forceinline__ int64_t given_column(const LogprobsBwdArgs& a, int64_t r, int i, const T* x, const uint8_t* mask, float m, float* g) {
+__device__ __forceinline__ int32_t given_column(const LogprobsBwdArgs& a, int64_t r, int i, const T* x, const uint8_t* mask, float m, float* g) {
     int64_t j;
     if (i < a.T) {
         j = a.g_logprob ? a.targets[r * a.T + i] : -1;
@@ -464,105 +800,170 @@ __device__ __forceinline__ int64_t given_column(const LogprobsBwdArgs& a, int64_
     // a column of probability zero passes no gradient
     if (j >= 0 && ((mask && !mask[j]) || (to_f32(x[j]) - m) * a.scale == minus_inf())) j = -1;
     if (j < 0) *g = 0.f;
-    return j;
+    return static_cast<int32_t>(j);
 }
 
-// dx_j = scale * (sum of what was given to j) + p_j * (A + B * u_j),
-// u_j = t_j - L (log2 p_j), A = -scale * (G + g_entropy * entropy),
+// dx_j = scale * (sum of what was given to j) + p_j * (A + B * log2 p_j),
+// log2 p_j = t_j - L, A = -scale * (G + g_entropy * entropy),
 // B = -scale * g_entropy * ln 2, G = the sum of all that was given.
-struct GradRow {
-    float m, l, A, B;
-    __device__ __forceinline__ float log2_p(float x, float c) const { return max_nan((x - m) * c - l, kNoExponent); }
-    __device__ __forceinline__ float dx(float x, float c) const {
-        const float u = log2_p(x, c);
-        return exp2_fast(u) * __fmaf_rn(u, B, A);
-    }
+
+// Pieces of a lane in flight, and blocks of 256 threads an SM holds at least.
+// Registers decide (4096 x 131072 bf16 by pieces and blocks: 4, 3: 370 us; 3, 4:
+// 324; 2, 5: 325; 8192 x 32768 with a mask for each row: 513; 327; 286).
+template <bool kMask>
+struct BwdCfg {
+    static constexpr int kPieces = kMask ? 2 : 3, kBlocks = kMask ? 5 : 4;
 };
 
-// kGroup threads take kPieces pieces each of one row's run; one group per
-// (row, run). No sums but those of the T + k given columns, which every run's
-// group adds up again. Bound by HBM.
-template <typename T, bool kMask, int kGroup, int kPieces>
-__global__ void __launch_bounds__(256) logprobs_bwd_kernel(const LogprobsBwdArgs a, int64_t runs, int64_t items) {
-    constexpr int kVec = Piece<T>::kVec;
-    const int t = threadIdx.x % kGroup;
-    __shared__ float sum_of[8];
-    for (int64_t item = static_cast<int64_t>(blockIdx.x) * (256 / kGroup) + threadIdx.x / kGroup; item < items;
-         item += static_cast<int64_t>(gridDim.x) * (256 / kGroup)) {
-        const int64_t r = item / runs, run = item - r * runs;
-        const T* x = static_cast<const T*>(a.x) + r * a.ld;
-        T* dx = static_cast<T*>(a.dx) + r * a.ld_dx;
-        const uint8_t* mask = kMask ? a.mask + r * a.ld_mask : nullptr;
-        const PiecedRow<T> row(x, mask, a.n);
-        const int32_t p0 = static_cast<int32_t>(run * kGroup * kPieces);
-        uint4 u[kPieces];
-        uint32_t bits[kPieces];
+// Calls f(column, gradient) in every lane for the given columns from c0 to c1,
+// in their order. Lane i holds the i-th of the first 32 (j, g); later ones are
+// read again.
+template <typename T, typename F>
+__device__ __forceinline__ void each_given(const LogprobsBwdArgs& a, int64_t r, const T* x, const uint8_t* mask, float m, int given, int32_t j,
+                                           float g, int32_t c0, int32_t c1, F&& f) {
+    for (int b = 0; b < given; b += 32) {
+        if (b > 0) j = b + static_cast<int>(threadIdx.x & 31) < given ? given_column(a, r, b + (threadIdx.x & 31), x, mask, m, &g) : -1;
+        for (uint32_t left = __ballot_sync(0xffffffffu, j >= c0 && j < c1); left; left &= left - 1) {
+            const int from = __ffs(left) - 1;
+            f(__shfl_sync(0xffffffffu, j, from), __shfl_sync(0xffffffffu, g, from));
+        }
+    }
+}
+
+// A warp per (row, run of `run` pieces): no warp waits for another. The given
+// columns' own gradients are added to the elements before they are rounded.
+// Pieces are those of dx, so that stores are whole; kShift: x's rows have
+// another phase, and its pieces are joined from the two aligned ones that hold
+// them. Bound by HBM.
+template <typename T, bool kMask, bool kShift>
+__global__ void __launch_bounds__(256, BwdCfg<kMask>::kBlocks) logprobs_bwd_kernel(const LogprobsBwdArgs a, int32_t run, int64_t runs, int64_t items) {
+    using P = PieceOf<T>;
+    constexpr int kVec = P::kVec, kBwdPieces = BwdCfg<kMask>::kPieces;
+    const int lane = threadIdx.x & 31;
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (item >= items) return;
+    const int64_t r = item / runs;
+    const T* x = static_cast<const T*>(a.x) + r * a.ld;
+    T* dx = static_cast<T*>(a.dx) + r * a.ld_dx;
+    const uint8_t* mask = kMask ? a.mask + r * a.ld_mask : nullptr;
+    const PiecedRow<T> row(x, mask, a.n, dx);
+    const int32_t first = static_cast<int32_t>(item - r * runs) * run, last = min(row.pieces, first + run);
+    const float2 m = *reinterpret_cast<const float2*>(a.stats + 2 * r);
+    const int given = a.T + (a.g_top ? a.k : 0);
+    // the first 32 given columns, one a lane; all of their gradients' sum
+    float g = 0.f, sum = 0.f;
+    int32_t j = -1;
+    if (lane < given) j = given_column(a, r, lane, x, mask, m.x, &g);
+    sum = g;
+    for (int i = lane + 32; i < given; i += 32) {
+        float more;
+        given_column(a, r, i, x, mask, m.x, &more);
+        sum += more;
+    }
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            const int32_t p = p0 + i * kGroup + t;
-            if (p < row.pieces) {
-                u[i] = row.load(p);
-                if constexpr (kMask) bits[i] = row.active(p);
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float gh = a.g_entropy ? a.g_entropy[r] : 0.f;
+    const float A = -a.scale * __fmaf_rn(gh, gh != 0.f ? a.entropy[r] : 0.f, sum), B = -a.scale * gh * kLn2;
+    const float2 ref = make_float2(-m.x, -m.x), c2 = make_float2(a.c, a.c), l2 = make_float2(-m.y, -m.y);
+    const float2 A2 = make_float2(A, A), B2 = make_float2(B, B);
+    const bool broken = !(m.x == m.x && m.y == m.y);  // a row of NaN: its inactive columns are 0 all the same
+    // whole pieces
+    const int32_t w0 = max(first, row.skip ? 1 : 0), w1 = min(last, (row.n + row.skip) / kVec);
+    const uint4 none = make_uint4(P::kMinusInf, P::kMinusInf, P::kMinusInf, P::kMinusInf);
+    uint4 next[kBwdPieces];
+    auto fetch = [&](int32_t p0) {
+#pragma unroll
+        for (int i = 0; i < kBwdPieces; ++i) {
+            const int32_t p = p0 + i * 32 + lane;
+            next[i] = p < w1 ? kShift ? row.template load<true>(p) : row.load_whole(p) : none;
+        }
+        if constexpr (kMask) {
+#pragma unroll
+            for (int i = 0; i < kBwdPieces; ++i) {
+                const int32_t p = p0 + i * 32 + lane;
+                if (p < w1) next[i] = row.template keep_active<true>(next[i], p);
             }
         }
-        const int given = a.T + (a.g_top ? a.k : 0);
-        const float m = a.stats[2 * r];
-        float sum = 0.f, g;
-        for (int i = t; i < given; i += kGroup) {
-            given_column(a, r, i, x, mask, m, &g);
-            sum += g;
-        }
+    };
+    fetch(w0);
+    for (int32_t p0 = w0; p0 < w1; p0 += 32 * kBwdPieces) {
+        uint4 u[kBwdPieces];
 #pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if constexpr (kGroup == 256) {
-            if ((t & 31) == 0) sum_of[t >> 5] = sum;
-            __syncthreads();
-            sum = 0.f;
+        for (int i = 0; i < kBwdPieces; ++i) u[i] = next[i];
+        fetch(p0 + 32 * kBwdPieces);
+        // exponents of minus infinity, as in add_piece
+        uint32_t least = P::min_words(u[0]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum += sum_of[i];
-        }
-        const float gh = a.g_entropy ? a.g_entropy[r] : 0.f;
-        const GradRow gr{m, a.stats[2 * r + 1], -a.scale * __fmaf_rn(gh, gh != 0.f ? a.entropy[r] : 0.f, sum), -a.scale * gh * kLn2};
+        for (int i = 1; i < kBwdPieces; ++i) least = P::min_words(least, P::min_words(u[i]));
+        const bool low = !((P::word_min(least) + ref.x) * a.c > -1e30f) || !(m.y < 1e30f);
+        const int32_t c0 = row.column(p0), c1 = c0 + 32 * kBwdPieces * kVec;
+        const uint32_t here = __ballot_sync(0xffffffffu, j >= c0 && j < c1);
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            const int32_t p = p0 + i * kGroup + t;
-            if (p >= row.pieces) continue;
-            Piece<T> e;
-            e.set(u[i]);
-            alignas(16) T o[kVec];
+        for (int i = 0; i < kBwdPieces; ++i) {
+            if (p0 + i * 32 >= w1) break;
+            const int32_t p = p0 + i * 32 + lane, at = row.column(p);
+            float2 d[kVec / 2];
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                const float d = gr.dx(e.v[j], a.c);
-                o[j] = from_f32<T>(kMask && !(bits[i] >> j & 1) ? 0.f : d);
+            for (int e = 0; e < kVec / 2; ++e) {
+                // log2 p, p, p * (A + B log2 p)
+                float2 t = fma2(add2(P::pair(u[i], e), ref), c2, l2);
+                if (low) {
+                    t.x = max_nan(t.x, kNoExponent);
+                    t.y = max_nan(t.y, kNoExponent);
+                }
+                d[e] = mul2(make_float2(exp2_fast(t.x), exp2_fast(t.y)), fma2(t, B2, A2));
             }
-            const int64_t at = row.column(p);
-            if (row.whole(p) && (reinterpret_cast<uintptr_t>(dx + at) & 15) == 0) {
-                *reinterpret_cast<uint4*>(dx + at) = *reinterpret_cast<const uint4*>(o);
-            } else {
+            if (kMask && broken && p < w1) {
+                uint32_t act[kVec / 4];
+                row.active(p, act);
 #pragma unroll
-                for (int j = 0; j < kVec; ++j)
-                    if (at + j >= 0 && at + j < a.n) dx[at + j] = o[j];
+                for (int e = 0; e < kVec / 2; ++e) {
+                    const uint32_t b = act[2 * e / 4] >> (2 * e % 4 * 8);
+                    if (!(b & 0x80u)) d[e].x = 0.f;
+                    if (!(b & 0x8000u)) d[e].y = 0.f;
+                }
             }
-        }
-        // the given columns of this run, each by the thread of its first mention
-        if constexpr (kGroup == 256) __syncthreads();
-        else __syncwarp();
-        const int64_t c0 = row.column(p0), c1 = row.column(p0 + kGroup * kPieces);
-        for (int i = t; i < given; i += kGroup) {
-            const int64_t j = given_column(a, r, i, x, mask, m, &g);
-            if (j < 0 || j < c0 || j >= c1) continue;
-            bool first = true;
-            float own = g;
-            for (int e = 0; e < given; ++e) {
-                if (e == i) continue;
-                float ge;
-                if (given_column(a, r, e, x, mask, m, &ge) != j) continue;
-                if (e < i) { first = false; break; }
-                own += ge;
+            if (here || given > 32) {
+                each_given(a, r, x, mask, m.x, given, j, g, c0, c1, [&](int32_t column, float v) {
+#pragma unroll
+                    for (int e = 0; e < kVec / 2; ++e) {
+                        if (column - at == 2 * e) d[e].x = __fmaf_rn(a.scale, v, d[e].x);
+                        if (column - at == 2 * e + 1) d[e].y = __fmaf_rn(a.scale, v, d[e].y);
+                    }
+                });
             }
-            if (first) dx[j] = from_f32<T>(__fmaf_rn(a.scale, own, gr.dx(to_f32(x[j]), a.c)));
+            if (p >= w1) continue;
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < kVec / 2; ++e) {
+                if constexpr (sizeof(T) == 4) {
+                    w[2 * e] = __float_as_uint(d[e].x);
+                    w[2 * e + 1] = __float_as_uint(d[e].y);
+                } else {
+                    w[e] = pack2<T>(d[e].x, d[e].y);
+                }
+            }
+            *reinterpret_cast<uint4*>(dx + at) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        if constexpr (kGroup == 256) __syncthreads();
+    }
+    // the row's ends: an element a lane, those in front of the first whole piece and those behind the last one
+    const bool head = first == 0 && row.skip, tail = last == row.pieces && (row.n + row.skip) % kVec != 0;
+    if (head || tail) {
+        const int32_t w_first = row.column(row.skip ? 1 : 0), w_end = row.column((row.n + row.skip) / kVec);
+        int32_t column = -1;
+        if (head && lane < kVec && lane < min(w_first, row.n)) column = lane;
+        if (tail && lane >= kVec && lane < 2 * kVec && max(w_end, 0) + lane - kVec < row.n && (w_end >= w_first || !head))
+            column = max(w_end, 0) + lane - kVec;
+        float d = 0.f;
+        const bool on = column >= 0 && !(kMask && !mask[column]);
+        if (on) {
+            const float t = max_nan(__fmaf_rn(to_f32(x[column]) - m.x, a.c, -m.y), kNoExponent);
+            d = exp2_fast(t) * __fmaf_rn(t, B, A);
+        }
+        each_given(a, r, x, mask, m.x, given, j, g, 0, row.n, [&](int32_t c, float v) {
+            if (c == column) d = __fmaf_rn(a.scale, v, d);
+        });
+        if (column >= 0) dx[column] = from_f32<T>(d);
     }
 }
 
