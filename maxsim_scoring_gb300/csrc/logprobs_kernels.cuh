@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(256) logprobs_warp_kernel(const LogprobsArgs a
 constexpr int kTopBuffer = 512;
 
 template <int kThreads>
-struct TopShared {
+struct alignas(16) TopShared {
     uint64_t found[kTopBuffer];
     uint64_t best[kLogprobsMaxTop];
     float slots[kTopSlots * kThreads];  // maxima of the threads' runs of batches
@@ -520,28 +520,47 @@ __device__ __forceinline__ void rank_found(TopShared<kThreads>* sh, int count, i
     __syncthreads();
     for (int i = threadIdx.x; i < count; i += kThreads) {
         const uint64_t mine = sh->found[i];
-        int rank = 0;
-#pragma unroll 4
-        for (int j = 0; j < count; ++j) rank += sh->found[j] > mine;
+        int rank = 0, j = 0;
+#pragma unroll 1
+        for (; j + 8 <= count; j += 8) {
+            ulonglong2 f[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = *reinterpret_cast<const ulonglong2*>(sh->found + j + 2 * e);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) rank += (f[e].x > mine) + (f[e].y > mine);
+        }
+#pragma unroll 1
+        for (; j < count; ++j) rank += sh->found[j] > mine;
         if (rank < k) sh->best[rank] = mine;
     }
     __syncthreads();
 }
 
-// The k largest of `lists` descending lists of k keys (0: none) into best: a
-// key's rank is its place in its own list and the number of larger keys in each
-// other one, found by halves.
+// The k largest of `lists` descending lists of k keys (0: none) into best. They
+// are gathered first: with the lists' common bound hardly more than k are left.
+// Where they are too many, a key's rank is its place in its own list and the
+// number of larger keys in each other one.
 template <int kThreads>
-__device__ __forceinline__ void merge_lists(uint64_t* best, const uint64_t* all, int lists, int k) {
-    for (int i = threadIdx.x; i < k; i += kThreads) best[i] = 0;
+__device__ __forceinline__ void merge_lists(TopShared<kThreads>* sh, const uint64_t* all, int lists, int k) {
+    if (threadIdx.x == 0) sh->count = 0;
     __syncthreads();
+    for (int i = threadIdx.x; i < lists * k; i += kThreads) {
+        if (all[i] == 0) continue;
+        const int at = atomicAdd(&sh->count, 1);
+        if (at < kTopBuffer) sh->found[at] = all[i];
+    }
+    __syncthreads();
+    const int count = sh->count;
+    if (count <= kTopBuffer) {
+        rank_found<kThreads>(sh, count, k);
+        return;
+    }
     for (int i = threadIdx.x; i < lists * k; i += kThreads) {
         const uint64_t mine = all[i];
         if (mine == 0) continue;
-        const int own = i / k;
-        int rank = i - own * k;
+        int rank = i % k;
         for (int l = 0; l < lists && rank < k; ++l) {
-            if (l == own) continue;
+            if (l == i / k) continue;
             int lo = 0, hi = k;  // the first place whose key is not larger
             while (lo < hi) {
                 const int mid = (lo + hi) >> 1;
@@ -550,7 +569,7 @@ __device__ __forceinline__ void merge_lists(uint64_t* best, const uint64_t* all,
             }
             rank += lo;
         }
-        if (rank < k) best[rank] = mine;
+        if (rank < k) sh->best[rank] = mine;
     }
     __syncthreads();
 }
@@ -649,38 +668,34 @@ __device__ __noinline__ void block_top(TopShared<kThreads>* sh, const PiecedRow<
         bound = sh->bound;
     }
     for (;;) {
-        if (upper(m, best) >= bound) {
+        const float value = bound > 1 ? key_value(bound) : minus_inf();  // what is below is below the bound
+        if (m >= value && upper(m, best) >= bound) {
+#pragma unroll 1
             for (int i = 0; i < kTopSlots; ++i) {
                 const int32_t p = first + threadIdx.x + i * per * kThreads;
                 if (p >= last) break;
-                if (upper(sh->slots[i * kThreads + threadIdx.x], p) >= bound)
-                    sh->list[atomicAdd(&sh->listed, 1)] = static_cast<uint16_t>(i * kThreads + threadIdx.x);
+                const float v = sh->slots[i * kThreads + threadIdx.x];
+                if (v >= value && upper(v, p) >= bound) sh->list[atomicAdd(&sh->listed, 1)] = static_cast<uint16_t>(i * kThreads + threadIdx.x);
             }
         }
         __syncthreads();
         const int32_t total = per * sh->listed;
-        for (int32_t i0 = threadIdx.x; i0 < total; i0 += 4 * kThreads) {
-            uint4 u[4];
-            int32_t at[4];
+#pragma unroll 2
+        for (int32_t i = threadIdx.x; i < total; i += kThreads) {
+            const int32_t e = sh->list[i / per], p = first + e % kThreads + (e / kThreads * per + i % per) * kThreads;
+            if (p >= last) continue;
+            const uint4 u = row.template get<kMask>(p);
+            uint32_t reach = 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int32_t i = i0 + j * kThreads, e = i < total ? sh->list[i / per] : 0;
-                at[j] = i < total ? first + e % kThreads + (e / kThreads * per + i % per) * kThreads : last;
-                if (at[j] < last) u[j] = row.template get<kMask>(at[j]);
+            for (int j = 0; j < kVec / 2; ++j) {
+                const float2 v = PieceOf<T>::pair(u, j);
+                reach |= (v.x >= value ? 1u : 0u) << (2 * j) | (v.y >= value ? 2u : 0u) << (2 * j);
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (at[j] >= last) continue;
-                if (upper(PieceOf<T>::word_max(PieceOf<T>::max_words(u[j])), at[j]) < bound) continue;
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    const float2 v = PieceOf<T>::pair(u[j], e / 2);
-                    const uint64_t key = rank_key(e & 1 ? v.y : v.x, row.column(at[j]) + e);
-                    if (key >= bound) {
-                        const int to = atomicAdd(&sh->count, 1);
-                        if (to < kTopBuffer) sh->found[to] = key;
-                    }
-                }
+            for (; reach; reach &= reach - 1) {
+                const uint64_t key = row.template key<kMask>(row.column(p) + __ffs(reach) - 1);
+                if (key < bound) continue;
+                const int to = atomicAdd(&sh->count, 1);
+                if (to < kTopBuffer) sh->found[to] = key;
             }
         }
         __syncthreads();
@@ -753,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, (kMask ? 5 : 4) * 256 / kThreads) lo
         }
         all = reduce_warp<32>(all, a.c);
         if constexpr (kTop) {
-            merge_lists<kThreads>(top.best, all_best, blocks, a.k);
+            merge_lists<kThreads>(&top, all_best, blocks, a.k);
         }
     }
     const RowStats st(all);
