@@ -31,8 +31,13 @@ struct LinearFp4Args {
 
 constexpr int kFp4TileM = 256;      // rows of A per tile: 128 on each CTA of a pair
 constexpr int kFp4TileK = 256;      // values of K per stage: 128 bytes of a row
-constexpr int kFp4Threads = 384;    // warp 0 TMA, warp 1 MMA (odd CTA: reports what landed), warps 4-11 epilogue
+constexpr int kFp4Threads = 384;    // warp 0 TMA, warp 1 MMA (odd CTA: reports what landed), warp 2 scales, warps 4-11 epilogue
 constexpr int kFp4EpiWarp0 = 4;
+// Registers a thread: the launch gives kFp4Regs, of which the first warpgroup
+// hands some to the epilogue's two, which hold a tile's sums between the
+// accumulator's hand-over and the stores.
+constexpr int kFp4Regs = 168, kFp4RegsCtl = 80, kFp4RegsEpi = 208;
+static_assert(kFp4RegsCtl + 2 * kFp4RegsEpi <= 3 * kFp4Regs, "register split");
 constexpr int kFp4MaxSplits = 4;
 
 template <int kTN>
@@ -65,9 +70,9 @@ struct LinearFp4TileArgs {
 };
 
 struct alignas(16) Fp4Ctl {
-    uint64_t full[8], empty[8];
+    uint64_t full[8], empty[8], scales[8];
     uint64_t acc_full[2], acc_empty[2];
-    uint64_t mma_done;
+    uint64_t mma_done, copies_done;
     uint32_t tmem_base;
     volatile int32_t abort;
 };
@@ -86,6 +91,21 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+// Both, to the same place of every CTA of the cluster in `mask`, whose barriers of
+// the same place each count the bytes.
+__device__ __forceinline__ void tma_load_2d_to(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y, uint16_t mask) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "h"(mask)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_to(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y, int32_t z, uint16_t mask) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "h"(mask)
+        : "memory");
+}
+
 // Shared-memory descriptor of a tile of scale words: 32 rows of 16 bytes, no
 // swizzle, eight rows (128 bytes) a core matrix.
 __device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
@@ -96,16 +116,6 @@ __device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
     return d;
 }
 
-// Copies a tile of scale words (512 bytes) to four columns of tensor memory, in
-// all four lane quarters, on both CTAs of the pair from their own shared memory;
-// from the elected lane.
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t sdesc) {
-    asm volatile(
-        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr), "l"(sdesc)
-        : "memory");
-}
-
 // Instruction descriptor of kind::mxf4nvf4: [4,6) B's scale word byte, [7,10)
 // and [10,12) A's and B's type (1 = E2M1), [17,23) N >> 3, [23] scales E8M0
 // instead of E4M3, [24,29) M >> 4, [29,31) A's scale word byte. Both operands K-major.
@@ -113,42 +123,82 @@ __host__ __device__ constexpr uint32_t idesc_fp4(uint32_t M, uint32_t N, bool e8
     return (byte << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | (e8m0 ? 1u << 23 : 0u) | ((M >> 4) << 24) | (byte << 29);
 }
 
-// The four K = 64 steps of a stage, from the elected lane: 32 bytes of A's and
-// B's rows a step (K-major, 128-byte swizzle). With blocks of 16 a step takes a
-// scale word of each row, with blocks of 32 half a word.
-template <uint32_t kSfbStep>
-__device__ __forceinline__ void mma_stage16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred e, p0, pt;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t.reg .b32 s1, s2, s3, t1, t2, t3;\n\t"
-        "setp.ne.b32 p0, %6, 0;\n\tsetp.eq.b32 pt, %6, %6;\n\t"
-        "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
-        "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
-        "add.u32 s1, %4, 4;\n\tadd.u32 s2, %4, 8;\n\tadd.u32 s3, %4, 12;\n\t"
-        "add.u32 t1, %5, %7;\n\tadd.u32 t2, %5, %8;\n\tadd.u32 t3, %5, %9;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p0;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], a1, b1, %3, [s1], [t1], pt;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], a2, b2, %3, [s2], [t2], pt;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], a3, b3, %3, [s3], [t3], pt;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "n"(kSfbStep), "n"(2 * kSfbStep), "n"(3 * kSfbStep)
-        : "memory");
+// The copies and the MMAs of a stage, from the elected lane, in one asm block
+// each (issued one by one they take 55 to 110 cycles each, several times what
+// they take to run). B's scales are one tile (512 bytes) a word, or two.
+#define MAXSIM_FP4_CP(TM, TOFF, SD, SOFF)                                         \
+    "add.u32 t, " TM ", " TOFF ";\n\tadd.s64 s, " SD ", " SOFF ";\n\t"            \
+    "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [t], s;\n\t"
+#define MAXSIM_FP4_COPY(TEXT)                                                     \
+    asm volatile("{\n\t.reg .pred e;\n\t.reg .b32 t;\n\t.reg .b64 s;\n\telect.sync _|e, 0xffffffff;\n\t" TEXT "}" ::"r"(sfa), "r"(sfb), \
+                 "l"(fa), "l"(fb) : "memory")
+
+// Scale tiles to tensor memory: four columns a tile, in all four lane quarters, on
+// both CTAs from their own shared memory. Word j of A's goes to sfa + 4 j, of B's
+// to sfb + 4 j, or 8 j and 8 j + 4; kByWord: B's tiles lie word by word in shared memory.
+template <int kWords, int kBTiles, bool kByWord>
+__device__ __forceinline__ void copy_scales(uint32_t sfa, uint32_t sfb, uint64_t fa, uint64_t fb) {
+    if constexpr (kBTiles == 1) {
+        MAXSIM_FP4_COPY(MAXSIM_FP4_CP("%0", "0", "%2", "0") MAXSIM_FP4_CP("%1", "0", "%3", "0")
+                        MAXSIM_FP4_CP("%0", "4", "%2", "32") MAXSIM_FP4_CP("%1", "4", "%3", "32"));
+        if constexpr (kWords == 4)
+            MAXSIM_FP4_COPY(MAXSIM_FP4_CP("%0", "8", "%2", "64") MAXSIM_FP4_CP("%1", "8", "%3", "64")
+                            MAXSIM_FP4_CP("%0", "12", "%2", "96") MAXSIM_FP4_CP("%1", "12", "%3", "96"));
+    } else if constexpr (kByWord) {
+        MAXSIM_FP4_COPY(MAXSIM_FP4_CP("%0", "0", "%2", "0") MAXSIM_FP4_CP("%1", "0", "%3", "0") MAXSIM_FP4_CP("%1", "4", "%3", "32")
+                        MAXSIM_FP4_CP("%0", "4", "%2", "32") MAXSIM_FP4_CP("%1", "8", "%3", "64") MAXSIM_FP4_CP("%1", "12", "%3", "96"));
+        if constexpr (kWords == 4)
+            MAXSIM_FP4_COPY(MAXSIM_FP4_CP("%0", "8", "%2", "64") MAXSIM_FP4_CP("%1", "16", "%3", "128") MAXSIM_FP4_CP("%1", "20", "%3", "160")
+                            MAXSIM_FP4_CP("%0", "12", "%2", "96") MAXSIM_FP4_CP("%1", "24", "%3", "192") MAXSIM_FP4_CP("%1", "28", "%3", "224"));
+    } else if constexpr (kWords == 4) {
+        MAXSIM_FP4_COPY(MAXSIM_FP4_CP("%0", "0", "%2", "0") MAXSIM_FP4_CP("%1", "0", "%3", "0") MAXSIM_FP4_CP("%1", "4", "%3", "128")
+                        MAXSIM_FP4_CP("%0", "4", "%2", "32") MAXSIM_FP4_CP("%1", "8", "%3", "32") MAXSIM_FP4_CP("%1", "12", "%3", "160")
+                        MAXSIM_FP4_CP("%0", "8", "%2", "64") MAXSIM_FP4_CP("%1", "16", "%3", "64") MAXSIM_FP4_CP("%1", "20", "%3", "192")
+                        MAXSIM_FP4_CP("%0", "12", "%2", "96") MAXSIM_FP4_CP("%1", "24", "%3", "96") MAXSIM_FP4_CP("%1", "28", "%3", "224"));
+    } else {
+        MAXSIM_FP4_COPY(MAXSIM_FP4_CP("%0", "0", "%2", "0") MAXSIM_FP4_CP("%1", "0", "%3", "0") MAXSIM_FP4_CP("%1", "4", "%3", "64")
+                        MAXSIM_FP4_CP("%0", "4", "%2", "32") MAXSIM_FP4_CP("%1", "8", "%3", "32") MAXSIM_FP4_CP("%1", "12", "%3", "96"));
+    }
 }
-template <uint32_t kSfbStep>
-__device__ __forceinline__ void mma_stage32(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t idesc_hi, uint32_t sfa, uint32_t sfb,
-                                            uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred e, p0, pt;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t.reg .b32 s1, t1;\n\t"
-        "setp.ne.b32 p0, %7, 0;\n\tsetp.eq.b32 pt, %7, %7;\n\t"
-        "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
-        "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
-        "add.u32 s1, %5, 4;\n\tadd.u32 t1, %6, %8;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p0;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], a1, b1, %4, [%5], [%6], pt;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], a2, b2, %3, [s1], [t1], pt;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], a3, b3, %4, [s1], [t1], pt;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(idesc_hi), "r"(sfa), "r"(sfb), "r"(accumulate), "n"(kSfbStep)
-        : "memory");
+#undef MAXSIM_FP4_CP
+#undef MAXSIM_FP4_COPY
+
+// Four K = 64 steps, 32 bytes of A's and B's rows a step (K-major, 128-byte
+// swizzle), the first accumulating only if `accumulate` is nonzero. With blocks
+// of 16 a step takes a scale word of each row, with blocks of 32 half a word
+// (idesc_hi: the upper half).
+#define MAXSIM_FP4_MMA(VEC, STEP, IDESC, AOFF, BOFF, PRED)                        \
+    "add.s64 x, %1, " STEP ";\n\tadd.s64 y, %2, " STEP ";\n\tadd.u32 s, %4, " AOFF ";\n\tadd.u32 t, %5, " BOFF ";\n\t" \
+    "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::" VEC " [%0], x, y, " IDESC ", [s], [t], " PRED ";\n\t"
+#define MAXSIM_FP4_STAGE(TEXT)                                                    \
+    asm volatile("{\n\t.reg .pred e, p0, pt;\n\t.reg .b32 s, t;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p0, %6, 0;\n\tsetp.eq.b32 pt, %6, %6;\n\t" \
+                 "elect.sync _|e, 0xffffffff;\n\t" TEXT "}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(idesc_hi) \
+                 : "memory")
+template <int kWords, int kBTiles>
+__device__ __forceinline__ void mma_stage(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t idesc_hi, uint32_t sfa, uint32_t sfb,
+                                          uint32_t accumulate) {
+    if constexpr (kWords == 4 && kBTiles == 1)
+        MAXSIM_FP4_STAGE(MAXSIM_FP4_MMA("4X", "0", "%3", "0", "0", "p0") MAXSIM_FP4_MMA("4X", "2", "%3", "4", "4", "pt")
+                         MAXSIM_FP4_MMA("4X", "4", "%3", "8", "8", "pt") MAXSIM_FP4_MMA("4X", "6", "%3", "12", "12", "pt"));
+    else if constexpr (kWords == 4)
+        MAXSIM_FP4_STAGE(MAXSIM_FP4_MMA("4X", "0", "%3", "0", "0", "p0") MAXSIM_FP4_MMA("4X", "2", "%3", "4", "8", "pt")
+                         MAXSIM_FP4_MMA("4X", "4", "%3", "8", "16", "pt") MAXSIM_FP4_MMA("4X", "6", "%3", "12", "24", "pt"));
+    else if constexpr (kBTiles == 1)
+        MAXSIM_FP4_STAGE(MAXSIM_FP4_MMA("2X", "0", "%3", "0", "0", "p0") MAXSIM_FP4_MMA("2X", "2", "%7", "0", "0", "pt")
+                         MAXSIM_FP4_MMA("2X", "4", "%3", "4", "4", "pt") MAXSIM_FP4_MMA("2X", "6", "%7", "4", "4", "pt"));
+    else
+        MAXSIM_FP4_STAGE(MAXSIM_FP4_MMA("2X", "0", "%3", "0", "0", "p0") MAXSIM_FP4_MMA("2X", "2", "%7", "0", "0", "pt")
+                         MAXSIM_FP4_MMA("2X", "4", "%3", "4", "8", "pt") MAXSIM_FP4_MMA("2X", "6", "%7", "4", "8", "pt"));
+}
+#undef MAXSIM_FP4_MMA
+#undef MAXSIM_FP4_STAGE
+
+// v, loaded from tensor memory, is not used before the wait in front of this.
+__device__ __forceinline__ void not_before(float (&v)[32]) {
+    asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]),
+                 "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]),
+                 "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]));
+    asm volatile("" : "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));
 }
 
 // Every thread of every CTA of the cluster, whatever its warp's other threads do.
@@ -161,15 +211,17 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 //    (128-byte swizzle) with the scale tiles of its rows of A and of all the
 //    tile's rows of B, which both CTAs' MMA halves need. What lies outside the
 //    operands reads as code 0 with scale 0;
-//  * warp 1 of the even CTA copies a stage's scales to tensor memory and issues
-//    its MMAs (M = 256, N = kTN, K = 64), which the hardware keeps in this order;
-//    warp 1 of the odd CTA reports to it what landed there;
+//  * warp 2 of the even CTA copies a stage's scales to tensor memory, warp 1
+//    issues its MMAs (M = 256, N = kTN, K = 64); one warp for both took 202 us for
+//    32768 x 4096 x 4096. Warp 1 of the odd CTA reports to them what landed there;
 //  * eight epilogue warps scale, add the bias, round once and store, as those of
 //    linear_tile_kernel do.
 // kRows16: rows of out start on 16-byte boundaries, and 16-bit ones end there.
+// kPairs = 2: two pairs of a cluster take neighbouring tiles of A against the same
+// rows of B, which each CTA loads a quarter of for those that need it.
 // splits > 1 (few tiles): the pairs of a cluster share a tile's K; the others'
 // sums pass to the first pair's shared memory and are added in their order.
-template <typename T, int kTN, bool kSwap, bool kRows16>
+template <typename T, int kTN, bool kSwap, bool kRows16, int kPairs>
 __global__ void __launch_bounds__(kFp4Threads, 1)
 linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_sfa,
                   const __grid_constant__ CUtensorMap tm_sfb, const __grid_constant__ CUtensorMap tm_out, const LinearFp4TileArgs a) {
@@ -184,18 +236,20 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
     Fp4Ctl* ctl = reinterpret_cast<Fp4Ctl*>(s_out + 8 * 4096);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t crank = cluster_ctarank(), rank = crank & 1u, even = crank & ~1u;
-    const int32_t split = static_cast<int32_t>(crank >> 1);
+    const int32_t split = kPairs == 1 ? static_cast<int32_t>(crank >> 1) : 0, pair = kPairs == 1 ? 0 : static_cast<int32_t>(crank >> 1);
     const int32_t words = a.block == 16 ? 4 : 2;  // scale words of a stage
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(smem_u32(&ctl->full[s]), rank == 0 ? 2 : 1);  // its own TMA; even CTA: and the odd CTA's report
-            mbar_init(smem_u32(&ctl->empty[s]), 1);
+            mbar_init(smem_u32(&ctl->scales[s]), 1);
+            mbar_init(smem_u32(&ctl->empty[s]), kPairs);  // a commit of every pair that the stage's loads go to
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&ctl->acc_full[b]), 1);
             mbar_init(smem_u32(&ctl->acc_empty[b]), 16);  // eight warps of each CTA
         }
         mbar_init(smem_u32(&ctl->mma_done), 1);
+        mbar_init(smem_u32(&ctl->copies_done), 1);
         ctl->abort = 0;
         fence_barrier_init();
         tma_prefetch_desc(&tm_a);
@@ -212,10 +266,13 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
     cluster_sync_all();  // barriers of all CTAs exist before any remote arrival
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;
-    const uint32_t ctas = 2u * static_cast<uint32_t>(a.splits);
+    const uint32_t ctas = 2u * (kPairs == 1 ? static_cast<uint32_t>(a.splits) : kPairs);
     const int64_t first = blockIdx.x / ctas, step = gridDim.x / ctas;
     const int32_t kb0 = split * a.kb_split, kb1 = min(a.kb, kb0 + a.kb_split);
 
+    // each branch runs under its own register budget
+    if (warp < kFp4EpiWarp0) {
+    regs_release<kFp4RegsCtl>();
     if (warp == 0) {
         // ---------------------------------------------------------------- TMA
         if (lane == 0) {
@@ -226,16 +283,25 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
             bool ok = true;
             for (int64_t it = first; it < a.items && ok; it += step) {
                 const int64_t row = it / a.tiles_b;
-                const int32_t a0 = static_cast<int32_t>(row * kFp4TileM) + static_cast<int32_t>(rank) * 128;
+                const int32_t a0 = static_cast<int32_t>((row * kPairs + pair) * kFp4TileM) + static_cast<int32_t>(rank) * 128;
                 const int32_t b0 = static_cast<int32_t>(it - row * a.tiles_b) * kTN;
                 for (int32_t kb = kb0; kb < kb1; ++kb) {
                     if (!tile_wait(a, ctl, &ctl->empty[stage], phase ^ 1u)) { ok = false; break; }
                     const uint32_t bar = smem_u32(&ctl->full[stage]);
                     mbar_arrive_expect_tx(bar, bytes);
                     tma_load_2d(smem_u32(s_a + stage * C::kA), &tm_a, bar, kb * 128, a0);
-                    tma_load_2d(smem_u32(s_b + stage * C::kB), &tm_b, bar, kb * 128, b0 + static_cast<int32_t>(rank) * C::kBRows);
                     tma_load_3d(smem_u32(s_sfa + stage * C::kSfa), &tm_sfa, bar, 0, kb * words, a0 >> 7);
-                    tma_load_3d(smem_u32(s_sfb + stage * C::kSfb), &tm_sfb, bar, 0, kb * words, b0 >> 7);
+                    if constexpr (kPairs == 1) {
+                        tma_load_2d(smem_u32(s_b + stage * C::kB), &tm_b, bar, kb * 128, b0 + static_cast<int32_t>(rank) * C::kBRows);
+                        tma_load_3d(smem_u32(s_sfb + stage * C::kSfb), &tm_sfb, bar, 0, kb * words, b0 >> 7);
+                    } else {  // each CTA loads its share for those that need it
+                        constexpr int kRowsShare = C::kBRows / kPairs;
+                        tma_load_2d_to(smem_u32(s_b + stage * C::kB + pair * kRowsShare * 128), &tm_b, bar, kb * 128,
+                                       b0 + static_cast<int32_t>(rank) * C::kBRows + pair * kRowsShare, static_cast<uint16_t>(5u << rank));
+                        for (int32_t u = static_cast<int32_t>(crank); u < words * C::kBTiles; u += 2 * kPairs)
+                            tma_load_3d_to(smem_u32(s_sfb + stage * C::kSfb + u * 512), &tm_sfb, bar, 0, kb * words + u / C::kBTiles,
+                                           (b0 >> 7) + u % C::kBTiles, 15);
+                    }
                     ++issued;
                     if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
                 }
@@ -257,9 +323,8 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
         if (rank == 0) {
             // ------------------------------------------------------------ MMA (even CTA)
             const uint64_t a_desc = sdesc_k_sw128(smem_u32(s_a)), b_desc = sdesc_k_sw128(smem_u32(s_b));
-            const uint64_t fa_desc = sdesc_scales(smem_u32(s_sfa)), fb_desc = sdesc_scales(smem_u32(s_sfb));
             const uint32_t sf0 = tmem + C::kAcc * kTN;
-            const uint16_t both = static_cast<uint16_t>(3u << even);
+            const uint16_t both = static_cast<uint16_t>(3u << even), all = kPairs == 1 ? both : static_cast<uint16_t>((1u << (2 * kPairs)) - 1);
             const bool b16 = a.block == 16;
             const uint32_t idesc = idesc_fp4(kFp4TileM, kTN, !b16, 0), idesc_hi = idesc_fp4(kFp4TileM, kTN, !b16, 2);
             int32_t buf = 0;
@@ -274,22 +339,16 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
                     tc_fence_after();
                     const uint32_t d = tmem + static_cast<uint32_t>(buf * kTN);
                     for (int32_t kb = s0; kb < s1; ++kb) {
-                        if (!tile_wait_warp<true>(a, ctl, &ctl->full[stage], phase)) { ok = false; break; }
+                        // the scales are there, so the stage is (the warp that copied them has seen it land)
+                        if (!tile_wait_warp<true>(a, ctl, &ctl->scales[stage], phase)) { ok = false; break; }
                         tc_fence_after();
-                        const uint32_t sfa = sf0 + static_cast<uint32_t>(stage * C::kSfCols), sfb = sfa + 16;
-                        const uint64_t fa = fa_desc + static_cast<uint64_t>((stage * C::kSfa) >> 4);
-                        const uint64_t fb = fb_desc + static_cast<uint64_t>((stage * C::kSfb) >> 4);
+                        const uint32_t sfa = sf0 + static_cast<uint32_t>(stage * C::kSfCols), sfb = sfa + 16 + sfb_off;
                         const uint64_t da = a_desc + static_cast<uint64_t>((stage * C::kA) >> 4);
                         const uint64_t db = b_desc + static_cast<uint64_t>((stage * C::kB) >> 4);
-                        for (int32_t j = 0; j < words; ++j) {
-                            copy_scales(sfa + 4 * j, fa + 32 * j);
-#pragma unroll
-                            for (int r = 0; r < C::kBTiles; ++r)
-                                copy_scales(sfb + (j * C::kBTiles + r) * 4, fb + 32 * (r * words + j));
-                        }
-                        if (b16) mma_stage16<4 * C::kBTiles>(d, da, db, idesc, sfa, sfb + sfb_off, kb > s0 ? 1u : 0u);
-                        else mma_stage32<4 * C::kBTiles>(d, da, db, idesc, idesc_hi, sfa, sfb + sfb_off, kb > s0 ? 1u : 0u);
-                        mma_commit_elect<2>(smem_u32(&ctl->empty[stage]), both);
+                        const uint32_t acc = kb > s0 ? 1u : 0u;
+                        if (b16) mma_stage<4, C::kBTiles>(d, da, db, idesc, idesc_hi, sfa, sfb, acc);
+                        else mma_stage<2, C::kBTiles>(d, da, db, idesc, idesc_hi, sfa, sfb, acc);
+                        mma_commit_elect<2>(smem_u32(&ctl->empty[stage]), all);
                         if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
                     }
                     if (!ok) break;
@@ -315,7 +374,45 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
                 }
             }
         }
-    } else if (warp >= kFp4EpiWarp0) {
+    } else if (warp == 2) {
+        // ---------------------------------------------------------------- scales (even CTA)
+        if (rank == 0) {
+            const uint64_t fa_desc = sdesc_scales(smem_u32(s_sfa)), fb_desc = sdesc_scales(smem_u32(s_sfb));
+            const uint32_t sf0 = tmem + C::kAcc * kTN;
+            int32_t stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int64_t it = first; it < a.items && ok; it += step) {
+                for (int32_t kb = kb0; kb < kb1; ++kb) {
+                    // the MMAs of the stage's last use are done: its loads waited for them
+                    if (!tile_wait_warp<true>(a, ctl, &ctl->full[stage], phase)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t sfa = sf0 + static_cast<uint32_t>(stage * C::kSfCols);
+                    const uint64_t fa = fa_desc + static_cast<uint64_t>((stage * C::kSfa) >> 4);
+                    const uint64_t fb = fb_desc + static_cast<uint64_t>((stage * C::kSfb) >> 4);
+                    if (words == 4) copy_scales<4, C::kBTiles, (kPairs > 1)>(sfa, sfa + 16, fa, fb);
+                    else copy_scales<2, C::kBTiles, (kPairs > 1)>(sfa, sfa + 16, fa, fb);
+                    mma_commit_elect<2>(smem_u32(&ctl->scales[stage]), static_cast<uint16_t>(1u << even));
+                    if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+                }
+            }
+            // every copy issued above completes before the CTA leaves
+            mma_commit_elect<2>(smem_u32(&ctl->copies_done), static_cast<uint16_t>(1u << even));
+            if (lane == 0) {
+                const uint64_t t0 = global_timer_ns();
+                while (!mbar_try_wait(smem_u32(&ctl->copies_done), 0) && global_timer_ns() - t0 < a.timeout_ns) {}
+            }
+            __syncwarp();
+        }
+    }
+    if (kPairs == 1 && a.splits > 1) {  // the epilogue warps' two meetings
+        cluster_arrive();
+        cluster_wait();
+        cluster_arrive();
+        cluster_wait();
+    }
+    } else {
+        regs_claim<kFp4RegsEpi>();
         // ---------------------------------------------------------------- epilogue
         // A warp owns 32 rows of A (a lane each) and half of the tile's columns.
         const int q = warp & 3, half = (warp - kFp4EpiWarp0) >> 2;
@@ -331,7 +428,7 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
         uint32_t buf_phase = 0;
         for (int64_t it = first; it < a.items; it += step) {
             const int64_t row = it / a.tiles_b;
-            const int64_t ra0 = row * kFp4TileM + rank * 128 + q * 32, rb0 = (it - row * a.tiles_b) * kTN + half * kCols;
+            const int64_t ra0 = (row * kPairs + pair) * kFp4TileM + rank * 128 + q * 32, rb0 = (it - row * a.tiles_b) * kTN + half * kCols;
             const int row_n = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(32), a.rows_a - ra0)));
             const bool in_a = lane < row_n;
             const float sa = scale_a && in_a ? __ldg(scale_a + ra0 + lane) : 1.f;
@@ -361,7 +458,7 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
             uint32_t held[kHold ? kChunks : 1][16];
             // other pairs' sums: [splits - 1][kTN][128], of this lane's row and first column
             const float* parts = reinterpret_cast<const float*>(s_a) + (half * kCols) * 128 + q * 32 + lane;
-            if (a.splits > 1) {
+            if (kPairs == 1 && a.splits > 1) {
                 const bool done = tile_wait_warp(a, ctl, &ctl->acc_full[buf], buf_phase);
                 tc_fence_after();
                 cluster_arrive();  // all MMAs of the cluster are done: the first pair's stages are free
@@ -384,46 +481,40 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
             bool ok = true;
             int32_t s0 = kb0;
             do {  // runs of stages, as the MMAs
-                if (a.splits == 1) {
+                if (kPairs > 1 || a.splits == 1) {
                     if (!(ok = tile_wait_warp(a, ctl, &ctl->acc_full[buf], buf_phase))) break;
                     tc_fence_after();
                 }
                 const uint32_t src = src0 + static_cast<uint32_t>(buf * kTN);
-                // one part is in flight while another is worked on
-                constexpr int kLoads = kCols / 16;
-                float v[2][16];
-                tmem_ld16(src, v[0]);
+                // all of the lane's sums, then the accumulator is handed back
+                float v[kChunks][32];
 #pragma unroll
-                for (int c = 0; c < kLoads; ++c) {
-                    tmem_wait_ld16(v[c & 1]);
-                    if (c + 1 < kLoads) {
-                        tmem_ld16(src + (c + 1) * 16, v[(c + 1) & 1]);
-                    } else {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_remote(map_shared_rank(smem_u32(&ctl->acc_empty[buf]), even));
+                for (int c = 0; c < kChunks; ++c) tmem_ld32(src + c * 32, v[c]);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) not_before(v[c]);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(map_shared_rank(smem_u32(&ctl->acc_empty[buf]), even));
+                if (kPairs == 1 && a.splits > 1) {
+                    for (int32_t s = 0; s + 1 < a.splits; ++s)
+#pragma unroll
+                        for (int i = 0; i < kCols; ++i) v[i / 32][i % 32] += parts[s * (kTN * 128) + i * 128];
+                }
+                if constexpr (kHold) {
+#pragma unroll
+                    for (int i = 0; i < kCols; i += 4) {
+                        const float* u = v[i / 32] + i % 32;
+                        const float4 s4 = *reinterpret_cast<const float4*>(tab + i);
+                        const float4 b4 = kSwap ? make_float4(bias_a, bias_a, bias_a, bias_a) : *reinterpret_cast<const float4*>(tab + kCols + i);
+                        const float2 lo = fma2(mul2(make_float2(u[0], u[1]), sa2), make_float2(s4.x, s4.y), make_float2(b4.x, b4.y));
+                        const float2 hi = fma2(mul2(make_float2(u[2], u[3]), sa2), make_float2(s4.z, s4.w), make_float2(b4.z, b4.w));
+                        held[i / 32][i % 32 / 2] = pack2<T>(lo.x, lo.y);
+                        held[i / 32][i % 32 / 2 + 1] = pack2<T>(hi.x, hi.y);
                     }
-                    float (&u)[16] = v[c & 1];
-                    if (a.splits > 1) {
-                        for (int32_t s = 0; s + 1 < a.splits; ++s)
+                } else {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) u[i] += parts[s * (kTN * 128) + (c * 16 + i) * 128];
-                    }
-                    if constexpr (kHold) {
-#pragma unroll
-                        for (int i = 0; i < 16; i += 4) {
-                            const float4 s4 = *reinterpret_cast<const float4*>(tab + c * 16 + i);
-                            const float4 b4 = kSwap ? make_float4(bias_a, bias_a, bias_a, bias_a)
-                                                    : *reinterpret_cast<const float4*>(tab + kCols + c * 16 + i);
-                            const float2 lo = fma2(mul2(make_float2(u[i], u[i + 1]), sa2), make_float2(s4.x, s4.y), make_float2(b4.x, b4.y));
-                            const float2 hi = fma2(mul2(make_float2(u[i + 2], u[i + 3]), sa2), make_float2(s4.z, s4.w), make_float2(b4.z, b4.w));
-                            held[c / 2][(c & 1) * 8 + i / 2] = pack2<T>(lo.x, lo.y);
-                            held[c / 2][(c & 1) * 8 + i / 2 + 1] = pack2<T>(hi.x, hi.y);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) sum[c * 16 + i] = s0 == kb0 ? u[i] : sum[c * 16 + i] + u[i];
-                    }
+                    for (int i = 0; i < kCols; ++i) sum[i] = s0 == kb0 ? v[i / 32][i % 32] : sum[i] + v[i / 32][i % 32];
                 }
                 if (++buf == C::kAcc) { buf = 0; buf_phase ^= 1u; }
                 s0 += a.kb_part;
@@ -484,12 +575,6 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
             }
         }
         if (kTma && lane == 0) bulk_wait();
-    }
-    if (a.splits > 1 && warp < kFp4EpiWarp0) {  // the epilogue warps' two meetings
-        cluster_arrive();
-        cluster_wait();
-        cluster_arrive();
-        cluster_wait();
     }
 
     tc_fence_before();
