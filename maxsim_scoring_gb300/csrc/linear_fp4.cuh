@@ -31,7 +31,7 @@ struct LinearFp4Args {
 
 constexpr int kFp4TileM = 256;      // rows of A per tile: 128 on each CTA of a pair
 constexpr int kFp4TileK = 256;      // values of K per stage: 128 bytes of a row
-constexpr int kFp4Threads = 384;    // warp 0 TMA, warp 1 MMA (odd CTA: reports what landed), warp 2 scales, warps 4-11 epilogue
+constexpr int kFp4Threads = 384;    // warps 0 and 3 TMA, warps 1 and 2 MMA and scales (even CTA), warps 4-11 epilogue
 constexpr int kFp4EpiWarp0 = 4;
 // Registers a thread: the launch gives kFp4Regs, of which the first warpgroup
 // hands some to the epilogue's two, which hold a tile's sums between the
@@ -83,26 +83,18 @@ constexpr size_t fp4_smem_bytes() {
     return 1024 + static_cast<size_t>(C::kStages) * C::kStage + 8 * 4096 + sizeof(Fp4Ctl);
 }
 
-// 3-D tiled load (x innermost).
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y, int32_t z) {
+// Tiled loads into this CTA's shared memory whose bytes count on a barrier of
+// either CTA of the pair (its shared::cluster address); x innermost.
+__device__ __forceinline__ void tma_load_pair_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_pair_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y, int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
-}
-
-// Both, to the same place of every CTA of the cluster in `mask`, whose barriers of
-// the same place each count the bytes.
-__device__ __forceinline__ void tma_load_2d_to(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y, uint16_t mask) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "h"(mask)
-        : "memory");
-}
-__device__ __forceinline__ void tma_load_3d_to(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y, int32_t z, uint16_t mask) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "h"(mask)
         : "memory");
 }
 
@@ -135,8 +127,8 @@ __host__ __device__ constexpr uint32_t idesc_fp4(uint32_t M, uint32_t N, bool e8
 
 // Scale tiles to tensor memory: four columns a tile, in all four lane quarters, on
 // both CTAs from their own shared memory. Word j of A's goes to sfa + 4 j, of B's
-// to sfb + 4 j, or 8 j and 8 j + 4; kByWord: B's tiles lie word by word in shared memory.
-template <int kWords, int kBTiles, bool kByWord>
+// to sfb + 4 j, or 8 j and 8 j + 4.
+template <int kWords, int kBTiles>
 __device__ __forceinline__ void copy_scales(uint32_t sfa, uint32_t sfb, uint64_t fa, uint64_t fb) {
     if constexpr (kBTiles == 1) {
         MAXSIM_FP4_COPY(MAXSIM_FP4_CP("%0", "0", "%2", "0") MAXSIM_FP4_CP("%1", "0", "%3", "0")
@@ -144,12 +136,6 @@ __device__ __forceinline__ void copy_scales(uint32_t sfa, uint32_t sfb, uint64_t
         if constexpr (kWords == 4)
             MAXSIM_FP4_COPY(MAXSIM_FP4_CP("%0", "8", "%2", "64") MAXSIM_FP4_CP("%1", "8", "%3", "64")
                             MAXSIM_FP4_CP("%0", "12", "%2", "96") MAXSIM_FP4_CP("%1", "12", "%3", "96"));
-    } else if constexpr (kByWord) {
-        MAXSIM_FP4_COPY(MAXSIM_FP4_CP("%0", "0", "%2", "0") MAXSIM_FP4_CP("%1", "0", "%3", "0") MAXSIM_FP4_CP("%1", "4", "%3", "32")
-                        MAXSIM_FP4_CP("%0", "4", "%2", "32") MAXSIM_FP4_CP("%1", "8", "%3", "64") MAXSIM_FP4_CP("%1", "12", "%3", "96"));
-        if constexpr (kWords == 4)
-            MAXSIM_FP4_COPY(MAXSIM_FP4_CP("%0", "8", "%2", "64") MAXSIM_FP4_CP("%1", "16", "%3", "128") MAXSIM_FP4_CP("%1", "20", "%3", "160")
-                            MAXSIM_FP4_CP("%0", "12", "%2", "96") MAXSIM_FP4_CP("%1", "24", "%3", "192") MAXSIM_FP4_CP("%1", "28", "%3", "224"));
     } else if constexpr (kWords == 4) {
         MAXSIM_FP4_COPY(MAXSIM_FP4_CP("%0", "0", "%2", "0") MAXSIM_FP4_CP("%1", "0", "%3", "0") MAXSIM_FP4_CP("%1", "4", "%3", "128")
                         MAXSIM_FP4_CP("%0", "4", "%2", "32") MAXSIM_FP4_CP("%1", "8", "%3", "32") MAXSIM_FP4_CP("%1", "12", "%3", "160")
@@ -207,21 +193,19 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 
 // One tile is 256 rows of A (128 on each CTA of a pair) x kTN rows of B (half on
 // each). A is the larger operand: x, or w when kSwap.
-//  * warp 0 brings stages of 256 values of K by TMA: its CTA's rows of A and B
-//    (128-byte swizzle) with the scale tiles of its rows of A and of all the
-//    tile's rows of B, which both CTAs' MMA halves need. What lies outside the
-//    operands reads as code 0 with scale 0;
+//  * warps 0 and 3 bring stages of 256 values of K by TMA: its CTA's rows of A
+//    and of B (128-byte swizzle) with the scale tiles of its rows of A and of all
+//    the tile's rows of B, which both CTAs' MMA halves need. What lies outside the
+//    operands reads as code 0 with scale 0. The bytes of both CTAs count on the
+//    even one's barrier;
 //  * warp 2 of the even CTA copies a stage's scales to tensor memory, warp 1
-//    issues its MMAs (M = 256, N = kTN, K = 64); one warp for both took 202 us for
-//    32768 x 4096 x 4096. Warp 1 of the odd CTA reports to them what landed there;
+//    issues its MMAs (M = 256, N = kTN, K = 64);
 //  * eight epilogue warps scale, add the bias, round once and store, as those of
 //    linear_tile_kernel do.
 // kRows16: rows of out start on 16-byte boundaries, and 16-bit ones end there.
-// kPairs = 2: two pairs of a cluster take neighbouring tiles of A against the same
-// rows of B, which each CTA loads a quarter of for those that need it.
 // splits > 1 (few tiles): the pairs of a cluster share a tile's K; the others'
 // sums pass to the first pair's shared memory and are added in their order.
-template <typename T, int kTN, bool kSwap, bool kRows16, int kPairs>
+template <typename T, int kTN, bool kSwap, bool kRows16>
 __global__ void __launch_bounds__(kFp4Threads, 1)
 linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_sfa,
                   const __grid_constant__ CUtensorMap tm_sfb, const __grid_constant__ CUtensorMap tm_out, const LinearFp4TileArgs a) {
@@ -236,13 +220,13 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
     Fp4Ctl* ctl = reinterpret_cast<Fp4Ctl*>(s_out + 8 * 4096);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t crank = cluster_ctarank(), rank = crank & 1u, even = crank & ~1u;
-    const int32_t split = kPairs == 1 ? static_cast<int32_t>(crank >> 1) : 0, pair = kPairs == 1 ? 0 : static_cast<int32_t>(crank >> 1);
+    const int32_t split = static_cast<int32_t>(crank >> 1);
     const int32_t words = a.block == 16 ? 4 : 2;  // scale words of a stage
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(smem_u32(&ctl->full[s]), rank == 0 ? 2 : 1);  // its own TMA; even CTA: and the odd CTA's report
+            mbar_init(smem_u32(&ctl->full[s]), 2);  // even CTA: its two TMA warps, and all the pair's bytes
             mbar_init(smem_u32(&ctl->scales[s]), 1);
-            mbar_init(smem_u32(&ctl->empty[s]), kPairs);  // a commit of every pair that the stage's loads go to
+            mbar_init(smem_u32(&ctl->empty[s]), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&ctl->acc_full[b]), 1);
@@ -266,52 +250,57 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
     cluster_sync_all();  // barriers of all CTAs exist before any remote arrival
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;
-    const uint32_t ctas = 2u * (kPairs == 1 ? static_cast<uint32_t>(a.splits) : kPairs);
+    const uint32_t ctas = 2u * static_cast<uint32_t>(a.splits);
     const int64_t first = blockIdx.x / ctas, step = gridDim.x / ctas;
     const int32_t kb0 = split * a.kb_split, kb1 = min(a.kb, kb0 + a.kb_split);
 
     // each branch runs under its own register budget
     if (warp < kFp4EpiWarp0) {
     regs_release<kFp4RegsCtl>();
-    if (warp == 0) {
-        // ---------------------------------------------------------------- TMA
+    if (warp == 0 || warp == 3) {
+        // ---------------------------------------------------------------- TMA: A with its scales, B with its scales
         if (lane == 0) {
-            const uint32_t bytes = static_cast<uint32_t>(C::kA + C::kB) + static_cast<uint32_t>(words) * 512u * (1 + C::kBTiles);
+            const bool is_a = warp == 0;
+            const CUtensorMap* map = is_a ? &tm_a : &tm_b;
+            const CUtensorMap* scale_map = is_a ? &tm_sfa : &tm_sfb;
+            const uint32_t codes = smem_u32(is_a ? s_a : s_b), scales = smem_u32(is_a ? s_sfa : s_sfb);
+            const uint32_t codes_step = is_a ? C::kA : C::kB, scales_step = is_a ? C::kSfa : C::kSfb;
+            // both CTAs' loads count on the even one's barrier, which expects them all
+            const uint32_t bars = map_shared_rank(smem_u32(&ctl->full[0]), even);
+            const uint32_t bytes = 2 * (codes_step + static_cast<uint32_t>(words) * 512u * (is_a ? 1 : C::kBTiles));
             int32_t stage = 0;
             uint32_t phase = 0;
             int64_t issued = 0;
             bool ok = true;
             for (int64_t it = first; it < a.items && ok; it += step) {
                 const int64_t row = it / a.tiles_b;
-                const int32_t a0 = static_cast<int32_t>((row * kPairs + pair) * kFp4TileM) + static_cast<int32_t>(rank) * 128;
-                const int32_t b0 = static_cast<int32_t>(it - row * a.tiles_b) * kTN;
+                // the codes' first row here, and the scales' first tile
+                int32_t y = static_cast<int32_t>(row * kFp4TileM) + static_cast<int32_t>(rank) * 128, z = y >> 7;
+                if (!is_a) {
+                    y = static_cast<int32_t>(it - row * a.tiles_b) * kTN;
+                    z = y >> 7;
+                    y += static_cast<int32_t>(rank) * C::kBRows;
+                }
                 for (int32_t kb = kb0; kb < kb1; ++kb) {
                     if (!tile_wait(a, ctl, &ctl->empty[stage], phase ^ 1u)) { ok = false; break; }
-                    const uint32_t bar = smem_u32(&ctl->full[stage]);
-                    mbar_arrive_expect_tx(bar, bytes);
-                    tma_load_2d(smem_u32(s_a + stage * C::kA), &tm_a, bar, kb * 128, a0);
-                    tma_load_3d(smem_u32(s_sfa + stage * C::kSfa), &tm_sfa, bar, 0, kb * words, a0 >> 7);
-                    if constexpr (kPairs == 1) {
-                        tma_load_2d(smem_u32(s_b + stage * C::kB), &tm_b, bar, kb * 128, b0 + static_cast<int32_t>(rank) * C::kBRows);
-                        tma_load_3d(smem_u32(s_sfb + stage * C::kSfb), &tm_sfb, bar, 0, kb * words, b0 >> 7);
-                    } else {  // each CTA loads its share for those that need it
-                        constexpr int kRowsShare = C::kBRows / kPairs;
-                        tma_load_2d_to(smem_u32(s_b + stage * C::kB + pair * kRowsShare * 128), &tm_b, bar, kb * 128,
-                                       b0 + static_cast<int32_t>(rank) * C::kBRows + pair * kRowsShare, static_cast<uint16_t>(5u << rank));
-                        for (int32_t u = static_cast<int32_t>(crank); u < words * C::kBTiles; u += 2 * kPairs)
-                            tma_load_3d_to(smem_u32(s_sfb + stage * C::kSfb + u * 512), &tm_sfb, bar, 0, kb * words + u / C::kBTiles,
-                                           (b0 >> 7) + u % C::kBTiles, 15);
-                    }
+                    if (rank == 0) mbar_arrive_expect_tx(smem_u32(&ctl->full[stage]), bytes);
+                    tma_load_pair_2d(codes + stage * codes_step, map, bars + stage * 8, kb * 128, y);
+                    tma_load_pair_3d(scales + stage * scales_step, scale_map, bars + stage * 8, 0, kb * words, z);
                     ++issued;
                     if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
                 }
             }
-            if (ctl->abort) {  // the copies still in flight land before the CTA leaves
-                const int64_t n = issued < C::kStages ? issued : C::kStages;
+            if (ctl->abort) {  // the pair's copies still in flight land before the CTAs leave together
+                const int64_t n = rank != 0 ? 0 : issued < C::kStages ? issued : C::kStages;
                 for (int64_t i = 0; i < n; ++i) {
                     if (--stage < 0) { stage = C::kStages - 1; phase ^= 1u; }
                     const uint64_t t0 = global_timer_ns();
                     while (!mbar_try_wait(smem_u32(&ctl->full[stage]), phase) && global_timer_ns() - t0 < a.timeout_ns) {}
+                }
+                // the odd CTA cannot see its copies land: it allows them a thousand times what they take
+                if (rank != 0 && issued > 0) {
+                    const uint64_t t0 = global_timer_ns();
+                    while (global_timer_ns() - t0 < a.timeout_ns / 500) {}
                 }
             }
         }
@@ -324,7 +313,7 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
             // ------------------------------------------------------------ MMA (even CTA)
             const uint64_t a_desc = sdesc_k_sw128(smem_u32(s_a)), b_desc = sdesc_k_sw128(smem_u32(s_b));
             const uint32_t sf0 = tmem + C::kAcc * kTN;
-            const uint16_t both = static_cast<uint16_t>(3u << even), all = kPairs == 1 ? both : static_cast<uint16_t>((1u << (2 * kPairs)) - 1);
+            const uint16_t both = static_cast<uint16_t>(3u << even);
             const bool b16 = a.block == 16;
             const uint32_t idesc = idesc_fp4(kFp4TileM, kTN, !b16, 0), idesc_hi = idesc_fp4(kFp4TileM, kTN, !b16, 2);
             int32_t buf = 0;
@@ -348,7 +337,7 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
                         const uint32_t acc = kb > s0 ? 1u : 0u;
                         if (b16) mma_stage<4, C::kBTiles>(d, da, db, idesc, idesc_hi, sfa, sfb, acc);
                         else mma_stage<2, C::kBTiles>(d, da, db, idesc, idesc_hi, sfa, sfb, acc);
-                        mma_commit_elect<2>(smem_u32(&ctl->empty[stage]), all);
+                        mma_commit_elect<2>(smem_u32(&ctl->empty[stage]), both);
                         if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
                     }
                     if (!ok) break;
@@ -364,15 +353,6 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
                 while (!mbar_try_wait(smem_u32(&ctl->mma_done), 0) && global_timer_ns() - t0 < a.timeout_ns) {}
             }
             __syncwarp();
-        } else {
-            // ------------------------------------------------------------ odd CTA: reports what landed
-            for (int64_t it = first; it < a.items && ok; it += step) {
-                for (int32_t kb = kb0; kb < kb1; ++kb) {
-                    if (!tile_wait_warp(a, ctl, &ctl->full[stage], phase)) { ok = false; break; }
-                    if (lane == 0) mbar_arrive_remote(map_shared_rank(smem_u32(&ctl->full[stage]), even));
-                    if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
-                }
-            }
         }
     } else if (warp == 2) {
         // ---------------------------------------------------------------- scales (even CTA)
@@ -390,8 +370,8 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
                     const uint32_t sfa = sf0 + static_cast<uint32_t>(stage * C::kSfCols);
                     const uint64_t fa = fa_desc + static_cast<uint64_t>((stage * C::kSfa) >> 4);
                     const uint64_t fb = fb_desc + static_cast<uint64_t>((stage * C::kSfb) >> 4);
-                    if (words == 4) copy_scales<4, C::kBTiles, (kPairs > 1)>(sfa, sfa + 16, fa, fb);
-                    else copy_scales<2, C::kBTiles, (kPairs > 1)>(sfa, sfa + 16, fa, fb);
+                    if (words == 4) copy_scales<4, C::kBTiles>(sfa, sfa + 16, fa, fb);
+                    else copy_scales<2, C::kBTiles>(sfa, sfa + 16, fa, fb);
                     mma_commit_elect<2>(smem_u32(&ctl->scales[stage]), static_cast<uint16_t>(1u << even));
                     if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
                 }
@@ -405,7 +385,7 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
             __syncwarp();
         }
     }
-    if (kPairs == 1 && a.splits > 1) {  // the epilogue warps' two meetings
+    if (a.splits > 1) {  // the epilogue warps' two meetings
         cluster_arrive();
         cluster_wait();
         cluster_arrive();
@@ -428,7 +408,7 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
         uint32_t buf_phase = 0;
         for (int64_t it = first; it < a.items; it += step) {
             const int64_t row = it / a.tiles_b;
-            const int64_t ra0 = (row * kPairs + pair) * kFp4TileM + rank * 128 + q * 32, rb0 = (it - row * a.tiles_b) * kTN + half * kCols;
+            const int64_t ra0 = row * kFp4TileM + rank * 128 + q * 32, rb0 = (it - row * a.tiles_b) * kTN + half * kCols;
             const int row_n = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(32), a.rows_a - ra0)));
             const bool in_a = lane < row_n;
             const float sa = scale_a && in_a ? __ldg(scale_a + ra0 + lane) : 1.f;
@@ -458,7 +438,7 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
             uint32_t held[kHold ? kChunks : 1][16];
             // other pairs' sums: [splits - 1][kTN][128], of this lane's row and first column
             const float* parts = reinterpret_cast<const float*>(s_a) + (half * kCols) * 128 + q * 32 + lane;
-            if (kPairs == 1 && a.splits > 1) {
+            if (a.splits > 1) {
                 const bool done = tile_wait_warp(a, ctl, &ctl->acc_full[buf], buf_phase);
                 tc_fence_after();
                 cluster_arrive();  // all MMAs of the cluster are done: the first pair's stages are free
@@ -481,7 +461,7 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
             bool ok = true;
             int32_t s0 = kb0;
             do {  // runs of stages, as the MMAs
-                if (kPairs > 1 || a.splits == 1) {
+                if (a.splits == 1) {
                     if (!(ok = tile_wait_warp(a, ctl, &ctl->acc_full[buf], buf_phase))) break;
                     tc_fence_after();
                 }
@@ -496,7 +476,7 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote(map_shared_rank(smem_u32(&ctl->acc_empty[buf]), even));
-                if (kPairs == 1 && a.splits > 1) {
+                if (a.splits > 1) {
                     for (int32_t s = 0; s + 1 < a.splits; ++s)
 #pragma unroll
                         for (int i = 0; i < kCols; ++i) v[i / 32][i % 32] += parts[s * (kTN * 128) + i * 128];

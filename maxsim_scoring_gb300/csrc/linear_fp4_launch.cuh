@@ -15,14 +15,11 @@
 
 namespace maxsim {
 
-constexpr int64_t kFp4Clusters4 = 36;  // clusters of four that a GB300 holds with a CTA on each SM (144 of its 152)
-
 struct LinearFp4Plan {
     bool swap = false;  // A is w, B is x
     int tn = 64;
     int64_t tiles = 0, tiles_b = 0;
     int32_t kb = 0, splits = 1, kb_split = 0;
-    int pairs = 1;       // pairs of a cluster that share tiles of B
 };
 
 // [rows, bytes] codes, rows ld bytes apart, in boxes of 128 bytes x box_rows.
@@ -43,10 +40,10 @@ inline bool encode_scales(EncodeTiledFn encode, CUtensorMap* map, const void* ba
                   CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int kTN, bool kSwap, bool kRows16, int kPairs>
+template <typename T, int kTN, bool kSwap, bool kRows16>
 maxsim_status launch_fp4_kernel(const LinearFp4Plan& p, const LinearFp4Args& l, int block, const HostDevice& dev, cudaStream_t st) {
     using C = Fp4Cfg<kTN>;
-    auto kern = linear_fp4_kernel<T, kTN, kSwap, kRows16, kPairs>;
+    auto kern = linear_fp4_kernel<T, kTN, kSwap, kRows16>;
     constexpr size_t kSmem = fp4_smem_bytes<kTN>();
     static_assert(kSmem <= kSmemBudget, "shared memory of one SM");
     static_assert(kTN != 64 || (kFp4MaxSplits - 1) * kTN * 128 * 4 <= C::kStages * (C::kA + C::kB), "the splits' sums lie in the stages");
@@ -63,7 +60,7 @@ maxsim_status launch_fp4_kernel(const LinearFp4Plan& p, const LinearFp4Args& l, 
     }
     LinearFp4TileArgs a{};
     a.l = l;
-    a.items = (p.tiles / p.tiles_b + kPairs - 1) / kPairs * p.tiles_b;
+    a.items = p.tiles;
     a.rows_a = kSwap ? l.N : l.M;
     a.rows_b = kSwap ? l.M : l.N;
     a.tiles_b = static_cast<int32_t>(p.tiles_b);
@@ -77,9 +74,9 @@ maxsim_status launch_fp4_kernel(const LinearFp4Plan& p, const LinearFp4Args& l, 
     CUtensorMap ta, tb, fa, fb;
     const uint32_t words = block == 16 ? 4 : 2;
     if (!encode_codes(dev.encode, &ta, kSwap ? l.w : l.x, l.K / 2, a.rows_a, kSwap ? l.ld_w : l.ld_x, 128) ||
-        !encode_codes(dev.encode, &tb, kSwap ? l.x : l.w, l.K / 2, a.rows_b, kSwap ? l.ld_x : l.ld_w, C::kBRows / kPairs) ||
+        !encode_codes(dev.encode, &tb, kSwap ? l.x : l.w, l.K / 2, a.rows_b, kSwap ? l.ld_x : l.ld_w, C::kBRows) ||
         !encode_scales(dev.encode, &fa, kSwap ? l.w_block : l.x_block, l.words, a.rows_a, words, 1) ||
-        !encode_scales(dev.encode, &fb, kSwap ? l.x_block : l.w_block, l.words, a.rows_b, kPairs == 1 ? words : 1, kPairs == 1 ? C::kBTiles : 1))
+        !encode_scales(dev.encode, &fb, kSwap ? l.x_block : l.w_block, l.words, a.rows_b, words, C::kBTiles))
         return MAXSIM_ERR_CUDA;
     CUtensorMap tout = ta;  // used by 16-bit outputs that are stored by TMA alone
     if constexpr (sizeof(T) == 2 && kRows16 && !kSwap) {
@@ -91,8 +88,8 @@ maxsim_status launch_fp4_kernel(const LinearFp4Plan& p, const LinearFp4Args& l, 
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return MAXSIM_ERR_CUDA;
     }
-    const unsigned cluster = 2u * (kPairs == 1 ? static_cast<unsigned>(p.splits) : kPairs);
-    const int64_t most = kPairs > 1 ? kFp4Clusters4 : p.splits > 1 ? p.tiles : std::max(1, dev.num_sms / 2);
+    const unsigned cluster = 2u * static_cast<unsigned>(p.splits);
+    const int64_t most = p.splits > 1 ? p.tiles : std::max(1, dev.num_sms / 2);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(a.items, most)) * cluster);
     cfg.blockDim = dim3(kFp4Threads);
@@ -112,15 +109,15 @@ maxsim_status launch_fp4_kernel(const LinearFp4Plan& p, const LinearFp4Args& l, 
     return MAXSIM_OK;
 }
 
-template <typename T, int kTN, int kPairs>
+template <typename T, int kTN>
 maxsim_status launch_fp4_tile(const LinearFp4Plan& p, const LinearFp4Args& l, int block, const HostDevice& dev, cudaStream_t st) {
-    if (p.swap) return launch_fp4_kernel<T, kTN, true, false, kPairs>(p, l, block, dev, st);
+    if (p.swap) return launch_fp4_kernel<T, kTN, true, false>(p, l, block, dev, st);
     // 16-bit outputs leave by TMA, which wants strides below 2^40 bytes and
     // writes an odd row's last element with the one behind it
     bool rows16 = ptr_aligned(l.out, 16) && l.ld_out * static_cast<int64_t>(sizeof(T)) % 16 == 0;
     if (sizeof(T) == 2) rows16 = rows16 && l.N % 8 == 0 && l.ld_out < (int64_t(1) << 38);
-    return rows16 ? launch_fp4_kernel<T, kTN, false, true, kPairs>(p, l, block, dev, st)
-                  : launch_fp4_kernel<T, kTN, false, false, kPairs>(p, l, block, dev, st);
+    return rows16 ? launch_fp4_kernel<T, kTN, false, true>(p, l, block, dev, st)
+                  : launch_fp4_kernel<T, kTN, false, false>(p, l, block, dev, st);
 }
 
 template <typename T>
@@ -130,10 +127,10 @@ maxsim_status run_linear_fp4(const LinearFp4Plan& p, const LinearFp4Args& l, int
         return launched();
     }
     if constexpr (sizeof(T) == 2) {
-        if (p.tn == 256) return p.pairs == 2 ? launch_fp4_tile<T, 256, 2>(p, l, block, dev, st) : launch_fp4_tile<T, 256, 1>(p, l, block, dev, st);
+        if (p.tn == 256) return launch_fp4_tile<T, 256>(p, l, block, dev, st);
     }
-    if (p.tn >= 128) return launch_fp4_tile<T, 128, 1>(p, l, block, dev, st);
-    return launch_fp4_tile<T, 64, 1>(p, l, block, dev, st);
+    if (p.tn >= 128) return launch_fp4_tile<T, 128>(p, l, block, dev, st);
+    return launch_fp4_tile<T, 64>(p, l, block, dev, st);
 }
 
 }  // namespace maxsim
