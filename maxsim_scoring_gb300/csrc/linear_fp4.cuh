@@ -65,6 +65,7 @@ struct LinearFp4TileArgs {
     int32_t splits;     // pairs of a cluster that share a tile's K
     int32_t kb_split;   // stages of each
     int32_t block;      // 16 or 32
+    int prefetch;       // tiles of A ahead
     int* status;
     uint64_t timeout_ns;
 };
@@ -96,6 +97,15 @@ __device__ __forceinline__ void tma_load_pair_3d(uint32_t dst, const CUtensorMap
         "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
+}
+
+// Tiled prefetches into L2.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int32_t x, int32_t y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int32_t x, int32_t y, int32_t z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z)
+                 : "memory");
 }
 
 // Shared-memory descriptor of a tile of scale words: 32 rows of 16 bytes, no
@@ -280,6 +290,17 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
                     y = static_cast<int32_t>(it - row * a.tiles_b) * kTN;
                     z = y >> 7;
                     y += static_cast<int32_t>(rank) * C::kBRows;
+                }
+                // The pairs that take one tile of A against all of B read its stages at the
+                // same time, each fresh from HBM: what is next of A they bring to L2 before,
+                // each its share.
+                if (is_a && a.prefetch && it + step < a.items) {
+                    const int64_t next = (it + step) / a.tiles_b;
+                    const int32_t y2 = static_cast<int32_t>(next * kFp4TileM) + static_cast<int32_t>(rank) * 128;
+                    for (int32_t kb = static_cast<int32_t>(it + step - next * a.tiles_b); kb < a.kb; kb += a.tiles_b) {
+                        tma_prefetch_2d(map, kb * 128, y2);
+                        tma_prefetch_3d(scale_map, 0, kb * words, y2 >> 7);
+                    }
                 }
                 for (int32_t kb = kb0; kb < kb1; ++kb) {
                     if (!tile_wait(a, ctl, &ctl->empty[stage], phase ^ 1u)) { ok = false; break; }

@@ -69,6 +69,7 @@ maxsim_status launch_fp4_kernel(const LinearFp4Plan& p, const LinearFp4Args& l, 
     a.splits = p.splits;
     a.kb_split = p.kb_split;
     a.block = block;
+    a.prefetch = p.tiles_b >= 4;
     a.status = dev.status;
     a.timeout_ns = kTimeoutNs;
     CUtensorMap ta, tb, fa, fb;
