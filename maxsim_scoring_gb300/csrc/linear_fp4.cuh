@@ -61,7 +61,6 @@ struct LinearFp4TileArgs {
     int32_t rows_b;
     int32_t tiles_b;
     int32_t kb;         // stages of K
-    int32_t kb_part;    // f32 outputs: stages summed in one accumulator
     int32_t splits;     // pairs of a cluster that share a tile's K
     int32_t kb_split;   // stages of each
     int32_t block;      // 16 or 32
@@ -342,30 +341,25 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
             for (int64_t it = first; it < a.items && ok; it += step) {
                 // kTN = 64: the odd tiles' rows are the upper half of a scale tile
                 const uint32_t sfb_off = kTN == 64 ? static_cast<uint32_t>((it % a.tiles_b) & 1) * 2u : 0u;
-                int32_t s0 = kb0;
-                do {  // a run of stages that are summed in one accumulator
-                    const int32_t s1 = std::is_same_v<T, float> ? min(kb1, s0 + a.kb_part) : kb1;
-                    if (!tile_wait_warp<true>(a, ctl, &ctl->acc_empty[buf], buf_phase ^ 1u)) { ok = false; break; }
+                if (!tile_wait_warp<true>(a, ctl, &ctl->acc_empty[buf], buf_phase ^ 1u)) break;
+                tc_fence_after();
+                const uint32_t d = tmem + static_cast<uint32_t>(buf * kTN);
+                for (int32_t kb = kb0; kb < kb1; ++kb) {
+                    // the scales are there, so the stage is (the warp that copied them has seen it land)
+                    if (!tile_wait_warp<true>(a, ctl, &ctl->scales[stage], phase)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t d = tmem + static_cast<uint32_t>(buf * kTN);
-                    for (int32_t kb = s0; kb < s1; ++kb) {
-                        // the scales are there, so the stage is (the warp that copied them has seen it land)
-                        if (!tile_wait_warp<true>(a, ctl, &ctl->scales[stage], phase)) { ok = false; break; }
-                        tc_fence_after();
-                        const uint32_t sfa = sf0 + static_cast<uint32_t>(stage * C::kSfCols), sfb = sfa + 16 + sfb_off;
-                        const uint64_t da = a_desc + static_cast<uint64_t>((stage * C::kA) >> 4);
-                        const uint64_t db = b_desc + static_cast<uint64_t>((stage * C::kB) >> 4);
-                        const uint32_t acc = kb > s0 ? 1u : 0u;
-                        if (b16) mma_stage<4, C::kBTiles>(d, da, db, idesc, idesc_hi, sfa, sfb, acc);
-                        else mma_stage<2, C::kBTiles>(d, da, db, idesc, idesc_hi, sfa, sfb, acc);
-                        mma_commit_elect<2>(smem_u32(&ctl->empty[stage]), both);
-                        if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
-                    }
-                    if (!ok) break;
-                    mma_commit_elect<2>(smem_u32(&ctl->acc_full[buf]), both);
-                    if (++buf == C::kAcc) { buf = 0; buf_phase ^= 1u; }
-                    s0 = s1;
-                } while (std::is_same_v<T, float> && s0 < kb1);
+                    const uint32_t sfa = sf0 + static_cast<uint32_t>(stage * C::kSfCols), sfb = sfa + 16 + sfb_off;
+                    const uint64_t da = a_desc + static_cast<uint64_t>((stage * C::kA) >> 4);
+                    const uint64_t db = b_desc + static_cast<uint64_t>((stage * C::kB) >> 4);
+                    const uint32_t acc = kb > kb0 ? 1u : 0u;
+                    if (b16) mma_stage<4, C::kBTiles>(d, da, db, idesc, idesc_hi, sfa, sfb, acc);
+                    else mma_stage<2, C::kBTiles>(d, da, db, idesc, idesc_hi, sfa, sfb, acc);
+                    mma_commit_elect<2>(smem_u32(&ctl->empty[stage]), both);
+                    if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+                }
+                if (!ok) break;
+                mma_commit_elect<2>(smem_u32(&ctl->acc_full[buf]), both);
+                if (++buf == C::kAcc) { buf = 0; buf_phase ^= 1u; }
             }
             // every MMA issued above completes before the CTA leaves
             mma_commit_elect<2>(smem_u32(&ctl->mma_done), static_cast<uint16_t>(1u << even));
@@ -455,7 +449,6 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
             }
             const float2 sa2 = make_float2(sa, sa);
             const uint32_t src0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * kCols);
-            float sum[kHold ? 1 : kCols];
             uint32_t held[kHold ? kChunks : 1][16];
             // other pairs' sums: [splits - 1][kTN][128], of this lane's row and first column
             const float* parts = reinterpret_cast<const float*>(s_a) + (half * kCols) * 128 + q * 32 + lane;
@@ -479,48 +472,39 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
                 cluster_wait();
                 if (split > 0 || !done) break;
             }
-            bool ok = true;
-            int32_t s0 = kb0;
-            do {  // runs of stages, as the MMAs
-                if (a.splits == 1) {
-                    if (!(ok = tile_wait_warp(a, ctl, &ctl->acc_full[buf], buf_phase))) break;
-                    tc_fence_after();
+            if (a.splits == 1) {
+                if (!tile_wait_warp(a, ctl, &ctl->acc_full[buf], buf_phase)) break;
+                tc_fence_after();
+            }
+            const uint32_t src = src0 + static_cast<uint32_t>(buf * kTN);
+            // all of the lane's sums, then the accumulator is handed back
+            float v[kChunks][32];
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) tmem_ld32(src + c * 32, v[c]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) not_before(v[c]);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(map_shared_rank(smem_u32(&ctl->acc_empty[buf]), even));
+            if (a.splits > 1) {
+                for (int32_t s = 0; s + 1 < a.splits; ++s)
+#pragma unroll
+                    for (int i = 0; i < kCols; ++i) v[i / 32][i % 32] += parts[s * (kTN * 128) + i * 128];
+            }
+            if constexpr (kHold) {
+#pragma unroll
+                for (int i = 0; i < kCols; i += 4) {
+                    const float* u = v[i / 32] + i % 32;
+                    const float4 s4 = *reinterpret_cast<const float4*>(tab + i);
+                    const float4 b4 = kSwap ? make_float4(bias_a, bias_a, bias_a, bias_a) : *reinterpret_cast<const float4*>(tab + kCols + i);
+                    const float2 lo = fma2(mul2(make_float2(u[0], u[1]), sa2), make_float2(s4.x, s4.y), make_float2(b4.x, b4.y));
+                    const float2 hi = fma2(mul2(make_float2(u[2], u[3]), sa2), make_float2(s4.z, s4.w), make_float2(b4.z, b4.w));
+                    held[i / 32][i % 32 / 2] = pack2<T>(lo.x, lo.y);
+                    held[i / 32][i % 32 / 2 + 1] = pack2<T>(hi.x, hi.y);
                 }
-                const uint32_t src = src0 + static_cast<uint32_t>(buf * kTN);
-                // all of the lane's sums, then the accumulator is handed back
-                float v[kChunks][32];
-#pragma unroll
-                for (int c = 0; c < kChunks; ++c) tmem_ld32(src + c * 32, v[c]);
-                tmem_wait_ld();
-#pragma unroll
-                for (int c = 0; c < kChunks; ++c) not_before(v[c]);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote(map_shared_rank(smem_u32(&ctl->acc_empty[buf]), even));
-                if (a.splits > 1) {
-                    for (int32_t s = 0; s + 1 < a.splits; ++s)
-#pragma unroll
-                        for (int i = 0; i < kCols; ++i) v[i / 32][i % 32] += parts[s * (kTN * 128) + i * 128];
-                }
-                if constexpr (kHold) {
-#pragma unroll
-                    for (int i = 0; i < kCols; i += 4) {
-                        const float* u = v[i / 32] + i % 32;
-                        const float4 s4 = *reinterpret_cast<const float4*>(tab + i);
-                        const float4 b4 = kSwap ? make_float4(bias_a, bias_a, bias_a, bias_a) : *reinterpret_cast<const float4*>(tab + kCols + i);
-                        const float2 lo = fma2(mul2(make_float2(u[0], u[1]), sa2), make_float2(s4.x, s4.y), make_float2(b4.x, b4.y));
-                        const float2 hi = fma2(mul2(make_float2(u[2], u[3]), sa2), make_float2(s4.z, s4.w), make_float2(b4.z, b4.w));
-                        held[i / 32][i % 32 / 2] = pack2<T>(lo.x, lo.y);
-                        held[i / 32][i % 32 / 2 + 1] = pack2<T>(hi.x, hi.y);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < kCols; ++i) sum[i] = s0 == kb0 ? v[i / 32][i % 32] : sum[i] + v[i / 32][i % 32];
-                }
-                if (++buf == C::kAcc) { buf = 0; buf_phase ^= 1u; }
-                s0 += a.kb_part;
-            } while (!kHold && s0 < kb1);
-            if (!ok) break;
+            }
+            if (++buf == C::kAcc) { buf = 0; buf_phase ^= 1u; }
             if constexpr (kHold) {
                 store_held<T, kCols, kSwap, kTma>(held, stage, out, ld, ra0, rb0, a.rows_b, row_n, &tm_out);
             } else {
@@ -528,20 +512,19 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
                 for (int c = 0; c < kChunks; ++c) {
                     const int64_t rb = rb0 + c * 32;
                     if (row_n == 0 || rb >= a.rows_b) break;
-                    const float* v = sum + c * 32;
                     if constexpr (kSwap) {
                         const int n = static_cast<int>(min(static_cast<int64_t>(32), a.rows_b - rb));
                         float* p = out + rb * ld + ra0 + lane;
 #pragma unroll
                         for (int i = 0; i < 32; ++i, p += ld) {
-                            const float y = __fmaf_rn(v[i] * __shfl_sync(0xffffffffu, sb[c], i), sa, bias_a);
+                            const float y = __fmaf_rn(v[c][i] * __shfl_sync(0xffffffffu, sb[c], i), sa, bias_a);
                             if (i < n && in_a) *p = y;
                         }
                     } else {
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
                             *reinterpret_cast<float4*>(stage + staged(lane, i)) =
-                                make_float4(v[4 * i] * sa, v[4 * i + 1] * sa, v[4 * i + 2] * sa, v[4 * i + 3] * sa);
+                                make_float4(v[c][4 * i] * sa, v[c][4 * i + 1] * sa, v[c][4 * i + 2] * sa, v[c][4 * i + 3] * sa);
                         __syncwarp();
                         if constexpr (kRows16) {
                             float ws[4], bs[4];  // this lane's four channels

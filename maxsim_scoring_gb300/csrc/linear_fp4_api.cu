@@ -19,21 +19,27 @@ constexpr int64_t kMaxRows = kI32Max - 1023;  // a tile past the last row still 
 
 constexpr int64_t kPairs = 76;                // CTA pairs of a GB300 (152 SMs): plans do not depend on the device
 
-// The tile's width, and the pairs that share its K where there are few tiles,
-// by the time they should take.
-LinearFp4Plan plan_linear_fp4(int64_t M, int64_t N, int64_t K, bool out32) {
+// The tile's width, and the pairs of a cluster that share a tile's K where there
+// are few tiles, by the time they should take, in cycles: the tiles of the
+// busiest pair, each its stages and a start and end. (Measured: a stage takes 600
+// cycles with 256 columns, and 490 and 460 with 128 and 64, where the MMA warp's
+// issue bounds it.) Clusters of four CTAs: a GB300 holds 36 of them; of eight only 15.
+LinearFp4Plan plan_linear_fp4(int64_t M, int64_t N, int64_t K) {
     LinearFp4Plan p;
     p.swap = N > M;
     p.kb = static_cast<int32_t>((K + kFp4TileK - 1) / kFp4TileK);
     const int64_t rows_a = p.swap ? N : M, rows_b = p.swap ? M : N;
     double best = 0.0;
-    for (int tn = out32 ? 128 : 256; tn >= 64; tn /= 2) {
+    for (int tn = 256; tn >= 64; tn /= 2) {
         const int64_t tiles_b = (rows_b + tn - 1) / tn, tiles = (rows_a + kFp4TileM - 1) / kFp4TileM * tiles_b;
-        const double stage = tn == 256 ? 900.0 : tn == 128 ? 650.0 : 500.0, ends = tn == 256 ? 3000.0 : tn == 128 ? 2000.0 : 1500.0;
+        const double stage = tn == 256 ? 600.0 : tn == 128 ? 490.0 : 460.0, ends = tn == 256 ? 2300.0 : tn == 128 ? 1000.0 : 700.0;
+        // the first stage's latency, and the last tile's way out
+        const double once = tn == 256 ? 6000.0 : tn == 128 ? 3500.0 : 2500.0;
         for (int32_t splits = 1; splits <= kFp4MaxSplits; splits *= 2) {
             const int32_t kb_split = (p.kb + splits - 1) / splits;
-            if (splits > 1 && (tn != 64 || tiles * splits > kPairs || kb_split * (splits - 1) >= p.kb)) continue;
-            const double cost = static_cast<double>((tiles * splits + kPairs - 1) / kPairs) * (kb_split * stage + ends) + (splits > 1 ? 2500.0 : 0.0);
+            const int64_t clusters = splits == 1 ? kPairs : splits == 2 ? 36 : 15;
+            if (splits > 1 && (tn != 64 || tiles > clusters || kb_split * (splits - 1) >= p.kb)) continue;
+            const double cost = static_cast<double>((tiles + clusters - 1) / clusters) * (kb_split * stage + ends) + once + (splits > 1 ? 1500.0 : 0.0);
             if (best == 0.0 || cost < best) {
                 best = cost;
                 p.tn = tn;
@@ -75,7 +81,7 @@ maxsim_status maxsim_linear_fp4(const uint8_t* x, int64_t ld_x, const uint8_t* x
     const LinearFp4Args a{x, w, x_block_scale, w_block_scale, ld_x, ld_w, ld_out, x_scale, w_scale, bias, out,
                           static_cast<int32_t>(M), static_cast<int32_t>(N), static_cast<int32_t>(K),
                           static_cast<int32_t>((K + 4 * block - 1) / (4 * block))};
-    const LinearFp4Plan p = plan_linear_fp4(M, N, K, out_dtype == MAXSIM_F32);
+    const LinearFp4Plan p = plan_linear_fp4(M, N, K);
     if (p.tiles > kI32Max) return MAXSIM_ERR_UNSUPPORTED;
     if (out_dtype == MAXSIM_F16) return run_linear_fp4<__half>(p, a, block, dev, st);
     if (out_dtype == MAXSIM_BF16) return run_linear_fp4<__nv_bfloat16>(p, a, block, dev, st);

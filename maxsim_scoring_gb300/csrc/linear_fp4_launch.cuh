@@ -65,7 +65,6 @@ maxsim_status launch_fp4_kernel(const LinearFp4Plan& p, const LinearFp4Args& l, 
     a.rows_b = kSwap ? l.M : l.N;
     a.tiles_b = static_cast<int32_t>(p.tiles_b);
     a.kb = p.kb;
-    a.kb_part = p.kb;
     a.splits = p.splits;
     a.kb_split = p.kb_split;
     a.block = block;
@@ -127,10 +126,8 @@ maxsim_status run_linear_fp4(const LinearFp4Plan& p, const LinearFp4Args& l, int
         linear_fp4_bias_kernel<T><<<grid_of(static_cast<int64_t>(l.M) * l.N, 256, int64_t(dev.num_sms) * 8), 256, 0, st>>>(l);
         return launched();
     }
-    if constexpr (sizeof(T) == 2) {
-        if (p.tn == 256) return launch_fp4_tile<T, 256>(p, l, block, dev, st);
-    }
-    if (p.tn >= 128) return launch_fp4_tile<T, 128>(p, l, block, dev, st);
+    if (p.tn == 256) return launch_fp4_tile<T, 256>(p, l, block, dev, st);
+    if (p.tn == 128) return launch_fp4_tile<T, 128>(p, l, block, dev, st);
     return launch_fp4_tile<T, 64>(p, l, block, dev, st);
 }
 

@@ -59,6 +59,25 @@ def test_quantize(block, dtype, rows, cols, pad, offset):
     assert whole.shape == (rows, 2 * q.shape[1]) and not whole[:, cols:].any()
 
 
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(5, 17), (40, 33), (9, 127), (6, 530), (3, 1030), (2, 4500)])
+def test_dequantize_into_rows_anywhere(dtype, rows, cols):
+    """Rows of every phase in a wider buffer: what is around them stays."""
+    x = rows_of(cols, rows, cols, "f32")
+    got = ms.quantize_rows_fp4(x, block=32)
+    want = ms.dequantize_rows_fp4(*got, block=32, cols=cols, out_dtype=DT[dtype])
+    lib, e = ms._native.lib(), DT[dtype].itemsize
+    for offset in range(9):
+        for ld in (cols, cols + 3):
+            buf = torch.full((offset + rows * ld + 9,), 7.0, dtype=DT[dtype], device="cuda")
+            rc = lib.maxsim_dequantize_rows_fp4(got[0].data_ptr(), got[0].shape[1], got[1].data_ptr(), None, rows, cols, 32,
+                                                {2: 0, 4: 2}[e], buf.data_ptr() + offset * e, ld, torch.cuda.current_stream().cuda_stream)
+            assert rc == 0
+            body = buf[offset:offset + rows * ld].view(rows, ld)
+            same = torch.equal(body[:, :cols], want)
+            assert same and (body[:, cols:] == 7).all() and (buf[:offset] == 7).all() and (buf[offset + rows * ld:] == 7).all()
+
+
 @pytest.mark.parametrize("block", [16, 32])
 def test_quantize_borders(block):
     """Every border between two codes, the values next to it, and ties, for every scale mantissa."""
