@@ -25,7 +25,9 @@ maxsim_status launch_group(const Fp4QuantizeArgs& a, const HostDevice& dev, cuda
 template <typename T, int kBlock, bool kWide>
 maxsim_status launch_quantize(const Fp4QuantizeArgs& a, const HostDevice& dev, cudaStream_t st) {
     if (a.chunks <= 2) return launch_group<T, kBlock, kWide, 2, 1>(a, dev, st);
+    if (a.chunks <= 4) return launch_group<T, kBlock, kWide, 4, 1>(a, dev, st);
     if (a.chunks <= 8) return launch_group<T, kBlock, kWide, 8, 1>(a, dev, st);
+    if (a.chunks <= 16) return launch_group<T, kBlock, kWide, 16, 1>(a, dev, st);
     if (a.chunks <= 32) return launch_group<T, kBlock, kWide, 32, 1>(a, dev, st);
     if (a.chunks <= 64) return launch_group<T, kBlock, kWide, 32, 2>(a, dev, st);
     if (a.chunks <= 96) return launch_group<T, kBlock, kWide, 32, 3>(a, dev, st);
@@ -57,7 +59,9 @@ void launch_dequantize_group(const Fp4DequantizeArgs& a, const HostDevice& dev, 
 template <typename T, int kBlock, bool kWide>
 maxsim_status launch_dequantize(const Fp4DequantizeArgs& a, const HostDevice& dev, cudaStream_t st) {
     if (a.cols <= 32) launch_dequantize_group<T, kBlock, kWide, 2, true>(a, dev, st);
+    else if (a.cols <= 64) launch_dequantize_group<T, kBlock, kWide, 4, true>(a, dev, st);
     else if (a.cols <= 128) launch_dequantize_group<T, kBlock, kWide, 8, true>(a, dev, st);
+    else if (a.cols <= 256) launch_dequantize_group<T, kBlock, kWide, 16, true>(a, dev, st);
     else if (a.cols <= 512) launch_dequantize_group<T, kBlock, kWide, 32, true>(a, dev, st);
     else if (a.cols <= 1024) launch_dequantize_group<T, kBlock, kWide, 64, true>(a, dev, st);
     else if (a.cols <= 2048) launch_dequantize_group<T, kBlock, kWide, 128, true>(a, dev, st);

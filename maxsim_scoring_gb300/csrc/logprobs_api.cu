@@ -50,8 +50,21 @@ maxsim_status launch_block(const LogprobsArgs& a, int blocks, const HostDevice& 
 template <typename T, bool kMask, bool kTop>
 maxsim_status launch_fwd(const LogprobsArgs& a, const HostDevice& dev, cudaStream_t st) {
     const int64_t pieces = (a.n * static_cast<int64_t>(sizeof(T)) + 15) / 16;
-    if (pieces <= 256) {
-        logprobs_warp_kernel<T, kMask, kTop><<<static_cast<unsigned>((a.rows + 7) / 8), 256, 0, st>>>(a);
+    const unsigned warps = static_cast<unsigned>((a.rows + 7) / 8);
+    // Short rows take a warp each. Their strongest columns by ranks or one after another (us for 16,384 f32 rows
+    // without any, by ranks, and for each listed one: 64 columns 8, 20, 1.5; 128: 8, 50, 1.6; 250 bf16: 11, 176, 1.5). A
+    // warp alone takes 0.3 us for each one, so that few rows are ranked sooner, or take a block (100 x 500 f32
+    // with 64 listed 19 and 8 us, with 8 5.4 and 5.7; 3000 x 2000 bf16 with 64 39 and 29, with 20 16 and 18).
+    const bool few = a.rows <= int64_t(dev.num_sms) * 8;
+    if constexpr (kTop) {
+        if (a.n <= kRankColumns && (a.n * a.n <= int64_t(600) * a.k || (few && a.k > 16))) {
+            logprobs_warp_kernel<T, kMask, 2><<<warps, 256, 0, st>>>(a);
+            return launched();
+        }
+    }
+    const bool block = few ? a.k > 8 && pieces > 32 : a.k >= 32 && a.rows <= int64_t(dev.num_sms) * 32 && pieces > 64;
+    if (pieces <= 256 && !block) {
+        logprobs_warp_kernel<T, kMask, kTop ? 1 : 0><<<warps, 256, 0, st>>>(a);
         return launched();
     }
     // few rows: the blocks of a cluster share one

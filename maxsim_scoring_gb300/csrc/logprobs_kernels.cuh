@@ -483,8 +483,37 @@ __device__ __forceinline__ void warp_top(const LogprobsArgs& a, int64_t r, const
     }
 }
 
-template <typename T, bool kMask, bool kTop>
+// Rows of up to kRankColumns columns: every column's rank is the number of larger keys.
+constexpr int kRankColumns = 256;
+template <typename T, bool kMask>
+__device__ __forceinline__ void warp_rank(const LogprobsArgs& a, int64_t r, const PiecedRow<T>& row, uint64_t* keys, const RowStats& st) {
+    const int lane = threadIdx.x & 31, n = row.n, even = (n + 1) & ~1;
+    int active = 0;
+    for (int j = lane; j < even; j += 32) {
+        const uint64_t key = row.template key<kMask>(j);  // 0 behind the end
+        keys[j] = key;
+        active += key != 0;
+    }
+    active = __reduce_add_sync(0xffffffffu, active);
+    __syncwarp();
+    for (int j = lane; j < n; j += 32) {
+        const uint64_t mine = keys[j];
+        if (mine == 0) continue;
+        int rank = 0;
+#pragma unroll 4
+        for (int i = 0; i < even; i += 2) {
+            const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(keys + i);
+            rank += (k.x > mine) + (k.y > mine);
+        }
+        if (rank < a.k) write_top(a, r, rank, mine, st);
+    }
+    for (int i = active + lane; i < a.k; i += 32) write_top(a, r, i, 0, st);
+}
+
+// kTop: 0 none, 1 one after another, 2 by ranks.
+template <typename T, bool kMask, int kTop>
 __global__ void __launch_bounds__(256) logprobs_warp_kernel(const LogprobsArgs a) {
+    __shared__ alignas(16) uint64_t keys[kTop == 2 ? 8 * kRankColumns : 2];
     const int lane = threadIdx.x & 31;
     const int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     if (r >= a.rows) return;
@@ -493,10 +522,11 @@ __global__ void __launch_bounds__(256) logprobs_warp_kernel(const LogprobsArgs a
     const PiecedRow<T> row(x, mask, a.n, x);
     const Ahead ahead(a, r, x, mask, lane);
     int32_t best = 0;
-    const Running mine = scan_row<T, kMask, kTop>(row, lane, row.pieces, 32, a.c, &best, nullptr, 0, 0);
+    const Running mine = scan_row<T, kMask, kTop == 1>(row, lane, row.pieces, 32, a.c, &best, nullptr, 0, 0);
     const RowStats st(reduce_warp<32>(mine, a.c));
     write_row(a, r, x, mask, st, ahead, lane, 32);
-    if constexpr (kTop) warp_top<T, kMask>(a, r, row, mine.m, best, st);
+    if constexpr (kTop == 1) warp_top<T, kMask>(a, r, row, mine.m, best, st);
+    if constexpr (kTop == 2) warp_rank<T, kMask>(a, r, row, keys + (threadIdx.x >> 5) * kRankColumns, st);
 }
 
 // ---------------------------------------------------------------- long rows: a block, or a cluster of blocks

@@ -777,9 +777,7 @@ def _logprobs_rows(logits: torch.Tensor, targets: Optional[torch.Tensor], mask: 
             targets = targets.contiguous()
     ld_mask = 0
     if mask is not None:
-        if mask.dtype is torch.bool:
-            mask = mask.view(torch.uint8)
-        if mask.dtype is not torch.uint8:
+        if mask.dtype is not torch.bool and mask.dtype is not torch.uint8:
             raise TypeError(f"mask must be bool or uint8, got {mask.dtype}")
         if mask.get_device() != index:
             raise ValueError("mask must be on logits' device")
@@ -865,7 +863,12 @@ def logprobs_bwd(logits: torch.Tensor, targets: Optional[torch.Tensor], mask: Op
             raise ValueError("grad_top needs the int32 top_idx of the forward")
         grad_top = _grad(grad_top, "grad_top", top_idx.shape, index)
         top_idx, k = top_idx.contiguous(), top_idx.shape[-1]
-    out = torch.empty(shape, dtype=logits.dtype, device=dev) if out is None else _given(out, "out", shape, logits.dtype, dev)
+    if out is not None:
+        out = _given(out, "out", shape, logits.dtype, dev)
+    elif logits.is_contiguous():
+        out = torch.empty_like(logits)  # half the time of torch.empty
+    else:
+        out = torch.empty(shape, dtype=logits.dtype, device=dev)
     rc = _native.lib().maxsim_logprobs_bwd(logits.data_ptr(), dt, rows, n, ld, _ptr(targets), T, _ptr(mask), ld_mask, scale,
                                            stats.data_ptr(), entropy.data_ptr(), _ptr(grad_logprob), _ptr(grad_entropy),
                                            _ptr(top_idx), _ptr(grad_top), k, out.data_ptr(), n, _raw_stream(index))
