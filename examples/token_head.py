@@ -5,7 +5,9 @@ embedding's width, L2 normalisation, MaxSim scores of every (query, document)
 pair, an in-batch contrastive loss, its gradient.
 Serving: the same head in 8-bit integers. Weights are quantised per channel
 once, hidden states per token; the INT8 product gives the embeddings, whose
-quantised unit rows are what the INT8 scoring and the top-k take.
+quantised unit rows are what the INT8 scoring and the top-k take. Or in 4 bits:
+weights and hidden states in 4-bit floating point, the index stored in 4 bits a
+value and read back for the scoring, the answer as probabilities.
 
     python examples/token_head.py
 """
@@ -56,6 +58,29 @@ class TokenHead:
         embeddings = ms.linear_int8(x, x_scale, *head, out_dtype=torch.float16)
         return ms.quantize_rows(embeddings, normalize=True)
 
+    def quantized4(self):
+        """The head in 4-bit floating point: codes, block scales, row scales."""
+        return ms.quantize_rows_fp4(self.weight.detach())
+
+    @staticmethod
+    def embed4(hidden, head):
+        """Unit token embeddings [..., dim] in bf16 through the 4-bit head."""
+        y = ms.linear_fp4(*ms.quantize_rows_fp4(hidden), *head, out_dtype=torch.bfloat16)
+        return torch.nn.functional.normalize(y.float(), dim=-1).to(torch.bfloat16)
+
+    @staticmethod
+    def index4(hidden, head):
+        """Unit token embeddings stored in 4 bits, with a scale for every 32 values."""
+        return ms.quantize_rows_fp4(TokenHead.embed4(hidden, head), block=32)
+
+
+def answer(q_hidden, index, head, given, k, temperature=0.1):
+    """Among the documents of a 4-bit index: the log probability of each query's given one, the entropy, and the k
+    likeliest with theirs."""
+    q, d = TokenHead.embed4(q_hidden, head), ms.dequantize_rows_fp4(*index, block=32, out_dtype=torch.bfloat16)
+    scores, _ = ms.maxsim_fwd(q, d)
+    return ms.logprobs_fwd(scores, given, scale=1 / (q.shape[1] * temperature), k=k)[:4]
+
 
 def search(q_hidden, index, head, k):
     """The k best documents of each query by INT8 MaxSim: (scores, indices)."""
@@ -82,6 +107,10 @@ def main(n=64, lq=32, ld=180, hidden=1024, dim=128, steps=20):
     _, best = search(q, TokenHead.index(d, served), served, k=5)
     hit = (best[:, 0].cpu() == torch.arange(n)).float().mean().item()
     print(f"own document first for {hit:.0%} of the queries")
+    head4 = head.quantized4()
+    logprob, entropy, best, _ = answer(q, TokenHead.index4(d, head4), head4, torch.arange(n, device=q.device), k=5)
+    print(f"in 4 bits: own document first for {(best[:, 0].cpu() == torch.arange(n)).float().mean().item():.0%}, "
+          f"its log probability {logprob.mean().item():.3f}, entropy {entropy.mean().item():.3f}")
     return losses, hit
 
 
