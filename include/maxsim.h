@@ -473,7 +473,8 @@ maxsim_status maxsim_dequantize_rows_fp4(const uint8_t *q, int64_t ld_q, const u
  * 0 and add nothing). The sum over k is accumulated in fp32, the scales and the
  * bias are applied in fp32 and the result is rounded once. The same call on
  * the same inputs gives the same bits. A NaN scale gives NaN in the outputs of
- * its row or column. 0 <= M, N, K < 2^31 - 1023. No workspace.
+ * its row or column. 0 <= M, N < 2^31 - 1023, K <= 2^28, row strides below 2^40.
+ * No workspace.
  */
 maxsim_status maxsim_linear_fp4(const uint8_t *x, int64_t ld_x, const uint8_t *x_block_scale, const float *x_scale,
                                 const uint8_t *w, int64_t ld_w, const uint8_t *w_block_scale, const float *w_scale,

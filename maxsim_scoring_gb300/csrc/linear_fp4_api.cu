@@ -16,6 +16,8 @@ extern template maxsim_status run_linear_fp4<float>(const LinearFp4Plan&, const 
 namespace {
 
 constexpr int64_t kMaxRows = kI32Max - 1023;  // a tile past the last row still has 32-bit coordinates
+constexpr int64_t kMaxK = int64_t(1) << 28;   // a tile's sums (a million stages) take well below the limit of a wait
+constexpr int64_t kMaxStride = int64_t(1) << 40;  // of a TMA descriptor
 
 constexpr int64_t kPairs = 76;                // CTA pairs of a GB300 (152 SMs): plans do not depend on the device
 
@@ -66,7 +68,8 @@ maxsim_status maxsim_linear_fp4(const uint8_t* x, int64_t ld_x, const uint8_t* x
                                 void* out, int64_t ld_out, void* stream) {
     if (!any_dtype(out_dtype) || M < 0 || N < 0 || K < 0 || (block != 16 && block != 32)) return MAXSIM_ERR_INVALID_ARG;
     if (K % 32 != 0 || !rows_fit(M, K / 2, ld_x) || !rows_fit(N, K / 2, ld_w) || !rows_fit(M, N, ld_out)) return MAXSIM_ERR_INVALID_ARG;
-    if (M > kMaxRows || N > kMaxRows || K > kI32Max - 1023) return MAXSIM_ERR_UNSUPPORTED;
+    if (M > kMaxRows || N > kMaxRows || K > kMaxK) return MAXSIM_ERR_UNSUPPORTED;
+    if ((M > 1 && ld_x >= kMaxStride) || (N > 1 && ld_w >= kMaxStride)) return MAXSIM_ERR_UNSUPPORTED;
     if ((M > 1 && ld_x % 16 != 0) || (N > 1 && ld_w % 16 != 0)) return MAXSIM_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return MAXSIM_OK;
     if (!out || !ptr_aligned(out, elem_bytes(out_dtype)) || !ptr_aligned(x_scale, 4) || !ptr_aligned(w_scale, 4) || !ptr_aligned(bias, 4))

@@ -113,6 +113,7 @@ def test_linear_host_validation(lib):
     assert linear(dt=7) == 1 and linear(block=0) == 1 and linear(M=-1) == 1 and linear(N=-1) == 1 and linear(K=-32) == 1
     assert linear(K=48) == 1 and linear(ld_x=16) == 1 and linear(ld_w=40) == 1 and linear(ld_out=7) == 1
     assert linear(M=1 << 31) == 2 and linear(K=1 << 31, ld_x=1 << 31, ld_w=1 << 31) == 2
+    assert linear(K=(1 << 28) + 32, ld_x=1 << 28, ld_w=1 << 28) == 2 and linear(ld_x=1 << 40) == 2 and linear(ld_w=1 << 40) == 2
     assert linear(x=None) == 1 and linear(w=None) == 1 and linear(xb=None) == 1 and linear(wb=None) == 1 and linear(out=None) == 1
     assert linear(x=FAKE + 8) == 1 and linear(w=FAKE + 1) == 1 and linear(xb=FAKE + 8) == 1 and linear(wb=FAKE + 4) == 1
     assert linear(xs=FAKE + 2) == 1 and linear(ws=FAKE + 2) == 1 and linear(bias=FAKE + 2) == 1 and linear(out=FAKE + 1) == 1

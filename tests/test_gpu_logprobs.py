@@ -198,6 +198,42 @@ def test_autograd_against_differences():
         torch.autograd.grad(g.sum(), x)
 
 
+def test_autograd_outputs_that_are_left_out():
+    x, t, _ = make(8, 6, 70, "bf16", 1)
+    x = x.clone().requires_grad_()
+    logprob, entropy, top_idx, top = ms.logprobs(x, None)
+    assert logprob is None and top_idx is None and top is None and entropy.requires_grad
+    (dx,) = torch.autograd.grad(entropy.sum(), x)
+    ref = ms.logprobs_fwd(x.detach(), None)
+    assert torch.equal(dx, ms.logprobs_bwd(x.detach(), None, None, ref[4], ref[1], grad_entropy=torch.ones(6, device="cuda")))
+    logprob, entropy, top_idx, top = ms.logprobs(x, t[:, 0], k=2)
+    assert not top_idx.requires_grad
+    (dx,) = torch.autograd.grad(top.sum(), x)
+    ref = ms.logprobs_fwd(x.detach(), t[:, 0], k=2)
+    assert torch.equal(dx, ms.logprobs_bwd(x.detach(), t[:, 0], None, ref[4], ref[1], top_idx=ref[2], grad_top=torch.ones(6, 2, device="cuda")))
+    assert ms.logprobs(x.detach(), t[:, 0])[0].requires_grad is False
+
+
+def test_two_streams_at_once():
+    """Calls of all operators on two streams, each with its own data, interleaved."""
+    data = [make(s, 300, 9000, "bf16", 1)[:2] for s in (1, 2)]
+    want = [ms.logprobs_fwd(x, t, k=7) for x, t in data]
+    rows = [torch.randn(700, 512, device="cuda") for _ in data]
+    w = ms.quantize_rows_fp4(torch.randn(300, 512, device="cuda"))
+    prod = [ms.linear_fp4(*ms.quantize_rows_fp4(r), *w) for r in rows]
+    streams = [torch.cuda.Stream() for _ in data]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append((ms.logprobs_fwd(*data[i], k=7), ms.linear_fp4(*ms.quantize_rows_fp4(rows[i]), *w)))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        for out, y in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(out, want[i])) and torch.equal(y, prod[i])
+
+
 def test_contrastive_step_through_the_scores():
     """MaxSim scores, the given document's log probability, the gradient back to the token embeddings."""
     g = torch.Generator().manual_seed(11)
