@@ -86,16 +86,16 @@ template <typename T, bool kMask>
 maxsim_status launch_bwd(const LogprobsBwdArgs& a, const HostDevice& dev, cudaStream_t st) {
     // a row off its 16-byte boundary touches one piece more
     const int64_t pieces = (a.n * static_cast<int64_t>(sizeof(T)) + 15) / 16 + 1;
+    const bool same = ((reinterpret_cast<uintptr_t>(a.x) - reinterpret_cast<uintptr_t>(a.dx)) & 15) == 0 &&
+                      (a.rows == 1 || (a.ld - a.ld_dx) * static_cast<int64_t>(sizeof(T)) % 16 == 0);
     // A warp's run: long ones read the row's numbers less often, but every SM wants warps.
-    const int64_t least = 32 * BwdCfg<kMask>::kPieces;
+    const int64_t least = 32 * BwdCfg::kPieces;
     int64_t run = 12 * least;
     while (run > least && a.rows * ((pieces + run - 1) / run) < int64_t(dev.num_sms) * 64) run /= 2;
     run = (run + least - 1) / least * least;
     const int64_t runs = (pieces + run - 1) / run, items = a.rows * runs;
     if ((items + 7) / 8 > kI32Max) return MAXSIM_ERR_UNSUPPORTED;
     const unsigned grid = static_cast<unsigned>((items + 7) / 8);
-    const bool same = ((reinterpret_cast<uintptr_t>(a.x) - reinterpret_cast<uintptr_t>(a.dx)) & 15) == 0 &&
-                      (a.rows == 1 || (a.ld - a.ld_dx) * static_cast<int64_t>(sizeof(T)) % 16 == 0);
     if (same) logprobs_bwd_kernel<T, kMask, false><<<grid, 256, 0, st>>>(a, static_cast<int32_t>(run), runs, items);
     else logprobs_bwd_kernel<T, kMask, true><<<grid, 256, 0, st>>>(a, static_cast<int32_t>(run), runs, items);
     return launched();

@@ -130,44 +130,47 @@ struct PiecedRow {
     const T* x;
     const uint8_t* mask;
     int32_t n, skip, pieces;
+    uint32_t x_by, mask_by;  // bytes that pieces of x, and of the mask, begin behind a 16- and a kVec-byte boundary
 
     // `place`: pieces are those of the row that starts here (a multiple of T's size)
     __device__ __forceinline__ PiecedRow(const T* row, const uint8_t* m, int64_t cols, const T* place)
         : x(row), mask(m), n(static_cast<int32_t>(cols)) {
         skip = static_cast<int32_t>(reinterpret_cast<uintptr_t>(place) / sizeof(T)) & (kVec - 1);
         pieces = static_cast<int32_t>((cols + skip + kVec - 1) / kVec);
+        x_by = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) - skip * sizeof(T)) & 15u;
+        mask_by = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(m) - skip) & (kVec - 1);
     }
+    // pieces around p are the row's too: the aligned pieces and mask words that hold p may be read
+    __device__ __forceinline__ bool interior(int32_t p) const { return column(p) >= kVec && column(p) + 2 * kVec <= n; }
     __device__ __forceinline__ int32_t column(int32_t p) const { return p * kVec - skip; }
     __device__ __forceinline__ bool whole(int32_t p) const { return column(p) >= 0 && column(p) + kVec <= n; }
     // whole piece p
     __device__ __forceinline__ uint4 load_whole(int32_t p) const { return __ldg(reinterpret_cast<const uint4*>(x + column(p))); }
-    // piece p; what is not the row's is minus infinity. kShift: x's phase is not `place`'s.
-    template <bool kShift = false>
+    // An interior piece of rows of another phase: the two aligned pieces that hold it, and it from them.
+    __device__ __forceinline__ void load_around(int32_t p, uint4& lo, uint4& hi) const {
+        const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(x + column(p)) & ~uintptr_t(15));
+        lo = __ldg(q);
+        hi = __ldg(q + 1);
+    }
+    __device__ __forceinline__ uint4 shifted(const uint4& lo, const uint4& hi) const {
+        uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        if (x_by & 8u) {
+#pragma unroll
+            for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+        }
+        if (x_by & 4u) {
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+        }
+        const uint32_t bits = (x_by & 3u) * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], bits);
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // Piece p, element by element where it is not whole or x has another phase; what is not the row's is minus infinity.
     __device__ __forceinline__ uint4 load(int32_t p) const {
         const int32_t at = column(p);
-        if constexpr (kShift) {
-            if (at >= kVec && at + 2 * kVec <= n) {  // the two aligned pieces that hold it are the row's
-                const uintptr_t from = reinterpret_cast<uintptr_t>(x + at);
-                const uint4 lo = __ldg(reinterpret_cast<const uint4*>(from & ~uintptr_t(15)));
-                const uint4 hi = __ldg(reinterpret_cast<const uint4*>((from & ~uintptr_t(15)) + 16));
-                uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-                const uint32_t by = static_cast<uint32_t>(from) & 15u;
-                if (by & 8u) {
-#pragma unroll
-                    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-                }
-                if (by & 4u) {
-#pragma unroll
-                    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-                }
-                const uint32_t bits = (by & 3u) * 8;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], bits);
-                return make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        } else {
-            if (at >= 0 && at + kVec <= n) return load_whole(p);
-        }
+        if (at >= 0 && at + kVec <= n && x_by == 0) return load_whole(p);
         T e[kVec];  // all loads before the first use
 #pragma unroll
         for (int i = 0; i < kVec; ++i) e[i] = x[min(max(at + i, 0), n - 1)];
@@ -176,30 +179,36 @@ struct PiecedRow {
         for (int i = 0; i < kVec; ++i) o[i] = at + i >= 0 && at + i < n ? e[i] : from_f32<T>(minus_inf());
         return *reinterpret_cast<const uint4*>(o);
     }
-    // the mask's bytes of piece p, a high bit for each active column
+    // The words that hold an interior piece's mask bytes, and from them a high bit for each active column.
+    struct MaskWords {
+        uint32_t v[kVec / 4 + 1];
+    };
+    __device__ __forceinline__ void load_mask(int32_t p, MaskWords& w) const {
+        const uint8_t* from = mask + column(p);
+        if (mask_by == 0) {
+            if constexpr (kVec == 8) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2*>(from));
+                w.v[0] = v.x;
+                w.v[1] = v.y;
+            } else {
+                w.v[0] = __ldg(reinterpret_cast<const uint32_t*>(from));
+            }
+            w.v[kVec / 4] = 0;
+        } else {
+            const uint32_t* q = reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(from) & ~uintptr_t(3));
+#pragma unroll
+            for (int i = 0; i <= kVec / 4; ++i) w.v[i] = __ldg(q + i);
+        }
+    }
+    __device__ __forceinline__ uint4 masked(const uint4& u, const MaskWords& w) const {
+        uint32_t m[kVec / 4];
+#pragma unroll
+        for (int i = 0; i < kVec / 4; ++i) m[i] = nonzero_bytes(__funnelshift_r(w.v[i], w.v[i + 1], (mask_by & 3u) * 8));
+        return P::masked(u, m);
+    }
+    // a high bit for each active column of any piece
     __device__ __forceinline__ void active(int32_t p, uint32_t (&m)[kVec / 4]) const {
         const int32_t at = column(p);
-        if (at >= 4 && at + kVec + 4 <= n) {  // the words that hold them are the mask's own
-            const uintptr_t from = reinterpret_cast<uintptr_t>(mask + at);
-            if ((from & (kVec - 1)) == 0) {
-                if constexpr (kVec == 8) {
-                    const uint2 v = __ldg(reinterpret_cast<const uint2*>(from));
-                    m[0] = nonzero_bytes(v.x);
-                    m[1] = nonzero_bytes(v.y);
-                } else {
-                    m[0] = nonzero_bytes(__ldg(reinterpret_cast<const uint32_t*>(from)));
-                }
-                return;
-            }
-            const uint32_t* w = reinterpret_cast<const uint32_t*>(from & ~uintptr_t(3));
-            const uint32_t bits = (static_cast<uint32_t>(from) & 3u) * 8;
-            uint32_t v[kVec / 4 + 1];
-#pragma unroll
-            for (int i = 0; i <= kVec / 4; ++i) v[i] = __ldg(w + i);
-#pragma unroll
-            for (int i = 0; i < kVec / 4; ++i) m[i] = nonzero_bytes(__funnelshift_r(v[i], v[i + 1], bits));
-            return;
-        }
 #pragma unroll
         for (int j = 0; j < kVec / 4; ++j) {
             uint8_t b[4];
@@ -214,6 +223,11 @@ struct PiecedRow {
     template <bool kMask>
     __device__ __forceinline__ uint4 keep_active(uint4 u, int32_t p) const {
         if constexpr (kMask) {
+            if (interior(p)) {
+                MaskWords w;
+                load_mask(p, w);
+                return masked(u, w);
+            }
             uint32_t m[kVec / 4];
             active(p, m);
             u = P::masked(u, m);
@@ -274,7 +288,7 @@ constexpr int kTopSlots = 8;       // parts of a thread's share whose maxima are
 // *best, and the maxima of up to kTopSlots runs of `slot` batches to slots[i *
 // threads]. Loads of one batch are in flight together, and other warps' beside them:
 // registers for a second batch cost more warps than they bring.
-template <typename T, bool kMask, bool kTop>
+template <typename T, bool kMask, bool kTop, bool kShort>
 __device__ __forceinline__ Running scan_row(const PiecedRow<T>& row, int32_t first, int32_t last, int32_t step, float c, int32_t* best,
                                             float* slots, int32_t slot, int32_t threads) {
     using P = PieceOf<T>;
@@ -286,11 +300,30 @@ __device__ __forceinline__ Running scan_row(const PiecedRow<T>& row, int32_t fir
     int32_t left = slot;
     for (int32_t p = first; p < last; p += step * kLogprobsBatch) {
         uint4 u[kLogprobsBatch];
-        if (row.whole(p) && p + 3 * step < last && row.whole(p + 3 * step)) {
+        const bool inside = p + 3 * step < last && (kMask ? row.interior(p) && row.interior(p + 3 * step) : row.whole(p) && row.whole(p + 3 * step));
+        if (inside && !(kMask && kShort)) {
 #pragma unroll
             for (int j = 0; j < kLogprobsBatch; ++j) u[j] = row.load_whole(p + j * step);
+            if constexpr (kMask) {  // all loads before the first use
+                typename PiecedRow<T>::MaskWords words[kLogprobsBatch];
 #pragma unroll
-            for (int j = 0; j < kLogprobsBatch; ++j) u[j] = row.template keep_active<kMask>(u[j], p + j * step);
+                for (int j = 0; j < kLogprobsBatch; ++j) row.load_mask(p + j * step, words[j]);
+#pragma unroll
+                for (int j = 0; j < kLogprobsBatch; ++j) u[j] = row.masked(u[j], words[j]);
+            }
+        } else if constexpr (kMask && kShort) {  // each piece for itself: a row's ends are a good part of its batches
+            typename PiecedRow<T>::MaskWords words[kLogprobsBatch];
+            bool in[kLogprobsBatch];
+#pragma unroll
+            for (int j = 0; j < kLogprobsBatch; ++j) {
+                in[j] = p + j * step < last && row.interior(p + j * step);
+                if (!in[j]) continue;
+                u[j] = row.load_whole(p + j * step);
+                row.load_mask(p + j * step, words[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < kLogprobsBatch; ++j)
+                u[j] = in[j] ? row.masked(u[j], words[j]) : p + j * step < last ? row.template get<true>(p + j * step) : none;
         } else {
 #pragma unroll
             for (int j = 0; j < kLogprobsBatch; ++j) u[j] = p + j * step < last ? row.template get<kMask>(p + j * step) : none;
@@ -522,7 +555,7 @@ __global__ void __launch_bounds__(256) logprobs_warp_kernel(const LogprobsArgs a
     const PiecedRow<T> row(x, mask, a.n, x);
     const Ahead ahead(a, r, x, mask, lane);
     int32_t best = 0;
-    const Running mine = scan_row<T, kMask, kTop == 1>(row, lane, row.pieces, 32, a.c, &best, nullptr, 0, 0);
+    const Running mine = scan_row<T, kMask, kTop == 1, true>(row, lane, row.pieces, 32, a.c, &best, nullptr, 0, 0);
     const RowStats st(reduce_warp<32>(mine, a.c));
     write_row(a, r, x, mask, st, ahead, lane, 32);
     if constexpr (kTop == 1) warp_top<T, kMask>(a, r, row, mine.m, best, st);
@@ -738,9 +771,10 @@ __device__ __noinline__ void block_top(TopShared<kThreads>* sh, const PiecedRow<
     }
 }
 
-// kThreads threads of each of a cluster's blocks share a row.
+// kThreads threads of each of a cluster's blocks share a row. 56 registers, nine
+// blocks of 128 threads an SM: 4096 x 131072 bf16 in 155 us, 6.9 TB/s (with eight 167).
 template <typename T, bool kMask, bool kTop, int kThreads>
-__global__ void __launch_bounds__(kThreads, (kMask ? 5 : 4) * 256 / kThreads) logprobs_block_kernel(const LogprobsArgs a, int blocks) {
+__global__ void __launch_bounds__(kThreads, kThreads == 128 ? 9 : 4) logprobs_block_kernel(const LogprobsArgs a, int blocks) {
     __shared__ float part[kThreads / 32][3];
     __shared__ float gathered[16][3];
     extern __shared__ uint64_t all_best[];  // kTop, blocks > 1: [blocks, k]
@@ -758,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, (kMask ? 5 : 4) * 256 / kThreads) lo
     int32_t best = 0;
     const int32_t per_thread = (share + kThreads * kLogprobsBatch - 1) / (kThreads * kLogprobsBatch);  // batches
     const int32_t slot = max(1, (per_thread + kTopSlots - 1) / kTopSlots);
-    const Running mine = scan_row<T, kMask, kTop>(row, p0 + threadIdx.x, p1, kThreads, a.c, &best, kTop ? top.slots + threadIdx.x : nullptr,
+    const Running mine = scan_row<T, kMask, kTop, false>(row, p0 + threadIdx.x, p1, kThreads, a.c, &best, kTop ? top.slots + threadIdx.x : nullptr,
                                                   slot, kThreads);
     const Running sum = reduce_warp<32>(mine, a.c);
     if (lane == 0) {
@@ -853,11 +887,12 @@ __device__ __forceinline__ int32_t given_column(const LogprobsBwdArgs& a, int64_
 // B = -scale * g_entropy * ln 2, G = the sum of all that was given.
 
 // Pieces of a lane in flight, and blocks of 256 threads an SM holds at least.
-// Registers decide (4096 x 131072 bf16 by pieces and blocks: 4, 3: 370 us; 3, 4:
-// 324; 2, 5: 325; 8192 x 32768 with a mask for each row: 513; 327; 286).
-template <bool kMask>
+// Registers decide. Plain rows have the next pieces in flight while some are worked
+// on (4096 x 131072 bf16 by pieces and blocks: 4, 3: 370 us; 3, 4: 324; 2, 5: 325).
+// Masked rows and rows of another phase load a batch at a time (8192 x 32768 bf16 with a
+// mask for each row: 4, 4: 223 us; 2, 5: 234; 3, 4: 215; 4, 3: 225).
 struct BwdCfg {
-    static constexpr int kPieces = kMask ? 2 : 3, kBlocks = kMask ? 5 : 4;
+    static constexpr int kPieces = 3, kBlocks = 4;
 };
 
 // Calls f(column, gradient) in every lane for the given columns from c0 to c1,
@@ -881,9 +916,10 @@ __device__ __forceinline__ void each_given(const LogprobsBwdArgs& a, int64_t r, 
 // another phase, and its pieces are joined from the two aligned ones that hold
 // them. Bound by HBM.
 template <typename T, bool kMask, bool kShift>
-__global__ void __launch_bounds__(256, BwdCfg<kMask>::kBlocks) logprobs_bwd_kernel(const LogprobsBwdArgs a, int32_t run, int64_t runs, int64_t items) {
+__global__ void __launch_bounds__(256, BwdCfg::kBlocks) logprobs_bwd_kernel(const LogprobsBwdArgs a, int32_t run, int64_t runs, int64_t items) {
     using P = PieceOf<T>;
-    constexpr int kVec = P::kVec, kBwdPieces = BwdCfg<kMask>::kPieces;
+    constexpr int kVec = P::kVec, kBwdPieces = BwdCfg::kPieces;
+    constexpr bool kPlain = !kMask && !kShift;
     const int lane = threadIdx.x & 31;
     const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     if (item >= items) return;
@@ -915,27 +951,45 @@ __global__ void __launch_bounds__(256, BwdCfg<kMask>::kBlocks) logprobs_bwd_kern
     // whole pieces
     const int32_t w0 = max(first, row.skip ? 1 : 0), w1 = min(last, (row.n + row.skip) / kVec);
     const uint4 none = make_uint4(P::kMinusInf, P::kMinusInf, P::kMinusInf, P::kMinusInf);
-    uint4 next[kBwdPieces];
+    uint4 next[kPlain ? kBwdPieces : 1];
     auto fetch = [&](int32_t p0) {
 #pragma unroll
         for (int i = 0; i < kBwdPieces; ++i) {
             const int32_t p = p0 + i * 32 + lane;
-            next[i] = p < w1 ? kShift ? row.template load<true>(p) : row.load_whole(p) : none;
+            next[kPlain ? i : 0] = p < w1 ? row.load_whole(p) : none;
         }
-        if constexpr (kMask) {
+    };
+    if constexpr (kPlain) fetch(w0);
+    for (int32_t p0 = w0; p0 < w1; p0 += 32 * kBwdPieces) {
+        uint4 u[kBwdPieces];
+        if constexpr (kPlain) {
+#pragma unroll
+            for (int i = 0; i < kBwdPieces; ++i) u[i] = next[i];
+            fetch(p0 + 32 * kBwdPieces);
+        } else {  // all loads before the first use
+            uint4 hi[kShift ? kBwdPieces : 1];
+            typename PiecedRow<T>::MaskWords words[kMask ? kBwdPieces : 1];
+            bool in[kBwdPieces];
 #pragma unroll
             for (int i = 0; i < kBwdPieces; ++i) {
                 const int32_t p = p0 + i * 32 + lane;
-                if (p < w1) next[i] = row.template keep_active<true>(next[i], p);
+                in[i] = p < w1 && row.interior(p);
+                if (!in[i]) continue;
+                if constexpr (kShift) row.load_around(p, u[i], hi[i]);
+                else u[i] = row.load_whole(p);
+                if constexpr (kMask) row.load_mask(p, words[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < kBwdPieces; ++i) {
+                const int32_t p = p0 + i * 32 + lane;
+                if (in[i]) {
+                    if constexpr (kShift) u[i] = row.shifted(u[i], hi[i]);
+                    if constexpr (kMask) u[i] = row.masked(u[i], words[i]);
+                } else {
+                    u[i] = p < w1 ? row.template get<kMask>(p) : none;
+                }
             }
         }
-    };
-    fetch(w0);
-    for (int32_t p0 = w0; p0 < w1; p0 += 32 * kBwdPieces) {
-        uint4 u[kBwdPieces];
-#pragma unroll
-        for (int i = 0; i < kBwdPieces; ++i) u[i] = next[i];
-        fetch(p0 + 32 * kBwdPieces);
         // exponents of minus infinity, as in add_piece
         uint32_t least = P::min_words(u[0]);
 #pragma unroll
