@@ -20,6 +20,7 @@ from . import _native
 
 _DT = {torch.float16: _native.F16, torch.bfloat16: _native.BF16}
 _DT_ANY = {**_DT, torch.float32: _native.F32}
+_U8 = torch.uint8
 
 
 _SIZE_MAX = ctypes.c_size_t(-1).value
@@ -630,32 +631,44 @@ def dropout_bwd(grad: torch.Tensor, p: float, seed: int, offset: int = 0, *,
 
 
 def _fp4_rows(q: torch.Tensor, block_scale: torch.Tensor, scale: Optional[torch.Tensor], name: str, block: int, index: int):
-    """(q, rows, row stride in bytes, block_scale, scale pointer, tensors to keep) of 4-bit rows, checked."""
-    if block not in (16, 32):
+    """(pointer, rows, row stride in bytes, block scales' pointer, row scales' pointer, the tensors) of 4-bit rows, checked."""
+    if block != 16 and block != 32:
         raise ValueError("block must be 16 or 32")
-    if q.dtype is not torch.uint8 or block_scale.dtype is not torch.uint8:
+    if q.dtype is not _U8 or block_scale.dtype is not _U8:
         raise TypeError(f"{name} and its block scales must be uint8")
-    if q.get_device() != index or block_scale.get_device() != index or (scale is not None and scale.get_device() != index):
+    if q.get_device() != index or block_scale.get_device() != index:
         raise ValueError(f"{name} and its scales must be on one device with the other operands")
     shape = q.shape
-    if not shape or shape[-1] % 16:
+    if not shape or shape[-1] & 15:
         raise ValueError(f"{name} must have rows of whole 16-byte pieces")
-    q, rows, ld = _rows(q, name)
-    if q.data_ptr() % 16 or (rows > 1 and ld % 16):
-        q, ld = q.clone(memory_format=torch.contiguous_format), shape[-1]
-    words = (shape[-1] * 2 + 4 * block - 1) // (4 * block)
-    if block_scale.shape != ((rows + 127) // 128, words, 32, 4, 4):
-        raise ValueError(f"{name}'s block scales must be {((rows + 127) // 128, words, 32, 4, 4)}, got {tuple(block_scale.shape)}")
-    if not block_scale.is_contiguous() or block_scale.data_ptr() % 16:
+    width = shape[-1]
+    if width and q.is_contiguous():
+        rows, ld = q.numel() // width, width
+    else:
+        q, rows, ld = _rows(q, name)
+    ptr = q.data_ptr()
+    if ptr & 15 or (ld & 15 and rows > 1):
+        q, ld = q.clone(memory_format=torch.contiguous_format), width
+        ptr = q.data_ptr()
+    tiles = ((rows + 127) >> 7, (2 * width + 4 * block - 1) // (4 * block), 32, 4, 4)
+    if block_scale.shape != tiles:
+        raise ValueError(f"{name}'s block scales must be {tiles}, got {tuple(block_scale.shape)}")
+    p_block = block_scale.data_ptr()
+    if p_block & 15 or not block_scale.is_contiguous():
         block_scale = block_scale.clone(memory_format=torch.contiguous_format)
+        p_block = block_scale.data_ptr()
+    p_scale = None
     if scale is not None:
         if scale.dtype is not torch.float32:
             raise TypeError(f"{name}'s row scales must be float32")
+        if scale.get_device() != index:
+            raise ValueError(f"{name} and its scales must be on one device with the other operands")
         if scale.shape != shape[:-1]:
             raise ValueError(f"{name}'s row scales must have its leading shape")
         if not scale.is_contiguous():
             scale = scale.contiguous()
-    return q, rows, ld, block_scale, scale
+        p_scale = scale.data_ptr()
+    return ptr, rows, ld, p_block, p_scale, (q, block_scale, scale)
 
 
 def quantize_rows_fp4(x: torch.Tensor, *, block: int = 16, q: Optional[torch.Tensor] = None,
@@ -705,15 +718,15 @@ def dequantize_rows_fp4(q: torch.Tensor, block_scale: torch.Tensor, scale: Optio
     index, shape, dev = _device(q, "q"), q.shape, q.device
     if index != _current_device():
         return _with_device(index, dequantize_rows_fp4, q, block_scale, scale, block=block, cols=cols, out_dtype=out_dtype, out=out)
-    q, rows, ld, block_scale, scale = _fp4_rows(q, block_scale, scale, "q", block, index)
+    pq, rows, ld, p_block, p_scale, _kept = _fp4_rows(q, block_scale, scale, "q", block, index)
     if cols is None:
         cols = 2 * shape[-1]
     if not 0 <= cols <= 2 * shape[-1] or (cols + 31) // 32 * 16 != shape[-1]:
         raise ValueError(f"rows of {shape[-1]} bytes do not hold {cols} columns")
     full = (*shape[:-1], cols)
     out = torch.empty(full, dtype=out_dtype, device=dev) if out is None else _given(out, "out", full, out_dtype, dev)
-    rc = _native.lib().maxsim_dequantize_rows_fp4(q.data_ptr(), ld, block_scale.data_ptr(), _ptr(scale), rows, cols, block, dt,
-                                                  out.data_ptr(), cols, _raw_stream(index))
+    rc = _native.lib().maxsim_dequantize_rows_fp4(pq, ld, p_block, p_scale, rows, cols, block, dt, out.data_ptr(), cols,
+                                                  _raw_stream(index))
     if rc:
         _native.check(rc, "maxsim_dequantize_rows_fp4")
     return out
@@ -732,11 +745,13 @@ def linear_fp4(x: torch.Tensor, x_block_scale: torch.Tensor, x_scale: Optional[t
     if index != _current_device():
         return _with_device(index, linear_fp4, x, x_block_scale, x_scale, w, w_block_scale, w_scale, bias, block=block,
                             out_dtype=out_dtype, out=out)
-    if w.dim() != 2 or not shape or w.shape[1] != shape[-1]:
+    channels = w.shape
+    if len(channels) != 2 or not shape or channels[1] != shape[-1]:
         raise ValueError("w must be [N, bytes] with x's bytes a row")
-    N = w.shape[0]
-    x, M, ld_x, x_block_scale, x_scale = _fp4_rows(x, x_block_scale, x_scale, "x", block, index)
-    w, _, ld_w, w_block_scale, w_scale = _fp4_rows(w, w_block_scale, w_scale, "w", block, index)
+    N, width = channels
+    px, M, ld_x, px_block, px_scale, _kept_x = _fp4_rows(x, x_block_scale, x_scale, "x", block, index)
+    pw, _, ld_w, pw_block, pw_scale, _kept_w = _fp4_rows(w, w_block_scale, w_scale, "w", block, index)
+    pb = None
     if bias is not None:
         if bias.dtype is not torch.float32:
             raise TypeError("bias must be float32")
@@ -746,10 +761,10 @@ def linear_fp4(x: torch.Tensor, x_block_scale: torch.Tensor, x_scale: Optional[t
             raise ValueError("bias must be [N]")
         if not bias.is_contiguous():
             bias = bias.contiguous()
+        pb = bias.data_ptr()
     full = (*shape[:-1], N)
     out = torch.empty(full, dtype=out_dtype, device=dev) if out is None else _given(out, "out", full, out_dtype, dev)
-    rc = _native.lib().maxsim_linear_fp4(x.data_ptr(), ld_x, x_block_scale.data_ptr(), _ptr(x_scale), w.data_ptr(), ld_w,
-                                         w_block_scale.data_ptr(), _ptr(w_scale), _ptr(bias), M, N, 2 * shape[-1], block, dt,
+    rc = _native.lib().maxsim_linear_fp4(px, ld_x, px_block, px_scale, pw, ld_w, pw_block, pw_scale, pb, M, N, 2 * width, block, dt,
                                          out.data_ptr(), N, _raw_stream(index))
     if rc:
         _native.check(rc, "maxsim_linear_fp4")
@@ -757,41 +772,49 @@ def linear_fp4(x: torch.Tensor, x_block_scale: torch.Tensor, x_scale: Optional[t
 
 
 def _logprobs_rows(logits: torch.Tensor, targets: Optional[torch.Tensor], mask: Optional[torch.Tensor], index: int):
-    """(logits, rows, row stride, targets, T, mask, mask stride) of the log probabilities' operands, checked."""
+    """(pointer, rows, n, row stride, targets' pointer, T, mask's pointer, mask's stride, leading shape, the tensors) of the
+    log probabilities' operands, checked."""
     shape = logits.shape
-    if not shape or not shape[-1]:
+    n = shape[-1] if shape else 0
+    if not n:
         raise ValueError("logits must have at least one column")
     lead = shape[:-1]
-    T = 0
+    T, p_targets = 0, None
     if targets is not None:
-        if targets.dtype is torch.int32:
-            targets = targets.to(torch.int64)
         if targets.dtype is not torch.int64:
-            raise TypeError(f"targets must be int64 or int32, got {targets.dtype}")
+            if targets.dtype is not torch.int32:
+                raise TypeError(f"targets must be int64 or int32, got {targets.dtype}")
+            targets = targets.to(torch.int64)
         if targets.get_device() != index:
             raise ValueError("targets must be on logits' device")
-        if targets.shape != lead and targets.shape[:-1] != lead:
+        given = targets.shape
+        if given == lead:
+            T = 1
+        elif given[:-1] == lead and len(given) > len(lead):
+            T = given[-1]
+        else:
             raise ValueError("targets must have logits' leading shape, with one more dimension for several a row")
-        T = 1 if targets.shape == lead else targets.shape[-1]
         if not targets.is_contiguous():
             targets = targets.contiguous()
-    ld_mask = 0
+        p_targets = targets.data_ptr()
+    ld_mask, p_mask = 0, None
     if mask is not None:
-        if mask.dtype is not torch.bool and mask.dtype is not torch.uint8:
+        if mask.dtype is not torch.bool and mask.dtype is not _U8:
             raise TypeError(f"mask must be bool or uint8, got {mask.dtype}")
         if mask.get_device() != index:
             raise ValueError("mask must be on logits' device")
-        if mask.shape == shape[-1:]:
-            if not mask.is_contiguous():
-                mask = mask.contiguous()
-        elif mask.shape == shape:
+        if mask.shape == shape and len(shape) > 1:
             mask, _, ld_mask = _rows(mask, "mask")
-        else:
+        elif mask.shape != shape[-1:]:
             raise ValueError("mask must have logits' shape, or be [n] for all rows")
-        if len(shape) == 1:
-            ld_mask = 0
-    logits, rows, ld = _rows(logits, "logits")
-    return logits, rows, ld, targets, T, mask, ld_mask
+        elif not mask.is_contiguous():
+            mask = mask.contiguous()
+        p_mask = mask.data_ptr()
+    if logits.is_contiguous():
+        rows, ld = logits.numel() // n, n
+    else:
+        logits, rows, ld = _rows(logits, "logits")
+    return logits.data_ptr(), rows, n, ld, p_targets, T, p_mask, ld_mask, lead, (logits, targets, mask)
 
 
 def logprobs_fwd(logits: torch.Tensor, targets: Optional[torch.Tensor], mask: Optional[torch.Tensor] = None, *,
@@ -806,21 +829,23 @@ def logprobs_fwd(logits: torch.Tensor, targets: Optional[torch.Tensor], mask: Op
     dt = _DT_ANY.get(logits.dtype)
     if dt is None:
         raise TypeError(f"logits must be float16, bfloat16 or float32, got {logits.dtype}")
-    index, shape, dev = _device(logits, "logits"), logits.shape, logits.device
+    index, dev = _device(logits, "logits"), logits.device
     if index != _current_device():
         return _with_device(index, logprobs_fwd, logits, targets, mask, scale=scale, k=k)
-    logits, rows, ld, targets, T, mask, ld_mask = _logprobs_rows(logits, targets, mask, index)
-    lead, n = shape[:-1], shape[-1]
-    logprob = None if targets is None else torch.empty(targets.shape, dtype=torch.float32, device=dev)
-    entropy = torch.empty(lead, dtype=torch.float32, device=dev)
-    stats = torch.empty((*lead, 2), dtype=torch.float32, device=dev)
-    top_idx = top_logprob = None
+    px, rows, n, ld, p_targets, T, p_mask, ld_mask, lead, _kept = _logprobs_rows(logits, targets, mask, index)
+    f32, empty = torch.float32, torch.empty
+    logprob = top_idx = top_logprob = p_logprob = p_idx = p_top = None
+    if targets is not None:
+        logprob = empty(targets.shape, dtype=f32, device=dev)
+        p_logprob = logprob.data_ptr()
+    entropy = empty(lead, dtype=f32, device=dev)
+    stats = empty((*lead, 2), dtype=f32, device=dev)
     if k:
-        top_idx = torch.empty((*lead, k), dtype=torch.int32, device=dev)
-        top_logprob = torch.empty((*lead, k), dtype=torch.float32, device=dev)
-    rc = _native.lib().maxsim_logprobs_fwd(logits.data_ptr(), dt, rows, n, ld, _ptr(targets), T, _ptr(mask), ld_mask, scale, k,
-                                           _ptr(logprob), entropy.data_ptr(), _ptr(top_idx), _ptr(top_logprob),
-                                           stats.data_ptr(), _raw_stream(index))
+        top_idx = empty((*lead, k), dtype=torch.int32, device=dev)
+        top_logprob = empty((*lead, k), dtype=f32, device=dev)
+        p_idx, p_top = top_idx.data_ptr(), top_logprob.data_ptr()
+    rc = _native.lib().maxsim_logprobs_fwd(px, dt, rows, n, ld, p_targets, T, p_mask, ld_mask, scale, k, p_logprob,
+                                           entropy.data_ptr(), p_idx, p_top, stats.data_ptr(), _raw_stream(index))
     if rc:
         _native.check(rc, "maxsim_logprobs_fwd")
     return logprob, entropy, top_idx, top_logprob, stats
@@ -850,8 +875,7 @@ def logprobs_bwd(logits: torch.Tensor, targets: Optional[torch.Tensor], mask: Op
     if index != _current_device():
         return _with_device(index, logprobs_bwd, logits, targets, mask, stats, entropy, grad_logprob=grad_logprob,
                             grad_entropy=grad_entropy, top_idx=top_idx, grad_top=grad_top, scale=scale, out=out)
-    logits, rows, ld, targets, T, mask, ld_mask = _logprobs_rows(logits, targets, mask, index)
-    lead, n = shape[:-1], shape[-1]
+    px, rows, n, ld, p_targets, T, p_mask, ld_mask, lead, _kept = _logprobs_rows(logits, targets, mask, index)
     stats, entropy = _grad(stats, "stats", (*lead, 2), index), _grad(entropy, "entropy", lead, index)
     if grad_logprob is not None and targets is None:
         raise ValueError("grad_logprob needs targets")
@@ -869,9 +893,9 @@ def logprobs_bwd(logits: torch.Tensor, targets: Optional[torch.Tensor], mask: Op
         out = torch.empty_like(logits)  # half the time of torch.empty
     else:
         out = torch.empty(shape, dtype=logits.dtype, device=dev)
-    rc = _native.lib().maxsim_logprobs_bwd(logits.data_ptr(), dt, rows, n, ld, _ptr(targets), T, _ptr(mask), ld_mask, scale,
-                                           stats.data_ptr(), entropy.data_ptr(), _ptr(grad_logprob), _ptr(grad_entropy),
-                                           _ptr(top_idx), _ptr(grad_top), k, out.data_ptr(), n, _raw_stream(index))
+    rc = _native.lib().maxsim_logprobs_bwd(px, dt, rows, n, ld, p_targets, T, p_mask, ld_mask, scale, stats.data_ptr(),
+                                           entropy.data_ptr(), _ptr(grad_logprob), _ptr(grad_entropy), _ptr(top_idx),
+                                           _ptr(grad_top), k, out.data_ptr(), n, _raw_stream(index))
     if rc:
         _native.check(rc, "maxsim_logprobs_bwd")
     return out
