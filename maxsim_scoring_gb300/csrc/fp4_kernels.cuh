@@ -357,7 +357,8 @@ __host__ __device__ constexpr int fp4_flight(int group, int chunks, bool wide) {
 // code) and the codes: x is read once. The rows of all blocks together are a
 // multiple of 128, so a thread's rows have the same place in their scale tiles and
 // all its addresses go on by constant steps. Bound by HBM for f32 and for block
-// 32, by the instructions for 16-bit rows with block 16.
+// 32, by the instructions for 16-bit rows with block 16 (5000000 x 128 f16, 239 us
+// at HBM's rate: block 32 238 us, block 16 313).
 template <typename T, int kBlock, bool kWide, int kGroup, int kChunks>
 __global__ void __launch_bounds__(fp4_threads(kGroup)) fp4_quantize_kernel(const Fp4QuantizeArgs a) {
     constexpr int kThreads = fp4_threads(kGroup), kRows = kThreads / kGroup, kFlight = fp4_flight(kGroup, kChunks, kWide);
