@@ -521,6 +521,7 @@ maxsim_status maxsim_logprobs_fwd(const void *logits, maxsim_dtype dtype, int64_
  * NULL for zero (k and top_idx are read with grad_top alone). A column given
  * several times has its gradients added in order; targets of -1 and columns
  * of probability zero (log p = minus infinity) pass none. Inactive columns get 0.
+ * dlogits shares no elements with logits: a call where it does is refused.
  */
 maxsim_status maxsim_logprobs_bwd(const void *logits, maxsim_dtype dtype, int64_t rows, int64_t n, int64_t ld,
                                   const int64_t *targets, int64_t T, const uint8_t *mask, int64_t ld_mask, double scale,

@@ -119,6 +119,17 @@ maxsim_status check_rows(const void* x, maxsim_dtype dtype, int64_t rows, int64_
     return MAXSIM_OK;
 }
 
+// Whether two [rows, n] operands may share elements: their ranges meet, and they
+// are not columns side by side of rows that are equally far apart.
+bool rows_overlap(const void* x, int64_t ld_x, const void* y, int64_t ld_y, int64_t rows, int64_t n, int64_t bytes) {
+    const uintptr_t px = reinterpret_cast<uintptr_t>(x), py = reinterpret_cast<uintptr_t>(y);
+    const uintptr_t end_x = px + static_cast<uintptr_t>(((rows - 1) * ld_x + n) * bytes), end_y = py + static_cast<uintptr_t>(((rows - 1) * ld_y + n) * bytes);
+    if (px >= end_y || py >= end_x) return false;
+    if (rows == 1 || ld_x != ld_y) return true;
+    const uintptr_t row = static_cast<uintptr_t>(ld_x * bytes), off = (py > px ? py - px : px - py) % row, wide = static_cast<uintptr_t>(n * bytes);
+    return off < wide || row - off < wide;
+}
+
 }  // namespace
 }  // namespace maxsim
 
@@ -158,6 +169,8 @@ maxsim_status maxsim_logprobs_bwd(const void* logits, maxsim_dtype dtype, int64_
     if (!dx || !ptr_aligned(dx, elem_bytes(dtype)) || !stats || !ptr_aligned(stats, 8) || (grad_entropy && !entropy) ||
         (grad_top && !top_idx))
         return MAXSIM_ERR_INVALID_ARG;
+    // every warp of a row reads the given columns' logits, those of other warps' runs among them
+    if (rows_overlap(logits, ld, dx, ld_dx, rows, n, elem_bytes(dtype))) return MAXSIM_ERR_INVALID_ARG;
     if (!ptr_aligned(entropy, 4) || !ptr_aligned(grad_logprob, 4) || !ptr_aligned(grad_entropy, 4) || !ptr_aligned(top_idx, 4) ||
         !ptr_aligned(grad_top, 4))
         return MAXSIM_ERR_INVALID_ARG;

@@ -867,7 +867,7 @@ def logprobs_bwd(logits: torch.Tensor, targets: Optional[torch.Tensor], mask: Op
                  grad_top: Optional[torch.Tensor] = None, scale: float = 1.0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The gradient in logits, in their type, of logprobs_fwd with the same
     arguments, from its stats and entropy and the f32 gradients of its outputs
-    (None: zero; grad_top belongs to top_idx)."""
+    (None: zero; grad_top belongs to top_idx). out shares no elements with logits."""
     dt = _DT_ANY.get(logits.dtype)
     if dt is None:
         raise TypeError(f"logits must be float16, bfloat16 or float32, got {logits.dtype}")

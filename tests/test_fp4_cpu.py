@@ -150,6 +150,14 @@ def test_logprobs_host_validation(lib, f):
         assert f(lib, dx=None) == 1 and f(lib, dx=FAKE + 2) == 1 and f(lib, ld_dx=99) == 1 and f(lib, gt=FAKE + 2) == 1
 
 
+def test_logprobs_gradient_over_the_logits(lib):
+    """Every warp reads the given columns' logits, so the gradient may not share elements with them."""
+    f = lambda **kw: logprobs_bwd(lib, **kw)  # noqa: E731
+    assert f(dx=FAKE) == 1 and f(dx=FAKE + 4) == 1 and f(dx=FAKE + 4 * 399) == 1 and f(dx=FAKE + 4 * 200, rows=1, n=201, ld=201, ld_dx=201) == 1
+    assert f(x=FAKE + 4 * 50, dx=FAKE, ld=250, ld_dx=250) == 1          # columns that overlap, of one buffer
+    assert f(dx=FAKE + 4 * 100, ld=200, ld_dx=250) == 1                 # rows that meet somewhere
+
+
 def test_binding_refusals():
     cpu = torch.zeros(4, 64)
     with pytest.raises(ValueError):

@@ -173,6 +173,44 @@ def test_shapes_and_outputs():
     assert torch.equal(i32[0], flat[0])
 
 
+def test_gradient_beside_the_logits_but_not_over_them():
+    x, t, _ = make(8, 40, 500, "bf16", 2)
+    _, h, _, _, st = ms.logprobs_fwd(x, t)
+    g = torch.ones(40, 2, device="cuda")
+    want = ms.logprobs_bwd(x, t, None, st, h, grad_logprob=g)
+    lib, stream = ms._native.lib(), torch.cuda.current_stream().cuda_stream
+    flat = torch.empty(40 * 1003, dtype=torch.bfloat16, device="cuda")
+    both = flat.view(40, 1003)  # rows of logits, their gradients beside them
+    for xs, ds in ((0, 500), (503, 0)):
+        both.fill_(9.0)
+        both[:, xs:xs + 500] = x
+        p = flat.data_ptr()
+        rc = lib.maxsim_logprobs_bwd(p + 2 * xs, 1, 40, 500, 1003, t.data_ptr(), 2, None, 0, 1.0, st.data_ptr(), h.data_ptr(), g.data_ptr(),
+                                     None, None, None, 0, p + 2 * ds, 1003, stream)
+        assert rc == 0
+        assert torch.equal(both[:, ds:ds + 500], want) and torch.equal(both[:, xs:xs + 500], x)
+    own = x.contiguous()
+    with pytest.raises(ms._native.MaxSimError):
+        ms.logprobs_bwd(own, t, None, st, h, grad_logprob=g, out=own)
+
+
+def test_mask_bytes_of_any_value():
+    for dtype in ("f32", "bf16"):
+        for n, at in ((40, 0), (3000, 0), (3001, 1), (60000, 3)):
+            x, t, _ = make(n, 6, n, dtype, 2)
+            g = torch.Generator().manual_seed(n)
+            values = torch.tensor([0, 1, 2, 127, 128, 129, 254, 255, 16], dtype=torch.uint8)
+            m = torch.empty(6 * n + at, dtype=torch.uint8)
+            m[at:] = values[torch.randint(0, 9, (6 * n,), generator=g)]
+            m = m.cuda()[at:].view(6, n)
+            one = ms.logprobs_fwd(x, t, m != 0, k=5)
+            got = ms.logprobs_fwd(x, t, m, k=5)
+            assert all(torch.equal(a, b) for a, b in zip(one, got))
+            g1 = torch.ones(6, 2, device="cuda")
+            assert torch.equal(ms.logprobs_bwd(x, t, m != 0, one[4], one[1], grad_logprob=g1),
+                               ms.logprobs_bwd(x, t, m, one[4], one[1], grad_logprob=g1))
+
+
 def test_autograd_against_differences():
     x, t, m = make(7, 6, 50, "f32", 2, "rows", spread=1.0)
     x = x.clone().requires_grad_()
