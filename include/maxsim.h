@@ -501,9 +501,10 @@ maxsim_status maxsim_linear_fp4(const uint8_t *x, int64_t ld_x, const uint8_t *x
  *   stats        [rows, 2] f32 (out): the largest active logit M, and
  *                log2 of sum 2^((logit - M) * scale * log2 e), which
  *                maxsim_logprobs_bwd takes
- * scale > 0 and finite (an inverse temperature); rows < 2^27; stats 8-byte aligned. A row without active columns
+ * scale > 0 and finite in fp32 (an inverse temperature); rows < 2^27; stats 8-byte aligned. A row without active columns
  * above minus infinity has entropy 0, log p = minus infinity throughout and no
- * gradient. A row whose active columns hold a NaN or plus infinity gives NaN.
+ * gradient. A row whose active columns hold a NaN or plus infinity gives NaN,
+ * for its columns of minus infinity too; inactive columns keep minus infinity.
  * A target that is neither -1 nor a column gives NaN and MAXSIM_ERR_DEVICE_INPUT
  * in maxsim_device_status. One pass over the logits, in fp32. n < 2^31 - 1024.
  */

@@ -111,7 +111,7 @@ maxsim_status check_rows(const void* x, maxsim_dtype dtype, int64_t rows, int64_
                          const uint8_t* mask, int64_t ld_mask, double scale, int64_t k) {
     if (!any_dtype(dtype) || rows < 0 || n < 1 || T < 0 || k < 0 || !(scale > 0.0) || !std::isfinite(static_cast<float>(scale * kLog2E)))
         return MAXSIM_ERR_INVALID_ARG;
-    if (static_cast<float>(scale * kLog2E) == 0.f || k > n) return MAXSIM_ERR_INVALID_ARG;
+    if (static_cast<float>(scale) == 0.f || k > n) return MAXSIM_ERR_INVALID_ARG;
     if (!rows_fit(rows, n, ld) || (mask && ld_mask != 0 && !rows_fit(rows, n, ld_mask))) return MAXSIM_ERR_INVALID_ARG;
     if (rows > kI32Max / 16 || n > kI32Max - 1024 || T > kMaxTargets || k > kLogprobsMaxTop) return MAXSIM_ERR_UNSUPPORTED;
     if (rows == 0) return MAXSIM_OK;

@@ -397,23 +397,20 @@ struct RowStats {
     }
 };
 
-// The log probability of a column of value x. (Not by way of t_j, which overflows earlier.)
-__device__ __forceinline__ float value_logprob(float x, const RowStats& st, float scale) {
-    return x == minus_inf() ? x : (x - st.m) * scale - kLn2 * st.l;
-}
+// The log probability of an active column of value x. (Not by way of t_j, which
+// overflows earlier.) Minus infinity gives itself, but in a row whose sum is NaN.
+__device__ __forceinline__ float value_logprob(float x, const RowStats& st, float scale) { return (x - st.m) * scale - kLn2 * st.l; }
 
-// A target's value: minus infinity where its column is not active. `kind`: 0 a
-// column, 1 none (-1), 2 not a column.
+// A target's value. `kind`: 0 an active column, 1 none (-1), 2 not a column, 3 an inactive column.
 template <typename T>
 __device__ __forceinline__ float target_value(const LogprobsArgs& a, int64_t r, int i, const T* row, const uint8_t* mask, int* kind) {
     const int64_t j = a.targets[r * a.T + i];
-    *kind = j >= 0 && j < a.n ? 0 : j == -1 ? 1 : 2;
-    if (*kind) return 0.f;
-    return mask && !mask[j] ? minus_inf() : to_f32(row[j]);
+    *kind = j >= 0 && j < a.n ? (mask && !mask[j] ? 3 : 0) : j == -1 ? 1 : 2;
+    return *kind ? 0.f : to_f32(row[j]);
 }
 __device__ __forceinline__ void write_target(const LogprobsArgs& a, int64_t r, int i, float x, int kind, const RowStats& st) {
     if (kind == 2) atomicCAS(a.status, 0, kDeviceInput);
-    a.logprob[r * a.T + i] = kind == 0 ? value_logprob(x, st, a.scale) : kind == 1 ? 0.f : __uint_as_float(0x7fffffffu);
+    a.logprob[r * a.T + i] = kind == 0 ? value_logprob(x, st, a.scale) : kind == 1 ? 0.f : kind == 3 ? minus_inf() : __uint_as_float(0x7fffffffu);
 }
 
 // The target of thread t of the group that holds the row, read before the scan.
