@@ -521,7 +521,9 @@ maxsim_status maxsim_logprobs_fwd(const void *logits, maxsim_dtype dtype, int64_
  * h = grad_top [rows, k] for top_idx, and grad_entropy [rows], all f32, each
  * NULL for zero (k and top_idx are read with grad_top alone). A column given
  * several times has its gradients added in order; targets of -1 and columns
- * of probability zero (log p = minus infinity) pass none. Inactive columns get 0.
+ * of probability zero (log p = minus infinity) pass none. Inactive columns, and
+ * rows without active ones above minus infinity, get 0, also where the given
+ * gradients are infinite or NaN (which reach a row's other columns).
  * dlogits shares no elements with logits: a call where it does is refused.
  */
 maxsim_status maxsim_logprobs_bwd(const void *logits, maxsim_dtype dtype, int64_t rows, int64_t n, int64_t ld,

@@ -35,6 +35,8 @@ constexpr float kLn2 = 0.693147180559945309f;
 constexpr int kLogprobsMaxTop = 64;
 constexpr int kDeviceInput = 6;  // MAXSIM_ERR_DEVICE_INPUT
 constexpr float kNoExponent = -1000.f;  // 2^t is 0 from here on
+constexpr float kLowExponent = -65536.f;  // exponents that are not cut to kNoExponent end here
+constexpr float kLargest = 0x1.fffffep127f;
 
 __device__ __forceinline__ float exp2_fast(float t) {  // 2^-22 relative
     float y;
@@ -941,10 +943,12 @@ __global__ void __launch_bounds__(256, BwdCfg::kBlocks) logprobs_bwd_kernel(cons
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const float gh = a.g_entropy ? a.g_entropy[r] : 0.f;
-    const float A = -a.scale * __fmaf_rn(gh, gh != 0.f ? a.entropy[r] : 0.f, sum), B = -a.scale * gh * kLn2;
+    float A = -a.scale * __fmaf_rn(gh, gh != 0.f ? a.entropy[r] : 0.f, sum), B = -a.scale * gh * kLn2;
+    if (m.y == -minus_inf()) A = B = 0.f;  // an empty row passes no gradient, whatever it is given
     const float2 ref = make_float2(-m.x, -m.x), c2 = make_float2(a.c, a.c), l2 = make_float2(-m.y, -m.y);
     const float2 A2 = make_float2(A, A), B2 = make_float2(B, B);
-    const bool broken = !(m.x == m.x && m.y == m.y);  // a row of NaN: its inactive columns are 0 all the same
+    // a row of NaN, or given gradients that are not finite: p * (A + B * log2 p) is NaN for p = 0 too, inactive columns are 0 all the same
+    const bool broken = !(m.x == m.x && m.y == m.y && fabsf(A) <= kLargest && fabsf(B) * -kNoExponent <= kLargest);
     // whole pieces
     const int32_t w0 = max(first, row.skip ? 1 : 0), w1 = min(last, (row.n + row.skip) / kVec);
     const uint4 none = make_uint4(P::kMinusInf, P::kMinusInf, P::kMinusInf, P::kMinusInf);
@@ -991,7 +995,7 @@ __global__ void __launch_bounds__(256, BwdCfg::kBlocks) logprobs_bwd_kernel(cons
         uint32_t least = P::min_words(u[0]);
 #pragma unroll
         for (int i = 1; i < kBwdPieces; ++i) least = P::min_words(least, P::min_words(u[i]));
-        const bool low = !((P::word_min(least) + ref.x) * a.c > -1e30f) || !(m.y < 1e30f);
+        const bool low = !((P::word_min(least) + ref.x) * a.c > kLowExponent) || !(m.y < 1e30f);
         const int32_t c0 = row.column(p0), c1 = c0 + 32 * kBwdPieces * kVec;
         const uint32_t here = __ballot_sync(0xffffffffu, j >= c0 && j < c1);
 #pragma unroll
