@@ -485,13 +485,58 @@ struct Fp4DequantizeArgs {
     int32_t cols, words;
 };
 
-// y = code * block scale * row scale, rounded once: a code times an E4M3 scale
-// has at most six bits, and the row scales that the quantisation gives are
-// powers of two, so 16-bit rows are exact wherever their exponents reach.
+// Both products a * b, each between fp32's neighbours of it rounded to the one
+// whose last bit is odd (an exact one stays): what is then rounded to fewer bits is
+// rounded as the exact product would be.
+__device__ __forceinline__ float2 mul2_odd(float2 a, float2 b) {
+    float2 lo, hi;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%4, %5};\n\tmov.b64 y, {%6, %7};\n\tmul.rm.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t"
+        "mul.rp.f32x2 z, x, y;\n\tmov.b64 {%2, %3}, z;\n\t}"
+        : "=f"(lo.x), "=f"(lo.y), "=f"(hi.x), "=f"(hi.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return make_float2(__float_as_uint(lo.x) & 1u ? lo.x : hi.x, __float_as_uint(lo.y) & 1u ? lo.y : hi.y);
+}
+
+// A code times an E8M0 scale of 2^126 or 2^127 may leave fp32's range where the row
+// scale brings it back: an eighth of the one then goes with eight times the other
+// (of a row scale so large that eight times it overflow, every product does).
+__device__ __forceinline__ void keep_range(uint32_t byte, float& b, float& s) {
+    if (byte > 252u) {
+        b *= 0.125f;
+        if (fabsf(s) < 0x1p125f) s *= 8.f;
+    }
+}
+
+// The values of 16 codes in a row whose scale is no power of two, for 16-bit
+// outputs. Not inlined: its registers would take a block from the SM.
+template <typename T>
+__device__ __noinline__ Sixteen<T> rounded16(uint2 codes, float b, float s) {
+    uint32_t h[2][4];
+    from_e2m1x8(codes.x, h[0]);
+    from_e2m1x8(codes.y, h[1]);
+    Sixteen<T> v;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 f = mul2_odd(mul2(unpack2<__half>(h[i >> 2][i & 3]), make_float2(b, b)), make_float2(s, s));
+        v.w[i] = pack2<T>(f.x, f.y);
+    }
+    return v;
+}
+
+// Blocks an SM holds at least: registers for more spill, and fewer leave HBM waiting.
+// Rows off their boundaries, 3 and 2: 1000000 x 300 f32, block 16, 299 and 319 us;
+// 262144 x 1023 f32, block 32, 282 and 273.
+template <typename T, int kBlock>
+__host__ __device__ constexpr int fp4_read_blocks(bool wide) { return wide ? 4 : sizeof(T) == 4 && kBlock == 32 ? 2 : 3; }
+
+// y = code * block scale * row scale, rounded once. A code times its block scale
+// has at most six bits, so with a row scale that is a power of two (the
+// quantisation gives no others) the product in fp32 is exact wherever a 16-bit
+// rounding could tell. Rows with other scales take a branch of their own
+// (5000000 x 128 bf16, block 16: 258 us, the branch 260; 262144 x 1023: 152 and 184).
 // kGroup threads of a row take 16 elements each; kFlight of a thread's pieces are
 // loaded together, of kFlight rows (kRowsAhead, short rows) or of one. Bound by HBM.
 template <typename T, int kBlock, bool kWide, int kGroup, bool kRowsAhead>
-__global__ void __launch_bounds__(256) fp4_dequantize_kernel(const Fp4DequantizeArgs a) {
+__global__ void __launch_bounds__(256, fp4_read_blocks<T, kBlock>(kWide)) fp4_dequantize_kernel(const Fp4DequantizeArgs a) {
     constexpr int kRows = 256 / kGroup, kFlight = 4;
     const int t = threadIdx.x % kGroup;
     const int32_t chunks = (a.cols >> 4) + ((a.cols & 15) != 0);
@@ -520,20 +565,28 @@ __global__ void __launch_bounds__(256) fp4_dequantize_kernel(const Fp4Dequantize
                 const int64_t row = kRowsAhead ? row0 + j * row_step : row0;
                 const int32_t chunk = c0 + t + (kRowsAhead ? 0 : j * kGroup);
                 const bool in = row < a.rows && chunk < chunks;
-                const float b = block_scale_value<kBlock>(byte[j]);
-                uint32_t h[2][4];
-                from_e2m1x8(codes[j].x, h[0]);
-                from_e2m1x8(codes[j].y, h[1]);
+                float b = block_scale_value<kBlock>(byte[j]), row_s = s[j];
+                if constexpr (kBlock == 32) keep_range(byte[j], b, row_s);
                 Sixteen<T> v;
+                bool whole = true;
+                if constexpr (sizeof(T) == 2) {
+                    whole = (__float_as_uint(row_s) & 0x7fffffu) == 0;
+                    if (!whole) v = rounded16<T>(codes[j], b, row_s);
+                }
+                if (whole) {
+                    uint32_t h[2][4];
+                    from_e2m1x8(codes[j].x, h[0]);
+                    from_e2m1x8(codes[j].y, h[1]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    // code * b first: its product with the row scale is the only one that may round
-                    const float2 f = mul2(mul2(unpack2<__half>(h[i >> 2][i & 3]), make_float2(b, b)), make_float2(s[j], s[j]));
-                    if constexpr (sizeof(T) == 4) {
-                        v.w[2 * i] = __float_as_uint(f.x);
-                        v.w[2 * i + 1] = __float_as_uint(f.y);
-                    } else {
-                        v.w[i] = pack2<T>(f.x, f.y);
+                    for (int i = 0; i < 8; ++i) {
+                        // code * b first: its product with the row scale is the only one that may round
+                        const float2 f = mul2(mul2(unpack2<__half>(h[i >> 2][i & 3]), make_float2(b, b)), make_float2(row_s, row_s));
+                        if constexpr (sizeof(T) == 4) {
+                            v.w[2 * i] = __float_as_uint(f.x);
+                            v.w[2 * i + 1] = __float_as_uint(f.y);
+                        } else {
+                            v.w[i] = pack2<T>(f.x, f.y);
+                        }
                     }
                 }
                 const int64_t at = static_cast<int64_t>(chunk) * 16;
