@@ -464,14 +464,16 @@ maxsim_status maxsim_dequantize_rows_fp4(const uint8_t *q, int64_t ld_q, const u
 
 /*
  * Matrix product of 4-bit floating-point rows:
- *   out[m, n] = (sum_k x[m, k] * w[n, k]) * x_scale[m] * w_scale[n] + bias[n]
+ *   out[m, n] = (sum_k x[m, k] * w[n, k]) * (x_scale[m] * w_scale[n]) + bias[n]
  * with x[m, k] and w[n, k] the codes times their block scales.
  *   x [M, K], w [N, K]: rows ld_x / ld_w bytes apart, with their block scales;
  *   x_scale [M], w_scale [N] f32 or NULL (1);  bias [N] f32 or NULL
  *   out [M, N] f16 / bf16 / f32 (out_dtype), rows ld_out elements apart
  * K counts what the rows hold, a multiple of 32 (codes behind a row's end are
- * 0 and add nothing). The sum over k is accumulated in fp32, the scales and the
- * bias are applied in fp32 and the result is rounded once. The same call on
+ * 0 and add nothing). The sum over k is accumulated in fp32; the scales' product
+ * x_scale[m] * w_scale[n], rounded to fp32's 24 digits but not to its range, takes
+ * it to the result in one multiplication and addition in fp32, and the result is
+ * rounded once more to 16 bits where out has them. The same call on
  * the same inputs gives the same bits. A NaN scale gives NaN in the outputs of
  * its row or column. 0 <= M, N < 2^31 - 1023, K <= 2^28, row strides below 2^40.
  * No workspace.

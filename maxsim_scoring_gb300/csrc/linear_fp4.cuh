@@ -1,4 +1,4 @@
-// out[m, n] = (sum_k x[m, k] w[n, k]) * x_scale[m] * w_scale[n] + bias[n] for
+// out[m, n] = (sum_k x[m, k] w[n, k]) * (x_scale[m] * w_scale[n]) + bias[n] for
 // rows of 4-bit floating-point values with block scales (fp4_kernels.cuh).
 //
 // The codes and their block scales go to the tensor cores as they are:
@@ -193,6 +193,39 @@ __device__ __forceinline__ void not_before(float (&v)[32]) {
                  "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]),
                  "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]));
     asm volatile("" : "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));
+}
+
+// The row scales' product s_x s_w comes first (its value does not depend on which
+// of the operands is A), rounded to fp32's digits; one fma takes it to the sum and
+// the bias. Where products of a warp's scales leave fp32's range, as those of rows
+// of 2^-100 and of 2^100 may where the results do not, part of their exponents goes
+// to the sums. What a scale asks of that: the exponents of its lowest and highest
+// bits (biased by 127); zeros, infinities and NaN nothing.
+__device__ __forceinline__ void scale_range(float s, int& low, int& high) {
+    const uint32_t bits = __float_as_uint(s) & 0x7fffffffu;
+    const int e = static_cast<int>(bits >> 23);
+    if (bits == 0 || e == 255) return;
+    low = min(low, e == 0 ? -22 : (bits & 0x7fffffu) ? e - 23 : e);
+    high = max(high, e);
+}
+// 2^-62 <= |s| < 2^62: no product of two leaves the range.
+__device__ __forceinline__ bool scale_near_one(float s) { return (__float_as_uint(s) & 0x7fffffffu) - (65u << 23) < (124u << 23); }
+// s = m 2^k with 1 <= |m| < 2 (zeros, infinities and NaN: m = s, k = 0).
+__device__ __forceinline__ void split_scale(float& s, int& k) {
+    const float up = s * 0x1p24f;
+    const bool tiny = fabsf(s) < 0x1p-126f;
+    const uint32_t bits = __float_as_uint(tiny ? up : s), e = bits >> 23 & 255u;
+    k = 0;
+    if (e == 0 || e == 255u) return;
+    k = static_cast<int>(e) - (tiny ? 151 : 127);
+    s = __uint_as_float((bits & 0x807fffffu) | 0x3f800000u);
+}
+__device__ __forceinline__ float power_of_two(int k) { return __uint_as_float(static_cast<uint32_t>(k + 127) << 23); }
+// sum * m 2^k + bias, |m| < 4: m 2^k within fp32's range, the rest of 2^k goes to the sum
+// (where it takes digits from it the result is far below fp32's least).
+__device__ __forceinline__ float scale_sum(float sum, float m, int k, float bias) {
+    const int near = max(-124, min(124, k)), rest = k - near, first = max(-126, min(127, rest));
+    return __fmaf_rn(sum * power_of_two(first) * power_of_two(rest - first), m * power_of_two(near), bias);
 }
 
 // Every thread of every CTA of the cluster, whatever its warp's other threads do.
@@ -429,8 +462,8 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
             const int64_t ra0 = row * kFp4TileM + rank * 128 + q * 32, rb0 = (it - row * a.tiles_b) * kTN + half * kCols;
             const int row_n = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(32), a.rows_a - ra0)));
             const bool in_a = lane < row_n;
-            const float sa = scale_a && in_a ? __ldg(scale_a + ra0 + lane) : 1.f;
-            const float bias_a = kSwap && a.l.bias && in_a ? __ldg(a.l.bias + ra0 + lane) : 0.f;
+            float sa = scale_a && in_a ? __ldg(scale_a + ra0 + lane) : 1.f;
+            float bias_a = kSwap && a.l.bias && in_a ? __ldg(a.l.bias + ra0 + lane) : 0.f;
             float sb[kChunks], bias[kChunks];
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
@@ -450,7 +483,6 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
                 }
                 __syncwarp();
             }
-            const float2 sa2 = make_float2(sa, sa);
             const uint32_t src0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * kCols);
             uint32_t held[kHold ? kChunks : 1][16];
             // other pairs' sums: [splits - 1][kTN][128], of this lane's row and first column
@@ -495,14 +527,52 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
 #pragma unroll
                     for (int i = 0; i < kCols; ++i) v[i / 32][i % 32] += parts[s * (kTN * 128) + i * 128];
             }
+            bool plain = scale_near_one(sa);
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) plain = plain && scale_near_one(sb[c]);
+            plain = __all_sync(0xffffffffu, plain);
+            if (!plain) {
+                // all products in range, and those of powers of two exact (zero rows have 2^-126)?
+                int low_a = 127, high_a = 127, low_b = 127, high_b = 127;
+                scale_range(sa, low_a, high_a);
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) scale_range(sb[c], low_b, high_b);
+                plain = __reduce_min_sync(0xffffffffu, low_a) + __reduce_min_sync(0xffffffffu, low_b) >= 254 - 149 &&
+                        __reduce_max_sync(0xffffffffu, high_a) + __reduce_max_sync(0xffffffffu, high_b) <= 254 + 126;
+            }
+            if (!plain) {  // results in place of the sums
+                int ka, kb[kChunks];
+                split_scale(sa, ka);
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) split_scale(sb[c], kb[c]);
+#pragma unroll
+                for (int i = 0; i < kCols; ++i) {
+                    const int c = i / 32;
+                    const float m = sa * __shfl_sync(0xffffffffu, sb[c], i % 32), more = kSwap ? bias_a : __shfl_sync(0xffffffffu, bias[c], i % 32);
+                    v[c][i % 32] = scale_sum(v[c][i % 32], m, ka + __shfl_sync(0xffffffffu, kb[c], i % 32), more);
+                }
+                sa = 1.f;
+                bias_a = 0.f;
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    sb[c] = 1.f;
+                    bias[c] = 0.f;
+                    if constexpr (kHold) {
+                        tab[c * 32 + lane] = 1.f;
+                        if constexpr (!kSwap) tab[kCols + c * 32 + lane] = 0.f;
+                    }
+                }
+                __syncwarp();
+            }
+            const float2 sa2 = make_float2(sa, sa);
             if constexpr (kHold) {
 #pragma unroll
                 for (int i = 0; i < kCols; i += 4) {
                     const float* u = v[i / 32] + i % 32;
                     const float4 s4 = *reinterpret_cast<const float4*>(tab + i);
                     const float4 b4 = kSwap ? make_float4(bias_a, bias_a, bias_a, bias_a) : *reinterpret_cast<const float4*>(tab + kCols + i);
-                    const float2 lo = fma2(mul2(make_float2(u[0], u[1]), sa2), make_float2(s4.x, s4.y), make_float2(b4.x, b4.y));
-                    const float2 hi = fma2(mul2(make_float2(u[2], u[3]), sa2), make_float2(s4.z, s4.w), make_float2(b4.z, b4.w));
+                    const float2 lo = fma2(make_float2(u[0], u[1]), mul2(make_float2(s4.x, s4.y), sa2), make_float2(b4.x, b4.y));
+                    const float2 hi = fma2(make_float2(u[2], u[3]), mul2(make_float2(s4.z, s4.w), sa2), make_float2(b4.z, b4.w));
                     held[i / 32][i % 32 / 2] = pack2<T>(lo.x, lo.y);
                     held[i / 32][i % 32 / 2 + 1] = pack2<T>(hi.x, hi.y);
                 }
@@ -520,14 +590,14 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
                         float* p = out + rb * ld + ra0 + lane;
 #pragma unroll
                         for (int i = 0; i < 32; ++i, p += ld) {
-                            const float y = __fmaf_rn(v[c][i] * __shfl_sync(0xffffffffu, sb[c], i), sa, bias_a);
+                            const float y = __fmaf_rn(v[c][i], __shfl_sync(0xffffffffu, sb[c], i) * sa, bias_a);
                             if (i < n && in_a) *p = y;
                         }
                     } else {
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
                             *reinterpret_cast<float4*>(stage + staged(lane, i)) =
-                                make_float4(v[c][4 * i] * sa, v[c][4 * i + 1] * sa, v[c][4 * i + 2] * sa, v[c][4 * i + 3] * sa);
+                                make_float4(v[c][4 * i], v[c][4 * i + 1], v[c][4 * i + 2], v[c][4 * i + 3]);
                         __syncwarp();
                         if constexpr (kRows16) {
                             float ws[4], bs[4];  // this lane's four channels
@@ -542,9 +612,10 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
 #pragma unroll
                             for (int i = 0; i < 8; ++i, at += 4 * ld) {
                                 const float4 y = *reinterpret_cast<const float4*>(stage + staged(4 * i + (lane >> 3), lane & 7));
+                                const float xs = __shfl_sync(0xffffffffu, sa, 4 * i + (lane >> 3));  // of the row
                                 if (4 * i + (lane >> 3) < row_n)
-                                    store4(out + at, n, __fmaf_rn(y.x, ws[0], bs[0]), __fmaf_rn(y.y, ws[1], bs[1]),
-                                           __fmaf_rn(y.z, ws[2], bs[2]), __fmaf_rn(y.w, ws[3], bs[3]));
+                                    store4(out + at, n, __fmaf_rn(y.x, ws[0] * xs, bs[0]), __fmaf_rn(y.y, ws[1] * xs, bs[1]),
+                                           __fmaf_rn(y.z, ws[2] * xs, bs[2]), __fmaf_rn(y.w, ws[3] * xs, bs[3]));
                             }
                         } else {  // rows off their 16-byte boundaries: a row at a time, a lane per column
                             const bool in_b = rb + lane < a.rows_b;
@@ -553,7 +624,8 @@ linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
 #pragma unroll 8
                             for (int r = 0; r < row_n; ++r, at += ld) {
                                 const float y = *reinterpret_cast<const float*>(from + staged(r, lane >> 2));
-                                if (in_b) out[at] = __fmaf_rn(y, sb[c], bias[c]);
+                                const float f = sb[c] * __shfl_sync(0xffffffffu, sa, r);
+                                if (in_b) out[at] = __fmaf_rn(y, f, bias[c]);
                             }
                         }
                         __syncwarp();
