@@ -162,6 +162,10 @@ maxsim_status maxsim_logprobs_bwd(const void* logits, maxsim_dtype dtype, int64_
                                   const float* stats, const float* entropy, const float* grad_logprob,
                                   const float* grad_entropy, const int32_t* top_idx, const float* grad_top, int64_t k,
                                   void* dx, int64_t ld_dx, void* stream) {
+    if (!grad_top) {  // neither is read
+        k = 0;
+        top_idx = nullptr;
+    }
     const maxsim_status ok = check_rows(logits, dtype, rows, n, ld, targets, T, mask, ld_mask, scale, k);
     if (ok != MAXSIM_OK) return ok;
     if (!rows_fit(rows, n, ld_dx)) return MAXSIM_ERR_INVALID_ARG;
