@@ -10,6 +10,7 @@
 #include <type_traits>
 
 #include "fp4_kernels.cuh"
+#include "linear_fp4_plan.h"
 #include "ptx.cuh"
 #include "tile_store.cuh"
 
@@ -29,8 +30,6 @@ struct LinearFp4Args {
     int32_t words;               // scale words of a row
 };
 
-constexpr int kFp4TileM = 256;      // rows of A per tile: 128 on each CTA of a pair
-constexpr int kFp4TileK = 256;      // values of K per stage: 128 bytes of a row
 constexpr int kFp4Threads = 384;    // warps 0 and 3 TMA, warps 1 and 2 MMA and scales (even CTA), warps 4-11 epilogue
 constexpr int kFp4EpiWarp0 = 4;
 // Registers a thread: the launch gives kFp4Regs, of which the first warpgroup
@@ -38,7 +37,6 @@ constexpr int kFp4EpiWarp0 = 4;
 // accumulator's hand-over and the stores.
 constexpr int kFp4Regs = 168, kFp4RegsCtl = 80, kFp4RegsEpi = 208;
 static_assert(kFp4RegsCtl + 2 * kFp4RegsEpi <= 3 * kFp4Regs, "register split");
-constexpr int kFp4MaxSplits = 4;
 
 template <int kTN>
 struct Fp4Cfg {

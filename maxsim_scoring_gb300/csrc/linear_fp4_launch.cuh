@@ -15,13 +15,6 @@
 
 namespace maxsim {
 
-struct LinearFp4Plan {
-    bool swap = false;  // A is w, B is x
-    int tn = 64;
-    int64_t tiles = 0, tiles_b = 0;
-    int32_t kb = 0, splits = 1, kb_split = 0;
-};
-
 // [rows, bytes] codes, rows ld bytes apart, in boxes of 128 bytes x box_rows.
 inline bool encode_codes(EncodeTiledFn encode, CUtensorMap* map, const void* base, int64_t bytes, int64_t rows, int64_t ld, uint32_t box_rows) {
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(bytes), static_cast<cuuint64_t>(rows)};
