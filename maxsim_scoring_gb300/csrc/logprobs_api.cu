@@ -70,9 +70,14 @@ maxsim_status launch_fwd(const LogprobsArgs& a, const HostDevice& dev, cudaStrea
     // few rows: the blocks of a cluster share one
     int blocks = 1;
     while (blocks < 16 && a.rows * blocks * 2 <= int64_t(dev.num_sms) * 4 && pieces / (blocks * 2) >= 512) blocks *= 2;
-    // Measured, blocks of 128 and of 256 threads: 4096 x 131072 bf16 158 and 162 us, with 5 columns listed 197 and
-    // 210, with 64 300 and 248; 1 x 1000000 f32 12.9 and 9.5.
-    if (pieces / blocks <= 8192 || (blocks == 1 && a.k <= 16)) return launch_block<T, kMask, kTop, 128>(a, blocks, dev, st);
+    // Threads of a block, by the GPU times with 128 and 256 (us). Where all blocks run at once, more threads pay for long
+    // shares: 1 x 300000 f32 5.9 and 4.7 (4,687 pieces a block), 600 x 1000000 bf16 239 and 185, but 150 x 65536 bf16 6.5
+    // and 7.7 (2,048 pieces). Where they take turns, more blocks do, until many columns are listed: 4096 x 131072 bf16
+    // without any 157 and 162, with 5 186 and 209, with 20 203 and 217, with 64 274 and 246; 5000 x 131072 f16 with 32
+    // 271 and 278, with 40 287 and 282; 8192 x 32768 bf16 with 64 157 and 185 (4,096 pieces). (f32 rows without any lose
+    // by it: 700 x 400000 183 and 158, 4096 x 32768 79 and 81.)
+    const bool at_once = a.rows * blocks <= int64_t(dev.num_sms) * 4;
+    if (at_once ? pieces / blocks <= 4096 : pieces <= 8192 || a.k < 40) return launch_block<T, kMask, kTop, 128>(a, blocks, dev, st);
     return launch_block<T, kMask, kTop, 256>(a, blocks, dev, st);
 }
 
