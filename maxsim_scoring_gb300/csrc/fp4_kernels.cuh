@@ -534,7 +534,9 @@ __host__ __device__ constexpr int fp4_read_blocks(bool wide) { return wide ? 4 :
 // rounding could tell. Rows with other scales take a branch of their own
 // (5000000 x 128 bf16, block 16: 258 us, the branch 260; 262144 x 1023: 152 and 184).
 // kGroup threads of a row take 16 elements each; kFlight of a thread's pieces are
-// loaded together, of kFlight rows (kRowsAhead, short rows) or of one. Bound by HBM.
+// loaded together, of kFlight rows (kRowsAhead, short rows) or of one. Bound by HBM;
+// rows off their boundaries by the instructions that join and shift pieces
+// (262144 x 1023 bf16: 152 us, HBM at 52 % of its rate; 262144 x 1024: 113).
 template <typename T, int kBlock, bool kWide, int kGroup, bool kRowsAhead>
 __global__ void __launch_bounds__(256, fp4_read_blocks<T, kBlock>(kWide)) fp4_dequantize_kernel(const Fp4DequantizeArgs a) {
     constexpr int kRows = 256 / kGroup, kFlight = 4;

@@ -245,8 +245,10 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // splits > 1 (few tiles): the pairs of a cluster share a tile's K; the others'
 // sums pass to the first pair's shared memory and are added in their order.
 // Measured: 32768 x 4096 x 4096 bf16, block 16, 176 us in short runs, 6.2 PFLOP/s;
-// a stage takes 600 cycles, 512 of them MMAs, and a tile's hand-over 2,300 (one
-// accumulator of 256 columns). 1048576 x 128 x 1024 f16: 129 us, 6.8 TB/s, HBM.
+// of a tile's 11,400 cycles (clock64) a stage takes 660, 512 of them MMAs, and 900
+// pass until the one accumulator of 256 columns is free: 680 of the last MMAs, 330
+// of the epilogue's reading it (whose 256-column tiles spill 40 bytes).
+// 1048576 x 128 x 1024 f16: 129 us, 6.8 TB/s, HBM.
 // 1 x 4096 x 4096: 7.6 us, latency.
 template <typename T, int kTN, bool kSwap, bool kRows16>
 __global__ void __launch_bounds__(kFp4Threads, 1)

@@ -19,9 +19,10 @@ struct LinearFp4Plan {
 
 // The tile's width, and the pairs of a cluster that share a tile's K where there
 // are few tiles, by the time they should take, in cycles: the tiles of the
-// busiest pair, each its stages and a start and end. (Measured: a stage takes 600
-// cycles with 256 columns, and 490 and 460 with 128 and 64, where the MMA warp's
-// issue bounds it.) Clusters of four CTAs: a GB300 holds 36 of them; of eight only 15.
+// busiest pair, each its stages and a start and end. (Fitted to the times of whole
+// products: a stage takes 600 cycles with 256 columns, and 490 and 460 with 128 and
+// 64, where the MMA warp's issue bounds it; the rest of a tile 2,300, 1,000 and 700.)
+// Clusters of four CTAs: a GB300 holds 36 of them; of eight only 15.
 inline LinearFp4Plan plan_linear_fp4(int64_t M, int64_t N, int64_t K) {
     LinearFp4Plan p;
     p.swap = N > M;
